@@ -264,6 +264,69 @@ void zn_tableset_free(zn_tableset *ts);
 
 const char *zn_status_str(zn_status s);
 
+/* ---- microscaled numbers ----
+ * Low-precision rows beside the codec: codes of ZN_FP8_E4M3 or ZN_FP4X2_E2M1
+ * (exactly the tensors of these dtypes that zn_compress takes) and one scale
+ * byte for every 32 consecutive values of a row (the block and the E8M0 byte
+ * of the OCP Microscaling Formats v1.0).  A value is code * 2^(s - 127); the
+ * byte s = 255 is a NaN, which makes the whole block NaN.
+ *
+ * A row of k values is stored as kp = 32 * ceil(k / 32) codes (kp bytes of
+ * E4M3, kp / 2 bytes of E2M1 pairs), zero past k, and kp / 32 scale bytes;
+ * rows follow each other without gaps.  Codes must be 16-byte aligned; scale
+ * bytes and plain rows may lie anywhere (plain elements at their own size;
+ * 16-byte aligned rows take wide loads).  Plain rows are `*_stride` elements
+ * apart; an input's stride may be 0 (one row read many times), an output's is
+ * at least the row (ZN_ERR_ARG).  k is 1 .. 2^30, rows at most 2^31 - 1; rows
+ * = 0 does nothing.
+ *
+ * The calls launch on the caller's stream for the current device, which has
+ * to be the memory's, allocate nothing and may be captured into a graph.
+ * Outputs must not overlap inputs except where stated.  Results do not depend
+ * on the launch: the same inputs give the same bits. */
+
+/* zn_mx_quantize -- plain rows (ZN_BF16 or ZN_FP32) to codes and scales:
+ * s = clamp(floor(log2 max|x|) + 127 - emax, 0, 254) over the block, emax 8
+ * (E4M3) or 2 (E2M1), s = 0 for a block of zeros; the codes are x / 2^(s-127)
+ * rounded to nearest even and saturated at 448 or 6, with the sign of x also
+ * on zeros.  A block that holds an infinity or a NaN gets s = 255 and zero
+ * codes. */
+zn_status zn_mx_quantize(zn_dtype dtype, const void *d_x, uint64_t x_stride, uint64_t rows, uint64_t k,
+                         zn_dtype fmt, void *d_codes, void *d_scales, hipStream_t stream);
+
+/* zn_mx_dequantize -- the first k values of every row as ZN_BF16 or ZN_FP32,
+ * rounded once (both are exact except among the type's subnormals and where
+ * code * 2^(s-127) exceeds the type's range, which gives infinity). */
+zn_status zn_mx_dequantize(zn_dtype fmt, const void *d_codes, const void *d_scales, uint64_t rows, uint64_t k,
+                           zn_dtype dtype, void *d_out, uint64_t out_stride, hipStream_t stream);
+
+/* zn_mx_rms_norm -- the residual's addition, the root-mean-square norm and
+ * the quantisation of its output in one pass:
+ *   h = x + residual, rounded to dtype and stored in d_residual_out;
+ *   y = h * weight / sqrt(mean(h^2) + eps), quantised as zn_mx_quantize does.
+ * d_residual and d_residual_out are both NULL for h = x (nothing is stored
+ * then).  x, residual, weight (k values) and the stored sum share one dtype.
+ * d_residual_out may be d_x or d_residual itself, with its stride.  The mean
+ * is summed in 64 bits: no finite row overflows.  eps is finite and >= 0. */
+zn_status zn_mx_rms_norm(zn_dtype dtype, const void *d_x, uint64_t x_stride, const void *d_residual,
+                         uint64_t residual_stride, const void *d_weight, float eps, uint64_t rows, uint64_t k,
+                         void *d_residual_out, uint64_t residual_out_stride, zn_dtype fmt, void *d_codes,
+                         void *d_scales, hipStream_t stream);
+
+/* zn_mx_matmul -- out[m][n] = sum over k of a[m][k] * w[n][k], both sides
+ * microscaled (either format each), summed in FP32 on the matrix units and
+ * rounded once to ZN_BF16 or ZN_FP32.  k is the stored length of a row, a
+ * multiple of 32.  Row m of the output starts at element m * out_stride.
+ * Needs zn_mx_matmul_scratch_bytes() bytes of 16-byte aligned device scratch
+ * (ZN_ERR_CAPACITY if it is less; 0 for many sizes, then d_scratch may be
+ * NULL); calls that may run at the same time, and graphs that may replay at
+ * the same time, need scratch of their own. */
+zn_status zn_mx_matmul_scratch_bytes(zn_dtype a_fmt, zn_dtype w_fmt, uint64_t m, uint64_t n, uint64_t k,
+                                     uint64_t *bytes);
+zn_status zn_mx_matmul(zn_dtype a_fmt, const void *d_a, const void *d_a_scales, zn_dtype w_fmt, const void *d_w,
+                       const void *d_w_scales, uint64_t m, uint64_t n, uint64_t k, zn_dtype out_dtype, void *d_out,
+                       uint64_t out_stride, void *d_scratch, uint64_t scratch_bytes, hipStream_t stream);
+
 /* ---- single steps, for parity tests of each stage (asynchronous) ----
  * zn_debug_histograms: order-0 histograms of every coded stream of every
  *   chunk of the plan: d_hist[n_chunks][n_coded][256] u32.

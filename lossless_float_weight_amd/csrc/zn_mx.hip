@@ -1,0 +1,386 @@
+// zn_mx.hip -- microscaled numbers (E4M3 or E2M1 codes, one E8M0 scale per 32
+// values): quantisation, reading back, and the root-mean-square norm whose
+// output is quantised in the same pass.
+#include "zn_mx.h"
+
+namespace zn {
+namespace {
+
+// Eight consecutive elements of a row from k0 on; zeros past k.  `fast`: the
+// row is 16-byte aligned, so a group that lies in it whole takes wide loads.
+template <int DT>
+__device__ __forceinline__ void load8(const uint8_t *row, uint32_t k0, uint32_t k, bool fast, float (&v)[8]) {
+  if (fast && k0 + 8 <= k) {
+    if constexpr (DT == BF16) {
+      const u32x4 w = *reinterpret_cast<const u32x4 *>(row + 2 * uint64_t(k0));
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[2 * i] = bf16_lo(w[i]);
+        v[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+      const f32x4 a = *reinterpret_cast<const f32x4 *>(row + 4 * uint64_t(k0));
+      const f32x4 b = *reinterpret_cast<const f32x4 *>(row + 4 * uint64_t(k0) + 16);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        v[i] = a[i];
+        v[4 + i] = b[i];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    v[i] = 0.0f;
+    if (k0 + i < k) {
+      if constexpr (DT == BF16)
+        v[i] = bf16_lo(*reinterpret_cast<const uint16_t *>(row + 2 * uint64_t(k0 + i)));
+      else
+        v[i] = *reinterpret_cast<const float *>(row + 4 * uint64_t(k0 + i));
+    }
+  }
+}
+
+// Eight consecutive elements of a row, those below k; v is already rounded
+// to DT's grid or is rounded here.
+template <int DT>
+__device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, bool fast, const float (&v)[8]) {
+  if (fast && k0 + 8 <= k) {
+    if constexpr (DT == BF16) {
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; i++) w[i] = f32_bf16(v[2 * i]) | (f32_bf16(v[2 * i + 1]) << 16);
+      *reinterpret_cast<u32x4 *>(row + 2 * uint64_t(k0)) = w;
+    } else {
+      f32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        a[i] = v[i];
+        b[i] = v[4 + i];
+      }
+      *reinterpret_cast<f32x4 *>(row + 4 * uint64_t(k0)) = a;
+      *reinterpret_cast<f32x4 *>(row + 4 * uint64_t(k0) + 16) = b;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; i++)
+    if (k0 + i < k) {
+      if constexpr (DT == BF16)
+        *reinterpret_cast<uint16_t *>(row + 2 * uint64_t(k0 + i)) = uint16_t(f32_bf16(v[i]));
+      else
+        *reinterpret_cast<float *>(row + 4 * uint64_t(k0 + i)) = v[i];
+    }
+}
+
+__device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
+  uint32_t t = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const uint32_t b = __float_as_uint(v[i]) & 0x7FFFFFFFu;
+    t = t > b ? t : b;
+  }
+  return t;
+}
+
+// Codes and scale byte of group gi (8 values, a quarter of a block) of a
+// tensor whose groups are numbered through all rows.  The four lanes of a
+// quad hold one block.
+template <int FMT>
+__device__ __forceinline__ void put_codes(uint8_t *codes, uint8_t *scales, uint64_t gi, const float (&v)[8], bool live) {
+  const uint32_t s = mx_scale_byte<FMT>(quad_max(top8(v)));
+  const u32x2 c = mx_codes8<FMT>(v, s);
+  if (!live) return;
+  if constexpr (FMT == FP8)
+    *reinterpret_cast<u32x2 *>(codes + 8 * gi) = c;
+  else
+    *reinterpret_cast<uint32_t *>(codes + 4 * gi) = c[0];
+  if ((gi & 3) == 0) scales[gi >> 2] = uint8_t(s);
+}
+
+// ---------------------------------------------------------------- quantise --
+// A lane takes 8 consecutive values (16 bytes of BF16), a quad one block of
+// 32; the block's maximum is exchanged inside the quad.
+template <int DT, int FMT, int U>
+__global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr, uint32_t groups, bool fast) {
+  const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+  float v[U][8];
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    const uint32_t gc = g < groups ? g : 0;
+    const uint32_t row = gpr.div(gc), k0 = (gc - row * gpr.d) * 8;
+    load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), fast, v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; u++) put_codes<FMT>(a.codes, a.scales, first + 256u * u, v[u], first + 256u * u < groups);
+}
+
+// ------------------------------------------------------------------- read --
+template <int FMT>
+__device__ __forceinline__ void values8(const uint8_t *codes, uint64_t gi, float s, float (&v)[8]) {
+  if constexpr (FMT == FP8) {
+    const u32x2 c = *reinterpret_cast<const u32x2 *>(codes + 8 * gi);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      const f32x2 p = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[i]), false), q = __builtin_amdgcn_cvt_pk_f32_fp8(int(c[i]), true);
+      v[4 * i] = p[0] * s;
+      v[4 * i + 1] = p[1] * s;
+      v[4 * i + 2] = q[0] * s;
+      v[4 * i + 3] = q[1] * s;
+    }
+  } else {
+    const uint32_t c = *reinterpret_cast<const uint32_t *>(codes + 4 * gi);
+    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+      v[i] = p0[i] * s;
+      v[2 + i] = p1[i] * s;
+      v[4 + i] = p2[i] * s;
+      v[6 + i] = p3[i] * s;
+    }
+  }
+}
+
+template <int FMT, int DT, int U>
+__global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv gpr, uint32_t groups, bool fast) {
+  const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+  float v[U][8];
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    const uint32_t gc = g < groups ? g : 0;
+    values8<FMT>(a.codes, gc, mx_scale_value(a.scales[gc >> 2]), v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    if (g >= groups) return;
+    const uint32_t row = gpr.div(g), k0 = (g - row * gpr.d) * 8;
+    store8<DT>(a.out + row * a.out_stride * esize(DT), k0, uint32_t(a.k), fast, v[u]);
+  }
+}
+
+// ------------------------------------------------------------------- norm --
+// y = h w / sqrt(mean(h^2) + eps), h = x + res rounded to DT, quantised.
+//
+// The squares are summed in 64 bits, so no finite row overflows or vanishes,
+// and 1 / sqrt is split into a power of two and a 24-bit fraction for the
+// same reason: h is scaled by the power exactly before it meets the fraction.
+struct RowScale {
+  int e;
+  float m;
+};
+__device__ __forceinline__ RowScale row_scale(double sum, uint32_t k, float eps) {
+  const double a = sum / double(k) + double(eps);
+  double r = __builtin_amdgcn_rsq(a);
+  // one Newton step takes the instruction's 2^-26 to 64-bit rounding
+  const double t = __builtin_fma(-a * r, r, 1.0);
+  const double n = __builtin_fma(0.5 * r, t, r);
+  r = (a > 0 && a < __builtin_inf()) ? n : r;  // 0 gives infinity, infinity gives 0, a NaN stays
+  RowScale s;
+  s.e = __builtin_amdgcn_frexp_exp(r);
+  s.m = float(__builtin_amdgcn_frexp_mant(r));
+  return s;
+}
+
+template <int DT>
+__device__ __forceinline__ float rounded(float v) {
+  return DT == BF16 ? __uint_as_float(f32_bf16(v) << 16) : v;
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+
+// h of one group: loaded, added, rounded, stored
+template <int DT>
+__device__ __forceinline__ void take8(const MxNormArgs &a, uint64_t row, uint32_t k0, bool fast, float (&h)[8]) {
+  load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), fast, h);
+  if (a.res) {
+    float r[8];
+    load8<DT>(a.res + row * a.res_stride * esize(DT), k0, uint32_t(a.k), fast, r);
+#pragma unroll
+    for (int i = 0; i < 8; i++) h[i] = rounded<DT>(h[i] + r[i]);
+    store8<DT>(a.h + row * a.h_stride * esize(DT), k0, uint32_t(a.k), fast, h);
+  }
+}
+
+__device__ __forceinline__ double squares8(const float (&h)[8]) {
+  double s = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) s = __builtin_fma(double(h[i]), double(h[i]), s);
+  return s;
+}
+
+template <int FMT>
+__device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, RowScale s, const float (&h)[8],
+                                      const float (&w)[8], bool live) {
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_ldexpf(h[i], s.e) * s.m * w[i];
+  put_codes<FMT>(a.codes, a.scales, gi, y, live);
+}
+
+// The sum over a team of TEAM lanes; `slot` alternates between rows so that
+// one barrier a row is enough.
+template <int TEAM>
+__device__ __forceinline__ double team_sum(double s, double (*part)[16], int slot) {
+  s = wave_sum(s);
+  if constexpr (TEAM > 64) {
+    if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = s;
+    __syncthreads();
+    s = 0;
+#pragma unroll
+    for (int i = 0; i < TEAM / 64; i++) s += part[slot][i];
+  }
+  return s;
+}
+
+// Rows of at most TEAM * CH * 8 elements stay in registers.
+template <int DT, int FMT, int TEAM, int CH>
+__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs a, uint32_t gpr, bool fast) {
+  constexpr int kTeams = TEAM < 256 ? 256 / TEAM : 1;
+  __shared__ double part[2][16];
+  const uint32_t t = threadIdx.x % TEAM;
+  float w[CH][8];
+#pragma unroll
+  for (int c = 0; c < CH; c++)
+    load8<DT>(a.w, (c * TEAM + t) * 8, uint32_t(a.k), (uintptr_t(a.w) & 15) == 0, w[c]);
+  int slot = 0;
+  const uint64_t step = uint64_t(gridDim.x) * kTeams;
+  for (uint64_t row = uint64_t(blockIdx.x) * kTeams + threadIdx.x / TEAM; row < a.rows; row += step, slot ^= 1) {
+    float h[CH][8];
+    double s = 0;
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+      take8<DT>(a, row, (c * TEAM + t) * 8, fast, h[c]);
+      s += squares8(h[c]);
+    }
+    const RowScale r = row_scale(team_sum<TEAM>(s, part, slot), uint32_t(a.k), a.eps);
+#pragma unroll
+    for (int c = 0; c < CH; c++) {
+      const uint32_t g = c * TEAM + t;
+      norm8<FMT>(a, row * gpr + g, r, h[c], w[c], g < gpr);
+    }
+  }
+}
+
+// Longer rows are read twice, the second time as they were stored.
+template <int DT, int FMT>
+__global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gpr, bool fast) {
+  __shared__ double part[2][16];
+  int slot = 0;
+  for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
+    double s = 0;
+    for (uint32_t g = threadIdx.x; g < gpr; g += 1024) {
+      float h[8];
+      take8<DT>(a, row, g * 8, fast, h);
+      s += squares8(h);
+    }
+    const RowScale r = row_scale(team_sum<1024>(s, part, slot), uint32_t(a.k), a.eps);
+    const uint8_t *src = a.res ? a.h + row * a.h_stride * esize(DT) : a.x + row * a.x_stride * esize(DT);
+    // gpr is a multiple of 4: the lanes of a quad stay together
+    for (uint32_t g = threadIdx.x; g < gpr; g += 1024) {
+      float h[8], w[8];
+      load8<DT>(src, g * 8, uint32_t(a.k), fast, h);
+      load8<DT>(a.w, g * 8, uint32_t(a.k), (uintptr_t(a.w) & 15) == 0, w);
+      norm8<FMT>(a, row * gpr + g, r, h, w, true);
+    }
+  }
+}
+
+bool aligned_rows(const void *p, uint64_t stride, int dt) {
+  return (uintptr_t(p) & 15) == 0 && (stride * esize(dt)) % 16 == 0;
+}
+
+// Calls f(first row, rows) for pieces whose groups of 8 stay below 2^31.
+template <class F>
+hipError_t by_pieces(uint64_t rows, uint32_t gpr, F f) {
+  const uint64_t most = 0x7FFF0000u / gpr;
+  for (uint64_t r = 0; r < rows; r += most) {
+    const hipError_t e = f(r, rows - r < most ? rows - r : most);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT, int FMT>
+hipError_t quantize(const MxQuantArgs &a, hipStream_t s) {
+  constexpr int U = 2;
+  const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
+  return by_pieces(a.rows, gpr, [&](uint64_t r0, uint64_t rows) {
+    MxQuantArgs p = a;
+    p.x += r0 * a.x_stride * esize(DT);
+    p.codes += r0 * gpr * (FMT == FP8 ? 8 : 4);
+    p.scales += r0 * (gpr / 4);
+    p.rows = rows;
+    const uint32_t groups = uint32_t(rows * gpr);
+    k_mx_quantize<DT, FMT, U><<<(groups + 256 * U - 1) / (256 * U), 256, 0, s>>>(
+        p, FastDiv(gpr), groups, aligned_rows(a.x, a.x_stride, DT));
+    return hipGetLastError();
+  });
+}
+
+template <int FMT, int DT>
+hipError_t dequantize(const MxDequantArgs &a, hipStream_t s) {
+  constexpr int U = 2;
+  const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
+  return by_pieces(a.rows, gpr, [&](uint64_t r0, uint64_t rows) {
+    MxDequantArgs p = a;
+    p.codes += r0 * gpr * (FMT == FP8 ? 8 : 4);
+    p.scales += r0 * (gpr / 4);
+    p.out += r0 * a.out_stride * esize(DT);
+    p.rows = rows;
+    const uint32_t groups = uint32_t(rows * gpr);
+    k_mx_dequantize<FMT, DT, U><<<(groups + 256 * U - 1) / (256 * U), 256, 0, s>>>(
+        p, FastDiv(gpr), groups, aligned_rows(a.out, a.out_stride, DT));
+    return hipGetLastError();
+  });
+}
+
+template <int DT, int FMT>
+hipError_t norm(const MxNormArgs &a, hipStream_t s) {
+  const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
+  const bool fast = aligned_rows(a.x, a.x_stride, DT) &&
+                    (!a.res || (aligned_rows(a.res, a.res_stride, DT) && aligned_rows(a.h, a.h_stride, DT)));
+  const auto grid = [&](uint32_t teams, uint32_t most) {
+    const uint64_t b = (a.rows + teams - 1) / teams;
+    return uint32_t(b < most ? b : most);
+  };
+  if (gpr <= 64)
+    k_mx_norm<DT, FMT, 64, 1><<<grid(4, 4096), 256, 0, s>>>(a, gpr, fast);
+  else if (gpr <= 128)
+    k_mx_norm<DT, FMT, 64, 2><<<grid(4, 4096), 256, 0, s>>>(a, gpr, fast);
+  else if (gpr <= 256)
+    k_mx_norm<DT, FMT, 256, 1><<<grid(1, 4096), 256, 0, s>>>(a, gpr, fast);
+  else if (gpr <= 512)
+    k_mx_norm<DT, FMT, 256, 2><<<grid(1, 4096), 256, 0, s>>>(a, gpr, fast);
+  else if (gpr <= 1024)
+    k_mx_norm<DT, FMT, 256, 4><<<grid(1, 2048), 256, 0, s>>>(a, gpr, fast);
+  else if (gpr <= 2048)
+    k_mx_norm<DT, FMT, 1024, 2><<<grid(1, 1024), 1024, 0, s>>>(a, gpr, fast);
+  else
+    k_mx_norm_long<DT, FMT><<<grid(1, 512), 1024, 0, s>>>(a, gpr, fast);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(int in_dtype, int fmt, const MxQuantArgs &a, hipStream_t s) {
+  if (in_dtype == BF16) return fmt == FP8 ? quantize<BF16, FP8>(a, s) : quantize<BF16, FP4X2>(a, s);
+  return fmt == FP8 ? quantize<FP32, FP8>(a, s) : quantize<FP32, FP4X2>(a, s);
+}
+hipError_t launch_mx_dequantize(int fmt, int out_dtype, const MxDequantArgs &a, hipStream_t s) {
+  if (out_dtype == BF16) return fmt == FP8 ? dequantize<FP8, BF16>(a, s) : dequantize<FP4X2, BF16>(a, s);
+  return fmt == FP8 ? dequantize<FP8, FP32>(a, s) : dequantize<FP4X2, FP32>(a, s);
+}
+hipError_t launch_mx_norm(int dtype, int fmt, const MxNormArgs &a, hipStream_t s) {
+  if (dtype == BF16) return fmt == FP8 ? norm<BF16, FP8>(a, s) : norm<BF16, FP4X2>(a, s);
+  return fmt == FP8 ? norm<FP32, FP8>(a, s) : norm<FP32, FP4X2>(a, s);
+}
+
+}  // namespace zn

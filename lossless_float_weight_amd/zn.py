@@ -8,6 +8,7 @@ is missing, every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import math
 import os
 from typing import Sequence
 
@@ -71,13 +72,19 @@ def lib() -> C.CDLL:
         L.zn_debug_histograms.argtypes = [P, P, P, P]
         L.zn_debug_code_lengths.argtypes = [P, I, I, I, P, P]
         L.zn_debug_kernel_events.argtypes = [C.c_char_p, P, P]
+        L.zn_mx_quantize.argtypes = [I, P, U64, U64, U64, I, P, P, P]
+        L.zn_mx_dequantize.argtypes = [I, P, P, U64, U64, I, P, U64, P]
+        L.zn_mx_rms_norm.argtypes = [I, P, U64, P, U64, P, C.c_float, U64, U64, P, U64, I, P, P, P]
+        L.zn_mx_matmul_scratch_bytes.argtypes = [I, I, U64, U64, U64, PU64]
+        L.zn_mx_matmul.argtypes = [I, P, P, I, P, P, U64, U64, U64, I, P, U64, P, U64, P]
         for f in ("zn_setup", "zn_setup_transfer", "zn_plan_from_container", "zn_header_info",
                   "zn_tableset_info", "zn_compress_bound",
                   "zn_scratch_bytes", "zn_compress", "zn_decompress", "zn_decompress_noalloc",
                   "zn_tableset_save",
                   "zn_tableset_load", "zn_tableset_lengths", "zn_tableset_map",
                   "zn_tableset_cost_history", "zn_debug_histograms", "zn_debug_code_lengths",
-                  "zn_debug_kernel_events"):
+                  "zn_debug_kernel_events", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
+                  "zn_mx_matmul_scratch_bytes", "zn_mx_matmul"):
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -387,6 +394,246 @@ def decompress_noalloc(ts: Tableset, blob: torch.Tensor, outs: Sequence[torch.Te
                                            C.c_void_p(status.data_ptr()) if status is not None else None,
                                            1 if sync else 0, _stream(stream)), "decompress_noalloc")
     return outs
+
+
+# ------------------------------------------------------- microscaled numbers --
+# Rows of FP8 E4M3 codes (torch.float8_e4m3fn) or FP4 E2M1 pairs (torch.uint8)
+# with one E8M0 scale byte (torch.float8_e8m0fnu, or the same as uint8) for
+# every 32 values; the last axis is the row, filled up to whole blocks.
+MX_BLOCK = 32
+_MX_FMT = {torch.float8_e4m3fn: FP8_E4M3, torch.uint8: FP4X2_E2M1}
+_MX_PLAIN = {torch.bfloat16: BF16, torch.float32: FP32}
+_MX_SCALE = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _mx_device(where: str, stream, **tensors) -> torch.device:
+    """The one CUDA device of the call's tensors (and of its stream)."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda or (dev is not None and t.device != dev):
+            raise ZnError(-1, f"{where}: {name} is on {t.device}, not on the call's CUDA device")
+        dev = t.device
+    if stream is not None and stream.device != dev:
+        raise ZnError(-1, f"{where}: the stream is on {stream.device}, the tensors on {dev}")
+    return dev
+
+
+def _mx_rows(where: str, name: str, t: torch.Tensor, write: bool = False):
+    """(rows, k, row stride) of a plain tensor whose last axis is dense and
+    whose other axes are evenly spaced rows."""
+    if t.dim() == 0:
+        raise ZnError(-1, f"{where}: {name} has no axis")
+    k = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // k if k else math.prod(t.shape[:-1])), k, k
+    stride, rows = None, 1
+    for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if n == 1:
+            continue
+        if stride is None:
+            stride = st
+        elif st != stride * rows:
+            stride = -1
+        rows *= n
+    if rows == 0:
+        return 0, k, k
+    if stride is None:
+        stride = k
+    if (k > 1 and t.stride(-1) != 1) or stride < 0 or (write and rows > 1 and stride < k):
+        raise ZnError(-1, f"{where}: {name} is not made of evenly spaced dense rows (pass .contiguous())")
+    return rows, k, stride
+
+
+def _mx_new(shape, dtype, dev, stream) -> torch.Tensor:
+    """An output on the stream that writes it; it may be used on the current
+    stream too (once that has waited for the call's)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _mx_given(where: str, name: str, t: torch.Tensor, shape, dtypes) -> None:
+    """A packed tensor of the call: type, shape, dense, and no view whose first
+    byte breaks the alignment of codes."""
+    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+        raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted {dtypes[0]} {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ZnError(-1, f"{where}: {name} is not contiguous (pass .contiguous())")
+
+
+def _mx_packed(where: str, name: str, codes: torch.Tensor, scales: torch.Tensor):
+    """(fmt, stored row length) of codes and their scales, checked."""
+    fmt = _MX_FMT.get(codes.dtype)
+    if fmt is None or codes.dim() == 0:
+        raise ZnError(-1, f"{where}: {name} is {codes.dtype}, wanted float8_e4m3fn, or uint8 pairs of E2M1, in rows")
+    kp = codes.shape[-1] * (2 if fmt == FP4X2_E2M1 else 1)
+    if kp == 0 or kp % MX_BLOCK:
+        raise ZnError(-1, f"{where}: {name} has rows of {kp} values, wanted whole blocks of {MX_BLOCK}")
+    if not codes.is_contiguous():
+        raise ZnError(-1, f"{where}: {name} is not contiguous (pass .contiguous())")
+    _mx_given(where, name + "'s scales", scales, (*codes.shape[:-1], kp // MX_BLOCK), _MX_SCALE)
+    return fmt, kp
+
+
+def _mx_use(stream, *tensors) -> None:
+    """Tensors of a call on another stream than the current one stay
+    allocated until that stream's work is done."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _mx_codes(where, lead, k, fmt, codes, scales, dev, stream):
+    """The output pair, given or made."""
+    if fmt not in (FP8_E4M3, FP4X2_E2M1):
+        raise ZnError(-1, f"{where}: fmt is {fmt!r}, wanted FP8_E4M3 or FP4X2_E2M1")
+    if k == 0:
+        raise ZnError(-1, f"{where}: rows of no values")
+    nb = -(-k // MX_BLOCK)
+    dt, width = (torch.float8_e4m3fn, MX_BLOCK) if fmt == FP8_E4M3 else (torch.uint8, MX_BLOCK // 2)
+    if codes is None:
+        codes = _mx_new((*lead, nb * width), dt, dev, stream)
+    else:
+        _mx_given(where, "codes", codes, (*lead, nb * width), (dt,))
+    if scales is None:
+        scales = _mx_new((*lead, nb), torch.float8_e8m0fnu, dev, stream)
+    else:
+        _mx_given(where, "scales", scales, (*lead, nb), _MX_SCALE)
+    return codes, scales
+
+
+def _mx_plain(where: str, name: str, dtype) -> int:
+    if dtype not in _MX_PLAIN:
+        raise ZnError(-1, f"{where}: {name} is {dtype}, wanted bfloat16 or float32")
+    return _MX_PLAIN[dtype]
+
+
+def mx_quantize(x: torch.Tensor, fmt: int = FP8_E4M3, codes: torch.Tensor | None = None,
+                scales: torch.Tensor | None = None, stream=None):
+    """zn_mx_quantize: rows of x (last axis; BF16 or FP32) to (codes, scales).
+    The codes are the tensors that a FP8_E4M3 or FP4X2_E2M1 plan compresses."""
+    where = "mx_quantize"
+    dt = _mx_plain(where, "x", x.dtype)
+    dev = _mx_device(where, stream, x=x, codes=codes, scales=scales)
+    rows, k, stride = _mx_rows(where, "x", x)
+    codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
+    with torch.cuda.device(dev):
+        _check(lib().zn_mx_quantize(dt, x.data_ptr(), stride, rows, k, fmt, codes.data_ptr(), scales.data_ptr(),
+                                    _stream(stream)), where)
+    _mx_use(stream, x, codes, scales)
+    return codes, scales
+
+
+def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int | None = None, dtype=torch.bfloat16,
+                  out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """zn_mx_dequantize: the values of the first k of every row (all stored
+    ones when None), in BF16 or FP32."""
+    where = "mx_dequantize"
+    fmt, kp = _mx_packed(where, "codes", codes, scales)
+    if k is None:
+        k = kp
+    if not kp - MX_BLOCK < k <= kp:
+        raise ZnError(-1, f"{where}: {k} values do not fill rows of {kp}")
+    dev = _mx_device(where, stream, codes=codes, scales=scales, out=out)
+    shape = (*codes.shape[:-1], k)
+    if out is None:
+        _mx_plain(where, "dtype", dtype)
+        out = _mx_new(shape, dtype, dev, stream)
+    elif tuple(out.shape) != shape:
+        raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {shape}")
+    dt = _mx_plain(where, "out", out.dtype)
+    rows, _, stride = _mx_rows(where, "out", out, write=True)
+    with torch.cuda.device(dev):
+        _check(lib().zn_mx_dequantize(fmt, codes.data_ptr(), scales.data_ptr(), rows, k, dt, out.data_ptr(), stride,
+                                      _stream(stream)), where)
+    _mx_use(stream, codes, scales, out)
+    return out
+
+
+def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-5,
+                fmt: int = FP8_E4M3, codes: torch.Tensor | None = None, scales: torch.Tensor | None = None,
+                residual_out: torch.Tensor | None = None, stream=None):
+    """zn_mx_rms_norm: (codes, scales, h) of h = x + residual normed and
+    quantised; h is stored in residual_out (x or residual itself is fine).
+    Without a residual h is x."""
+    where = "mx_rms_norm"
+    dt = _mx_plain(where, "x", x.dtype)
+    dev = _mx_device(where, stream, x=x, weight=weight, residual=residual, residual_out=residual_out, codes=codes,
+                     scales=scales)
+    rows, k, stride = _mx_rows(where, "x", x)
+    if weight.dtype != x.dtype or tuple(weight.shape) != (k,) or not weight.is_contiguous():
+        raise ZnError(-1, f"{where}: weight is {weight.dtype} {tuple(weight.shape)}, wanted dense {x.dtype} {(k,)}")
+    if residual is None and residual_out is not None:
+        raise ZnError(-1, f"{where}: residual_out without a residual")
+    if not math.isfinite(eps) or eps < 0:
+        raise ZnError(-1, f"{where}: eps is {eps}")
+    rs = hs = 0
+    if residual is not None:
+        if residual.dtype != x.dtype or residual.shape != x.shape:
+            raise ZnError(-1, f"{where}: residual is {residual.dtype} {tuple(residual.shape)}, x {x.dtype} {tuple(x.shape)}")
+        rs = _mx_rows(where, "residual", residual)[2]
+        if residual_out is None:
+            residual_out = _mx_new(x.shape, x.dtype, dev, stream)
+        elif residual_out.dtype != x.dtype or residual_out.shape != x.shape:
+            raise ZnError(-1, f"{where}: residual_out is {residual_out.dtype} {tuple(residual_out.shape)}, "
+                              f"x {x.dtype} {tuple(x.shape)}")
+        hs = _mx_rows(where, "residual_out", residual_out, write=True)[2]
+    codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
+    with torch.cuda.device(dev):
+        _check(lib().zn_mx_rms_norm(dt, x.data_ptr(), stride, residual.data_ptr() if residual is not None else None,
+                                    rs, weight.data_ptr(), eps, rows, k,
+                                    residual_out.data_ptr() if residual is not None else None, hs, fmt,
+                                    codes.data_ptr(), scales.data_ptr(), _stream(stream)), where)
+    _mx_use(stream, x, weight, residual, residual_out, codes, scales)
+    return codes, scales, (x if residual is None else residual_out)
+
+
+def mx_matmul_scratch_bytes(a_fmt: int, w_fmt: int, m: int, n: int, k: int) -> int:
+    """zn_mx_matmul_scratch_bytes: device scratch of a product of m rows with
+    n rows of stored length k."""
+    b = C.c_uint64()
+    _check(lib().zn_mx_matmul_scratch_bytes(a_fmt, w_fmt, m, n, k, C.byref(b)), "mx_matmul_scratch_bytes")
+    return b.value
+
+
+def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
+              dtype=torch.bfloat16, out: torch.Tensor | None = None, scratch: torch.Tensor | None = None,
+              stream=None) -> torch.Tensor:
+    """zn_mx_matmul: a [..., k] by the rows of w [n, k], both microscaled (FP8
+    or FP4 each), as BF16 or FP32 [..., n]."""
+    where = "mx_matmul"
+    fa, k = _mx_packed(where, "a", a, a_scales)
+    fw, kw = _mx_packed(where, "w", w, w_scales)
+    if w.dim() != 2 or kw != k:
+        raise ZnError(-1, f"{where}: w has rows of {kw} values and {w.dim()} axes, wanted {k} and 2")
+    dev = _mx_device(where, stream, a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out, scratch=scratch)
+    n = w.shape[0]
+    shape = (*a.shape[:-1], n)
+    if out is None:
+        _mx_plain(where, "dtype", dtype)
+        out = _mx_new(shape, dtype, dev, stream)
+    elif tuple(out.shape) != shape:
+        raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {shape}")
+    dt = _mx_plain(where, "out", out.dtype)
+    m, _, stride = _mx_rows(where, "out", out, write=True)
+    need = mx_matmul_scratch_bytes(fa, fw, m, n, k)
+    if scratch is None:
+        scratch = _mx_new((need,), torch.uint8, dev, stream) if need else None
+    elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
+        raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
+    with torch.cuda.device(dev):
+        _check(lib().zn_mx_matmul(fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(), w_scales.data_ptr(),
+                                  m, n, k, dt, out.data_ptr(), stride,
+                                  scratch.data_ptr() if scratch is not None else None,
+                                  scratch.numel() if scratch is not None else 0, _stream(stream)), where)
+    _mx_use(stream, a, a_scales, w, w_scales, out, scratch)
+    return out
 
 
 def debug_histograms(ts: Tableset, tensors: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
