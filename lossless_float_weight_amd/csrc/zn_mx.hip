@@ -49,7 +49,7 @@ __device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, bo
     if constexpr (DT == BF16) {
       u32x4 w;
 #pragma unroll
-      for (int i = 0; i < 4; i++) w[i] = f32_bf16(v[2 * i]) | (f32_bf16(v[2 * i + 1]) << 16);
+      for (int i = 0; i < 4; i++) w[i] = f32_bf16x2(v[2 * i], v[2 * i + 1]);
       *reinterpret_cast<u32x4 *>(row + 2 * uint64_t(k0)) = w;
     } else {
       f32x4 a, b;
@@ -67,7 +67,7 @@ __device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, bo
   for (int i = 0; i < 8; i++)
     if (k0 + i < k) {
       if constexpr (DT == BF16)
-        *reinterpret_cast<uint16_t *>(row + 2 * uint64_t(k0 + i)) = uint16_t(f32_bf16(v[i]));
+        *reinterpret_cast<uint16_t *>(row + 2 * uint64_t(k0 + i)) = f32_bf16(v[i]);
       else
         *reinterpret_cast<float *>(row + 4 * uint64_t(k0 + i)) = v[i];
     }
@@ -187,7 +187,7 @@ __device__ __forceinline__ RowScale row_scale(double sum, uint32_t k, float eps)
 
 template <int DT>
 __device__ __forceinline__ float rounded(float v) {
-  return DT == BF16 ? __uint_as_float(f32_bf16(v) << 16) : v;
+  return DT == BF16 ? __uint_as_float(uint32_t(f32_bf16(v)) << 16) : v;
 }
 
 __device__ __forceinline__ double wave_sum(double v) {

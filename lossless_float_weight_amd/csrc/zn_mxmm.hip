@@ -27,11 +27,20 @@ __device__ __forceinline__ f32x4 mfma(i32x8 w, i32x8 a, f32x4 c, uint32_t sw, ui
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, c, kFmtBits<FW>, kFmtBits<FA>, 0, int(sw), 0, int(sa));
 }
 
+// The instruction's operand; 4-bit codes leave its upper half unread.
+template <int F>
+__device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi) {
+  if constexpr (F == FP8) {
+    return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
+    return __builtin_bit_cast(i32x8, __builtin_shufflevector(lo, lo, 0, 1, 2, 3, -1, -1, -1, -1));
+  }
+}
+
 // A lane's operand for step t from its row in memory; blocks past nb are
 // zero codes under scale 1.
 template <int F>
 __device__ __forceinline__ i32x8 load_codes(const uint8_t *row, uint32_t t, uint32_t g, uint32_t nb) {
-  i32x8 v = {0, 0, 0, 0, 0, 0, 0, 0};
   u32x4 lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
   if constexpr (F == FP8) {
     const uint8_t *p = row + 128ull * t + 16 * g;
@@ -40,12 +49,7 @@ __device__ __forceinline__ i32x8 load_codes(const uint8_t *row, uint32_t t, uint
   } else {
     if (4 * t + g < nb) lo = *reinterpret_cast<const u32x4 *>(row + 64ull * t + 16 * g);
   }
-#pragma unroll
-  for (int i = 0; i < 4; i++) {
-    v[i] = int(lo[i]);
-    v[4 + i] = int(hi[i]);
-  }
-  return v;
+  return operand<F>(lo, hi);
 }
 __device__ __forceinline__ uint32_t load_scale(const uint8_t *row, uint32_t t, uint32_t g, uint32_t nb) {
   return 4 * t + g < nb ? row[4 * t + g] : 127u;
@@ -58,7 +62,7 @@ __device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64
   uint8_t *row = p.out + m * p.out_stride * esize(OUT);
   if (wide && n + 4 <= p.n) {
     if constexpr (OUT == BF16) {
-      const u32x2 v = {f32_bf16(c[0]) | (f32_bf16(c[1]) << 16), f32_bf16(c[2]) | (f32_bf16(c[3]) << 16)};
+      const u32x2 v = {f32_bf16x2(c[0], c[1]), f32_bf16x2(c[2], c[3])};
       *reinterpret_cast<u32x2 *>(row + 2 * n) = v;
     } else {
       *reinterpret_cast<f32x4 *>(row + 4 * n) = c;
@@ -69,7 +73,7 @@ __device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64
   for (int i = 0; i < 4; i++)
     if (n + i < p.n) {
       if constexpr (OUT == BF16)
-        *reinterpret_cast<uint16_t *>(row + 2 * (n + i)) = uint16_t(f32_bf16(c[i]));
+        *reinterpret_cast<uint16_t *>(row + 2 * (n + i)) = f32_bf16(c[i]);
       else
         *reinterpret_cast<float *>(row + 4 * (n + i)) = c[i];
     }
@@ -122,11 +126,320 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb,
   }
 }
 
+// ------------------------------------------------------------- tiled form --
+// A workgroup of WM x WN waves makes BM m by BN n; a wave 16 TM by 16 TN, its
+// sums in registers.  Steps of 128 k go from memory to LDS without passing
+// registers (16 bytes a lane), kBuf steps ahead; while the matrix unit works
+// on the operands of step t, those of step t + 1 are read from LDS.
+//
+// LDS holds a step's rows as the wave's loads lay them down, 1 KB at a time;
+// the 16-byte pieces of a row are exchanged by the row's low bits (at the
+// source, a lane may load from anywhere) so that the 16 rows of an operand
+// lie in different banks.  The weight rows of 64 are taken in the order that
+// leaves a lane 16 consecutive n over four tiles, a whole line over four lane
+// groups.
+//
+// Asynchronous copies are written as instructions because the compiler makes
+// every later LDS read wait for the builtin's; they have no register output.
+// A copy's end is waited for with vmcnt by the wave that issued it, then by
+// all at the barrier that ends a step.  The base's two scalar registers may
+// come from vector instructions (uniform), which takes 5 wait states before a
+// memory instruction that the compiler does not see: s_nop 4.
+__device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
+  const uint64_t v = uint64_t(uintptr_t(p));
+  return reinterpret_cast<const uint8_t *>(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
+                                           (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32));
+}
+__device__ __forceinline__ uint32_t lds_offset(const void *p) {
+  return uint32_t(uintptr_t((__attribute__((address_space(3))) const void *)p));
+}
+__device__ __forceinline__ void copy16(uint32_t lds, const uint8_t *base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t lds, const uint8_t *base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy1(uint32_t lds, const uint8_t *base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+__device__ __forceinline__ void barrier() {
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Bytes of a row in one step, its 16-byte pieces, and where piece p of row r lies.
+template <int F>
+struct Lay {
+  static constexpr uint32_t kRow = F == FP8 ? 128 : 64, kPieces = kRow / 16;
+  __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return F == FP8 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
+};
+
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kDwords>
+struct Tiled {
+  static constexpr int kWaves = WM * WN, kBM = 16 * TM * WM, kBN = 16 * TN * WN;
+  static constexpr uint32_t kABytes = kBM * Lay<FA>::kRow, kWBytes = kBN * Lay<FW>::kRow;
+  // scale bytes: a dword of four blocks a row, or a dword for each block
+  static constexpr uint32_t kSRow = kDwords ? 4 : 16, kSBytes = (kBM + kBN) * kSRow;
+  static constexpr uint32_t kStage = kABytes + kWBytes + kSBytes;
+  static constexpr int kBuf = 3 * kStage <= 160 * 1024 ? 3 : 2;
+  static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
+  static constexpr int kSChunks = (kBM + kBN) / 64 * (kDwords ? 1 : 4), kSC = (kSChunks + kWaves - 1) / kWaves;
+  static constexpr int kPerStep = kAC + kWC + kSC;
+  static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 4 == 0, "tile");
+  static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
+  static_assert(kBuf * kStage <= 160 * 1024 && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
+};
+
+// Weight row of LDS row r: tile i, row 4 g + q of it stands for n = 16 g + 4 i + q of the 64.
+__device__ __forceinline__ uint32_t weight_row(uint32_t r) {
+  return (r & ~63u) + ((r >> 2) & 3) * 16 + ((r >> 4) & 3) * 4 + (r & 3);
+}
+
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kDwords>
+__global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint32_t nb, uint32_t mt, uint32_t nt, bool wide) {
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kDwords>;
+  constexpr int kBuf = T::kBuf;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuf * T::kStage];
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
+  const uint32_t wm = wave % WM, wn = wave / WM;
+
+  // tiles of one XCD (workgroups go round the 8 of them) are neighbours, in
+  // columns of 8 along m: their operands meet in its L2
+  uint32_t tm, tn;
+  {
+    const uint32_t total = mt * nt, x = blockIdx.x % 8, i = blockIdx.x / 8;
+    const uint32_t id = x * (total / 8) + (x < total % 8 ? x : total % 8) + i;
+    const uint32_t col = id / (8 * nt), height = mt - 8 * col < 8 ? mt - 8 * col : 8;
+    tm = 8 * col + (id - 8 * nt * col) % height;
+    tn = (id - 8 * nt * col) / height;
+  }
+  const uint64_t m0 = uint64_t(tm) * T::kBM, n0 = uint64_t(tn) * T::kBN;
+  const uint32_t mr = uint32_t(p.m - m0 < uint64_t(T::kBM) ? p.m - m0 : T::kBM);  // rows of this tile
+  const uint32_t nr = uint32_t(p.n - n0 < uint64_t(T::kBN) ? p.n - n0 : T::kBN);
+  const uint32_t pa = nb * code_bytes<FA>(), pw = nb * code_bytes<FW>();
+  const uint8_t *a0 = p.a + m0 * pa, *w0 = p.w + n0 * pw, *as0 = p.as + m0 * nb, *ws0 = p.ws + n0 * nb;
+
+  // offsets of this lane's copies from the tile's first row; rows past the
+  // end are read as the last one
+  uint32_t oa[T::kAC], ow[T::kWC], os[T::kSC];
+#pragma unroll
+  for (int c = 0; c < T::kAC; c++) {
+    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FA>::kPieces, from = row < mr ? row : mr - 1;
+    oa[c] = from * pa + 16 * Lay<FA>::piece(row, q % Lay<FA>::kPieces);
+  }
+#pragma unroll
+  for (int c = 0; c < T::kWC; c++) {
+    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FW>::kPieces, n = weight_row(row), from = n < nr ? n : nr - 1;
+    ow[c] = from * pw + 16 * Lay<FW>::piece(row, q % Lay<FW>::kPieces);
+  }
+  const uint8_t *sbase[T::kSC];
+  uint32_t sto[T::kSC], sblock[T::kSC];
+#pragma unroll
+  for (int c = 0; c < T::kSC; c++) {
+    uint32_t q = c * T::kWaves + wave;
+    q = q < uint32_t(T::kSChunks) ? q : T::kSChunks - 1;  // the same copy twice
+    const uint32_t chunk = kDwords ? q : q / 4, row = chunk * 64 + lane;
+    const bool isa = chunk < T::kBM / 64;
+    const uint32_t n = weight_row(isa ? 0 : row - T::kBM);
+    const uint32_t from = isa ? (row < mr ? row : mr - 1) : (n < nr ? n : nr - 1);
+    os[c] = from * nb;
+    sbase[c] = isa ? as0 : ws0;
+    sblock[c] = q & 3;
+    sto[c] = T::kABytes + T::kWBytes + q * 256;
+  }
+  const uint32_t lds0 = lds_offset(lds);
+  // A last step of fewer than four blocks: absent pieces of the activations
+  // are zeros, those of the weights and the scales repeat the row's last
+  // block.  A NaN that this multiplies by zero is one that the row has anyway.
+  const uint32_t steps = (nb + 3) / 4, rest = nb % 4;
+  const uint32_t pa_piece = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
+  const uint32_t pw_piece = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
+  const bool absent = rest && pa_piece / (FA == FP8 ? 2 : 1) >= rest;
+  const uint32_t back = rest && pw_piece / (FW == FP8 ? 2 : 1) >= rest ? 16 * (pw_piece - (FW == FP8 ? 2 * rest - 1 : rest - 1)) : 0;
+  const auto copy = [&](uint32_t t) {
+    const uint32_t stage = (t % kBuf) * T::kStage, to = __builtin_amdgcn_readfirstlane(lds0 + stage);
+    const uint32_t s = t < steps ? t : steps - 1;  // past the end: copied, never used
+    const bool last = s == steps - 1;
+    const uint8_t *a = uniform(a0 + uint64_t(s) * Lay<FA>::kRow), *w = uniform(w0 + uint64_t(s) * Lay<FW>::kRow);
+    if (!last || !absent) {
+#pragma unroll
+      for (int c = 0; c < T::kAC; c++) copy16(to + (c * T::kWaves + wave) * 1024, a, oa[c]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < T::kAC; c++)
+        *reinterpret_cast<u32x4 *>(lds + stage + (c * T::kWaves + wave) * 1024 + 16 * lane) = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int c = 0; c < T::kWC; c++)
+      copy16(to + T::kABytes + (c * T::kWaves + wave) * 1024, w, ow[c] - (last ? back : 0));
+#pragma unroll
+    for (int c = 0; c < T::kSC; c++) {
+      if constexpr (kDwords) {
+        copy4(to + sto[c], uniform(sbase[c] + 4 * s), os[c]);
+      } else {
+        const uint32_t b = 4 * s + sblock[c];
+        copy1(to + sto[c], uniform(sbase[c] + (b < nb ? b : nb - 1)), os[c]);
+      }
+    }
+  };
+
+  // this lane's places in a stage
+  const uint32_t la = (wm * 16 * TM + r) * Lay<FA>::kRow, lw = T::kABytes + (wn * 16 * TN + r) * Lay<FW>::kRow;
+  const uint32_t la0 = la + 16 * Lay<FA>::piece(r, g), la1 = la + 16 * Lay<FA>::piece(r, 4 + g);
+  const uint32_t lw0 = lw + 16 * Lay<FW>::piece(r, g), lw1 = lw + 16 * Lay<FW>::piece(r, 4 + g);
+  const auto read = [&](auto f, uint32_t lo, uint32_t hi) {
+    const u32x4 x = *reinterpret_cast<const u32x4 *>(lds + lo);
+    if constexpr (decltype(f)::value == FP8)
+      return operand<FP8>(x, *reinterpret_cast<const u32x4 *>(lds + hi));
+    else
+      return operand<FP4X2>(x, x);
+  };
+  const uint32_t srow = T::kABytes + T::kWBytes;
+  const auto scale = [&](uint32_t stage, uint32_t row) -> uint32_t {  // row: a multiple of 16, of A then W
+    if constexpr (kDwords)
+      return lds[stage + srow + (row + r) * 4 + g];
+    else
+      return lds[stage + srow + (row / 64) * 1024 + g * 256 + (row % 64 + r) * 4];
+  };
+  using IA = std::integral_constant<int, FA>;
+  using IW = std::integral_constant<int, FW>;
+
+  f32x4 acc[TN][TM];
+#pragma unroll
+  for (int i = 0; i < TN; i++)
+#pragma unroll
+    for (int j = 0; j < TM; j++) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  // The operands are held once.  A step's products come in two halves, the
+  // lower tiles of the activations with every weight tile, then the upper
+  // ones; during each half the operands whose last use is over are read anew,
+  // so every LDS read has half a step (32 matrix instructions) to arrive:
+  //   lower half of step t:  the upper activations of step t
+  //   upper half of step t:  the lower activations and the weights of t + 1
+  // Between the halves all waves are done with the LDS of step t and the
+  // copies of step t + 1 have landed; step t + kBuf is copied over step t.
+  constexpr int kHalf = TM / 2;
+  i32x8 xa[TM], xw[TN];
+  uint32_t sa[TM], sw[TN];
+  const auto read_a = [&](uint32_t stage, int j) {
+    xa[j] = read(IA{}, stage + la0 + j * 16 * Lay<FA>::kRow, stage + la1 + j * 16 * Lay<FA>::kRow);
+    sa[j] = scale(stage, wm * 16 * TM + 16 * j);
+  };
+  const auto read_w = [&](uint32_t stage, int i) {
+    xw[i] = read(IW{}, stage + lw0 + i * 16 * Lay<FW>::kRow, stage + lw1 + i * 16 * Lay<FW>::kRow);
+    sw[i] = scale(stage, T::kBM + wn * 16 * TN + 16 * i);
+  };
+  {
+#pragma unroll
+    for (int t = 0; t < kBuf; t++) copy(t);
+    wait_copies<(kBuf - 1) * T::kPerStep>();
+    wait_lds();
+    barrier();
+#pragma unroll
+    for (int i = 0; i < TN; i++) read_w(0, i);
+#pragma unroll
+    for (int j = 0; j < kHalf; j++) read_a(0, j);
+    uint32_t here = 0;
+    for (uint32_t t = 0; t < steps; t++) {
+      const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+#pragma unroll
+        for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
+        if (i < kHalf) read_a(here, kHalf + i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_copies<(kBuf - 2) * T::kPerStep>();
+      wait_lds();
+      barrier();
+      copy(t + kBuf);
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+#pragma unroll
+        for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
+        read_w(next, i);
+        if (i < kHalf) read_a(next, i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      here = next;
+    }
+    wait_copies<0>();  // none may land after the workgroup's end
+  }
+
+  if (wide && mr == T::kBM && nr == T::kBN) {
+    uint8_t *to = p.out + ((m0 + wm * 16 * TM + r) * p.out_stride + n0 + wn * 16 * TN + 16 * g) * esize(OUT);
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+#pragma unroll
+      for (int i = 0; i < TN; i += 4) {
+        if constexpr (OUT == BF16) {
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            const f32x4 u = acc[i + 2 * h][j], v = acc[i + 2 * h + 1][j];
+            *reinterpret_cast<u32x4 *>(to + 32 * i + 16 * h) =
+                u32x4{f32_bf16x2(u[0], u[1]), f32_bf16x2(u[2], u[3]), f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 4; h++) *reinterpret_cast<f32x4 *>(to + 64 * i + 16 * h) = acc[i + h][j];
+        }
+      }
+      to += 16 * p.out_stride * esize(OUT);
+    }
+    return;
+  }
+  // tiles at the edges and rows without the alignment: 16 m of a wave at a
+  // time through LDS of its own, then one n a lane
+  barrier();
+  constexpr uint32_t kLine = 16 * TN + 4;  // floats: rows of a column fall in different banks
+  static_assert(T::kWaves * 16 * kLine * 4 <= kBuf * T::kStage, "edge rows");
+  float *mine = reinterpret_cast<float *>(lds) + wave * 16 * kLine;
+#pragma unroll
+  for (int j = 0; j < TM; j++) {
+#pragma unroll
+    for (int i = 0; i < TN; i++)
+      *reinterpret_cast<f32x4 *>(mine + r * kLine + 64 * (i / 4) + 16 * g + 4 * (i % 4)) = acc[i][j];
+    wait_lds();
+    const uint32_t ml = wm * 16 * TM + 16 * j;
+    for (uint32_t x = 0; x < 16 && ml + x < mr; x++)
+      for (uint32_t y = lane; y < 16 * TN && wn * 16 * TN + y < nr; y += 64) {
+        const float v = mine[x * kLine + y];
+        uint8_t *to = p.out + ((m0 + ml + x) * p.out_stride + n0 + wn * 16 * TN + y) * esize(OUT);
+        if constexpr (OUT == BF16)
+          *reinterpret_cast<uint16_t *>(to) = f32_bf16(v);
+        else
+          *reinterpret_cast<float *>(to) = v;
+      }
+    wait_lds();
+  }
+}
+
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
+hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, false>;
+  const bool wide = (uintptr_t(p.out) & 15) == 0 && (p.out_stride * esize(OUT)) % 16 == 0;
+  const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
+  const bool dwords = nb % 4 == 0 && uintptr_t(p.as) % 4 == 0 && uintptr_t(p.ws) % 4 == 0;
+  if (dwords)
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<mt * nt, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, wide);
+  else
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<mt * nt, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, wide);
+  return hipGetLastError();
+}
+
 template <int FA, int FW, int OUT>
 hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
   const bool wide = (uintptr_t(p.out) & 15) == 0 && p.out_stride % 4 == 0;
   const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 15) / 16;
+  // offsets inside a tile are 32-bit, and so are the tiles' numbers
+  if (p.m > 64 && nb <= (1u << 18) && p.m * p.n < (1ull << 46))
+    return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, s);
   if (mt == 1)
     k_mx_few<FA, FW, OUT, 1, 8><<<dim3(uint32_t(nt), 1), 512, 0, s>>>(p, nb, wide);
   else
