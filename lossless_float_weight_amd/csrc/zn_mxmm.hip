@@ -156,6 +156,9 @@ __device__ __forceinline__ uint32_t lds_offset(const void *p) {
 __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t *base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
+__device__ __forceinline__ void copy16(uint32_t lds, const uint8_t *from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+}
 __device__ __forceinline__ void copy4(uint32_t lds, const uint8_t *base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
 }
@@ -171,6 +174,8 @@ __device__ __forceinline__ void barrier() {
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 }
+
+__device__ const uint8_t kZeros[16] = {};
 
 // Bytes of a row in one step, its 16-byte pieces, and where piece p of row r lies.
 template <int F>
@@ -201,7 +206,8 @@ __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
 }
 
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kDwords>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint32_t nb, uint32_t mt, uint32_t nt, bool wide) {
+__global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint32_t nb, uint32_t mt, uint32_t nt, uint32_t per,
+                                                           uint64_t part, bool wide) {
   using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kDwords>;
   constexpr int kBuf = T::kBuf;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuf * T::kStage];
@@ -222,7 +228,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   const uint32_t mr = uint32_t(p.m - m0 < uint64_t(T::kBM) ? p.m - m0 : T::kBM);  // rows of this tile
   const uint32_t nr = uint32_t(p.n - n0 < uint64_t(T::kBN) ? p.n - n0 : T::kBN);
   const uint32_t pa = nb * code_bytes<FA>(), pw = nb * code_bytes<FW>();
-  const uint8_t *a0 = p.a + m0 * pa, *w0 = p.w + n0 * pw, *as0 = p.as + m0 * nb, *ws0 = p.ws + n0 * nb;
+  // this workgroup's piece of k: `per` steps from the first on, its sums to
+  // an output of its own
+  const uint32_t first = blockIdx.y * per, blocks = nb - 4 * first < 4 * per ? nb - 4 * first : 4 * per;
+  const uint8_t *a0 = p.a + m0 * pa + uint64_t(first) * Lay<FA>::kRow, *w0 = p.w + n0 * pw + uint64_t(first) * Lay<FW>::kRow;
+  const uint8_t *as0 = p.as + m0 * nb + 4 * first, *ws0 = p.ws + n0 * nb + 4 * first;
+  p.out += blockIdx.y * part;
 
   // offsets of this lane's copies from the tile's first row; rows past the
   // end are read as the last one
@@ -253,37 +264,40 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     sto[c] = T::kABytes + T::kWBytes + q * 256;
   }
   const uint32_t lds0 = lds_offset(lds);
-  // A last step of fewer than four blocks: absent pieces of the activations
-  // are zeros, those of the weights and the scales repeat the row's last
-  // block.  A NaN that this multiplies by zero is one that the row has anyway.
-  const uint32_t steps = (nb + 3) / 4, rest = nb % 4;
-  const uint32_t pa_piece = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
-  const uint32_t pw_piece = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
-  const bool absent = rest && pa_piece / (FA == FP8 ? 2 : 1) >= rest;
-  const uint32_t back = rest && pw_piece / (FW == FP8 ? 2 : 1) >= rest ? 16 * (pw_piece - (FW == FP8 ? 2 * rest - 1 : rest - 1)) : 0;
-  const auto copy = [&](uint32_t t) {
-    const uint32_t stage = (t % kBuf) * T::kStage, to = __builtin_amdgcn_readfirstlane(lds0 + stage);
-    const uint32_t s = t < steps ? t : steps - 1;  // past the end: copied, never used
+  // A last step of fewer than four blocks (there is none where scales come in
+  // dwords): the absent pieces of the activations are copied from zeros,
+  // those of the weights and the scales repeat the row's last block.  A NaN
+  // that this multiplies by zero is one that the row has anyway.
+  const uint32_t steps = (blocks + 3) / 4, rest = kDwords ? 0 : blocks % 4;
+  const uint32_t pa0 = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
+  const uint32_t pw0 = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
+  const bool absent = rest && pa0 / (FA == FP8 ? 2 : 1) >= rest;
+  const uint32_t last_piece = (FW == FP8 ? 2 : 1) * rest - 1, back = rest && pw0 > last_piece ? 16 * (pw0 - last_piece) : 0;
+  // copies `from` to `to` of step t's kPerStep; past the end the last step is
+  // copied again and never used
+  const auto copy = [&](uint32_t t, uint32_t stage, int from, int to) {
+    const uint32_t s = t < steps ? t : steps - 1, at = lds0 + stage;
     const bool last = s == steps - 1;
-    const uint8_t *a = uniform(a0 + uint64_t(s) * Lay<FA>::kRow), *w = uniform(w0 + uint64_t(s) * Lay<FW>::kRow);
-    if (!last || !absent) {
 #pragma unroll
-      for (int c = 0; c < T::kAC; c++) copy16(to + (c * T::kWaves + wave) * 1024, a, oa[c]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < T::kAC; c++)
-        *reinterpret_cast<u32x4 *>(lds + stage + (c * T::kWaves + wave) * 1024 + 16 * lane) = u32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int c = 0; c < T::kWC; c++)
-      copy16(to + T::kABytes + (c * T::kWaves + wave) * 1024, w, ow[c] - (last ? back : 0));
-#pragma unroll
-    for (int c = 0; c < T::kSC; c++) {
-      if constexpr (kDwords) {
-        copy4(to + sto[c], uniform(sbase[c] + 4 * s), os[c]);
+    for (int u = from; u < to; u++) {
+      if (u < T::kAC) {
+        const uint8_t *a = a0 + uint64_t(s) * Lay<FA>::kRow;
+        if constexpr (kDwords)
+          copy16(at + (u * T::kWaves + wave) * 1024, uniform(a), oa[u]);
+        else
+          copy16(at + (u * T::kWaves + wave) * 1024, last && absent ? kZeros : a + oa[u]);
+      } else if (u < T::kAC + T::kWC) {
+        const int c = u - T::kAC;
+        copy16(at + T::kABytes + (c * T::kWaves + wave) * 1024, uniform(w0 + uint64_t(s) * Lay<FW>::kRow),
+               kDwords ? ow[c] : ow[c] - (last ? back : 0));
       } else {
-        const uint32_t b = 4 * s + sblock[c];
-        copy1(to + sto[c], uniform(sbase[c] + (b < nb ? b : nb - 1)), os[c]);
+        const int c = u - T::kAC - T::kWC;
+        if constexpr (kDwords) {
+          copy4(at + sto[c], uniform(sbase[c] + 4 * s), os[c]);
+        } else {
+          const uint32_t b = 4 * s + sblock[c];
+          copy1(at + sto[c], uniform(sbase[c] + (b < blocks ? b : blocks - 1)), os[c]);
+        }
       }
     }
   };
@@ -334,42 +348,52 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     xw[i] = read(IW{}, stage + lw0 + i * 16 * Lay<FW>::kRow, stage + lw1 + i * 16 * Lay<FW>::kRow);
     sw[i] = scale(stage, T::kBM + wn * 16 * TN + 16 * i);
   };
-  {
+  // An empty statement that takes the sums keeps a group of products from
+  // being moved past the copies and waits behind it, which they do not touch.
+  const auto keep = [&](int i, int j) {
 #pragma unroll
-    for (int t = 0; t < kBuf; t++) copy(t);
-    wait_copies<(kBuf - 1) * T::kPerStep>();
+    for (int q = 0; q < kHalf; q++) asm volatile("" : "+a"(acc[i][j + q]));
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // The copies of a step are spread over the products, for the address unit
+  // takes 16 cycles for each and would hold the wave up: half of those of step
+  // t + kBuf go out in the upper half of step t, half in the next lower half.
+  constexpr int kMid = T::kPerStep / 2;
+#pragma unroll
+  for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kPerStep : kMid);
+  wait_copies<(kBuf - 2) * T::kPerStep + kMid>();
+  barrier();
+#pragma unroll
+  for (int i = 0; i < TN; i++) read_w(0, i);
+#pragma unroll
+  for (int j = 0; j < kHalf; j++) read_a(0, j);
+  uint32_t here = 0, before = (kBuf - 1) * T::kStage;
+  for (uint32_t t = 0; t < steps; t++) {
+    const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
+#pragma unroll
+    for (int i = 0; i < TN; i++) {
+#pragma unroll
+      for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
+      if (i < kHalf) read_a(here, kHalf + i);
+      copy(t + kBuf - 1, before, kMid + i * (T::kPerStep - kMid) / TN, kMid + (i + 1) * (T::kPerStep - kMid) / TN);
+      keep(i, 0);
+    }
+    wait_copies<(kBuf - 2) * T::kPerStep>();
     wait_lds();
     barrier();
 #pragma unroll
-    for (int i = 0; i < TN; i++) read_w(0, i);
+    for (int i = 0; i < TN; i++) {
 #pragma unroll
-    for (int j = 0; j < kHalf; j++) read_a(0, j);
-    uint32_t here = 0;
-    for (uint32_t t = 0; t < steps; t++) {
-      const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
-#pragma unroll
-      for (int i = 0; i < TN; i++) {
-#pragma unroll
-        for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
-        if (i < kHalf) read_a(here, kHalf + i);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      wait_copies<(kBuf - 2) * T::kPerStep>();
-      wait_lds();
-      barrier();
-      copy(t + kBuf);
-#pragma unroll
-      for (int i = 0; i < TN; i++) {
-#pragma unroll
-        for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
-        read_w(next, i);
-        if (i < kHalf) read_a(next, i);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      here = next;
+      for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
+      read_w(next, i);
+      if (i < kHalf) read_a(next, i);
+      copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
+      keep(i, kHalf);
     }
-    wait_copies<0>();  // none may land after the workgroup's end
+    before = here;
+    here = next;
   }
+  wait_copies<0>();  // none may land after the workgroup's end
 
   if (wide && mr == T::kBM && nr == T::kBN) {
     uint8_t *to = p.out + ((m0 + wm * 16 * TM + r) * p.out_stride + n0 + wn * 16 * TN + 16 * g) * esize(OUT);
@@ -419,27 +443,81 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   }
 }
 
+// The pieces' sums, joined in their order: four n a lane.
+template <int OUT>
+__global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces, uint64_t np, uint32_t quads, bool wide) {
+  const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x, m = i / quads, n = 4 * (i % quads);
+  if (m >= p.m) return;
+  const float *from = reinterpret_cast<const float *>(p.scratch) + m * np + n;
+  f32x4 s = *reinterpret_cast<const f32x4 *>(from);
+  for (uint32_t j = 1; j < pieces; j++) s += *reinterpret_cast<const f32x4 *>(from + j * p.m * np);
+  store4<OUT>(p, m, n, s, wide);
+}
+
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
-hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
+hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t pieces, hipStream_t s) {
   using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, false>;
   const bool wide = (uintptr_t(p.out) & 15) == 0 && (p.out_stride * esize(OUT)) % 16 == 0;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
   const bool dwords = nb % 4 == 0 && uintptr_t(p.as) % 4 == 0 && uintptr_t(p.ws) % 4 == 0;
+  const uint32_t steps = (nb + 3) / 4, per = (steps + pieces - 1) / pieces;
+  const uint64_t part = p.m * p.out_stride * esize(OUT);
+  const dim3 grid(mt * nt, (steps + per - 1) / per);
   if (dwords)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<mt * nt, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<mt * nt, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
   return hipGetLastError();
 }
+
+enum Form { kFew, kSmall, kMiddle, kLarge };
+struct Plan {
+  Form form;
+  uint32_t pieces;
+};
+
+template <int FA, int FW, int OUT>
+hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t pieces, hipStream_t s) {
+  if (f == kSmall) return tiled<FA, FW, OUT, 2, 4, 2, 1>(p, nb, pieces, s);
+  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2>(p, nb, pieces, s);
+  return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, pieces, s);
+}
+
+// Which form and how many pieces of k.
+Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
+  const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
+  // offsets inside a tile are 32-bit, and so are the tiles' numbers
+  if (m <= 16 || nb > (1u << 18) || m * n >= (1ull << 42)) return {kFew, 1};
+  const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+  if (tiles(256, 256) >= 200) return {kLarge, 1};
+  if (tiles(128, 128) >= 200) return {kMiddle, 1};
+  const uint64_t t = tiles(64, 64);
+  uint32_t pieces = uint32_t(t >= 512 ? 1 : (512 + t - 1) / t);
+  if (pieces > steps / 8) pieces = steps / 8 ? steps / 8 : 1;
+  // whole pieces: none may be empty
+  const uint32_t per = (steps + pieces - 1) / pieces;
+  return {kSmall, (steps + per - 1) / per};
+}
+
+uint64_t padded(uint64_t n) { return (n + 3) & ~uint64_t(3); }
 
 template <int FA, int FW, int OUT>
 hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
   const bool wide = (uintptr_t(p.out) & 15) == 0 && p.out_stride % 4 == 0;
+  const Plan plan = plan_of(p.m, p.n, p.k);
+  if (plan.form != kFew) {
+    if (plan.pieces == 1) return tiled_form<FA, FW, OUT>(plan.form, p, nb, 1, s);
+    MxMatmulArgs q = p;
+    q.out = p.scratch;
+    q.out_stride = padded(p.n);
+    const hipError_t e = tiled_form<FA, FW, FP32>(plan.form, q, nb, plan.pieces, s);
+    if (e != hipSuccess) return e;
+    const uint32_t quads = uint32_t(q.out_stride / 4);
+    k_mx_join<OUT><<<uint32_t((p.m * quads + 255) / 256), 256, 0, s>>>(p, plan.pieces, q.out_stride, quads, wide);
+    return hipGetLastError();
+  }
   const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 15) / 16;
-  // offsets inside a tile are 32-bit, and so are the tiles' numbers
-  if (p.m > 64 && nb <= (1u << 18) && p.m * p.n < (1ull << 46))
-    return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, s);
   if (mt == 1)
     k_mx_few<FA, FW, OUT, 1, 8><<<dim3(uint32_t(nt), 1), 512, 0, s>>>(p, nb, wide);
   else
@@ -463,7 +541,10 @@ hipError_t matmul_out(int out_dtype, const MxMatmulArgs &p, hipStream_t s) {
 
 }  // namespace
 
-uint64_t mx_matmul_scratch(int, int, uint64_t, uint64_t, uint64_t) { return 0; }
+uint64_t mx_matmul_scratch(int, int, uint64_t m, uint64_t n, uint64_t k) {
+  const Plan p = plan_of(m, n, k);
+  return p.pieces > 1 ? p.pieces * m * padded(n) * 4 : 0;
+}
 
 hipError_t launch_mx_matmul(int a_fmt, int w_fmt, int out_dtype, const MxMatmulArgs &p, hipStream_t s) {
   if (a_fmt == FP8) return w_fmt == FP8 ? matmul_out<FP8, FP8>(out_dtype, p, s) : matmul_out<FP8, FP4X2>(out_dtype, p, s);

@@ -406,18 +406,29 @@ _MX_PLAIN = {torch.bfloat16: BF16, torch.float32: FP32}
 _MX_SCALE = (torch.float8_e8m0fnu, torch.uint8)
 
 
-def _mx_device(where: str, stream, **tensors) -> torch.device:
+def _mx_device(where: str, stream, first: torch.Tensor, *others) -> torch.device:
     """The one CUDA device of the call's tensors (and of its stream)."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda or (dev is not None and t.device != dev):
-            raise ZnError(-1, f"{where}: {name} is on {t.device}, not on the call's CUDA device")
-        dev = t.device
-    if stream is not None and stream.device != dev:
-        raise ZnError(-1, f"{where}: the stream is on {stream.device}, the tensors on {dev}")
-    return dev
+    i = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != i:
+            raise ZnError(-1, f"{where}: tensors on {first.device} and {t.device}")
+    if i < 0:
+        raise ZnError(-1, f"{where}: the tensors are on {first.device}, not on a CUDA device")
+    if stream is not None and stream.device.index != i:
+        raise ZnError(-1, f"{where}: the stream is on {stream.device}, the tensors on {first.device}")
+    return first.device
+
+
+def _mx_call(where: str, dev: torch.device, stream, function, *args) -> None:
+    """The library call on the tensors' device and the stream (its current one when None)."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            return _mx_call(where, dev, stream, function, *args)
+    # the handle alone: making a Stream object takes longer than the launch
+    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    rc = function(*args, raw)
+    if rc:
+        raise ZnError(rc, where)
 
 
 def _mx_rows(where: str, name: str, t: torch.Tensor, write: bool = False):
@@ -427,7 +438,8 @@ def _mx_rows(where: str, name: str, t: torch.Tensor, write: bool = False):
         raise ZnError(-1, f"{where}: {name} has no axis")
     k = t.shape[-1]
     if t.is_contiguous():
-        return (t.numel() // k if k else math.prod(t.shape[:-1])), k, k
+        n = t.numel()
+        return (n // k if n else math.prod(t.shape[:-1])), k, k
     stride, rows = None, 1
     for n, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
         if n == 1:
@@ -520,12 +532,11 @@ def mx_quantize(x: torch.Tensor, fmt: int = FP8_E4M3, codes: torch.Tensor | None
     The codes are the tensors that a FP8_E4M3 or FP4X2_E2M1 plan compresses."""
     where = "mx_quantize"
     dt = _mx_plain(where, "x", x.dtype)
-    dev = _mx_device(where, stream, x=x, codes=codes, scales=scales)
+    dev = _mx_device(where, stream, x, codes, scales)
     rows, k, stride = _mx_rows(where, "x", x)
     codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
-    with torch.cuda.device(dev):
-        _check(lib().zn_mx_quantize(dt, x.data_ptr(), stride, rows, k, fmt, codes.data_ptr(), scales.data_ptr(),
-                                    _stream(stream)), where)
+    _mx_call(where, dev, stream, lib().zn_mx_quantize, dt, x.data_ptr(), stride, rows, k, fmt, codes.data_ptr(),
+             scales.data_ptr())
     _mx_use(stream, x, codes, scales)
     return codes, scales
 
@@ -540,7 +551,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int | None = Non
         k = kp
     if not kp - MX_BLOCK < k <= kp:
         raise ZnError(-1, f"{where}: {k} values do not fill rows of {kp}")
-    dev = _mx_device(where, stream, codes=codes, scales=scales, out=out)
+    dev = _mx_device(where, stream, codes, scales, out)
     shape = (*codes.shape[:-1], k)
     if out is None:
         _mx_plain(where, "dtype", dtype)
@@ -549,9 +560,8 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int | None = Non
         raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {shape}")
     dt = _mx_plain(where, "out", out.dtype)
     rows, _, stride = _mx_rows(where, "out", out, write=True)
-    with torch.cuda.device(dev):
-        _check(lib().zn_mx_dequantize(fmt, codes.data_ptr(), scales.data_ptr(), rows, k, dt, out.data_ptr(), stride,
-                                      _stream(stream)), where)
+    _mx_call(where, dev, stream, lib().zn_mx_dequantize, fmt, codes.data_ptr(), scales.data_ptr(), rows, k, dt,
+             out.data_ptr(), stride)
     _mx_use(stream, codes, scales, out)
     return out
 
@@ -564,8 +574,7 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     Without a residual h is x."""
     where = "mx_rms_norm"
     dt = _mx_plain(where, "x", x.dtype)
-    dev = _mx_device(where, stream, x=x, weight=weight, residual=residual, residual_out=residual_out, codes=codes,
-                     scales=scales)
+    dev = _mx_device(where, stream, x, weight, residual, residual_out, codes, scales)
     rows, k, stride = _mx_rows(where, "x", x)
     if weight.dtype != x.dtype or tuple(weight.shape) != (k,) or not weight.is_contiguous():
         raise ZnError(-1, f"{where}: weight is {weight.dtype} {tuple(weight.shape)}, wanted dense {x.dtype} {(k,)}")
@@ -585,11 +594,9 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
                               f"x {x.dtype} {tuple(x.shape)}")
         hs = _mx_rows(where, "residual_out", residual_out, write=True)[2]
     codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
-    with torch.cuda.device(dev):
-        _check(lib().zn_mx_rms_norm(dt, x.data_ptr(), stride, residual.data_ptr() if residual is not None else None,
-                                    rs, weight.data_ptr(), eps, rows, k,
-                                    residual_out.data_ptr() if residual is not None else None, hs, fmt,
-                                    codes.data_ptr(), scales.data_ptr(), _stream(stream)), where)
+    _mx_call(where, dev, stream, lib().zn_mx_rms_norm, dt, x.data_ptr(), stride,
+             residual.data_ptr() if residual is not None else None, rs, weight.data_ptr(), eps, rows, k,
+             residual_out.data_ptr() if residual is not None else None, hs, fmt, codes.data_ptr(), scales.data_ptr())
     _mx_use(stream, x, weight, residual, residual_out, codes, scales)
     return codes, scales, (x if residual is None else residual_out)
 
@@ -612,7 +619,7 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     fw, kw = _mx_packed(where, "w", w, w_scales)
     if w.dim() != 2 or kw != k:
         raise ZnError(-1, f"{where}: w has rows of {kw} values and {w.dim()} axes, wanted {k} and 2")
-    dev = _mx_device(where, stream, a=a, a_scales=a_scales, w=w, w_scales=w_scales, out=out, scratch=scratch)
+    dev = _mx_device(where, stream, a, a_scales, w, w_scales, out, scratch)
     n = w.shape[0]
     shape = (*a.shape[:-1], n)
     if out is None:
@@ -627,11 +634,9 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
         scratch = _mx_new((need,), torch.uint8, dev, stream) if need else None
     elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
         raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
-    with torch.cuda.device(dev):
-        _check(lib().zn_mx_matmul(fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(), w_scales.data_ptr(),
-                                  m, n, k, dt, out.data_ptr(), stride,
-                                  scratch.data_ptr() if scratch is not None else None,
-                                  scratch.numel() if scratch is not None else 0, _stream(stream)), where)
+    _mx_call(where, dev, stream, lib().zn_mx_matmul, fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(),
+             w_scales.data_ptr(), m, n, k, dt, out.data_ptr(), stride,
+             scratch.data_ptr() if scratch is not None else None, scratch.numel() if scratch is not None else 0)
     _mx_use(stream, a, a_scales, w, w_scales, out, scratch)
     return out
 
