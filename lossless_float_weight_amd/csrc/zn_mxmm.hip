@@ -145,10 +145,12 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb,
 // all at the barrier that ends a step.  The base's two scalar registers may
 // come from vector instructions (uniform), which takes 5 wait states before a
 // memory instruction that the compiler does not see: s_nop 4.
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
+         (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32);
+}
 __device__ __forceinline__ const uint8_t *uniform(const uint8_t *p) {
-  const uint64_t v = uint64_t(uintptr_t(p));
-  return reinterpret_cast<const uint8_t *>(uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
-                                           (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32));
+  return reinterpret_cast<const uint8_t *>(uniform(uint64_t(uintptr_t(p))));
 }
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
   return uint32_t(uintptr_t((__attribute__((address_space(3))) const void *)p));
@@ -158,6 +160,11 @@ __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t *base, uint32
 }
 __device__ __forceinline__ void copy16(uint32_t lds, const uint8_t *from) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(lds), "v"(from) : "memory");
+}
+// for the lanes of a mask, in code that all lanes run
+__device__ __forceinline__ void copy16_of(uint32_t lds, const uint8_t *base, uint32_t off, uint64_t lanes) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
+               ::"s"(lds), "v"(off), "s"(base), "s"(lanes) : "memory");
 }
 __device__ __forceinline__ void copy4(uint32_t lds, const uint8_t *base, uint32_t off) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
@@ -184,20 +191,32 @@ struct Lay {
   __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return F == FP8 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
 };
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kDwords>
+// How the scale bytes reach LDS.  A copy of a lane is a request of its own
+// (rows lie far apart), so the wider ones leave the caches more room.
+enum ScaleWay {
+  kByBytes,   // any k: a byte of a block, a dword of LDS
+  kByDwords,  // whole steps: the four blocks of a step
+  kByQuads    // whole fours of steps: their 16 blocks
+};
+
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, ScaleWay kWay>
 struct Tiled {
   static constexpr int kWaves = WM * WN, kBM = 16 * TM * WM, kBN = 16 * TN * WN;
   static constexpr uint32_t kABytes = kBM * Lay<FA>::kRow, kWBytes = kBN * Lay<FW>::kRow;
-  // scale bytes: a dword of four blocks a row, or a dword for each block
-  static constexpr uint32_t kSRow = kDwords ? 4 : 16, kSBytes = (kBM + kBN) * kSRow;
+  static constexpr uint32_t kSBytes = kWay == kByQuads ? 0 : (kBM + kBN) * (kWay == kByDwords ? 4 : 16);
   static constexpr uint32_t kStage = kABytes + kWBytes + kSBytes;
-  static constexpr int kBuf = 3 * kStage <= 160 * 1024 ? 3 : 2;
+  static constexpr uint32_t kQuad = kWay == kByQuads ? (kBM + kBN) * 16 : 0;  // two of them, beside the stages
+  static constexpr int kBuf = 3 * kStage + 2 * kQuad <= 160 * 1024 ? 3 : 2;
+  static constexpr uint32_t kLds = kBuf * kStage + 2 * kQuad;
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
-  static constexpr int kSChunks = (kBM + kBN) / 64 * (kDwords ? 1 : 4), kSC = (kSChunks + kWaves - 1) / kWaves;
-  static constexpr int kPerStep = kAC + kWC + kSC;
-  static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 4 == 0, "tile");
+  static constexpr int kSChunks = (kBM + kBN) / 64 * (kWay == kByDwords ? 1 : 4);
+  static constexpr int kSC = kWay == kByQuads ? 1 : (kSChunks + kWaves - 1) / kWaves;
+  // copies of a wave in a step, those spread over the two halves, and those of the upper half
+  static constexpr int kPerStep = kAC + kWC + kSC, kSpread = kPerStep - (kWay == kByQuads ? 1 : 0), kMid = kSpread / 2;
+  static constexpr uint32_t kRowsA = kBM / kWaves, kRowsW = kBN / kWaves;
+  static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 4 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
   static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
-  static_assert(kBuf * kStage <= 160 * 1024 && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
+  static_assert(kLds <= 160 * 1024 && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
 };
 
 // Weight row of LDS row r: tile i, row 4 g + q of it stands for n = 16 g + 4 i + q of the 64.
@@ -205,12 +224,12 @@ __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
   return (r & ~63u) + ((r >> 2) & 3) * 16 + ((r >> 4) & 3) * 4 + (r & 3);
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kDwords>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, ScaleWay kWay>
 __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint32_t nb, uint32_t mt, uint32_t nt, uint32_t per,
                                                            uint64_t part, bool wide) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kDwords>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kWay>;
   constexpr int kBuf = T::kBuf;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kBuf * T::kStage];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
   const uint32_t wm = wave % WM, wn = wave / WM;
 
@@ -249,26 +268,31 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     ow[c] = from * pw + 16 * Lay<FW>::piece(row, q % Lay<FW>::kPieces);
   }
   const uint8_t *sbase[T::kSC];
-  uint32_t sto[T::kSC], sblock[T::kSC];
+  uint32_t sto[T::kSC], sblock[T::kSC], osa = 0, osw = 0;
+  if constexpr (kWay == kByQuads) {
+    const uint32_t row = wave * T::kRowsA + lane, n = weight_row(wave * T::kRowsW + lane);
+    osa = (row < mr ? row : mr - 1) * nb;
+    osw = (n < nr ? n : nr - 1) * nb;
+  } else {
 #pragma unroll
-  for (int c = 0; c < T::kSC; c++) {
-    uint32_t q = c * T::kWaves + wave;
-    q = q < uint32_t(T::kSChunks) ? q : T::kSChunks - 1;  // the same copy twice
-    const uint32_t chunk = kDwords ? q : q / 4, row = chunk * 64 + lane;
-    const bool isa = chunk < T::kBM / 64;
-    const uint32_t n = weight_row(isa ? 0 : row - T::kBM);
-    const uint32_t from = isa ? (row < mr ? row : mr - 1) : (n < nr ? n : nr - 1);
-    os[c] = from * nb;
-    sbase[c] = isa ? as0 : ws0;
-    sblock[c] = q & 3;
-    sto[c] = T::kABytes + T::kWBytes + q * 256;
+    for (int c = 0; c < T::kSC; c++) {
+      uint32_t q = c * T::kWaves + wave;
+      q = q < uint32_t(T::kSChunks) ? q : T::kSChunks - 1;  // the same copy twice
+      const uint32_t chunk = kWay == kByDwords ? q : q / 4, row = chunk * 64 + lane;
+      const bool isa = chunk < T::kBM / 64;
+      const uint32_t n = weight_row(isa ? 0 : row - T::kBM);
+      const uint32_t from = isa ? (row < mr ? row : mr - 1) : (n < nr ? n : nr - 1);
+      os[c] = from * nb;
+      sbase[c] = isa ? as0 : ws0;
+      sblock[c] = q & 3;
+      sto[c] = T::kABytes + T::kWBytes + q * 256;
+    }
   }
   const uint32_t lds0 = lds_offset(lds);
-  // A last step of fewer than four blocks (there is none where scales come in
-  // dwords): the absent pieces of the activations are copied from zeros,
+  // A last step of fewer than four blocks (only where scales come in bytes): the absent pieces of the activations are copied from zeros,
   // those of the weights and the scales repeat the row's last block.  A NaN
   // that this multiplies by zero is one that the row has anyway.
-  const uint32_t steps = (blocks + 3) / 4, rest = kDwords ? 0 : blocks % 4;
+  const uint32_t steps = (blocks + 3) / 4, rest = kWay != kByBytes ? 0 : blocks % 4;
   const uint32_t pa0 = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
   const uint32_t pw0 = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
   const bool absent = rest && pa0 / (FA == FP8 ? 2 : 1) >= rest;
@@ -276,29 +300,42 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   // copies `from` to `to` of step t's kPerStep; past the end the last step is
   // copied again and never used
   const auto copy = [&](uint32_t t, uint32_t stage, int from, int to) {
-    const uint32_t s = t < steps ? t : steps - 1, at = lds0 + stage;
+    const uint32_t s = t < steps ? t : steps - 1, at = __builtin_amdgcn_readfirstlane(lds0 + stage);
     const bool last = s == steps - 1;
 #pragma unroll
     for (int u = from; u < to; u++) {
       if (u < T::kAC) {
         const uint8_t *a = a0 + uint64_t(s) * Lay<FA>::kRow;
-        if constexpr (kDwords)
+        if constexpr (kWay != kByBytes)
           copy16(at + (u * T::kWaves + wave) * 1024, uniform(a), oa[u]);
         else
           copy16(at + (u * T::kWaves + wave) * 1024, last && absent ? kZeros : a + oa[u]);
       } else if (u < T::kAC + T::kWC) {
         const int c = u - T::kAC;
         copy16(at + T::kABytes + (c * T::kWaves + wave) * 1024, uniform(w0 + uint64_t(s) * Lay<FW>::kRow),
-               kDwords ? ow[c] : ow[c] - (last ? back : 0));
-      } else {
+               kWay != kByBytes ? ow[c] : ow[c] - (last ? back : 0));
+      } else if constexpr (kWay != kByQuads) {
         const int c = u - T::kAC - T::kWC;
-        if constexpr (kDwords) {
+        if constexpr (kWay == kByDwords) {
           copy4(at + sto[c], uniform(sbase[c] + 4 * s), os[c]);
         } else {
           const uint32_t b = 4 * s + sblock[c];
           copy1(at + sto[c], uniform(sbase[c] + (b < blocks ? b : blocks - 1)), os[c]);
         }
       }
+    }
+  };
+
+  // The 16 scale bytes of steps 4 q .. 4 q + 3 of every row, one copy of a wave
+  // at a time: `side` 0 the activations', 1 the weights', else none (the copy
+  // is issued for no lane, so that every step counts the same).
+  const auto copy_quad = [&](uint32_t q, uint32_t side) {
+    if constexpr (kWay == kByQuads) {
+      const uint32_t at = lds0 + kBuf * T::kStage + (q & 1) * T::kQuad;
+      const uint32_t c = 4 * q < steps ? q : steps / 4 - 1;
+      const uint64_t lanes = side > 1 ? 0 : ~0ull >> (64 - (side ? T::kRowsW : T::kRowsA));
+      const uint32_t to = at + 16 * (side ? T::kBM + wave * T::kRowsW : wave * T::kRowsA);
+      copy16_of(__builtin_amdgcn_readfirstlane(to), uniform((side ? ws0 : as0) + 16 * c), side ? osw : osa, uniform(lanes));
     }
   };
 
@@ -313,13 +350,20 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     else
       return operand<FP4X2>(x, x);
   };
+  // the scale of step t (in `stage`) for 16 rows from `row` on, of A then W;
+  // the instruction reads the low byte only
   const uint32_t srow = T::kABytes + T::kWBytes;
-  const auto scale = [&](uint32_t stage, uint32_t row) -> uint32_t {  // row: a multiple of 16, of A then W
-    if constexpr (kDwords)
-      return lds[stage + srow + (row + r) * 4 + g];
-    else
-      return lds[stage + srow + (row / 64) * 1024 + g * 256 + (row % 64 + r) * 4];
+  const auto scale = [&](uint32_t t, uint32_t stage, uint32_t row) -> uint32_t {
+    if constexpr (kWay == kByQuads) {
+      const uint32_t quad = kBuf * T::kStage + ((t >> 2) & 1) * T::kQuad + 4 * (t & 3);
+      return *reinterpret_cast<const uint32_t *>(lds + quad + 16 * r + 16 * row);
+    } else if constexpr (kWay == kByDwords) {
+      return *reinterpret_cast<const uint32_t *>(lds + stage + srow + (row + r) * 4);
+    } else {
+      return *reinterpret_cast<const uint32_t *>(lds + stage + srow + (row / 64) * 1024 + g * 256 + (row % 64 + r) * 4);
+    }
   };
+  const uint32_t shift = kWay == kByBytes ? 0 : 8 * g;  // to the lane group's block
   using IA = std::integral_constant<int, FA>;
   using IW = std::integral_constant<int, FW>;
 
@@ -340,13 +384,13 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   constexpr int kHalf = TM / 2;
   i32x8 xa[TM], xw[TN];
   uint32_t sa[TM], sw[TN];
-  const auto read_a = [&](uint32_t stage, int j) {
+  const auto read_a = [&](uint32_t t, uint32_t stage, int j) {
     xa[j] = read(IA{}, stage + la0 + j * 16 * Lay<FA>::kRow, stage + la1 + j * 16 * Lay<FA>::kRow);
-    sa[j] = scale(stage, wm * 16 * TM + 16 * j);
+    sa[j] = scale(t, stage, wm * 16 * TM + 16 * j);
   };
-  const auto read_w = [&](uint32_t stage, int i) {
+  const auto read_w = [&](uint32_t t, uint32_t stage, int i) {
     xw[i] = read(IW{}, stage + lw0 + i * 16 * Lay<FW>::kRow, stage + lw1 + i * 16 * Lay<FW>::kRow);
-    sw[i] = scale(stage, T::kBM + wn * 16 * TN + 16 * i);
+    sw[i] = scale(t, stage, T::kBM + wn * 16 * TN + 16 * i);
   };
   // An empty statement that takes the sums keeps a group of products from
   // being moved past the copies and waits behind it, which they do not touch.
@@ -358,24 +402,30 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   // The copies of a step are spread over the products, for the address unit
   // takes 16 cycles for each and would hold the wave up: half of those of step
   // t + kBuf go out in the upper half of step t, half in the next lower half.
-  constexpr int kMid = T::kPerStep / 2;
+  // Scales by quads: those of quad q + 1 go out in the upper halves of steps
+  // 4 q - 1 and 4 q, when quad q - 1, which lay there, has been read, and are
+  // first read in the upper half of step 4 q + 3, two waits later.
+  constexpr int kMid = T::kMid, kRest = T::kSpread - kMid;
+  copy_quad(0, 0);
+  copy_quad(0, 1);
 #pragma unroll
-  for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kPerStep : kMid);
-  wait_copies<(kBuf - 2) * T::kPerStep + kMid>();
+  for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
+  copy_quad(1, 0);
+  wait_copies<(kBuf - 2) * T::kSpread + kMid + (kWay == kByQuads ? 1 : 0)>();
   barrier();
 #pragma unroll
-  for (int i = 0; i < TN; i++) read_w(0, i);
+  for (int i = 0; i < TN; i++) read_w(0, 0, i);
 #pragma unroll
-  for (int j = 0; j < kHalf; j++) read_a(0, j);
+  for (int j = 0; j < kHalf; j++) read_a(0, 0, j);
   uint32_t here = 0, before = (kBuf - 1) * T::kStage;
   for (uint32_t t = 0; t < steps; t++) {
     const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
 #pragma unroll
     for (int i = 0; i < TN; i++) {
 #pragma unroll
-      for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
-      if (i < kHalf) read_a(here, kHalf + i);
-      copy(t + kBuf - 1, before, kMid + i * (T::kPerStep - kMid) / TN, kMid + (i + 1) * (T::kPerStep - kMid) / TN);
+      for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i] >> shift, sa[j] >> shift);
+      if (i < kHalf) read_a(t, here, kHalf + i);
+      copy(t + kBuf - 1, before, kMid + i * kRest / TN, kMid + (i + 1) * kRest / TN);
       keep(i, 0);
     }
     wait_copies<(kBuf - 2) * T::kPerStep>();
@@ -384,10 +434,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
 #pragma unroll
     for (int i = 0; i < TN; i++) {
 #pragma unroll
-      for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i], sa[j]);
-      read_w(next, i);
-      if (i < kHalf) read_a(next, i);
+      for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i] >> shift, sa[j] >> shift);
+      read_w(t + 1, next, i);
+      if (i < kHalf) read_a(t + 1, next, i);
       copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
+      if (i == TN - 1) copy_quad((t + 1) / 4 + 1, (t + 1) & 3);
       keep(i, kHalf);
     }
     before = here;
@@ -455,48 +506,51 @@ __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces
 }
 
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
-hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t pieces, hipStream_t s) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, false>;
+hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kByBytes>;
   const bool wide = (uintptr_t(p.out) & 15) == 0 && (p.out_stride * esize(OUT)) % 16 == 0;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
-  const bool dwords = nb % 4 == 0 && uintptr_t(p.as) % 4 == 0 && uintptr_t(p.ws) % 4 == 0;
-  const uint32_t steps = (nb + 3) / 4, per = (steps + pieces - 1) / pieces;
+  const uint32_t steps = (nb + 3) / 4;
+  const uintptr_t at = uintptr_t(p.as) | uintptr_t(p.ws);
   const uint64_t part = p.m * p.out_stride * esize(OUT);
   const dim3 grid(mt * nt, (steps + per - 1) / per);
-  if (dwords)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
+  if (nb % 16 == 0 && per % 4 == 0 && at % 16 == 0)
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByQuads><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
+  else if (nb % 4 == 0 && at % 4 == 0)
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByDwords><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByBytes><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
   return hipGetLastError();
 }
 
 enum Form { kFew, kSmall, kMiddle, kLarge };
 struct Plan {
   Form form;
-  uint32_t pieces;
+  uint32_t per, pieces;  // steps of a piece of k, and their number
 };
 
 template <int FA, int FW, int OUT>
-hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t pieces, hipStream_t s) {
-  if (f == kSmall) return tiled<FA, FW, OUT, 2, 4, 2, 1>(p, nb, pieces, s);
-  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2>(p, nb, pieces, s);
-  return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, pieces, s);
+hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
+  if (f == kSmall) return tiled<FA, FW, OUT, 2, 4, 2, 1>(p, nb, per, s);
+  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2>(p, nb, per, s);
+  return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, per, s);
 }
 
 // Which form and how many pieces of k.
 Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
   const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
   // offsets inside a tile are 32-bit, and so are the tiles' numbers
-  if (m <= 16 || nb > (1u << 18) || m * n >= (1ull << 42)) return {kFew, 1};
+  if (m <= 16 || nb > (1u << 18) || m * n >= (1ull << 42)) return {kFew, steps, 1};
   const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  if (tiles(256, 256) >= 200) return {kLarge, 1};
-  if (tiles(128, 128) >= 200) return {kMiddle, 1};
+  if (tiles(256, 256) >= 200) return {kLarge, steps, 1};
+  if (tiles(128, 128) >= 200) return {kMiddle, steps, 1};
   const uint64_t t = tiles(64, 64);
   uint32_t pieces = uint32_t(t >= 512 ? 1 : (512 + t - 1) / t);
   if (pieces > steps / 8) pieces = steps / 8 ? steps / 8 : 1;
-  // whole pieces: none may be empty
-  const uint32_t per = (steps + pieces - 1) / pieces;
-  return {kSmall, (steps + per - 1) / per};
+  // whole fours of steps where k has them, and no empty piece
+  uint32_t per = (steps + pieces - 1) / pieces;
+  if (nb % 16 == 0) per = (per + 3) & ~3u;
+  return {kSmall, per, (steps + per - 1) / per};
 }
 
 uint64_t padded(uint64_t n) { return (n + 3) & ~uint64_t(3); }
@@ -507,11 +561,11 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const bool wide = (uintptr_t(p.out) & 15) == 0 && p.out_stride % 4 == 0;
   const Plan plan = plan_of(p.m, p.n, p.k);
   if (plan.form != kFew) {
-    if (plan.pieces == 1) return tiled_form<FA, FW, OUT>(plan.form, p, nb, 1, s);
+    if (plan.pieces == 1) return tiled_form<FA, FW, OUT>(plan.form, p, nb, plan.per, s);
     MxMatmulArgs q = p;
     q.out = p.scratch;
     q.out_stride = padded(p.n);
-    const hipError_t e = tiled_form<FA, FW, FP32>(plan.form, q, nb, plan.pieces, s);
+    const hipError_t e = tiled_form<FA, FW, FP32>(plan.form, q, nb, plan.per, s);
     if (e != hipSuccess) return e;
     const uint32_t quads = uint32_t(q.out_stride / 4);
     k_mx_join<OUT><<<uint32_t((p.m * quads + 255) / 256), 256, 0, s>>>(p, plan.pieces, q.out_stride, quads, wide);
