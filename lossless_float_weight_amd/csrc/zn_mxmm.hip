@@ -135,9 +135,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb,
 // LDS holds a step's rows as the wave's loads lay them down, 1 KB at a time;
 // the 16-byte pieces of a row are exchanged by the row's low bits (at the
 // source, a lane may load from anywhere) so that the 16 rows of an operand
-// lie in different banks.  The weight rows of 64 are taken in the order that
-// leaves a lane 16 consecutive n over four tiles, a whole line over four lane
-// groups.
+// lie in different banks.
 //
 // Asynchronous copies are written as instructions because the compiler makes
 // every later LDS read wait for the builtin's; they have no register output.
@@ -191,43 +189,39 @@ struct Lay {
   __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return F == FP8 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
 };
 
-// How the scale bytes reach LDS.  A copy of a lane is a request of its own
-// (rows lie far apart), so the wider ones leave the caches more room.
-enum ScaleWay {
-  kByBytes,   // any k: a byte of a block, a dword of LDS
-  kByDwords,  // whole steps: the four blocks of a step
-  kByQuads    // whole fours of steps: their 16 blocks
-};
-
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, ScaleWay kWay>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
 struct Tiled {
   static constexpr int kWaves = WM * WN, kBM = 16 * TM * WM, kBN = 16 * TN * WN;
   static constexpr uint32_t kABytes = kBM * Lay<FA>::kRow, kWBytes = kBN * Lay<FW>::kRow;
-  static constexpr uint32_t kSBytes = kWay == kByQuads ? 0 : (kBM + kBN) * (kWay == kByDwords ? 4 : 16);
-  static constexpr uint32_t kStage = kABytes + kWBytes + kSBytes;
-  static constexpr uint32_t kQuad = kWay == kByQuads ? (kBM + kBN) * 16 : 0;  // two of them, beside the stages
-  static constexpr int kBuf = 3 * kStage + 2 * kQuad <= 160 * 1024 ? 3 : 2;
+  static constexpr uint32_t kStage = kABytes + kWBytes;
+  // the scales of four steps, 16 bytes a row; two of them, beside the stages
+  static constexpr uint32_t kQuad = (kBM + kBN) * 16;
+  // workgroups that a CU should hold at a time: two where the sums leave room
+  static constexpr int kGroups = TM * TN * 4 <= 128 && 2 * (2 * kStage + 2 * kQuad) <= 160 * 1024 ? 2 : 1;
+  static constexpr int kBuf = kGroups * (3 * kStage + 2 * kQuad) <= 160 * 1024 ? 3 : 2;
   static constexpr uint32_t kLds = kBuf * kStage + 2 * kQuad;
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
-  static constexpr int kSChunks = (kBM + kBN) / 64 * (kWay == kByDwords ? 1 : 4);
-  static constexpr int kSC = kWay == kByQuads ? 1 : (kSChunks + kWaves - 1) / kWaves;
-  // copies of a wave in a step, those spread over the two halves, and those of the upper half
-  static constexpr int kPerStep = kAC + kWC + kSC, kSpread = kPerStep - (kWay == kByQuads ? 1 : 0), kMid = kSpread / 2;
+  // copies of a wave in a step: operands, and one of scales
+  static constexpr int kSpread = kAC + kWC, kPerStep = kSpread + 1, kMid = kSpread / 2;
   static constexpr uint32_t kRowsA = kBM / kWaves, kRowsW = kBN / kWaves;
-  static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 4 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
+  static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 2 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
   static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
   static_assert(kLds <= 160 * 1024 && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
 };
 
-// Weight row of LDS row r: tile i, row 4 g + q of it stands for n = 16 g + 4 i + q of the 64.
+// Weight row (from the tile's first) of LDS row r.  For BF16, rows 4 g + q of
+// tiles 2 i and 2 i + 1 stand for n = 32 i + 8 g + 0..3 and + 4..7: a lane has 8
+// consecutive n, 16 bytes, and the four lane groups a run of 64 bytes.  FP32 has
+// that run in one tile.
+template <int OUT>
 __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
-  return (r & ~63u) + ((r >> 2) & 3) * 16 + ((r >> 4) & 3) * 4 + (r & 3);
+  return OUT == BF16 ? (r & ~31u) + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3) : r;
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, ScaleWay kWay>
-__global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint32_t nb, uint32_t mt, uint32_t nt, uint32_t per,
-                                                           uint64_t part, bool wide) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kWay>;
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kWhole>
+__global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::kGroups)) void k_mx_tiled(
+    MxMatmulArgs p, uint32_t nb, uint32_t pitch, uint32_t mt, uint32_t nt, uint32_t per, uint64_t part, bool wide) {
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
   constexpr int kBuf = T::kBuf;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -251,12 +245,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   // an output of its own
   const uint32_t first = blockIdx.y * per, blocks = nb - 4 * first < 4 * per ? nb - 4 * first : 4 * per;
   const uint8_t *a0 = p.a + m0 * pa + uint64_t(first) * Lay<FA>::kRow, *w0 = p.w + n0 * pw + uint64_t(first) * Lay<FW>::kRow;
-  const uint8_t *as0 = p.as + m0 * nb + 4 * first, *ws0 = p.ws + n0 * nb + 4 * first;
+  const uint8_t *as0 = p.as + m0 * pitch + 4 * first, *ws0 = p.ws + n0 * pitch + 4 * first;
   p.out += blockIdx.y * part;
 
   // offsets of this lane's copies from the tile's first row; rows past the
   // end are read as the last one
-  uint32_t oa[T::kAC], ow[T::kWC], os[T::kSC];
+  uint32_t oa[T::kAC], ow[T::kWC];
 #pragma unroll
   for (int c = 0; c < T::kAC; c++) {
     const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FA>::kPieces, from = row < mr ? row : mr - 1;
@@ -264,40 +258,22 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   }
 #pragma unroll
   for (int c = 0; c < T::kWC; c++) {
-    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FW>::kPieces, n = weight_row(row), from = n < nr ? n : nr - 1;
+    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FW>::kPieces, n = weight_row<OUT>(row), from = n < nr ? n : nr - 1;
     ow[c] = from * pw + 16 * Lay<FW>::piece(row, q % Lay<FW>::kPieces);
   }
-  const uint8_t *sbase[T::kSC];
-  uint32_t sto[T::kSC], sblock[T::kSC], osa = 0, osw = 0;
-  if constexpr (kWay == kByQuads) {
-    const uint32_t row = wave * T::kRowsA + lane, n = weight_row(wave * T::kRowsW + lane);
-    osa = (row < mr ? row : mr - 1) * nb;
-    osw = (n < nr ? n : nr - 1) * nb;
-  } else {
-#pragma unroll
-    for (int c = 0; c < T::kSC; c++) {
-      uint32_t q = c * T::kWaves + wave;
-      q = q < uint32_t(T::kSChunks) ? q : T::kSChunks - 1;  // the same copy twice
-      const uint32_t chunk = kWay == kByDwords ? q : q / 4, row = chunk * 64 + lane;
-      const bool isa = chunk < T::kBM / 64;
-      const uint32_t n = weight_row(isa ? 0 : row - T::kBM);
-      const uint32_t from = isa ? (row < mr ? row : mr - 1) : (n < nr ? n : nr - 1);
-      os[c] = from * nb;
-      sbase[c] = isa ? as0 : ws0;
-      sblock[c] = q & 3;
-      sto[c] = T::kABytes + T::kWBytes + q * 256;
-    }
-  }
+  const uint32_t ra = wave * T::kRowsA + lane, rw = weight_row<OUT>(wave * T::kRowsW + lane);
+  const uint32_t osa = (ra < mr ? ra : mr - 1) * pitch, osw = (rw < nr ? rw : nr - 1) * pitch;
   const uint32_t lds0 = lds_offset(lds);
-  // A last step of fewer than four blocks (only where scales come in bytes): the absent pieces of the activations are copied from zeros,
-  // those of the weights and the scales repeat the row's last block.  A NaN
-  // that this multiplies by zero is one that the row has anyway.
-  const uint32_t steps = (blocks + 3) / 4, rest = kWay != kByBytes ? 0 : blocks % 4;
+  // A last step of fewer than four blocks: the absent pieces of the activations
+  // are copied from zeros, those of the weights repeat the row's last block
+  // and the scales are 1.  A NaN that this multiplies by zero is one that the
+  // row has anyway.
+  const uint32_t steps = (blocks + 3) / 4, rest = blocks % 4;
   const uint32_t pa0 = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
   const uint32_t pw0 = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
   const bool absent = rest && pa0 / (FA == FP8 ? 2 : 1) >= rest;
   const uint32_t last_piece = (FW == FP8 ? 2 : 1) * rest - 1, back = rest && pw0 > last_piece ? 16 * (pw0 - last_piece) : 0;
-  // copies `from` to `to` of step t's kPerStep; past the end the last step is
+  // copies `from` to `to` of step t's kSpread; past the end the last step is
   // copied again and never used
   const auto copy = [&](uint32_t t, uint32_t stage, int from, int to) {
     const uint32_t s = t < steps ? t : steps - 1, at = __builtin_amdgcn_readfirstlane(lds0 + stage);
@@ -306,22 +282,14 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     for (int u = from; u < to; u++) {
       if (u < T::kAC) {
         const uint8_t *a = a0 + uint64_t(s) * Lay<FA>::kRow;
-        if constexpr (kWay != kByBytes)
+        if constexpr (kWhole)
           copy16(at + (u * T::kWaves + wave) * 1024, uniform(a), oa[u]);
         else
           copy16(at + (u * T::kWaves + wave) * 1024, last && absent ? kZeros : a + oa[u]);
-      } else if (u < T::kAC + T::kWC) {
+      } else {
         const int c = u - T::kAC;
         copy16(at + T::kABytes + (c * T::kWaves + wave) * 1024, uniform(w0 + uint64_t(s) * Lay<FW>::kRow),
-               kWay != kByBytes ? ow[c] : ow[c] - (last ? back : 0));
-      } else if constexpr (kWay != kByQuads) {
-        const int c = u - T::kAC - T::kWC;
-        if constexpr (kWay == kByDwords) {
-          copy4(at + sto[c], uniform(sbase[c] + 4 * s), os[c]);
-        } else {
-          const uint32_t b = 4 * s + sblock[c];
-          copy1(at + sto[c], uniform(sbase[c] + (b < blocks ? b : blocks - 1)), os[c]);
-        }
+               kWhole ? ow[c] : ow[c] - (last ? back : 0));
       }
     }
   };
@@ -330,13 +298,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   // at a time: `side` 0 the activations', 1 the weights', else none (the copy
   // is issued for no lane, so that every step counts the same).
   const auto copy_quad = [&](uint32_t q, uint32_t side) {
-    if constexpr (kWay == kByQuads) {
-      const uint32_t at = lds0 + kBuf * T::kStage + (q & 1) * T::kQuad;
-      const uint32_t c = 4 * q < steps ? q : steps / 4 - 1;
-      const uint64_t lanes = side > 1 ? 0 : ~0ull >> (64 - (side ? T::kRowsW : T::kRowsA));
-      const uint32_t to = at + 16 * (side ? T::kBM + wave * T::kRowsW : wave * T::kRowsA);
-      copy16_of(__builtin_amdgcn_readfirstlane(to), uniform((side ? ws0 : as0) + 16 * c), side ? osw : osa, uniform(lanes));
-    }
+    const uint32_t at = lds0 + kBuf * T::kStage + (q & 1) * T::kQuad;
+    const uint32_t c = 4 * q < steps ? q : (steps - 1) / 4;
+    const uint64_t lanes = side > 1 ? 0 : ~0ull >> (64 - (side ? T::kRowsW : T::kRowsA));
+    const uint32_t to = at + 16 * (side ? T::kBM + wave * T::kRowsW : wave * T::kRowsA);
+    copy16_of(__builtin_amdgcn_readfirstlane(to), uniform((side ? ws0 : as0) + 16 * c), side ? osw : osa, uniform(lanes));
   };
 
   // this lane's places in a stage
@@ -350,20 +316,12 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
     else
       return operand<FP4X2>(x, x);
   };
-  // the scale of step t (in `stage`) for 16 rows from `row` on, of A then W;
-  // the instruction reads the low byte only
-  const uint32_t srow = T::kABytes + T::kWBytes;
-  const auto scale = [&](uint32_t t, uint32_t stage, uint32_t row) -> uint32_t {
-    if constexpr (kWay == kByQuads) {
-      const uint32_t quad = kBuf * T::kStage + ((t >> 2) & 1) * T::kQuad + 4 * (t & 3);
-      return *reinterpret_cast<const uint32_t *>(lds + quad + 16 * r + 16 * row);
-    } else if constexpr (kWay == kByDwords) {
-      return *reinterpret_cast<const uint32_t *>(lds + stage + srow + (row + r) * 4);
-    } else {
-      return *reinterpret_cast<const uint32_t *>(lds + stage + srow + (row / 64) * 1024 + g * 256 + (row % 64 + r) * 4);
-    }
+  // the scales of step t for 16 rows from `row` on, of A then W: a dword of the
+  // step's four blocks, shifted to the lane group's at its use
+  const auto scale = [&](uint32_t t, uint32_t row) {
+    return *reinterpret_cast<const uint32_t *>(lds + kBuf * T::kStage + ((t >> 2) & 1) * T::kQuad + 4 * (t & 3) + 16 * r + 16 * row);
   };
-  const uint32_t shift = kWay == kByBytes ? 0 : 8 * g;  // to the lane group's block
+  const uint32_t shift = 8 * g;
   using IA = std::integral_constant<int, FA>;
   using IW = std::integral_constant<int, FW>;
 
@@ -386,11 +344,11 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   uint32_t sa[TM], sw[TN];
   const auto read_a = [&](uint32_t t, uint32_t stage, int j) {
     xa[j] = read(IA{}, stage + la0 + j * 16 * Lay<FA>::kRow, stage + la1 + j * 16 * Lay<FA>::kRow);
-    sa[j] = scale(t, stage, wm * 16 * TM + 16 * j);
+    sa[j] = scale(t, wm * 16 * TM + 16 * j);
   };
   const auto read_w = [&](uint32_t t, uint32_t stage, int i) {
     xw[i] = read(IW{}, stage + lw0 + i * 16 * Lay<FW>::kRow, stage + lw1 + i * 16 * Lay<FW>::kRow);
-    sw[i] = scale(t, stage, T::kBM + wn * 16 * TN + 16 * i);
+    sw[i] = scale(t, T::kBM + wn * 16 * TN + 16 * i);
   };
   // An empty statement that takes the sums keeps a group of products from
   // being moved past the copies and waits behind it, which they do not touch.
@@ -411,7 +369,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
 #pragma unroll
   for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
   copy_quad(1, 0);
-  wait_copies<(kBuf - 2) * T::kSpread + kMid + (kWay == kByQuads ? 1 : 0)>();
+  wait_copies<(kBuf - 2) * T::kSpread + kMid + 1>();
   barrier();
 #pragma unroll
   for (int i = 0; i < TN; i++) read_w(0, 0, i);
@@ -447,21 +405,17 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   wait_copies<0>();  // none may land after the workgroup's end
 
   if (wide && mr == T::kBM && nr == T::kBN) {
-    uint8_t *to = p.out + ((m0 + wm * 16 * TM + r) * p.out_stride + n0 + wn * 16 * TN + 16 * g) * esize(OUT);
+    uint8_t *to = p.out + ((m0 + wm * 16 * TM + r) * p.out_stride + n0 + wn * 16 * TN) * esize(OUT) + 16 * g;
 #pragma unroll
     for (int j = 0; j < TM; j++) {
 #pragma unroll
-      for (int i = 0; i < TN; i += 4) {
+      for (int i = 0; i < TN; i += OUT == BF16 ? 2 : 1) {
         if constexpr (OUT == BF16) {
-#pragma unroll
-          for (int h = 0; h < 2; h++) {
-            const f32x4 u = acc[i + 2 * h][j], v = acc[i + 2 * h + 1][j];
-            *reinterpret_cast<u32x4 *>(to + 32 * i + 16 * h) =
-                u32x4{f32_bf16x2(u[0], u[1]), f32_bf16x2(u[2], u[3]), f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
-          }
+          const f32x4 u = acc[i][j], v = acc[i + 1][j];
+          *reinterpret_cast<u32x4 *>(to + 32 * i) =
+              u32x4{f32_bf16x2(u[0], u[1]), f32_bf16x2(u[2], u[3]), f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
         } else {
-#pragma unroll
-          for (int h = 0; h < 4; h++) *reinterpret_cast<f32x4 *>(to + 64 * i + 16 * h) = acc[i + h][j];
+          *reinterpret_cast<f32x4 *>(to + 64 * i) = acc[i][j];
         }
       }
       to += 16 * p.out_stride * esize(OUT);
@@ -478,7 +432,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   for (int j = 0; j < TM; j++) {
 #pragma unroll
     for (int i = 0; i < TN; i++)
-      *reinterpret_cast<f32x4 *>(mine + r * kLine + 64 * (i / 4) + 16 * g + 4 * (i % 4)) = acc[i][j];
+      *reinterpret_cast<f32x4 *>(mine + r * kLine + (OUT == BF16 ? 32 * (i / 2) + 8 * g + 4 * (i % 2) : 16 * i + 4 * g)) = acc[i][j];
     wait_lds();
     const uint32_t ml = wm * 16 * TM + 16 * j;
     for (uint32_t x = 0; x < 16 && ml + x < mr; x++)
@@ -494,6 +448,23 @@ __global__ __launch_bounds__(64 * WM * WN) void k_mx_tiled(MxMatmulArgs p, uint3
   }
 }
 
+// Scale rows on a pitch of 16 bytes, which the tiled form's copies need: where
+// the caller's are not, both sides are laid out in the scratch first, scale 1
+// after the row's end.
+__host__ __device__ constexpr uint32_t pitch_of(uint32_t nb) { return (nb + 15) & ~15u; }
+__global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, FastDiv dwords, uint64_t count) {
+  const uint64_t base = uint64_t(blockIdx.y) << 30, i = base + uint64_t(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= count) return;
+  // rows past 2^31 dwords are reached by whole blocks of rows: 64-bit division there
+  const uint64_t row = count < 0x7FFFFFFFull ? dwords.div(uint32_t(i)) : i / dwords.d;
+  const uint32_t b = uint32_t(i - row * dwords.d) * 4;
+  const uint8_t *from = row < p.m ? p.as + row * nb : p.ws + (row - p.m) * nb;
+  uint32_t v = 0;
+#pragma unroll
+  for (uint32_t j = 0; j < 4; j++) v |= (b + j < nb ? uint32_t(from[b + j]) : 127u) << (8 * j);
+  *reinterpret_cast<uint32_t *>(p.scratch + 4 * i) = v;
+}
+
 // The pieces' sums, joined in their order: four n a lane.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces, uint64_t np, uint32_t quads, bool wide) {
@@ -507,19 +478,16 @@ __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces
 
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
 hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, kByBytes>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
   const bool wide = (uintptr_t(p.out) & 15) == 0 && (p.out_stride * esize(OUT)) % 16 == 0;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
   const uint32_t steps = (nb + 3) / 4;
-  const uintptr_t at = uintptr_t(p.as) | uintptr_t(p.ws);
   const uint64_t part = p.m * p.out_stride * esize(OUT);
   const dim3 grid(mt * nt, (steps + per - 1) / per);
-  if (nb % 16 == 0 && per % 4 == 0 && at % 16 == 0)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByQuads><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
-  else if (nb % 4 == 0 && at % 4 == 0)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByDwords><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
+  if (nb % 4 == 0)
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part, wide);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, kByBytes><<<grid, 64 * WM * WN, 0, s>>>(p, nb, mt, nt, per, part, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part, wide);
   return hipGetLastError();
 }
 
@@ -547,22 +515,36 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
   const uint64_t t = tiles(64, 64);
   uint32_t pieces = uint32_t(t >= 512 ? 1 : (512 + t - 1) / t);
   if (pieces > steps / 8) pieces = steps / 8 ? steps / 8 : 1;
-  // whole fours of steps where k has them, and no empty piece
-  uint32_t per = (steps + pieces - 1) / pieces;
-  if (nb % 16 == 0) per = (per + 3) & ~3u;
+  // whole fours of steps, whose scales are copied together, and no empty piece
+  const uint32_t per = ((steps + pieces - 1) / pieces + 3) & ~3u;
   return {kSmall, per, (steps + per - 1) / per};
 }
 
 uint64_t padded(uint64_t n) { return (n + 3) & ~uint64_t(3); }
+uint64_t part_bytes(const Plan &plan, uint64_t m, uint64_t n) {
+  return plan.pieces > 1 ? align16(plan.pieces * m * padded(n) * 4) : 0;
+}
 
 template <int FA, int FW, int OUT>
 hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
   const bool wide = (uintptr_t(p.out) & 15) == 0 && p.out_stride % 4 == 0;
   const Plan plan = plan_of(p.m, p.n, p.k);
-  if (plan.form != kFew) {
-    if (plan.pieces == 1) return tiled_form<FA, FW, OUT>(plan.form, p, nb, plan.per, s);
+  // scale rows that could be copied as they lie but for the first one's
+  // address have no room in the scratch: any m goes the way of few rows
+  const bool apart = nb % 16 == 0 && (uintptr_t(p.as) | uintptr_t(p.ws)) % 16;
+  if (plan.form != kFew && !apart) {
     MxMatmulArgs q = p;
+    if (nb % 16) {
+      const uint32_t pitch = pitch_of(nb);
+      q.scratch = p.scratch + part_bytes(plan, p.m, p.n);
+      const uint64_t count = (p.m + p.n) * (pitch / 4);
+      const uint32_t x = uint32_t((count < (1ull << 30) ? count + 255 : 1ull << 30) / 256);
+      k_mx_pitch<<<dim3(x, uint32_t(((count - 1) >> 30) + 1)), 256, 0, s>>>(q, nb, FastDiv(pitch / 4), count);
+      q.as = q.scratch;
+      q.ws = q.scratch + p.m * pitch;
+    }
+    if (plan.pieces == 1) return tiled_form<FA, FW, OUT>(plan.form, q, nb, plan.per, s);
     q.out = p.scratch;
     q.out_stride = padded(p.n);
     const hipError_t e = tiled_form<FA, FW, FP32>(plan.form, q, nb, plan.per, s);
@@ -597,7 +579,7 @@ hipError_t matmul_out(int out_dtype, const MxMatmulArgs &p, hipStream_t s) {
 
 uint64_t mx_matmul_scratch(int, int, uint64_t m, uint64_t n, uint64_t k) {
   const Plan p = plan_of(m, n, k);
-  return p.pieces > 1 ? p.pieces * m * padded(n) * 4 : 0;
+  return p.form == kFew ? 0 : part_bytes(p, m, n) + (k % 512 ? (m + n) * pitch_of(uint32_t(k / kMxBlock)) : 0);
 }
 
 hipError_t launch_mx_matmul(int a_fmt, int w_fmt, int out_dtype, const MxMatmulArgs &p, hipStream_t s) {
