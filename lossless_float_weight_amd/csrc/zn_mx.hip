@@ -6,21 +6,20 @@
 namespace zn {
 namespace {
 
-// Eight consecutive elements of a row from k0 on; zeros past k.  `fast`: the
-// row is 16-byte aligned, so a group that lies in it whole takes wide loads.
+// Eight consecutive elements of a row from k0 on; zeros past k.
 template <int DT>
-__device__ __forceinline__ void load8(const uint8_t *row, uint32_t k0, uint32_t k, bool fast, float (&v)[8]) {
-  if (fast && k0 + 8 <= k) {
+__device__ __forceinline__ void load8(const uint8_t *row, uint32_t k0, uint32_t k, float (&v)[8]) {
+  if (k0 + 8 <= k) {
     if constexpr (DT == BF16) {
-      const u32x4 w = *reinterpret_cast<const u32x4 *>(row + 2 * uint64_t(k0));
+      const u32x4 w = *reinterpret_cast<const u32x4_any *>(row + 2 * uint64_t(k0));
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         v[2 * i] = bf16_lo(w[i]);
         v[2 * i + 1] = bf16_hi(w[i]);
       }
     } else {
-      const f32x4 a = *reinterpret_cast<const f32x4 *>(row + 4 * uint64_t(k0));
-      const f32x4 b = *reinterpret_cast<const f32x4 *>(row + 4 * uint64_t(k0) + 16);
+      const f32x4 a = *reinterpret_cast<const f32x4_any *>(row + 4 * uint64_t(k0));
+      const f32x4 b = *reinterpret_cast<const f32x4_any *>(row + 4 * uint64_t(k0) + 16);
 #pragma unroll
       for (int i = 0; i < 4; i++) {
         v[i] = a[i];
@@ -44,13 +43,13 @@ __device__ __forceinline__ void load8(const uint8_t *row, uint32_t k0, uint32_t 
 // Eight consecutive elements of a row, those below k; v is already rounded
 // to DT's grid or is rounded here.
 template <int DT>
-__device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, bool fast, const float (&v)[8]) {
-  if (fast && k0 + 8 <= k) {
+__device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, const float (&v)[8]) {
+  if (k0 + 8 <= k) {
     if constexpr (DT == BF16) {
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; i++) w[i] = f32_bf16x2(v[2 * i], v[2 * i + 1]);
-      *reinterpret_cast<u32x4 *>(row + 2 * uint64_t(k0)) = w;
+      *reinterpret_cast<u32x4_any *>(row + 2 * uint64_t(k0)) = w;
     } else {
       f32x4 a, b;
 #pragma unroll
@@ -58,8 +57,8 @@ __device__ __forceinline__ void store8(uint8_t *row, uint32_t k0, uint32_t k, bo
         a[i] = v[i];
         b[i] = v[4 + i];
       }
-      *reinterpret_cast<f32x4 *>(row + 4 * uint64_t(k0)) = a;
-      *reinterpret_cast<f32x4 *>(row + 4 * uint64_t(k0) + 16) = b;
+      *reinterpret_cast<f32x4_any *>(row + 4 * uint64_t(k0)) = a;
+      *reinterpret_cast<f32x4_any *>(row + 4 * uint64_t(k0) + 16) = b;
     }
     return;
   }
@@ -102,7 +101,7 @@ __device__ __forceinline__ void put_codes(uint8_t *codes, uint8_t *scales, uint6
 // A lane takes 8 consecutive values (16 bytes of BF16), a quad one block of
 // 32; the block's maximum is exchanged inside the quad.
 template <int DT, int FMT, int U>
-__global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr, uint32_t groups, bool fast) {
+__global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr, uint32_t groups) {
   const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
   float v[U][8];
 #pragma unroll
@@ -110,7 +109,7 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr,
     const uint32_t g = first + 256u * u;
     const uint32_t gc = g < groups ? g : 0;
     const uint32_t row = gpr.div(gc), k0 = (gc - row * gpr.d) * 8;
-    load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), fast, v[u]);
+    load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), v[u]);
   }
 #pragma unroll
   for (int u = 0; u < U; u++) put_codes<FMT>(a.codes, a.scales, first + 256u * u, v[u], first + 256u * u < groups);
@@ -144,7 +143,7 @@ __device__ __forceinline__ void values8(const uint8_t *codes, uint64_t gi, float
 }
 
 template <int FMT, int DT, int U>
-__global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv gpr, uint32_t groups, bool fast) {
+__global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv gpr, uint32_t groups) {
   const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
   float v[U][8];
 #pragma unroll
@@ -158,7 +157,7 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
     const uint32_t g = first + 256u * u;
     if (g >= groups) return;
     const uint32_t row = gpr.div(g), k0 = (g - row * gpr.d) * 8;
-    store8<DT>(a.out + row * a.out_stride * esize(DT), k0, uint32_t(a.k), fast, v[u]);
+    store8<DT>(a.out + row * a.out_stride * esize(DT), k0, uint32_t(a.k), v[u]);
   }
 }
 
@@ -198,14 +197,14 @@ __device__ __forceinline__ double wave_sum(double v) {
 
 // h of one group: loaded, added, rounded, stored
 template <int DT>
-__device__ __forceinline__ void take8(const MxNormArgs &a, uint64_t row, uint32_t k0, bool fast, float (&h)[8]) {
-  load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), fast, h);
+__device__ __forceinline__ void take8(const MxNormArgs &a, uint64_t row, uint32_t k0, float (&h)[8]) {
+  load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), h);
   if (a.res) {
     float r[8];
-    load8<DT>(a.res + row * a.res_stride * esize(DT), k0, uint32_t(a.k), fast, r);
+    load8<DT>(a.res + row * a.res_stride * esize(DT), k0, uint32_t(a.k), r);
 #pragma unroll
     for (int i = 0; i < 8; i++) h[i] = rounded<DT>(h[i] + r[i]);
-    store8<DT>(a.h + row * a.h_stride * esize(DT), k0, uint32_t(a.k), fast, h);
+    store8<DT>(a.h + row * a.h_stride * esize(DT), k0, uint32_t(a.k), h);
   }
 }
 
@@ -242,14 +241,14 @@ __device__ __forceinline__ double team_sum(double s, double (*part)[16], int slo
 
 // Rows of at most TEAM * CH * 8 elements stay in registers.
 template <int DT, int FMT, int TEAM, int CH>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs a, uint32_t gpr, bool fast) {
+__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs a, uint32_t gpr) {
   constexpr int kTeams = TEAM < 256 ? 256 / TEAM : 1;
   __shared__ double part[2][16];
   const uint32_t t = threadIdx.x % TEAM;
   float w[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; c++)
-    load8<DT>(a.w, (c * TEAM + t) * 8, uint32_t(a.k), (uintptr_t(a.w) & 15) == 0, w[c]);
+    load8<DT>(a.w, (c * TEAM + t) * 8, uint32_t(a.k), w[c]);
   int slot = 0;
   const uint64_t step = uint64_t(gridDim.x) * kTeams;
   for (uint64_t row = uint64_t(blockIdx.x) * kTeams + threadIdx.x / TEAM; row < a.rows; row += step, slot ^= 1) {
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs 
     double s = 0;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      take8<DT>(a, row, (c * TEAM + t) * 8, fast, h[c]);
+      take8<DT>(a, row, (c * TEAM + t) * 8, h[c]);
       s += squares8(h[c]);
     }
     const RowScale r = row_scale(team_sum<TEAM>(s, part, slot), uint32_t(a.k), a.eps);
@@ -271,14 +270,14 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs 
 
 // Longer rows are read twice, the second time as they were stored.
 template <int DT, int FMT>
-__global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gpr, bool fast) {
+__global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gpr) {
   __shared__ double part[2][16];
   int slot = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
     double s = 0;
     for (uint32_t g = threadIdx.x; g < gpr; g += 1024) {
       float h[8];
-      take8<DT>(a, row, g * 8, fast, h);
+      take8<DT>(a, row, g * 8, h);
       s += squares8(h);
     }
     const RowScale r = row_scale(team_sum<1024>(s, part, slot), uint32_t(a.k), a.eps);
@@ -286,15 +285,11 @@ __global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gp
     // gpr is a multiple of 4: the lanes of a quad stay together
     for (uint32_t g = threadIdx.x; g < gpr; g += 1024) {
       float h[8], w[8];
-      load8<DT>(src, g * 8, uint32_t(a.k), fast, h);
-      load8<DT>(a.w, g * 8, uint32_t(a.k), (uintptr_t(a.w) & 15) == 0, w);
+      load8<DT>(src, g * 8, uint32_t(a.k), h);
+      load8<DT>(a.w, g * 8, uint32_t(a.k), w);
       norm8<FMT>(a, row * gpr + g, r, h, w, true);
     }
   }
-}
-
-bool aligned_rows(const void *p, uint64_t stride, int dt) {
-  return (uintptr_t(p) & 15) == 0 && (stride * esize(dt)) % 16 == 0;
 }
 
 // Calls f(first row, rows) for pieces whose groups of 8 stay below 2^31.
@@ -320,7 +315,7 @@ hipError_t quantize(const MxQuantArgs &a, hipStream_t s) {
     p.rows = rows;
     const uint32_t groups = uint32_t(rows * gpr);
     k_mx_quantize<DT, FMT, U><<<(groups + 256 * U - 1) / (256 * U), 256, 0, s>>>(
-        p, FastDiv(gpr), groups, aligned_rows(a.x, a.x_stride, DT));
+        p, FastDiv(gpr), groups);
     return hipGetLastError();
   });
 }
@@ -337,7 +332,7 @@ hipError_t dequantize(const MxDequantArgs &a, hipStream_t s) {
     p.rows = rows;
     const uint32_t groups = uint32_t(rows * gpr);
     k_mx_dequantize<FMT, DT, U><<<(groups + 256 * U - 1) / (256 * U), 256, 0, s>>>(
-        p, FastDiv(gpr), groups, aligned_rows(a.out, a.out_stride, DT));
+        p, FastDiv(gpr), groups);
     return hipGetLastError();
   });
 }
@@ -345,26 +340,24 @@ hipError_t dequantize(const MxDequantArgs &a, hipStream_t s) {
 template <int DT, int FMT>
 hipError_t norm(const MxNormArgs &a, hipStream_t s) {
   const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
-  const bool fast = aligned_rows(a.x, a.x_stride, DT) &&
-                    (!a.res || (aligned_rows(a.res, a.res_stride, DT) && aligned_rows(a.h, a.h_stride, DT)));
   const auto grid = [&](uint32_t teams, uint32_t most) {
     const uint64_t b = (a.rows + teams - 1) / teams;
     return uint32_t(b < most ? b : most);
   };
   if (gpr <= 64)
-    k_mx_norm<DT, FMT, 64, 1><<<grid(4, 4096), 256, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 64, 1><<<grid(4, 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 128)
-    k_mx_norm<DT, FMT, 64, 2><<<grid(4, 4096), 256, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 64, 2><<<grid(4, 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 256)
-    k_mx_norm<DT, FMT, 256, 1><<<grid(1, 4096), 256, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 256, 1><<<grid(1, 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 512)
-    k_mx_norm<DT, FMT, 256, 2><<<grid(1, 4096), 256, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 256, 2><<<grid(1, 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 1024)
-    k_mx_norm<DT, FMT, 256, 4><<<grid(1, 2048), 256, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 256, 4><<<grid(1, 2048), 256, 0, s>>>(a, gpr);
   else if (gpr <= 2048)
-    k_mx_norm<DT, FMT, 1024, 2><<<grid(1, 1024), 1024, 0, s>>>(a, gpr, fast);
+    k_mx_norm<DT, FMT, 1024, 2><<<grid(1, 1024), 1024, 0, s>>>(a, gpr);
   else
-    k_mx_norm_long<DT, FMT><<<grid(1, 512), 1024, 0, s>>>(a, gpr, fast);
+    k_mx_norm_long<DT, FMT><<<grid(1, 512), 1024, 0, s>>>(a, gpr);
   return hipGetLastError();
 }
 

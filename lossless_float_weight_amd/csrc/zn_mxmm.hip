@@ -57,15 +57,15 @@ __device__ __forceinline__ uint32_t load_scale(const uint8_t *row, uint32_t t, u
 
 // Four consecutive n of row m.
 template <int OUT>
-__device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64_t n, f32x4 c, bool wide) {
+__device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64_t n, f32x4 c) {
   if (m >= p.m) return;
   uint8_t *row = p.out + m * p.out_stride * esize(OUT);
-  if (wide && n + 4 <= p.n) {
+  if (n + 4 <= p.n) {
     if constexpr (OUT == BF16) {
       const u32x2 v = {f32_bf16x2(c[0], c[1]), f32_bf16x2(c[2], c[3])};
-      *reinterpret_cast<u32x2 *>(row + 2 * n) = v;
+      *reinterpret_cast<u32x2_any *>(row + 2 * n) = v;
     } else {
-      *reinterpret_cast<f32x4 *>(row + 4 * n) = c;
+      *reinterpret_cast<f32x4_any *>(row + 4 * n) = c;
     }
     return;
   }
@@ -82,7 +82,7 @@ __device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64
 // Few rows: a workgroup of KS waves makes 16 n by 16 MT m, each wave a piece
 // of k straight from memory, joined in LDS in the order of the waves.
 template <int FA, int FW, int OUT, int MT, int KS>
-__global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb, bool wide) {
+__global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb) {
   __shared__ f32x4 part[KS > 1 ? KS : 1][MT][64];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const uint64_t n0 = uint64_t(blockIdx.x) * 16, m0 = uint64_t(blockIdx.y) * (16 * MT);
@@ -122,7 +122,7 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb,
     } else {
       s = c[i];
     }
-    store4<OUT>(p, m0 + 16 * i + r, n0 + 4 * g, s, wide);
+    store4<OUT>(p, m0 + 16 * i + r, n0 + 4 * g, s);
   }
 }
 
@@ -194,19 +194,23 @@ struct Tiled {
   static constexpr int kWaves = WM * WN, kBM = 16 * TM * WM, kBN = 16 * TN * WN;
   static constexpr uint32_t kABytes = kBM * Lay<FA>::kRow, kWBytes = kBN * Lay<FW>::kRow;
   static constexpr uint32_t kStage = kABytes + kWBytes;
-  // the scales of four steps, 16 bytes a row; two of them, beside the stages
+  // the scales of four steps, 16 bytes a row, beside the stages: two of them,
+  // or four where more than three steps are copied ahead
   static constexpr uint32_t kQuad = (kBM + kBN) * 16;
+  static constexpr uint32_t kRoom = 160 * 1024;
   // workgroups that a CU should hold at a time: two where the sums leave room
-  static constexpr int kGroups = TM * TN * 4 <= 128 && 2 * (2 * kStage + 2 * kQuad) <= 160 * 1024 ? 2 : 1;
-  static constexpr int kBuf = kGroups * (3 * kStage + 2 * kQuad) <= 160 * 1024 ? 3 : 2;
-  static constexpr uint32_t kLds = kBuf * kStage + 2 * kQuad;
+  static constexpr int kGroups = TM * TN * 4 <= 128 && 2 * (2 * kStage + 2 * kQuad) <= kRoom ? 2 : 1;
+  static constexpr int kFit = (kRoom / kGroups - 4 * kQuad) / kStage;
+  static constexpr int kBuf = kFit > 6 ? 6 : kFit > 3 ? kFit : kGroups * (3 * kStage + 2 * kQuad) <= kRoom ? 3 : 2;
+  static constexpr int kQuads = kBuf > 3 ? 4 : 2;
+  static constexpr uint32_t kLds = kBuf * kStage + kQuads * kQuad;
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
   // copies of a wave in a step: operands, and one of scales
   static constexpr int kSpread = kAC + kWC, kPerStep = kSpread + 1, kMid = kSpread / 2;
   static constexpr uint32_t kRowsA = kBM / kWaves, kRowsW = kBN / kWaves;
   static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 2 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
   static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
-  static_assert(kLds <= 160 * 1024 && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
+  static_assert(kLds <= kRoom && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
 };
 
 // Weight row (from the tile's first) of LDS row r.  For BF16, rows 4 g + q of
@@ -220,7 +224,7 @@ __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
 
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kWhole>
 __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::kGroups)) void k_mx_tiled(
-    MxMatmulArgs p, uint32_t nb, uint32_t pitch, uint32_t mt, uint32_t nt, uint32_t per, uint64_t part, bool wide) {
+    MxMatmulArgs p, uint32_t nb, uint32_t pitch, uint32_t mt, uint32_t nt, uint32_t per, uint64_t part) {
   using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
   constexpr int kBuf = T::kBuf;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // at a time: `side` 0 the activations', 1 the weights', else none (the copy
   // is issued for no lane, so that every step counts the same).
   const auto copy_quad = [&](uint32_t q, uint32_t side) {
-    const uint32_t at = lds0 + kBuf * T::kStage + (q & 1) * T::kQuad;
+    const uint32_t at = lds0 + kBuf * T::kStage + (q % T::kQuads) * T::kQuad;
     const uint32_t c = 4 * q < steps ? q : (steps - 1) / 4;
     const uint64_t lanes = side > 1 ? 0 : ~0ull >> (64 - (side ? T::kRowsW : T::kRowsA));
     const uint32_t to = at + 16 * (side ? T::kBM + wave * T::kRowsW : wave * T::kRowsA);
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // the scales of step t for 16 rows from `row` on, of A then W: a dword of the
   // step's four blocks, shifted to the lane group's at its use
   const auto scale = [&](uint32_t t, uint32_t row) {
-    return *reinterpret_cast<const uint32_t *>(lds + kBuf * T::kStage + ((t >> 2) & 1) * T::kQuad + 4 * (t & 3) + 16 * r + 16 * row);
+    return *reinterpret_cast<const uint32_t *>(lds + kBuf * T::kStage + ((t >> 2) % T::kQuads) * T::kQuad + 4 * (t & 3) + 16 * r + 16 * row);
   };
   const uint32_t shift = 8 * g;
   using IA = std::integral_constant<int, FA>;
@@ -360,15 +364,20 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // The copies of a step are spread over the products, for the address unit
   // takes 16 cycles for each and would hold the wave up: half of those of step
   // t + kBuf go out in the upper half of step t, half in the next lower half.
-  // Scales by quads: those of quad q + 1 go out in the upper halves of steps
-  // 4 q - 1 and 4 q, when quad q - 1, which lay there, has been read, and are
-  // first read in the upper half of step 4 q + 3, two waits later.
+  // The scales of quad q + kQuads - 1 go out in the upper halves of steps 4 q - 1
+  // and 4 q, when quad q - 1, which lay there, has been read.  With two quads
+  // they are first read in the upper half of step 4 q + 3 and have landed two
+  // waits after step 4 q; with four, eight steps later, a wait leaves the last
+  // four steps' copies out.
   constexpr int kMid = T::kMid, kRest = T::kSpread - kMid;
-  copy_quad(0, 0);
-  copy_quad(0, 1);
+#pragma unroll
+  for (int q = 0; q < T::kQuads - 1; q++) {
+    copy_quad(q, 0);
+    copy_quad(q, 1);
+  }
 #pragma unroll
   for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
-  copy_quad(1, 0);
+  copy_quad(T::kQuads - 1, 0);
   wait_copies<(kBuf - 2) * T::kSpread + kMid + 1>();
   barrier();
 #pragma unroll
@@ -396,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
       read_w(t + 1, next, i);
       if (i < kHalf) read_a(t + 1, next, i);
       copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
-      if (i == TN - 1) copy_quad((t + 1) / 4 + 1, (t + 1) & 3);
+      if (i == TN - 1) copy_quad((t + 1) / 4 + T::kQuads - 1, (t + 1) & 3);
       keep(i, kHalf);
     }
     before = here;
@@ -404,7 +413,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   }
   wait_copies<0>();  // none may land after the workgroup's end
 
-  if (wide && mr == T::kBM && nr == T::kBN) {
+  if (mr == T::kBM && nr == T::kBN) {
     uint8_t *to = p.out + ((m0 + wm * 16 * TM + r) * p.out_stride + n0 + wn * 16 * TN) * esize(OUT) + 16 * g;
 #pragma unroll
     for (int j = 0; j < TM; j++) {
@@ -412,17 +421,17 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
       for (int i = 0; i < TN; i += OUT == BF16 ? 2 : 1) {
         if constexpr (OUT == BF16) {
           const f32x4 u = acc[i][j], v = acc[i + 1][j];
-          *reinterpret_cast<u32x4 *>(to + 32 * i) =
+          *reinterpret_cast<u32x4_any *>(to + 32 * i) =
               u32x4{f32_bf16x2(u[0], u[1]), f32_bf16x2(u[2], u[3]), f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
         } else {
-          *reinterpret_cast<f32x4 *>(to + 64 * i) = acc[i][j];
+          *reinterpret_cast<f32x4_any *>(to + 64 * i) = acc[i][j];
         }
       }
       to += 16 * p.out_stride * esize(OUT);
     }
     return;
   }
-  // tiles at the edges and rows without the alignment: 16 m of a wave at a
+  // tiles at the edges: 16 m of a wave at a
   // time through LDS of its own, then one n a lane
   barrier();
   constexpr uint32_t kLine = 16 * TN + 4;  // floats: rows of a column fall in different banks
@@ -435,8 +444,9 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
       *reinterpret_cast<f32x4 *>(mine + r * kLine + (OUT == BF16 ? 32 * (i / 2) + 8 * g + 4 * (i % 2) : 16 * i + 4 * g)) = acc[i][j];
     wait_lds();
     const uint32_t ml = wm * 16 * TM + 16 * j;
-    for (uint32_t x = 0; x < 16 && ml + x < mr; x++)
-      for (uint32_t y = lane; y < 16 * TN && wn * 16 * TN + y < nr; y += 64) {
+    for (uint32_t xy = lane; xy < 16 * 16 * TN; xy += 64) {
+      const uint32_t x = xy / (16 * TN), y = xy % (16 * TN);
+      if (ml + x < mr && wn * 16 * TN + y < nr) {
         const float v = mine[x * kLine + y];
         uint8_t *to = p.out + ((m0 + ml + x) * p.out_stride + n0 + wn * 16 * TN + y) * esize(OUT);
         if constexpr (OUT == BF16)
@@ -444,6 +454,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
         else
           *reinterpret_cast<float *>(to) = v;
       }
+    }
     wait_lds();
   }
 }
@@ -467,27 +478,26 @@ __global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, F
 
 // The pieces' sums, joined in their order: four n a lane.
 template <int OUT>
-__global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces, uint64_t np, uint32_t quads, bool wide) {
+__global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces, uint64_t np, uint32_t quads) {
   const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x, m = i / quads, n = 4 * (i % quads);
   if (m >= p.m) return;
   const float *from = reinterpret_cast<const float *>(p.scratch) + m * np + n;
   f32x4 s = *reinterpret_cast<const f32x4 *>(from);
   for (uint32_t j = 1; j < pieces; j++) s += *reinterpret_cast<const f32x4 *>(from + j * p.m * np);
-  store4<OUT>(p, m, n, s, wide);
+  store4<OUT>(p, m, n, s);
 }
 
 template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
 hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
   using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
-  const bool wide = (uintptr_t(p.out) & 15) == 0 && (p.out_stride * esize(OUT)) % 16 == 0;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
   const uint32_t steps = (nb + 3) / 4;
   const uint64_t part = p.m * p.out_stride * esize(OUT);
   const dim3 grid(mt * nt, (steps + per - 1) / per);
   if (nb % 4 == 0)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part, wide);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   return hipGetLastError();
 }
 
@@ -528,7 +538,6 @@ uint64_t part_bytes(const Plan &plan, uint64_t m, uint64_t n) {
 template <int FA, int FW, int OUT>
 hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
-  const bool wide = (uintptr_t(p.out) & 15) == 0 && p.out_stride % 4 == 0;
   const Plan plan = plan_of(p.m, p.n, p.k);
   // scale rows that could be copied as they lie but for the first one's
   // address have no room in the scratch: any m goes the way of few rows
@@ -550,12 +559,12 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
     const hipError_t e = tiled_form<FA, FW, FP32>(plan.form, q, nb, plan.per, s);
     if (e != hipSuccess) return e;
     const uint32_t quads = uint32_t(q.out_stride / 4);
-    k_mx_join<OUT><<<uint32_t((p.m * quads + 255) / 256), 256, 0, s>>>(p, plan.pieces, q.out_stride, quads, wide);
+    k_mx_join<OUT><<<uint32_t((p.m * quads + 255) / 256), 256, 0, s>>>(p, plan.pieces, q.out_stride, quads);
     return hipGetLastError();
   }
   const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 15) / 16;
   if (mt == 1)
-    k_mx_few<FA, FW, OUT, 1, 8><<<dim3(uint32_t(nt), 1), 512, 0, s>>>(p, nb, wide);
+    k_mx_few<FA, FW, OUT, 1, 8><<<dim3(uint32_t(nt), 1), 512, 0, s>>>(p, nb);
   else
     for (uint64_t y = 0; y < (mt + 3) / 4; y += 65535) {
       MxMatmulArgs q = p;
@@ -565,7 +574,7 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
       q.out += rows * p.out_stride * esize(OUT);
       q.m -= rows;
       const uint64_t left = (mt + 3) / 4 - y;
-      k_mx_few<FA, FW, OUT, 4, 4><<<dim3(uint32_t(nt), uint32_t(left < 65535 ? left : 65535)), 256, 0, s>>>(q, nb, wide);
+      k_mx_few<FA, FW, OUT, 4, 4><<<dim3(uint32_t(nt), uint32_t(left < 65535 ? left : 65535)), 256, 0, s>>>(q, nb);
     }
   return hipGetLastError();
 }
