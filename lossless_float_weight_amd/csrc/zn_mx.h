@@ -32,6 +32,7 @@ struct MxNormArgs {
   uint8_t *h;                   // the stored sum (NULL without res)
   uint64_t rows, k, x_stride, res_stride, h_stride;
   float eps;
+  double over_k;                // 1 / k
   uint8_t *codes, *scales;
 };
 struct MxMatmulArgs {

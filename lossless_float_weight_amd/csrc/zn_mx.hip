@@ -171,8 +171,8 @@ struct RowScale {
   int e;
   float m;
 };
-__device__ __forceinline__ RowScale row_scale(double sum, uint32_t k, float eps) {
-  const double a = sum / double(k) + double(eps);
+__device__ __forceinline__ RowScale row_scale(double sum, double over_k, float eps) {
+  const double a = sum * over_k + double(eps);
   double r = __builtin_amdgcn_rsq(a);
   // one Newton step takes the instruction's 2^-26 to 64-bit rounding
   const double t = __builtin_fma(-a * r, r, 1.0);
@@ -224,45 +224,41 @@ __device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, RowScale
   put_codes<FMT>(a.codes, a.scales, gi, y, live);
 }
 
-// The sum over a team of TEAM lanes; `slot` alternates between rows so that
-// one barrier a row is enough.
-template <int TEAM>
-__device__ __forceinline__ double team_sum(double s, double (*part)[16], int slot) {
+// The sum over a workgroup; `slot` alternates between rows so that one barrier
+// a row is enough.
+__device__ __forceinline__ double group_sum(double s, double (*part)[16], int slot) {
   s = wave_sum(s);
-  if constexpr (TEAM > 64) {
-    if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = s;
-    __syncthreads();
-    s = 0;
-#pragma unroll
-    for (int i = 0; i < TEAM / 64; i++) s += part[slot][i];
-  }
+  if (blockDim.x == 64) return s;
+  if ((threadIdx.x & 63) == 0) part[slot][threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = 0;
+  for (uint32_t i = 0; i < blockDim.x / 64; i++) s += part[slot][i];
   return s;
 }
 
-// Rows of at most TEAM * CH * 8 elements stay in registers.
-template <int DT, int FMT, int TEAM, int CH>
-__global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void k_mx_norm(MxNormArgs a, uint32_t gpr) {
-  constexpr int kTeams = TEAM < 256 ? 256 / TEAM : 1;
+// Rows of at most CH groups of 8 a lane stay in registers; a workgroup has as
+// many waves as its row needs.  kFour: rows of one wave, four to a workgroup.
+template <int DT, int FMT, int CH, bool kFour>
+__global__ __launch_bounds__(kFour ? 256 : 1024) void k_mx_norm(MxNormArgs a, uint32_t gpr) {
   __shared__ double part[2][16];
-  const uint32_t t = threadIdx.x % TEAM;
+  const uint32_t t = kFour ? threadIdx.x & 63 : threadIdx.x, team = kFour ? 64 : blockDim.x;
   float w[CH][8];
 #pragma unroll
-  for (int c = 0; c < CH; c++)
-    load8<DT>(a.w, (c * TEAM + t) * 8, uint32_t(a.k), w[c]);
+  for (int c = 0; c < CH; c++) load8<DT>(a.w, (c * team + t) * 8, uint32_t(a.k), w[c]);
   int slot = 0;
-  const uint64_t step = uint64_t(gridDim.x) * kTeams;
-  for (uint64_t row = uint64_t(blockIdx.x) * kTeams + threadIdx.x / TEAM; row < a.rows; row += step, slot ^= 1) {
+  const uint64_t step = uint64_t(gridDim.x) * (kFour ? 4 : 1);
+  for (uint64_t row = uint64_t(blockIdx.x) * (kFour ? 4 : 1) + (kFour ? threadIdx.x >> 6 : 0); row < a.rows; row += step, slot ^= 1) {
     float h[CH][8];
     double s = 0;
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      take8<DT>(a, row, (c * TEAM + t) * 8, h[c]);
+      take8<DT>(a, row, (c * team + t) * 8, h[c]);
       s += squares8(h[c]);
     }
-    const RowScale r = row_scale(team_sum<TEAM>(s, part, slot), uint32_t(a.k), a.eps);
+    const RowScale r = row_scale(kFour ? wave_sum(s) : group_sum(s, part, slot), a.over_k, a.eps);
 #pragma unroll
     for (int c = 0; c < CH; c++) {
-      const uint32_t g = c * TEAM + t;
+      const uint32_t g = c * team + t;
       norm8<FMT>(a, row * gpr + g, r, h[c], w[c], g < gpr);
     }
   }
@@ -280,7 +276,7 @@ __global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gp
       take8<DT>(a, row, g * 8, h);
       s += squares8(h);
     }
-    const RowScale r = row_scale(team_sum<1024>(s, part, slot), uint32_t(a.k), a.eps);
+    const RowScale r = row_scale(group_sum(s, part, slot), a.over_k, a.eps);
     const uint8_t *src = a.res ? a.h + row * a.h_stride * esize(DT) : a.x + row * a.x_stride * esize(DT);
     // gpr is a multiple of 4: the lanes of a quad stay together
     for (uint32_t g = threadIdx.x; g < gpr; g += 1024) {
@@ -340,24 +336,19 @@ hipError_t dequantize(const MxDequantArgs &a, hipStream_t s) {
 template <int DT, int FMT>
 hipError_t norm(const MxNormArgs &a, hipStream_t s) {
   const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
-  const auto grid = [&](uint32_t teams, uint32_t most) {
-    const uint64_t b = (a.rows + teams - 1) / teams;
-    return uint32_t(b < most ? b : most);
-  };
+  const uint32_t grid = uint32_t(a.rows < 4096 ? a.rows : 4096);
+  // One group of 8 a lane wherever 1024 lanes are enough: against two a lane it
+  // took, at 8192 x 4096 BF16 with the addition, 36.1 us for 37.7 (2.8 for 3.5
+  // on a single row), and at 4096 x 8192 38.9 for 42.2.  Waves as needed and no
+  // power of two of them: 613 x 5003 FP32 6.6 us for 7.2.
   if (gpr <= 64)
-    k_mx_norm<DT, FMT, 64, 1><<<grid(4, 4096), 256, 0, s>>>(a, gpr);
-  else if (gpr <= 128)
-    k_mx_norm<DT, FMT, 64, 2><<<grid(4, 4096), 256, 0, s>>>(a, gpr);
-  else if (gpr <= 256)
-    k_mx_norm<DT, FMT, 256, 1><<<grid(1, 4096), 256, 0, s>>>(a, gpr);
-  else if (gpr <= 512)
-    k_mx_norm<DT, FMT, 256, 2><<<grid(1, 4096), 256, 0, s>>>(a, gpr);
+    k_mx_norm<DT, FMT, 1, true><<<uint32_t((a.rows + 3) / 4 < 4096 ? (a.rows + 3) / 4 : 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 1024)
-    k_mx_norm<DT, FMT, 256, 4><<<grid(1, 2048), 256, 0, s>>>(a, gpr);
+    k_mx_norm<DT, FMT, 1, false><<<grid, (gpr + 63) / 64 * 64, 0, s>>>(a, gpr);
   else if (gpr <= 2048)
-    k_mx_norm<DT, FMT, 1024, 2><<<grid(1, 1024), 1024, 0, s>>>(a, gpr);
+    k_mx_norm<DT, FMT, 2, false><<<grid, (gpr + 127) / 128 * 64, 0, s>>>(a, gpr);
   else
-    k_mx_norm_long<DT, FMT><<<grid(1, 512), 1024, 0, s>>>(a, gpr);
+    k_mx_norm_long<DT, FMT><<<grid, 1024, 0, s>>>(a, gpr);
   return hipGetLastError();
 }
 

@@ -78,6 +78,7 @@ extern "C" zn_status zn_mx_rms_norm(zn_dtype dtype, const void *d_x, uint64_t x_
   a.res_stride = residual_stride;
   a.h_stride = residual_out_stride;
   a.eps = eps;
+  a.over_k = 1.0 / double(k);
   a.codes = static_cast<uint8_t *>(d_codes);
   a.scales = static_cast<uint8_t *>(d_scales);
   return done(launch_mx_norm(dtype, fmt, a, stream));

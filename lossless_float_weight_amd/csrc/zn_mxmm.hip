@@ -18,7 +18,7 @@ namespace zn {
 namespace {
 
 template <int F>
-__device__ __forceinline__ constexpr int code_bytes() { return F == FP8 ? 32 : 16; }  // of one block
+__host__ __device__ __forceinline__ constexpr int code_bytes() { return F == FP8 ? 32 : 16; }  // of one block
 template <int F>
 constexpr int kFmtBits = F == FP8 ? 0 : 4;  // the instruction's format field
 
@@ -51,6 +51,12 @@ __device__ __forceinline__ i32x8 load_codes(const uint8_t *row, uint32_t t, uint
   }
   return operand<F>(lo, hi);
 }
+// of a step whose four blocks are all there
+template <int F>
+__device__ __forceinline__ i32x8 load_whole(const uint8_t *row, uint32_t t, uint32_t g) {
+  const u32x4 *p = reinterpret_cast<const u32x4 *>(row + uint64_t(t) * (4 * code_bytes<F>()) + 16 * g);
+  return operand<F>(p[0], p[F == FP8 ? 4 : 0]);
+}
 __device__ __forceinline__ uint32_t load_scale(const uint8_t *row, uint32_t t, uint32_t g, uint32_t nb) {
   return 4 * t + g < nb ? row[4 * t + g] : 127u;
 }
@@ -79,14 +85,17 @@ __device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64
     }
 }
 
-// Few rows: a workgroup of KS waves makes 16 n by 16 MT m, each wave a piece
-// of k straight from memory, joined in LDS in the order of the waves.
+// Few rows: a workgroup of KS waves makes 16 n by 16 MT m, each wave a piece of
+// k straight from memory to registers, joined in LDS in the order of the waves.
+// What bounds it is the weights' way from memory, so a wave asks for four
+// steps at a time: 256 bytes of each of 16 weight rows (E2M1), and their 16
+// scale bytes in one load, before it multiplies.
 template <int FA, int FW, int OUT, int MT, int KS>
 __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb) {
   __shared__ f32x4 part[KS > 1 ? KS : 1][MT][64];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
   const uint64_t n0 = uint64_t(blockIdx.x) * 16, m0 = uint64_t(blockIdx.y) * (16 * MT);
-  const uint32_t steps = (nb + 3) / 4, per = (steps + KS - 1) / KS;
+  const uint32_t steps = (nb + 3) / 4, fours = (steps + 3) / 4, per = 4 * ((fours + KS - 1) / KS);
   const uint32_t t0 = wave * per, t1 = t0 + per < steps ? t0 + per : steps;
   // rows past the end are read as the last row and never stored
   const uint64_t n = n0 + r < p.n ? n0 + r : p.n - 1;
@@ -101,7 +110,25 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb)
   f32x4 c[MT];
 #pragma unroll
   for (int i = 0; i < MT; i++) c[i] = f32x4{0, 0, 0, 0};
-  for (uint32_t t = t0; t < t1; t++) {
+  uint32_t t = t0;
+  for (; t + 4 <= t1 && 4 * t + 16 <= nb; t += 4) {
+    i32x8 x[4], y[MT][4];
+    const u32x4 sx = *reinterpret_cast<const u32x4_any *>(ws + 4 * t);
+    u32x4 sy[MT];
+#pragma unroll
+    for (int s = 0; s < 4; s++) x[s] = load_whole<FW>(w, t + s, g);
+#pragma unroll
+    for (int i = 0; i < MT; i++) {
+      sy[i] = *reinterpret_cast<const u32x4_any *>(as[i] + 4 * t);
+#pragma unroll
+      for (int s = 0; s < 4; s++) y[i][s] = load_whole<FA>(a[i], t + s, g);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; s++)
+#pragma unroll
+      for (int i = 0; i < MT; i++) c[i] = mfma<FW, FA>(x[s], y[i][s], c[i], sx[s] >> (8 * g), sy[i][s] >> (8 * g));
+  }
+  for (; t < t1; t++) {
     const i32x8 x = load_codes<FW>(w, t, g, nb);
     const uint32_t sx = load_scale(ws, t, g, nb);
 #pragma unroll
@@ -113,7 +140,9 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb)
     for (int i = 0; i < MT; i++) part[wave][i][lane] = c[i];
     __syncthreads();
   }
-  for (int i = wave; i < MT; i += KS) {
+#pragma unroll
+  for (int i = 0; i < MT; i++) {
+    if (KS > 1 && uint32_t(i % KS) != wave) continue;
     f32x4 s;
     if constexpr (KS > 1) {
       s = part[0][i][lane];
@@ -375,10 +404,15 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
     copy_quad(q, 0);
     copy_quad(q, 1);
   }
+  // counted as in the loop, a copy of scales to a step: the waits go by counts
+  constexpr int kFill = kBuf > 3 ? kBuf - 3 : 0;
 #pragma unroll
-  for (int t = 0; t < kBuf; t++) copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
+  for (int t = 0; t < kBuf; t++) {
+    if (t >= 2 && t < kBuf - 1) copy_quad(0, 2);
+    copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
+  }
   copy_quad(T::kQuads - 1, 0);
-  wait_copies<(kBuf - 2) * T::kSpread + kMid + 1>();
+  wait_copies<(kBuf - 2) * T::kSpread + kFill + kMid + 1>();
   barrier();
 #pragma unroll
   for (int i = 0; i < TN; i++) read_w(0, 0, i);
@@ -509,7 +543,7 @@ struct Plan {
 
 template <int FA, int FW, int OUT>
 hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  if (f == kSmall) return tiled<FA, FW, OUT, 2, 4, 2, 1>(p, nb, per, s);
+  if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2>(p, nb, per, s);
   if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2>(p, nb, per, s);
   return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, per, s);
 }
@@ -533,6 +567,29 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
 uint64_t padded(uint64_t n) { return (n + 3) & ~uint64_t(3); }
 uint64_t part_bytes(const Plan &plan, uint64_t m, uint64_t n) {
   return plan.pieces > 1 ? align16(plan.pieces * m * padded(n) * 4) : 0;
+}
+
+template <int FA, int FW, int OUT, int MT, int KS>
+hipError_t few_form(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
+  const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 16 * MT - 1) / (16 * MT);
+  for (uint64_t y = 0; y < mt; y += 65535) {  // the grid's limit
+    MxMatmulArgs q = p;
+    const uint64_t rows = y * 16 * MT;
+    q.a += rows * nb * code_bytes<FA>();
+    q.as += rows * nb;
+    q.out += rows * p.out_stride * esize(OUT);
+    q.m -= rows;
+    k_mx_few<FA, FW, OUT, MT, KS><<<dim3(uint32_t(nt), uint32_t(mt - y < 65535 ? mt - y : 65535)), 64 * KS, 0, s>>>(q, nb);
+  }
+  return hipGetLastError();
+}
+template <int FA, int FW, int OUT>
+hipError_t few(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
+  const uint32_t mt = p.m <= 16 ? 1 : p.m <= 32 ? 2 : p.m <= 48 ? 3 : 4;
+  if (mt == 1) return few_form<FA, FW, OUT, 1, 8>(p, nb, s);
+  if (mt == 2) return few_form<FA, FW, OUT, 2, 8>(p, nb, s);
+  if (mt == 3) return few_form<FA, FW, OUT, 3, 8>(p, nb, s);
+  return few_form<FA, FW, OUT, 4, 8>(p, nb, s);
 }
 
 template <int FA, int FW, int OUT>
@@ -562,21 +619,7 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
     k_mx_join<OUT><<<uint32_t((p.m * quads + 255) / 256), 256, 0, s>>>(p, plan.pieces, q.out_stride, quads);
     return hipGetLastError();
   }
-  const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 15) / 16;
-  if (mt == 1)
-    k_mx_few<FA, FW, OUT, 1, 8><<<dim3(uint32_t(nt), 1), 512, 0, s>>>(p, nb);
-  else
-    for (uint64_t y = 0; y < (mt + 3) / 4; y += 65535) {
-      MxMatmulArgs q = p;
-      const uint64_t rows = y * 64;
-      q.a += rows * nb * (FA == FP8 ? 32 : 16);
-      q.as += rows * nb;
-      q.out += rows * p.out_stride * esize(OUT);
-      q.m -= rows;
-      const uint64_t left = (mt + 3) / 4 - y;
-      k_mx_few<FA, FW, OUT, 4, 4><<<dim3(uint32_t(nt), uint32_t(left < 65535 ? left : 65535)), 256, 0, s>>>(q, nb);
-    }
-  return hipGetLastError();
+  return few<FA, FW, OUT>(p, nb, s);
 }
 
 template <int FA, int FW>
