@@ -211,17 +211,20 @@ __device__ __forceinline__ void barrier() {
 
 __device__ const uint8_t kZeros[16] = {};
 
-// Bytes of a row in one step, its 16-byte pieces, and where piece p of row r lies.
-template <int F>
+// Bytes of a row in one step of S times 128 k, its 16-byte pieces, and where
+// piece p of row r lies.
+template <int F, int S>
 struct Lay {
-  static constexpr uint32_t kRow = F == FP8 ? 128 : 64, kPieces = kRow / 16;
-  __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return F == FP8 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
+  static constexpr uint32_t kRow = (F == FP8 ? 128 : 64) * S, kPieces = kRow / 16, kPerBlock = F == FP8 ? 2 : 1;
+  __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return kRow >= 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
 };
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S>
 struct Tiled {
+  using LA = Lay<FA, S>;
+  using LW = Lay<FW, S>;
   static constexpr int kWaves = WM * WN, kBM = 16 * TM * WM, kBN = 16 * TN * WN;
-  static constexpr uint32_t kABytes = kBM * Lay<FA>::kRow, kWBytes = kBN * Lay<FW>::kRow;
+  static constexpr uint32_t kABytes = kBM * LA::kRow, kWBytes = kBN * LW::kRow;
   static constexpr uint32_t kStage = kABytes + kWBytes;
   // the scales of four steps, 16 bytes a row, beside the stages: two of them,
   // or four where more than three steps are copied ahead
@@ -230,14 +233,15 @@ struct Tiled {
   // workgroups that a CU should hold at a time: two where the sums leave room
   static constexpr int kGroups = TM * TN * 4 <= 128 && 2 * (2 * kStage + 2 * kQuad) <= kRoom ? 2 : 1;
   static constexpr int kFit = (kRoom / kGroups - 4 * kQuad) / kStage;
-  static constexpr int kBuf = kFit > 6 ? 6 : kFit > 3 ? kFit : kGroups * (3 * kStage + 2 * kQuad) <= kRoom ? 3 : 2;
-  static constexpr int kQuads = kBuf > 3 ? 4 : 2;
+  static constexpr int kBuf = kFit > 6 ? 6 : kFit > 3 - (S == 2) ? kFit : S == 1 && kGroups * (3 * kStage + 2 * kQuad) <= kRoom ? 3 : 2;
+  static constexpr int kQuads = kBuf > (S == 2 ? 2 : 3) ? 4 : 2;
   static constexpr uint32_t kLds = kBuf * kStage + kQuads * kQuad;
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
   // copies of a wave in a step: operands, and one of scales
   static constexpr int kSpread = kAC + kWC, kPerStep = kSpread + 1, kMid = kSpread / 2;
   static constexpr uint32_t kRowsA = kBM / kWaves, kRowsW = kBN / kWaves;
   static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 2 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
+  static_assert(S == 1 || (S == 2 && kWaves % 2 == 0), "a step");
   static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
   static_assert(kLds <= kRoom && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
 };
@@ -251,10 +255,12 @@ __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
   return OUT == BF16 ? (r & ~31u) + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3) : r;
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, bool kWhole>
-__global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::kGroups)) void k_mx_tiled(
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S, bool kWhole>
+__global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN, S>::kGroups)) void k_mx_tiled(
     MxMatmulArgs p, uint32_t nb, uint32_t pitch, uint32_t mt, uint32_t nt, uint32_t per, uint64_t part) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S>;
+  using LA = typename T::LA;
+  using LW = typename T::LW;
   constexpr int kBuf = T::kBuf;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[T::kLds];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, g = lane >> 4;
@@ -277,7 +283,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // this workgroup's piece of k: `per` steps from the first on, its sums to
   // an output of its own
   const uint32_t first = blockIdx.y * per, blocks = nb - 4 * first < 4 * per ? nb - 4 * first : 4 * per;
-  const uint8_t *a0 = p.a + m0 * pa + uint64_t(first) * Lay<FA>::kRow, *w0 = p.w + n0 * pw + uint64_t(first) * Lay<FW>::kRow;
+  const uint8_t *a0 = p.a + m0 * pa + uint64_t(first) * (LA::kRow / S), *w0 = p.w + n0 * pw + uint64_t(first) * (LW::kRow / S);
   const uint8_t *as0 = p.as + m0 * pitch + 4 * first, *ws0 = p.ws + n0 * pitch + 4 * first;
   p.out += blockIdx.y * part;
 
@@ -286,26 +292,26 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   uint32_t oa[T::kAC], ow[T::kWC];
 #pragma unroll
   for (int c = 0; c < T::kAC; c++) {
-    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FA>::kPieces, from = row < mr ? row : mr - 1;
-    oa[c] = from * pa + 16 * Lay<FA>::piece(row, q % Lay<FA>::kPieces);
+    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / LA::kPieces, from = row < mr ? row : mr - 1;
+    oa[c] = from * pa + 16 * LA::piece(row, q % LA::kPieces);
   }
 #pragma unroll
   for (int c = 0; c < T::kWC; c++) {
-    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / Lay<FW>::kPieces, n = weight_row<OUT>(row), from = n < nr ? n : nr - 1;
-    ow[c] = from * pw + 16 * Lay<FW>::piece(row, q % Lay<FW>::kPieces);
+    const uint32_t q = (c * T::kWaves + wave) * 64 + lane, row = q / LW::kPieces, n = weight_row<OUT>(row), from = n < nr ? n : nr - 1;
+    ow[c] = from * pw + 16 * LW::piece(row, q % LW::kPieces);
   }
   const uint32_t ra = wave * T::kRowsA + lane, rw = weight_row<OUT>(wave * T::kRowsW + lane);
   const uint32_t osa = (ra < mr ? ra : mr - 1) * pitch, osw = (rw < nr ? rw : nr - 1) * pitch;
   const uint32_t lds0 = lds_offset(lds);
-  // A last step of fewer than four blocks: the absent pieces of the activations
+  // A last step of fewer blocks: the absent pieces of the activations
   // are copied from zeros, those of the weights repeat the row's last block
   // and the scales are 1.  A NaN that this multiplies by zero is one that the
   // row has anyway.
-  const uint32_t steps = (blocks + 3) / 4, rest = blocks % 4;
-  const uint32_t pa0 = Lay<FA>::piece(lane / Lay<FA>::kPieces, lane % Lay<FA>::kPieces);
-  const uint32_t pw0 = Lay<FW>::piece(lane / Lay<FW>::kPieces, lane % Lay<FW>::kPieces);
-  const bool absent = rest && pa0 / (FA == FP8 ? 2 : 1) >= rest;
-  const uint32_t last_piece = (FW == FP8 ? 2 : 1) * rest - 1, back = rest && pw0 > last_piece ? 16 * (pw0 - last_piece) : 0;
+  const uint32_t steps = (blocks + 4 * S - 1) / (4 * S), rest = blocks % (4 * S);
+  const uint32_t q0 = wave * 64 + lane;  // the piece is the same in all of a wave's copies
+  const uint32_t pa0 = LA::piece(q0 / LA::kPieces, q0 % LA::kPieces), pw0 = LW::piece(q0 / LW::kPieces, q0 % LW::kPieces);
+  const bool absent = rest && pa0 / LA::kPerBlock >= rest;
+  const uint32_t last_piece = LW::kPerBlock * rest - 1, back = rest && pw0 > last_piece ? 16 * (pw0 - last_piece) : 0;
   // copies `from` to `to` of step t's kSpread; past the end the last step is
   // copied again and never used
   const auto copy = [&](uint32_t t, uint32_t stage, int from, int to) {
@@ -314,14 +320,14 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
 #pragma unroll
     for (int u = from; u < to; u++) {
       if (u < T::kAC) {
-        const uint8_t *a = a0 + uint64_t(s) * Lay<FA>::kRow;
+        const uint8_t *a = a0 + uint64_t(s) * LA::kRow;
         if constexpr (kWhole)
           copy16(at + (u * T::kWaves + wave) * 1024, uniform(a), oa[u]);
         else
           copy16(at + (u * T::kWaves + wave) * 1024, last && absent ? kZeros : a + oa[u]);
       } else {
         const int c = u - T::kAC;
-        copy16(at + T::kABytes + (c * T::kWaves + wave) * 1024, uniform(w0 + uint64_t(s) * Lay<FW>::kRow),
+        copy16(at + T::kABytes + (c * T::kWaves + wave) * 1024, uniform(w0 + uint64_t(s) * LW::kRow),
                kWhole ? ow[c] : ow[c] - (last ? back : 0));
       }
     }
@@ -332,16 +338,22 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // is issued for no lane, so that every step counts the same).
   const auto copy_quad = [&](uint32_t q, uint32_t side) {
     const uint32_t at = lds0 + kBuf * T::kStage + (q % T::kQuads) * T::kQuad;
-    const uint32_t c = 4 * q < steps ? q : (steps - 1) / 4;
+    const uint32_t c = 16 * q < blocks ? q : (blocks - 1) / 16;
     const uint64_t lanes = side > 1 ? 0 : ~0ull >> (64 - (side ? T::kRowsW : T::kRowsA));
     const uint32_t to = at + 16 * (side ? T::kBM + wave * T::kRowsW : wave * T::kRowsA);
     copy16_of(__builtin_amdgcn_readfirstlane(to), uniform((side ? ws0 : as0) + 16 * c), side ? osw : osa, uniform(lanes));
   };
 
   // this lane's places in a stage
-  const uint32_t la = (wm * 16 * TM + r) * Lay<FA>::kRow, lw = T::kABytes + (wn * 16 * TN + r) * Lay<FW>::kRow;
-  const uint32_t la0 = la + 16 * Lay<FA>::piece(r, g), la1 = la + 16 * Lay<FA>::piece(r, 4 + g);
-  const uint32_t lw0 = lw + 16 * Lay<FW>::piece(r, g), lw1 = lw + 16 * Lay<FW>::piece(r, 4 + g);
+  const uint32_t la = (wm * 16 * TM + r) * LA::kRow, lw = T::kABytes + (wn * 16 * TN + r) * LW::kRow;
+  uint32_t la0[S], la1[S], lw0[S], lw1[S];  // a lane's pieces of each 128 k
+#pragma unroll
+  for (int s = 0; s < S; s++) {
+    la0[s] = la + 16 * LA::piece(r, 4 * LA::kPerBlock * s + g);
+    la1[s] = la + 16 * LA::piece(r, 4 * LA::kPerBlock * s + 4 + g);
+    lw0[s] = lw + 16 * LW::piece(r, 4 * LW::kPerBlock * s + g);
+    lw1[s] = lw + 16 * LW::piece(r, 4 * LW::kPerBlock * s + 4 + g);
+  }
   const auto read = [&](auto f, uint32_t lo, uint32_t hi) {
     const u32x4 x = *reinterpret_cast<const u32x4 *>(lds + lo);
     if constexpr (decltype(f)::value == FP8)
@@ -349,7 +361,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
     else
       return operand<FP4X2>(x, x);
   };
-  // the scales of step t for 16 rows from `row` on, of A then W: a dword of the
+  // the scales of 128 k, number t, for 16 rows from `row` on, of A then W: a dword of the
   // step's four blocks, shifted to the lane group's at its use
   const auto scale = [&](uint32_t t, uint32_t row) {
     return *reinterpret_cast<const uint32_t *>(lds + kBuf * T::kStage + ((t >> 2) % T::kQuads) * T::kQuad + 4 * (t & 3) + 16 * r + 16 * row);
@@ -373,15 +385,28 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // Between the halves all waves are done with the LDS of step t and the
   // copies of step t + 1 have landed; step t + kBuf is copied over step t.
   constexpr int kHalf = TM / 2;
-  i32x8 xa[TM], xw[TN];
-  uint32_t sa[TM], sw[TN];
+  i32x8 xa[TM][S], xw[TN][S];
+  uint32_t sa[TM][S], sw[TN][S];
   const auto read_a = [&](uint32_t t, uint32_t stage, int j) {
-    xa[j] = read(IA{}, stage + la0 + j * 16 * Lay<FA>::kRow, stage + la1 + j * 16 * Lay<FA>::kRow);
-    sa[j] = scale(t, wm * 16 * TM + 16 * j);
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+      xa[j][s] = read(IA{}, stage + la0[s] + j * 16 * LA::kRow, stage + la1[s] + j * 16 * LA::kRow);
+      sa[j][s] = scale(S * t + s, wm * 16 * TM + 16 * j);
+    }
   };
   const auto read_w = [&](uint32_t t, uint32_t stage, int i) {
-    xw[i] = read(IW{}, stage + lw0 + i * 16 * Lay<FW>::kRow, stage + lw1 + i * 16 * Lay<FW>::kRow);
-    sw[i] = scale(t, T::kBM + wn * 16 * TN + 16 * i);
+#pragma unroll
+    for (int s = 0; s < S; s++) {
+      xw[i][s] = read(IW{}, stage + lw0[s] + i * 16 * LW::kRow, stage + lw1[s] + i * 16 * LW::kRow);
+      sw[i][s] = scale(S * t + s, T::kBM + wn * 16 * TN + 16 * i);
+    }
+  };
+  const auto multiply = [&](int i, int from) {
+#pragma unroll
+    for (int s = 0; s < S; s++)
+#pragma unroll
+      for (int j = from; j < from + kHalf; j++)
+        acc[i][j] = mfma<FW, FA>(xw[i][s], xa[j][s], acc[i][j], sw[i][s] >> shift, sa[j][s] >> shift);
   };
   // An empty statement that takes the sums keeps a group of products from
   // being moved past the copies and waits behind it, which they do not touch.
@@ -393,11 +418,12 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
   // The copies of a step are spread over the products, for the address unit
   // takes 16 cycles for each and would hold the wave up: half of those of step
   // t + kBuf go out in the upper half of step t, half in the next lower half.
-  // The scales of quad q + kQuads - 1 go out in the upper halves of steps 4 q - 1
-  // and 4 q, when quad q - 1, which lay there, has been read.  With two quads
-  // they are first read in the upper half of step 4 q + 3 and have landed two
-  // waits after step 4 q; with four, eight steps later, a wait leaves the last
-  // four steps' copies out.
+  // A quad's scales serve kFour steps.  Those of quad q + kQuads - 1 go out in
+  // the upper halves of steps kFour q - 1 and kFour q, when quad q - 1, which lay
+  // there, has been read, and are first read in the upper half of step
+  // kFour (q + kQuads - 1) - 1: more steps later than a wait leaves copies out.
+  constexpr int kFour = 4 / S;
+  static_assert(kFour * (T::kQuads - 1) - 1 > kBuf - 2, "scales in time");
   constexpr int kMid = T::kMid, kRest = T::kSpread - kMid;
 #pragma unroll
   for (int q = 0; q < T::kQuads - 1; q++) {
@@ -423,8 +449,7 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
     const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
 #pragma unroll
     for (int i = 0; i < TN; i++) {
-#pragma unroll
-      for (int j = 0; j < kHalf; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i] >> shift, sa[j] >> shift);
+      multiply(i, 0);
       if (i < kHalf) read_a(t, here, kHalf + i);
       copy(t + kBuf - 1, before, kMid + i * kRest / TN, kMid + (i + 1) * kRest / TN);
       keep(i, 0);
@@ -434,12 +459,11 @@ __global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN>::
     barrier();
 #pragma unroll
     for (int i = 0; i < TN; i++) {
-#pragma unroll
-      for (int j = kHalf; j < TM; j++) acc[i][j] = mfma<FW, FA>(xw[i], xa[j], acc[i][j], sw[i] >> shift, sa[j] >> shift);
+      multiply(i, kHalf);
       read_w(t + 1, next, i);
       if (i < kHalf) read_a(t + 1, next, i);
       copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
-      if (i == TN - 1) copy_quad((t + 1) / 4 + T::kQuads - 1, (t + 1) & 3);
+      if (i == TN - 1) copy_quad((t + 1) / kFour + T::kQuads - 1, (t + 1) % kFour);
       keep(i, kHalf);
     }
     before = here;
@@ -521,17 +545,17 @@ __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces
   store4<OUT>(p, m, n, s);
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S>
 hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S>;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
   const uint32_t steps = (nb + 3) / 4;
   const uint64_t part = p.m * p.out_stride * esize(OUT);
   const dim3 grid(mt * nt, (steps + per - 1) / per);
-  if (nb % 4 == 0)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
+  if (nb % (4 * S) == 0)
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   return hipGetLastError();
 }
 
@@ -543,9 +567,9 @@ struct Plan {
 
 template <int FA, int FW, int OUT>
 hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2>(p, nb, per, s);
-  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2>(p, nb, per, s);
-  return tiled<FA, FW, OUT, 8, 8, 2, 2>(p, nb, per, s);
+  if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2, 2>(p, nb, per, s);
+  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2, 1>(p, nb, per, s);
+  return tiled<FA, FW, OUT, 8, 8, 2, 2, FA == FP4X2 && FW == FP4X2 ? 2 : 1>(p, nb, per, s);
 }
 
 // Which form and how many pieces of k.
@@ -557,7 +581,7 @@ Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
   if (tiles(256, 256) >= 200) return {kLarge, steps, 1};
   if (tiles(128, 128) >= 200) return {kMiddle, steps, 1};
   const uint64_t t = tiles(64, 64);
-  uint32_t pieces = uint32_t(t >= 512 ? 1 : (512 + t - 1) / t);
+  uint32_t pieces = uint32_t(t >= 256 ? 1 : (256 + t - 1) / t);
   if (pieces > steps / 8) pieces = steps / 8 ? steps / 8 : 1;
   // whole fours of steps, whose scales are copied together, and no empty piece
   const uint32_t per = ((steps + pieces - 1) / pieces + 3) & ~3u;
