@@ -219,7 +219,7 @@ struct Lay {
   __device__ static __forceinline__ uint32_t piece(uint32_t r, uint32_t p) { return kRow >= 128 ? p ^ (r & 7) : p ^ ((r >> 1) & 3); }
 };
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S, int G>
 struct Tiled {
   using LA = Lay<FA, S>;
   using LW = Lay<FW, S>;
@@ -230,10 +230,9 @@ struct Tiled {
   // or four where more than three steps are copied ahead
   static constexpr uint32_t kQuad = (kBM + kBN) * 16;
   static constexpr uint32_t kRoom = 160 * 1024;
-  // workgroups that a CU should hold at a time: two where the sums leave room
-  static constexpr int kGroups = TM * TN * 4 <= 128 && 2 * (2 * kStage + 2 * kQuad) <= kRoom ? 2 : 1;
-  static constexpr int kFit = (kRoom / kGroups - 4 * kQuad) / kStage;
-  static constexpr int kBuf = kFit > 6 ? 6 : kFit > 3 - (S == 2) ? kFit : S == 1 && kGroups * (3 * kStage + 2 * kQuad) <= kRoom ? 3 : 2;
+  // steps that are copied ahead: what LDS holds where a CU has G workgroups
+  static constexpr int kFit = (kRoom / G - 4 * kQuad) / kStage;
+  static constexpr int kBuf = kFit > 6 ? 6 : kFit > 3 - (S == 2) ? kFit : S == 1 && G * (3 * kStage + 2 * kQuad) <= kRoom ? 3 : 2;
   static constexpr int kQuads = kBuf > (S == 2 ? 2 : 3) ? 4 : 2;
   static constexpr uint32_t kLds = kBuf * kStage + kQuads * kQuad;
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
@@ -243,7 +242,7 @@ struct Tiled {
   static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 2 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
   static_assert(S == 1 || (S == 2 && kWaves % 2 == 0), "a step");
   static_assert(kAC * 1024 * kWaves == kABytes && kWC * 1024 * kWaves == kWBytes, "whole copies");
-  static_assert(kLds <= kRoom && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
+  static_assert(G * kLds <= kRoom && (kBuf - 1) * kPerStep < 64, "LDS and the count of copies");
 };
 
 // Weight row (from the tile's first) of LDS row r.  For BF16, rows 4 g + q of
@@ -255,10 +254,10 @@ __device__ __forceinline__ uint32_t weight_row(uint32_t r) {
   return OUT == BF16 ? (r & ~31u) + ((r >> 2) & 3) * 8 + ((r >> 4) & 1) * 4 + (r & 3) : r;
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S, bool kWhole>
-__global__ __launch_bounds__(64 * WM * WN, (Tiled<FA, FW, OUT, TM, TN, WM, WN, S>::kGroups)) void k_mx_tiled(
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S, int G, bool kWhole>
+__global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
     MxMatmulArgs p, uint32_t nb, uint32_t pitch, uint32_t mt, uint32_t nt, uint32_t per, uint64_t part) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S, G>;
   using LA = typename T::LA;
   using LW = typename T::LW;
   constexpr int kBuf = T::kBuf;
@@ -545,47 +544,72 @@ __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces
   store4<OUT>(p, m, n, s);
 }
 
-template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S>
+template <int FA, int FW, int OUT, int TM, int TN, int WM, int WN, int S, int G>
 hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S>;
+  using T = Tiled<FA, FW, OUT, TM, TN, WM, WN, S, G>;
   const uint32_t mt = uint32_t((p.m + T::kBM - 1) / T::kBM), nt = uint32_t((p.n + T::kBN - 1) / T::kBN);
   const uint32_t steps = (nb + 3) / 4;
   const uint64_t part = p.m * p.out_stride * esize(OUT);
   const dim3 grid(mt * nt, (steps + per - 1) / per);
   if (nb % (4 * S) == 0)
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, G, true><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   else
-    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
+    k_mx_tiled<FA, FW, OUT, TM, TN, WM, WN, S, G, false><<<grid, 64 * WM * WN, 0, s>>>(p, nb, pitch_of(nb), mt, nt, per, part);
   return hipGetLastError();
 }
 
-enum Form { kFew, kSmall, kMiddle, kLarge };
+enum Form { kFew, kSmall, kSmaller, kMiddle, kWide, kLarge };
 struct Plan {
   Form form;
-  uint32_t per, pieces;  // steps of a piece of k, and their number
+  uint32_t per, pieces;  // steps of 128 of a piece of k, and their number
 };
 
+// Tiles (m by n), steps and workgroups to a CU of the forms.  A CU's time is
+// bounded by the matrix unit in the large ones and by what a step waits for
+// (LDS reads, a barrier) in the small ones, which therefore take 256 k at a
+// step where the registers allow it.
 template <int FA, int FW, int OUT>
 hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
-  if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2, 2>(p, nb, per, s);
-  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2, 1>(p, nb, per, s);
-  return tiled<FA, FW, OUT, 8, 8, 2, 2, FA == FP4X2 && FW == FP4X2 ? 2 : 1>(p, nb, per, s);
+  constexpr bool k44 = FA == FP4X2 && FW == FP4X2, k88 = FA == FP8 && FW == FP8, k84 = FA == FP8 && FW == FP4X2;
+  if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2, k88 ? 1 : 2, k88 ? 3 : 2>(p, nb, per, s);
+  if (f == kSmaller) return tiled<FA, FW, OUT, 2, 2, 2, 2, k88 ? 1 : 2, 3>(p, nb, per, s);
+  if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2, k44 ? 2 : 1, 2>(p, nb, per, s);
+  if constexpr (k84)
+    if (f == kWide) return tiled<FA, FW, OUT, 4, 8, 2, 2, 1, 2>(p, nb, per, s);
+  return tiled<FA, FW, OUT, 8, 8, 2, 2, k44 ? 2 : 1, 1>(p, nb, per, s);
 }
 
-// Which form and how many pieces of k.
-Plan plan_of(uint64_t m, uint64_t n, uint64_t k) {
+// Which form, and how many pieces of k.  Times at m x n x k, FP8 by FP4:
+//  - 256 x 256 tiles from about a CU each: 1024 x 14336 x 4096 50 us, 63 with
+//    128 x 128; 128 x 128 then, 1024 x 4096 x 4096 24 us, 35 with 256 x 256,
+//    and 64 x 64 below, 512 x 4096 x 4096 16 us, 23 with 128 x 128.
+//  - two workgroups of 128 x 256 to a CU are 7% slower than one of 256 x 256
+//    (8192 x 28672 x 4096 802 us for 750) but end less raggedly: where the
+//    last round of large tiles would leave many CUs idle they are taken
+//    (4096 x 14336 x 4096, 3.5 rounds: 189 us for 197).
+//  - three 64 x 64 workgroups to a CU, with fewer steps copied ahead, where
+//    two would need a second round: 600 x 4096 x 4096 19.5 us for 22.4, but
+//    512 x 4096 x 4096, one round, 16.9 for 15.3.
+//  - pieces of k only where there are fewer tiles than CUs and a piece saves
+//    more than 20 steps, about the time of joining them: 48 x 4096 x 14336 14 us
+//    in 4 pieces, 28 in one; 128 x 4096 x 4096 10.0 in one, 11.1 in two.
+Plan plan_of(int a_fmt, int w_fmt, uint64_t m, uint64_t n, uint64_t k) {
   const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
   // offsets inside a tile are 32-bit, and so are the tiles' numbers
   if (m <= 16 || nb > (1u << 18) || m * n >= (1ull << 42)) return {kFew, steps, 1};
   const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  if (tiles(256, 256) >= 200) return {kLarge, steps, 1};
+  const uint64_t large = tiles(256, 256), t = tiles(64, 64);
+  if (large >= 200) {
+    const uint64_t wide = tiles(128, 256), left = wide % 512;
+    const uint64_t rounds = 100 * ((large + 255) / 256), wide_rounds = 107 * (wide / 512) + (left == 0 ? 0 : left <= 256 ? 59 : 107);
+    return {a_fmt == FP8 && w_fmt == FP4X2 && wide_rounds < rounds ? kWide : kLarge, steps, 1};
+  }
   if (tiles(128, 128) >= 200) return {kMiddle, steps, 1};
-  const uint64_t t = tiles(64, 64);
-  uint32_t pieces = uint32_t(t >= 256 ? 1 : (256 + t - 1) / t);
-  if (pieces > steps / 8) pieces = steps / 8 ? steps / 8 : 1;
-  // whole fours of steps, whose scales are copied together, and no empty piece
-  const uint32_t per = ((steps + pieces - 1) / pieces + 3) & ~3u;
-  return {kSmall, per, (steps + per - 1) / per};
+  if (t > 512) return {kSmaller, steps, 1};
+  const uint32_t pieces = t >= 256 ? 1 : uint32_t(256 / t);
+  const uint32_t per = ((steps + pieces - 1) / pieces + 3) & ~3u;  // whole fours: their scales are copied together
+  if (steps <= per + 20) return {kSmall, steps, 1};
+  return {kSmall, per, (steps + per - 1) / per};  // none is empty
 }
 
 uint64_t padded(uint64_t n) { return (n + 3) & ~uint64_t(3); }
@@ -619,7 +643,7 @@ hipError_t few(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
 template <int FA, int FW, int OUT>
 hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
-  const Plan plan = plan_of(p.m, p.n, p.k);
+  const Plan plan = plan_of(FA, FW, p.m, p.n, p.k);
   // scale rows that could be copied as they lie but for the first one's
   // address have no room in the scratch: any m goes the way of few rows
   const bool apart = nb % 16 == 0 && (uintptr_t(p.as) | uintptr_t(p.ws)) % 16;
@@ -653,8 +677,8 @@ hipError_t matmul_out(int out_dtype, const MxMatmulArgs &p, hipStream_t s) {
 
 }  // namespace
 
-uint64_t mx_matmul_scratch(int, int, uint64_t m, uint64_t n, uint64_t k) {
-  const Plan p = plan_of(m, n, k);
+uint64_t mx_matmul_scratch(int a_fmt, int w_fmt, uint64_t m, uint64_t n, uint64_t k) {
+  const Plan p = plan_of(a_fmt, w_fmt, m, n, k);
   return p.form == kFew ? 0 : part_bytes(p, m, n) + (k % 512 ? (m + n) * pitch_of(uint32_t(k / kMxBlock)) : 0);
 }
 
