@@ -8,6 +8,7 @@ is missing, every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import os
 from typing import Sequence
@@ -421,7 +422,7 @@ def _mx_device(where: str, stream, first: torch.Tensor, *others) -> torch.device
 
 def _mx_call(where: str, dev: torch.device, stream, function, *args) -> None:
     """The library call on the tensors' device and the stream (its current one when None)."""
-    if torch.cuda.current_device() != dev.index:
+    if torch._C._cuda_getDevice() != dev.index:
         with torch.cuda.device(dev):
             return _mx_call(where, dev, stream, function, *args)
     # the handle alone: making a Stream object takes longer than the launch
@@ -458,63 +459,65 @@ def _mx_rows(where: str, name: str, t: torch.Tensor, write: bool = False):
     return rows, k, stride
 
 
-def _mx_new(shape, dtype, dev, stream) -> torch.Tensor:
+def _mx_new(dtype, dev, stream, *shape) -> torch.Tensor:
     """An output on the stream that writes it; it may be used on the current
     stream too (once that has waited for the call's)."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(*shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(*shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream(dev))
     return t
 
 
 def _mx_given(where: str, name: str, t: torch.Tensor, shape, dtypes) -> None:
-    """A packed tensor of the call: type, shape, dense, and no view whose first
-    byte breaks the alignment of codes."""
-    if t.dtype not in dtypes or tuple(t.shape) != tuple(shape):
+    """A packed tensor of the call: type, shape and dense rows."""
+    if t.dtype not in dtypes or t.shape != shape:
         raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted {dtypes[0]} {tuple(shape)}")
     if not t.is_contiguous():
         raise ZnError(-1, f"{where}: {name} is not contiguous (pass .contiguous())")
 
 
 def _mx_packed(where: str, name: str, codes: torch.Tensor, scales: torch.Tensor):
-    """(fmt, stored row length) of codes and their scales, checked."""
+    """(fmt, stored row length, leading shape) of codes and their scales, checked."""
     fmt = _MX_FMT.get(codes.dtype)
-    if fmt is None or codes.dim() == 0:
+    shape = codes.shape
+    if fmt is None or not shape:
         raise ZnError(-1, f"{where}: {name} is {codes.dtype}, wanted float8_e4m3fn, or uint8 pairs of E2M1, in rows")
-    kp = codes.shape[-1] * (2 if fmt == FP4X2_E2M1 else 1)
+    lead, kp = shape[:-1], shape[-1] if fmt == FP8_E4M3 else shape[-1] * 2
     if kp == 0 or kp % MX_BLOCK:
         raise ZnError(-1, f"{where}: {name} has rows of {kp} values, wanted whole blocks of {MX_BLOCK}")
     if not codes.is_contiguous():
         raise ZnError(-1, f"{where}: {name} is not contiguous (pass .contiguous())")
-    _mx_given(where, name + "'s scales", scales, (*codes.shape[:-1], kp // MX_BLOCK), _MX_SCALE)
-    return fmt, kp
+    _mx_given(where, name + "'s scales", scales, (*lead, kp // MX_BLOCK), _MX_SCALE)
+    return fmt, kp, lead
 
 
 def _mx_use(stream, *tensors) -> None:
     """Tensors of a call on another stream than the current one stay
     allocated until that stream's work is done."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def _mx_codes(where, lead, k, fmt, codes, scales, dev, stream):
     """The output pair, given or made."""
-    if fmt not in (FP8_E4M3, FP4X2_E2M1):
+    if fmt == FP8_E4M3:
+        dt, width = torch.float8_e4m3fn, MX_BLOCK
+    elif fmt == FP4X2_E2M1:
+        dt, width = torch.uint8, MX_BLOCK // 2
+    else:
         raise ZnError(-1, f"{where}: fmt is {fmt!r}, wanted FP8_E4M3 or FP4X2_E2M1")
     if k == 0:
         raise ZnError(-1, f"{where}: rows of no values")
     nb = -(-k // MX_BLOCK)
-    dt, width = (torch.float8_e4m3fn, MX_BLOCK) if fmt == FP8_E4M3 else (torch.uint8, MX_BLOCK // 2)
     if codes is None:
-        codes = _mx_new((*lead, nb * width), dt, dev, stream)
+        codes = _mx_new(dt, dev, stream, *lead, nb * width)
     else:
         _mx_given(where, "codes", codes, (*lead, nb * width), (dt,))
     if scales is None:
-        scales = _mx_new((*lead, nb), torch.float8_e8m0fnu, dev, stream)
+        scales = _mx_new(torch.float8_e8m0fnu, dev, stream, *lead, nb)
     else:
         _mx_given(where, "scales", scales, (*lead, nb), _MX_SCALE)
     return codes, scales
@@ -524,6 +527,18 @@ def _mx_plain(where: str, name: str, dtype) -> int:
     if dtype not in _MX_PLAIN:
         raise ZnError(-1, f"{where}: {name} is {dtype}, wanted bfloat16 or float32")
     return _MX_PLAIN[dtype]
+
+
+def _mx_out(where, lead, n, dtype, out, dev, stream):
+    """(tensor, type, rows, row stride) of a plain output, given or made."""
+    if out is None:
+        dt = _mx_plain(where, "dtype", dtype)
+        return _mx_new(dtype, dev, stream, *lead, n), dt, math.prod(lead), n
+    if out.shape != (*lead, n):
+        raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {(*lead, n)}")
+    dt = _mx_plain(where, "out", out.dtype)
+    rows, _, stride = _mx_rows(where, "out", out, write=True)
+    return out, dt, rows, stride
 
 
 def mx_quantize(x: torch.Tensor, fmt: int = FP8_E4M3, codes: torch.Tensor | None = None,
@@ -537,7 +552,8 @@ def mx_quantize(x: torch.Tensor, fmt: int = FP8_E4M3, codes: torch.Tensor | None
     codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
     _mx_call(where, dev, stream, lib().zn_mx_quantize, dt, x.data_ptr(), stride, rows, k, fmt, codes.data_ptr(),
              scales.data_ptr())
-    _mx_use(stream, x, codes, scales)
+    if stream is not None:
+        _mx_use(stream, x, codes, scales)
     return codes, scales
 
 
@@ -546,23 +562,17 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int | None = Non
     """zn_mx_dequantize: the values of the first k of every row (all stored
     ones when None), in BF16 or FP32."""
     where = "mx_dequantize"
-    fmt, kp = _mx_packed(where, "codes", codes, scales)
+    fmt, kp, lead = _mx_packed(where, "codes", codes, scales)
     if k is None:
         k = kp
     if not kp - MX_BLOCK < k <= kp:
         raise ZnError(-1, f"{where}: {k} values do not fill rows of {kp}")
     dev = _mx_device(where, stream, codes, scales, out)
-    shape = (*codes.shape[:-1], k)
-    if out is None:
-        _mx_plain(where, "dtype", dtype)
-        out = _mx_new(shape, dtype, dev, stream)
-    elif tuple(out.shape) != shape:
-        raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {shape}")
-    dt = _mx_plain(where, "out", out.dtype)
-    rows, _, stride = _mx_rows(where, "out", out, write=True)
+    out, dt, rows, stride = _mx_out(where, lead, k, dtype, out, dev, stream)
     _mx_call(where, dev, stream, lib().zn_mx_dequantize, fmt, codes.data_ptr(), scales.data_ptr(), rows, k, dt,
              out.data_ptr(), stride)
-    _mx_use(stream, codes, scales, out)
+    if stream is not None:
+        _mx_use(stream, codes, scales, out)
     return out
 
 
@@ -576,7 +586,7 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
     dt = _mx_plain(where, "x", x.dtype)
     dev = _mx_device(where, stream, x, weight, residual, residual_out, codes, scales)
     rows, k, stride = _mx_rows(where, "x", x)
-    if weight.dtype != x.dtype or tuple(weight.shape) != (k,) or not weight.is_contiguous():
+    if weight.dtype != x.dtype or weight.shape != (k,) or not weight.is_contiguous():
         raise ZnError(-1, f"{where}: weight is {weight.dtype} {tuple(weight.shape)}, wanted dense {x.dtype} {(k,)}")
     if residual is None and residual_out is not None:
         raise ZnError(-1, f"{where}: residual_out without a residual")
@@ -588,19 +598,22 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
             raise ZnError(-1, f"{where}: residual is {residual.dtype} {tuple(residual.shape)}, x {x.dtype} {tuple(x.shape)}")
         rs = _mx_rows(where, "residual", residual)[2]
         if residual_out is None:
-            residual_out = _mx_new(x.shape, x.dtype, dev, stream)
+            residual_out, hs = _mx_new(x.dtype, dev, stream, *x.shape), k
         elif residual_out.dtype != x.dtype or residual_out.shape != x.shape:
             raise ZnError(-1, f"{where}: residual_out is {residual_out.dtype} {tuple(residual_out.shape)}, "
                               f"x {x.dtype} {tuple(x.shape)}")
-        hs = _mx_rows(where, "residual_out", residual_out, write=True)[2]
+        else:
+            hs = _mx_rows(where, "residual_out", residual_out, write=True)[2]
     codes, scales = _mx_codes(where, x.shape[:-1], k, fmt, codes, scales, dev, stream)
     _mx_call(where, dev, stream, lib().zn_mx_rms_norm, dt, x.data_ptr(), stride,
              residual.data_ptr() if residual is not None else None, rs, weight.data_ptr(), eps, rows, k,
              residual_out.data_ptr() if residual is not None else None, hs, fmt, codes.data_ptr(), scales.data_ptr())
-    _mx_use(stream, x, weight, residual, residual_out, codes, scales)
+    if stream is not None:
+        _mx_use(stream, x, weight, residual, residual_out, codes, scales)
     return codes, scales, (x if residual is None else residual_out)
 
 
+@functools.lru_cache(maxsize=4096)
 def mx_matmul_scratch_bytes(a_fmt: int, w_fmt: int, m: int, n: int, k: int) -> int:
     """zn_mx_matmul_scratch_bytes: device scratch of a product of m rows with
     n rows of stored length k."""
@@ -615,29 +628,23 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     """zn_mx_matmul: a [..., k] by the rows of w [n, k], both microscaled (FP8
     or FP4 each), as BF16 or FP32 [..., n]."""
     where = "mx_matmul"
-    fa, k = _mx_packed(where, "a", a, a_scales)
-    fw, kw = _mx_packed(where, "w", w, w_scales)
-    if w.dim() != 2 or kw != k:
+    fa, k, lead = _mx_packed(where, "a", a, a_scales)
+    fw, kw, wlead = _mx_packed(where, "w", w, w_scales)
+    if len(wlead) != 1 or kw != k:
         raise ZnError(-1, f"{where}: w has rows of {kw} values and {w.dim()} axes, wanted {k} and 2")
     dev = _mx_device(where, stream, a, a_scales, w, w_scales, out, scratch)
-    n = w.shape[0]
-    shape = (*a.shape[:-1], n)
-    if out is None:
-        _mx_plain(where, "dtype", dtype)
-        out = _mx_new(shape, dtype, dev, stream)
-    elif tuple(out.shape) != shape:
-        raise ZnError(-1, f"{where}: out is {tuple(out.shape)}, wanted {shape}")
-    dt = _mx_plain(where, "out", out.dtype)
-    m, _, stride = _mx_rows(where, "out", out, write=True)
+    n = wlead[0]
+    out, dt, m, stride = _mx_out(where, lead, n, dtype, out, dev, stream)
     need = mx_matmul_scratch_bytes(fa, fw, m, n, k)
     if scratch is None:
-        scratch = _mx_new((need,), torch.uint8, dev, stream) if need else None
+        scratch = _mx_new(torch.uint8, dev, stream, need) if need else None
     elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
         raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
     _mx_call(where, dev, stream, lib().zn_mx_matmul, fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(),
              w_scales.data_ptr(), m, n, k, dt, out.data_ptr(), stride,
              scratch.data_ptr() if scratch is not None else None, scratch.numel() if scratch is not None else 0)
-    _mx_use(stream, a, a_scales, w, w_scales, out, scratch)
+    if stream is not None:
+        _mx_use(stream, a, a_scales, w, w_scales, out, scratch)
     return out
 
 
