@@ -90,68 +90,82 @@ __device__ __forceinline__ void store4(const MxMatmulArgs &p, uint64_t m, uint64
 // What bounds it is the weights' way from memory, so a wave asks for four
 // steps at a time: 256 bytes of each of 16 weight rows (E2M1), and their 16
 // scale bytes in one load, before it multiplies.
-template <int FA, int FW, int OUT, int MT, int KS>
+template <int FA, int FW, int OUT, int MT, int NT, int KS>
 __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb) {
-  __shared__ f32x4 part[KS > 1 ? KS : 1][MT][64];
+  __shared__ f32x4 part[KS][NT * MT][64];
   const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, g = lane >> 4;
-  const uint64_t n0 = uint64_t(blockIdx.x) * 16, m0 = uint64_t(blockIdx.y) * (16 * MT);
+  const uint64_t n0 = uint64_t(blockIdx.x) * (16 * NT), m0 = uint64_t(blockIdx.y) * (16 * MT);
   const uint32_t steps = (nb + 3) / 4, fours = (steps + 3) / 4, per = 4 * ((fours + KS - 1) / KS);
   const uint32_t t0 = wave * per, t1 = t0 + per < steps ? t0 + per : steps;
   // rows past the end are read as the last row and never stored
-  const uint64_t n = n0 + r < p.n ? n0 + r : p.n - 1;
-  const uint8_t *w = p.w + n * nb * code_bytes<FW>(), *ws = p.ws + n * nb;
-  const uint8_t *a[MT], *as[MT];
+  const uint8_t *w[NT], *ws[NT], *a[MT], *as[MT];
 #pragma unroll
-  for (int i = 0; i < MT; i++) {
-    const uint64_t m = m0 + 16 * i + r < p.m ? m0 + 16 * i + r : p.m - 1;
-    a[i] = p.a + m * nb * code_bytes<FA>();
-    as[i] = p.as + m * nb;
+  for (int i = 0; i < NT; i++) {
+    const uint64_t n = n0 + 16 * i + r < p.n ? n0 + 16 * i + r : p.n - 1;
+    w[i] = p.w + n * nb * code_bytes<FW>();
+    ws[i] = p.ws + n * nb;
   }
-  f32x4 c[MT];
 #pragma unroll
-  for (int i = 0; i < MT; i++) c[i] = f32x4{0, 0, 0, 0};
+  for (int j = 0; j < MT; j++) {
+    const uint64_t m = m0 + 16 * j + r < p.m ? m0 + 16 * j + r : p.m - 1;
+    a[j] = p.a + m * nb * code_bytes<FA>();
+    as[j] = p.as + m * nb;
+  }
+  f32x4 c[NT][MT];
+#pragma unroll
+  for (int i = 0; i < NT; i++)
+#pragma unroll
+    for (int j = 0; j < MT; j++) c[i][j] = f32x4{0, 0, 0, 0};
   uint32_t t = t0;
   for (; t + 4 <= t1 && 4 * t + 16 <= nb; t += 4) {
-    i32x8 x[4], y[MT][4];
-    const u32x4 sx = *reinterpret_cast<const u32x4_any *>(ws + 4 * t);
-    u32x4 sy[MT];
+    i32x8 x[NT][4], y[MT][4];
+    u32x4 sx[NT], sy[MT];
 #pragma unroll
-    for (int s = 0; s < 4; s++) x[s] = load_whole<FW>(w, t + s, g);
+    for (int i = 0; i < NT; i++) {
+      sx[i] = *reinterpret_cast<const u32x4_any *>(ws[i] + 4 * t);
 #pragma unroll
-    for (int i = 0; i < MT; i++) {
-      sy[i] = *reinterpret_cast<const u32x4_any *>(as[i] + 4 * t);
+      for (int s = 0; s < 4; s++) x[i][s] = load_whole<FW>(w[i], t + s, g);
+    }
 #pragma unroll
-      for (int s = 0; s < 4; s++) y[i][s] = load_whole<FA>(a[i], t + s, g);
+    for (int j = 0; j < MT; j++) {
+      sy[j] = *reinterpret_cast<const u32x4_any *>(as[j] + 4 * t);
+#pragma unroll
+      for (int s = 0; s < 4; s++) y[j][s] = load_whole<FA>(a[j], t + s, g);
     }
 #pragma unroll
     for (int s = 0; s < 4; s++)
 #pragma unroll
-      for (int i = 0; i < MT; i++) c[i] = mfma<FW, FA>(x[s], y[i][s], c[i], sx[s] >> (8 * g), sy[i][s] >> (8 * g));
+      for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < MT; j++)
+          c[i][j] = mfma<FW, FA>(x[i][s], y[j][s], c[i][j], sx[i][s] >> (8 * g), sy[j][s] >> (8 * g));
   }
   for (; t < t1; t++) {
-    const i32x8 x = load_codes<FW>(w, t, g, nb);
-    const uint32_t sx = load_scale(ws, t, g, nb);
+    i32x8 y[MT];
+    uint32_t sy[MT];
 #pragma unroll
-    for (int i = 0; i < MT; i++)
-      c[i] = mfma<FW, FA>(x, load_codes<FA>(a[i], t, g, nb), c[i], sx, load_scale(as[i], t, g, nb));
-  }
-  if constexpr (KS > 1) {
-#pragma unroll
-    for (int i = 0; i < MT; i++) part[wave][i][lane] = c[i];
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < MT; i++) {
-    if (KS > 1 && uint32_t(i % KS) != wave) continue;
-    f32x4 s;
-    if constexpr (KS > 1) {
-      s = part[0][i][lane];
-#pragma unroll
-      for (int j = 1; j < KS; j++) s += part[j][i][lane];
-    } else {
-      s = c[i];
+    for (int j = 0; j < MT; j++) {
+      y[j] = load_codes<FA>(a[j], t, g, nb);
+      sy[j] = load_scale(as[j], t, g, nb);
     }
-    store4<OUT>(p, m0 + 16 * i + r, n0 + 4 * g, s);
+#pragma unroll
+    for (int i = 0; i < NT; i++) {
+      const i32x8 x = load_codes<FW>(w[i], t, g, nb);
+      const uint32_t sx = load_scale(ws[i], t, g, nb);
+#pragma unroll
+      for (int j = 0; j < MT; j++) c[i][j] = mfma<FW, FA>(x, y[j], c[i][j], sx, sy[j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NT; i++)
+#pragma unroll
+    for (int j = 0; j < MT; j++) part[wave][i * MT + j][lane] = c[i][j];
+  __syncthreads();
+  for (uint32_t q = wave; q < NT * MT; q += KS) {
+    f32x4 s = part[0][q][lane];
+#pragma unroll
+    for (int k = 1; k < KS; k++) s += part[k][q][lane];
+    store4<OUT>(p, m0 + 16 * (q % MT) + r, n0 + 16 * (q / MT) + 4 * g, s);
   }
 }
 
@@ -238,6 +252,7 @@ struct Tiled {
   static constexpr int kAC = kABytes / 1024 / kWaves, kWC = kWBytes / 1024 / kWaves;
   // copies of a wave in a step: operands, and one of scales
   static constexpr int kSpread = kAC + kWC, kPerStep = kSpread + 1, kMid = kSpread / 2;
+  static constexpr bool kTwice = TM * TN <= 4 && FA == FW;  // operands held twice
   static constexpr uint32_t kRowsA = kBM / kWaves, kRowsW = kBN / kWaves;
   static_assert(kBM % 64 == 0 && kBN % 64 == 0 && TN % 2 == 0 && kRowsA <= 64 && kRowsW <= 64, "tile");
   static_assert(S == 1 || (S == 2 && kWaves % 2 == 0), "a step");
@@ -375,38 +390,34 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
 #pragma unroll
     for (int j = 0; j < TM; j++) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // The operands are held once.  A step's products come in two halves, the
-  // lower tiles of the activations with every weight tile, then the upper
-  // ones; during each half the operands whose last use is over are read anew,
-  // so every LDS read has half a step (32 matrix instructions) to arrive:
-  //   lower half of step t:  the upper activations of step t
-  //   upper half of step t:  the lower activations and the weights of t + 1
-  // Between the halves all waves are done with the LDS of step t and the
-  // copies of step t + 1 have landed; step t + kBuf is copied over step t.
-  constexpr int kHalf = TM / 2;
-  i32x8 xa[TM][S], xw[TN][S];
-  uint32_t sa[TM][S], sw[TN][S];
-  const auto read_a = [&](uint32_t t, uint32_t stage, int j) {
+  constexpr bool kTwice = T::kTwice;
+  constexpr int kSets = kTwice ? 2 : 1, kHalf = kTwice ? TM : TM / 2;
+  i32x8 xa[kSets][TM][S], xw[kSets][TN][S];
+  uint32_t sa[kSets][TM][S], sw[kSets][TN][S];
+  const auto read_a = [&](auto set, uint32_t t, uint32_t stage, int j) {
+    constexpr int c = decltype(set)::value;
 #pragma unroll
     for (int s = 0; s < S; s++) {
-      xa[j][s] = read(IA{}, stage + la0[s] + j * 16 * LA::kRow, stage + la1[s] + j * 16 * LA::kRow);
-      sa[j][s] = scale(S * t + s, wm * 16 * TM + 16 * j);
+      xa[c][j][s] = read(IA{}, stage + la0[s] + j * 16 * LA::kRow, stage + la1[s] + j * 16 * LA::kRow);
+      sa[c][j][s] = scale(S * t + s, wm * 16 * TM + 16 * j);
     }
   };
-  const auto read_w = [&](uint32_t t, uint32_t stage, int i) {
+  const auto read_w = [&](auto set, uint32_t t, uint32_t stage, int i) {
+    constexpr int c = decltype(set)::value;
 #pragma unroll
     for (int s = 0; s < S; s++) {
-      xw[i][s] = read(IW{}, stage + lw0[s] + i * 16 * LW::kRow, stage + lw1[s] + i * 16 * LW::kRow);
-      sw[i][s] = scale(S * t + s, T::kBM + wn * 16 * TN + 16 * i);
+      xw[c][i][s] = read(IW{}, stage + lw0[s] + i * 16 * LW::kRow, stage + lw1[s] + i * 16 * LW::kRow);
+      sw[c][i][s] = scale(S * t + s, T::kBM + wn * 16 * TN + 16 * i);
     }
   };
-  const auto multiply = [&](int i, int from) {
+  const auto multiply = [&](auto set, int i, int s, int from) {
+    constexpr int c = decltype(set)::value;
 #pragma unroll
-    for (int s = 0; s < S; s++)
-#pragma unroll
-      for (int j = from; j < from + kHalf; j++)
-        acc[i][j] = mfma<FW, FA>(xw[i][s], xa[j][s], acc[i][j], sw[i][s] >> shift, sa[j][s] >> shift);
+    for (int j = from; j < from + kHalf; j++)
+      acc[i][j] = mfma<FW, FA>(xw[c][i][s], xa[c][j][s], acc[i][j], sw[c][i][s] >> shift, sa[c][j][s] >> shift);
   };
+  using Set0 = std::integral_constant<int, 0>;
+  using Set1 = std::integral_constant<int, kTwice ? 1 : 0>;
   // An empty statement that takes the sums keeps a group of products from
   // being moved past the copies and waits behind it, which they do not touch.
   const auto keep = [&](int i, int j) {
@@ -414,59 +425,119 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
     for (int q = 0; q < kHalf; q++) asm volatile("" : "+a"(acc[i][j + q]));
     __builtin_amdgcn_sched_barrier(0);
   };
-  // The copies of a step are spread over the products, for the address unit
-  // takes 16 cycles for each and would hold the wave up: half of those of step
-  // t + kBuf go out in the upper half of step t, half in the next lower half.
   // A quad's scales serve kFour steps.  Those of quad q + kQuads - 1 go out in
   // the upper halves of steps kFour q - 1 and kFour q, when quad q - 1, which lay
   // there, has been read, and are first read in the upper half of step
   // kFour (q + kQuads - 1) - 1: more steps later than a wait leaves copies out.
   constexpr int kFour = 4 / S;
   static_assert(kFour * (T::kQuads - 1) - 1 > kBuf - 2, "scales in time");
-  constexpr int kMid = T::kMid, kRest = T::kSpread - kMid;
 #pragma unroll
   for (int q = 0; q < T::kQuads - 1; q++) {
     copy_quad(q, 0);
     copy_quad(q, 1);
   }
-  // counted as in the loop, a copy of scales to a step: the waits go by counts
-  constexpr int kFill = kBuf > 3 ? kBuf - 3 : 0;
+  if constexpr (kTwice) {
+    // Small tiles of one format: the operands are held twice, and while a step's
+    // products run the next step's are read.  A step waits once: its operands
+    // have been read by all waves (the copies of step t + kBuf may follow) and
+    // the copies of the next have landed.  256 x 4096 x 4096 took 8.2 us for 9.5
+    // in 4 bits and 13.1 for 13.6 in FP8; FP8 by FP4, 10.4 for 10.3, is bounded
+    // by the copies (24 KB a step and CU, about 25 bytes a cycle) either way.
+    copy_quad(T::kQuads - 1, 0);
 #pragma unroll
-  for (int t = 0; t < kBuf; t++) {
-    if (t >= 2 && t < kBuf - 1) copy_quad(0, 2);
-    copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
-  }
-  copy_quad(T::kQuads - 1, 0);
-  wait_copies<(kBuf - 2) * T::kSpread + kFill + kMid + 1>();
-  barrier();
-#pragma unroll
-  for (int i = 0; i < TN; i++) read_w(0, 0, i);
-#pragma unroll
-  for (int j = 0; j < kHalf; j++) read_a(0, 0, j);
-  uint32_t here = 0, before = (kBuf - 1) * T::kStage;
-  for (uint32_t t = 0; t < steps; t++) {
-    const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
-#pragma unroll
-    for (int i = 0; i < TN; i++) {
-      multiply(i, 0);
-      if (i < kHalf) read_a(t, here, kHalf + i);
-      copy(t + kBuf - 1, before, kMid + i * kRest / TN, kMid + (i + 1) * kRest / TN);
-      keep(i, 0);
+    for (int t = 0; t < kBuf; t++) {
+      copy(t, t * T::kStage, 0, T::kSpread);
+      if (t >= 2) copy_quad(0, 2);  // counted as in the loop, a copy of scales to a step: the waits go by counts
     }
-    wait_copies<(kBuf - 2) * T::kPerStep>();
-    wait_lds();
+    wait_copies<T::kSpread + (kBuf - 2) * T::kPerStep>();
     barrier();
 #pragma unroll
-    for (int i = 0; i < TN; i++) {
-      multiply(i, kHalf);
-      read_w(t + 1, next, i);
-      if (i < kHalf) read_a(t + 1, next, i);
-      copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
-      if (i == TN - 1) copy_quad((t + 1) / kFour + T::kQuads - 1, (t + 1) % kFour);
-      keep(i, kHalf);
+    for (int i = 0; i < TN; i++) read_w(Set0{}, 0, 0, i);
+#pragma unroll
+    for (int j = 0; j < TM; j++) read_a(Set0{}, 0, 0, j);
+    uint32_t here = 0;
+    const auto step = [&](uint32_t t, auto now, auto then) {
+      const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
+      wait_copies<(kBuf - 2) * T::kPerStep>();
+      wait_lds();
+      barrier();
+#pragma unroll
+      for (int i = 0; i < TN; i++) read_w(then, t + 1, next, i);
+#pragma unroll
+      for (int j = 0; j < TM; j++) read_a(then, t + 1, next, j);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int s = 0; s < S; s++)
+#pragma unroll
+        for (int i = 0; i < TN; i++) {
+          multiply(now, i, s, 0);
+          const int u = s * TN + i, n = S * TN;
+          copy(t + kBuf, here, u * T::kSpread / n, (u + 1) * T::kSpread / n);
+          if (u == n - 1) copy_quad((t + 1) / kFour + T::kQuads - 1, (t + 1) % kFour);
+          keep(i, 0);
+        }
+      here = next;
+    };
+    uint32_t t = 0;
+    for (; t + 2 <= steps; t += 2) {
+      step(t, Set0{}, Set1{});
+      step(t + 1, Set1{}, Set0{});
     }
-    before = here;
-    here = next;
+    if (t < steps) step(t, Set0{}, Set1{});
+  } else {
+    // The operands are held once.  A step's products come in two halves, the
+    // lower tiles of the activations with every weight tile, then the upper
+    // ones; during each half the operands whose last use is over are read anew,
+    // so every LDS read has half a step (32 matrix instructions) to arrive:
+    //   lower half of step t:  the upper activations of step t
+    //   upper half of step t:  the lower activations and the weights of t + 1
+    // Between the halves all waves are done with the LDS of step t and the
+    // copies of step t + 1 have landed; step t + kBuf is copied over step t.
+    // The copies of a step are spread over the products, for the address unit
+    // takes 16 cycles for each and would hold the wave up: half of those of step
+    // t + kBuf go out in the upper half of step t, half in the next lower half.
+    constexpr int kMid = T::kMid, kRest = T::kSpread - kMid;
+    // counted as in the loop, a copy of scales to a step: the waits go by counts
+    constexpr int kFill = kBuf > 3 ? kBuf - 3 : 0;
+#pragma unroll
+    for (int t = 0; t < kBuf; t++) {
+      if (t >= 2 && t < kBuf - 1) copy_quad(0, 2);
+      copy(t, t * T::kStage, 0, t < kBuf - 1 ? T::kSpread : kMid);
+    }
+    copy_quad(T::kQuads - 1, 0);
+    wait_copies<(kBuf - 2) * T::kSpread + kFill + kMid + 1>();
+    barrier();
+#pragma unroll
+    for (int i = 0; i < TN; i++) read_w(Set0{}, 0, 0, i);
+#pragma unroll
+    for (int j = 0; j < kHalf; j++) read_a(Set0{}, 0, 0, j);
+    uint32_t here = 0, before = (kBuf - 1) * T::kStage;
+    for (uint32_t t = 0; t < steps; t++) {
+      const uint32_t next = here + T::kStage == kBuf * T::kStage ? 0 : here + T::kStage;
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+#pragma unroll
+        for (int s = 0; s < S; s++) multiply(Set0{}, i, s, 0);
+        if (i < kHalf) read_a(Set0{}, t, here, kHalf + i);
+        copy(t + kBuf - 1, before, kMid + i * kRest / TN, kMid + (i + 1) * kRest / TN);
+        keep(i, 0);
+      }
+      wait_copies<(kBuf - 2) * T::kPerStep>();
+      wait_lds();
+      barrier();
+#pragma unroll
+      for (int i = 0; i < TN; i++) {
+#pragma unroll
+        for (int s = 0; s < S; s++) multiply(Set0{}, i, s, kHalf);
+        read_w(Set0{}, t + 1, next, i);
+        if (i < kHalf) read_a(Set0{}, t + 1, next, i);
+        copy(t + kBuf, here, i * kMid / TN, (i + 1) * kMid / TN);
+        if (i == TN - 1) copy_quad((t + 1) / kFour + T::kQuads - 1, (t + 1) % kFour);
+        keep(i, kHalf);
+      }
+      before = here;
+      here = next;
+    }
   }
   wait_copies<0>();  // none may land after the workgroup's end
 
@@ -539,8 +610,17 @@ __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces
   const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x, m = i / quads, n = 4 * (i % quads);
   if (m >= p.m) return;
   const float *from = reinterpret_cast<const float *>(p.scratch) + m * np + n;
+  const uint64_t part = p.m * np;
   f32x4 s = *reinterpret_cast<const f32x4 *>(from);
-  for (uint32_t j = 1; j < pieces; j++) s += *reinterpret_cast<const f32x4 *>(from + j * p.m * np);
+  // four loads in flight; those past the last piece read it again
+  for (uint32_t j = 1; j < pieces; j += 4) {
+    f32x4 v[4];
+#pragma unroll
+    for (uint32_t i = 0; i < 4; i++) v[i] = *reinterpret_cast<const f32x4 *>(from + (j + i < pieces ? j + i : pieces - 1) * part);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; i++)
+      if (j + i < pieces) s += v[i];
+  }
   store4<OUT>(p, m, n, s);
 }
 
@@ -558,7 +638,7 @@ hipError_t tiled(const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s
   return hipGetLastError();
 }
 
-enum Form { kFew, kSmall, kSmaller, kMiddle, kWide, kLarge };
+enum Form { kFew, kSmall, kSmall3, kMiddle, kWide, kLarge };
 struct Plan {
   Form form;
   uint32_t per, pieces;  // steps of 128 of a piece of k, and their number
@@ -572,7 +652,7 @@ template <int FA, int FW, int OUT>
 hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
   constexpr bool k44 = FA == FP4X2 && FW == FP4X2, k88 = FA == FP8 && FW == FP8, k84 = FA == FP8 && FW == FP4X2;
   if (f == kSmall) return tiled<FA, FW, OUT, 2, 2, 2, 2, k88 ? 1 : 2, k88 ? 3 : 2>(p, nb, per, s);
-  if (f == kSmaller) return tiled<FA, FW, OUT, 2, 2, 2, 2, k88 ? 1 : 2, 3>(p, nb, per, s);
+  if (f == kSmall3) return tiled<FA, FW, OUT, 2, 2, 2, 2, k88 ? 1 : 2, 3>(p, nb, per, s);
   if (f == kMiddle) return tiled<FA, FW, OUT, 4, 4, 2, 2, k44 ? 2 : 1, 2>(p, nb, per, s);
   if constexpr (k84)
     if (f == kWide) return tiled<FA, FW, OUT, 4, 8, 2, 2, 1, 2>(p, nb, per, s);
@@ -605,8 +685,9 @@ Plan plan_of(int a_fmt, int w_fmt, uint64_t m, uint64_t n, uint64_t k) {
     return {a_fmt == FP8 && w_fmt == FP4X2 && wide_rounds < rounds ? kWide : kLarge, steps, 1};
   }
   if (tiles(128, 128) >= 200) return {kMiddle, steps, 1};
-  if (t > 512) return {kSmaller, steps, 1};
-  const uint32_t pieces = t >= 256 ? 1 : uint32_t(256 / t);
+  if (t > 512) return {kSmall3, steps, 1};
+  if (t > 256) return {kSmall, steps, 1};
+  const uint32_t pieces = uint32_t(256 / t);
   const uint32_t per = ((steps + pieces - 1) / pieces + 3) & ~3u;  // whole fours: their scales are copied together
   if (steps <= per + 20) return {kSmall, steps, 1};
   return {kSmall, per, (steps + per - 1) / per};  // none is empty
@@ -617,9 +698,9 @@ uint64_t part_bytes(const Plan &plan, uint64_t m, uint64_t n) {
   return plan.pieces > 1 ? align16(plan.pieces * m * padded(n) * 4) : 0;
 }
 
-template <int FA, int FW, int OUT, int MT, int KS>
+template <int FA, int FW, int OUT, int MT, int NT, int KS>
 hipError_t few_form(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
-  const uint64_t nt = (p.n + 15) / 16, mt = (p.m + 16 * MT - 1) / (16 * MT);
+  const uint64_t nt = (p.n + 16 * NT - 1) / (16 * NT), mt = (p.m + 16 * MT - 1) / (16 * MT);
   for (uint64_t y = 0; y < mt; y += 65535) {  // the grid's limit
     MxMatmulArgs q = p;
     const uint64_t rows = y * 16 * MT;
@@ -627,17 +708,23 @@ hipError_t few_form(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
     q.as += rows * nb;
     q.out += rows * p.out_stride * esize(OUT);
     q.m -= rows;
-    k_mx_few<FA, FW, OUT, MT, KS><<<dim3(uint32_t(nt), uint32_t(mt - y < 65535 ? mt - y : 65535)), 64 * KS, 0, s>>>(q, nb);
+    k_mx_few<FA, FW, OUT, MT, NT, KS><<<dim3(uint32_t(nt), uint32_t(mt - y < 65535 ? mt - y : 65535)), 64 * KS, 0, s>>>(q, nb);
   }
   return hipGetLastError();
 }
 template <int FA, int FW, int OUT>
 hipError_t few(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
-  const uint32_t mt = p.m <= 16 ? 1 : p.m <= 32 ? 2 : p.m <= 48 ? 3 : 4;
-  if (mt == 1) return few_form<FA, FW, OUT, 1, 8>(p, nb, s);
-  if (mt == 2) return few_form<FA, FW, OUT, 2, 8>(p, nb, s);
-  if (mt == 3) return few_form<FA, FW, OUT, 3, 8>(p, nb, s);
-  return few_form<FA, FW, OUT, 4, 8>(p, nb, s);
+  if (p.m > 16) return few_form<FA, FW, OUT, 4, 1, 8>(p, nb, s);  // what the tiled form cannot address
+  // Weight tiles of a wave: more of them share the activations' loads, fewer
+  // leave more workgroups.  FP8 by FP4, in us with 1, 2, 4 tiles:
+  //   1 x 28672 x 4096   13.6 14.3 13.1     16 x 28672 x 4096  23.8 19.8 15.7
+  //   1 x 14336 x 4096    8.8  8.0  8.3     16 x 14336 x 4096  14.8 11.1  9.2
+  //   1 x  4096 x 4096    3.6  5.2  7.6     16 x  4096 x 14336 12.6 15.9 22.7
+  //   1 x  6144 x 4096    5.1  5.3          16 x  6144 x 4096   8.0  6.6
+  const uint64_t nt = (p.n + 15) / 16;
+  if (nt >= 1536 || (p.m > 4 && nt >= 768)) return few_form<FA, FW, OUT, 1, 4, 8>(p, nb, s);
+  if (nt >= (p.m > 4 ? 384 : 512)) return few_form<FA, FW, OUT, 1, 2, 8>(p, nb, s);
+  return few_form<FA, FW, OUT, 1, 1, 8>(p, nb, s);
 }
 
 template <int FA, int FW, int OUT>
