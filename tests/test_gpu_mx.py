@@ -307,7 +307,8 @@ def up(c, fmt):
 
 PRODUCTS = [(1, 1, 32), (1, 16, 128), (1, 100, 96), (2, 17, 160), (15, 33, 352), (16, 64, 512), (17, 300, 2016),
             (33, 31, 1056), (48, 130, 4096), (64, 128, 1024), (65, 1000, 224), (100, 257, 3104), (128, 128, 128),
-            (129, 255, 640), (200, 513, 1120), (256, 256, 256), (257, 300, 2016), (513, 770, 416), (1000, 1030, 1184)]
+            (129, 255, 640), (200, 513, 1120), (256, 256, 256), (257, 300, 2016), (513, 770, 416), (1000, 1030, 1184),
+            (1025, 2300, 160), (2049, 1700, 384), (3600, 3650, 288), (4096, 3800, 512)]
 
 
 @pytest.mark.parametrize("fmts", ["fp8 fp8", "fp8 fp4", "fp4 fp8", "fp4 fp4"])
@@ -347,6 +348,22 @@ def test_product_of_random_numbers(size, fmts):
     assert (np.abs(f64(zn.mx_matmul(*args)) - want) <= bound + 2.0 ** -8 * (np.abs(want) + bound)).all()
 
 
+@pytest.mark.parametrize("fmts", ["fp8 fp8", "fp8 fp4", "fp4 fp8"])
+@pytest.mark.parametrize("size", [(1, 80), (40, 80), (300, 80), (1030, 2050), (2600, 2570)])
+def test_product_fp32_keeps_what_lies_far_below_a_neighbour(size, fmts):
+    # every eighth product is 256, the others 2^-8, 16 bits below: the sum of 256
+    # of them, 8192.875, and every partial sum have at most 22 bits
+    (m, n), (fa, fw) = size, fmts.split()
+    k = 256
+    far = np.where(np.arange(k) % 8 == 0, 0x78, 0x02).astype(np.uint8)
+    one8, one4 = np.full(k, 0x38, np.uint8), np.full(k // 2, 0x22, np.uint8)
+    a = np.tile(far if fa == "fp8" else one4, (m, 1))
+    w = np.tile((one8 if fa == "fp8" else far) if fw == "fp8" else one4, (n, 1))
+    sa, sw = (torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda") for r in (m, n))
+    got = zn.mx_matmul(up(a, fa), sa, up(w, fw), sw, dtype=torch.float32)
+    assert bool((got == 8192.875).all())
+
+
 @pytest.mark.parametrize("size", [(3, 40, 224), (300, 300, 224)])
 def test_product_scales_of_all_sizes(size):
     # one nonzero block a row: products of the extreme scales, which leave FP32's range at both ends
@@ -383,6 +400,34 @@ def test_product_nans_stay_in_their_rows(size, fmts):
         bad[:, 3] = True
     assert np.isnan(got[bad]).all()
     np.testing.assert_array_equal(got[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_product_scales_at_any_address(m):
+    # k a multiple of 512 (scale rows of 16 bytes) and not, scale bytes one past an aligned address
+    for k in (512, 96):
+        (a, sa), (w, sw) = whole(m, k, "fp8", 3), whole(50, k, "fp4", 4)
+        off = []
+        for s in (sa, sw):
+            b = torch.zeros(s.size + 1, dtype=torch.uint8, device="cuda")
+            b[1:] = torch.from_numpy(s.reshape(-1)).cuda()
+            off.append(b[1:].view(s.shape))
+        got = zn.mx_matmul(up(a, "fp8"), off[0], up(w, "fp4"), off[1], dtype=torch.float32)
+        np.testing.assert_array_equal(f64(got), mx.matmul(mx.values(a, sa, "fp8"), mx.values(w, sw, "fp4")))
+
+
+def test_product_takes_the_scratch_it_asks_for():
+    m, n, k = 40, 300, 8224           # pieces of k and scale rows of 257 bytes
+    need = zn.mx_matmul_scratch_bytes(zn.FP8_E4M3, zn.FP4X2_E2M1, m, n, k)
+    assert need > 0
+    (a, sa), (w, sw) = whole(m, k, "fp8", 3), whole(n, k, "fp4", 4)
+    args = (up(a, "fp8"), torch.from_numpy(sa).cuda(), up(w, "fp4"), torch.from_numpy(sw).cuda())
+    buf = torch.full((need + 64,), 0x55, dtype=torch.uint8, device="cuda")
+    got = zn.mx_matmul(*args, dtype=torch.float32, scratch=buf[:need])
+    np.testing.assert_array_equal(f64(got), mx.matmul(mx.values(a, sa, "fp8"), mx.values(w, sw, "fp4")))
+    assert bool((buf[need:] == 0x55).all())
+    with pytest.raises(zn.ZnError):
+        zn.mx_matmul(*args, scratch=buf[:need - 1])
 
 
 def test_product_shapes_and_empty_sides():
