@@ -671,17 +671,22 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
 // the caller's are not, both sides are laid out in the scratch first, scale 1
 // after the row's end.
 __host__ __device__ constexpr uint32_t pitch_of(uint32_t nb) { return (nb + 15) & ~15u; }
-__global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, FastDiv dwords, uint64_t count) {
-  const uint64_t base = uint64_t(blockIdx.y) << 30, i = base + uint64_t(blockIdx.x) * 256 + threadIdx.x;
+__global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, uint32_t per_row, uint64_t count) {
+  const uint64_t i = (uint64_t(blockIdx.y) << 30) + uint64_t(blockIdx.x) * 256 + threadIdx.x;
   if (i >= count) return;
-  // rows past 2^31 dwords are reached by whole blocks of rows: 64-bit division there
-  const uint64_t row = count < 0x7FFFFFFFull ? dwords.div(uint32_t(i)) : i / dwords.d;
-  const uint32_t b = uint32_t(i - row * dwords.d) * 4;
-  const uint8_t *from = row < p.m ? p.as + row * nb : p.ws + (row - p.m) * nb;
-  uint32_t v = 0;
+  const uint64_t row = count < (1ull << 32) ? uint32_t(i) / per_row : i / per_row;
+  const uint32_t b = uint32_t(i - row * per_row) * 16;
+  const uint8_t *from = (row < p.m ? p.as + row * nb : p.ws + (row - p.m) * nb) + b;
+  u32x4 v;
+  if (b + 16 <= nb) {
+    v = *reinterpret_cast<const u32x4_byte *>(from);
+  } else {
+    uint8_t t[16];
 #pragma unroll
-  for (uint32_t j = 0; j < 4; j++) v |= (b + j < nb ? uint32_t(from[b + j]) : 127u) << (8 * j);
-  *reinterpret_cast<uint32_t *>(p.scratch + 4 * i) = v;
+    for (uint32_t j = 0; j < 16; j++) t[j] = b + j < nb ? from[j] : 127;
+    v = __builtin_bit_cast(u32x4, t);
+  }
+  *reinterpret_cast<u32x4 *>(p.scratch + 16 * i) = v;
 }
 
 // The pieces' sums, joined in their order: four n a lane.
@@ -762,8 +767,8 @@ hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, 
 //    in 4 pieces, 28 in one; 128 x 4096 x 4096 10.0 in one, 11.1 in two.
 Plan plan_of(int a_fmt, int w_fmt, bool fine, uint64_t m, uint64_t n, uint64_t k) {
   const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
-  // offsets inside a tile are 32-bit, and so are the tiles' numbers
-  if (m <= 16 || nb > (1u << 18) || m * n >= (1ull << 42)) return {kFew, steps, 1};
+  // offsets inside a tile stay below 2^31, and so do the tiles' numbers
+  if (m <= 16 || nb > (1u << 16) || m * n >= (1ull << 42)) return {kFew, steps, 1};
   const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
   const uint64_t large = tiles(256, 256), t = tiles(64, 64);
   if (large >= 200 && !fine) {
@@ -827,9 +832,9 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
     if (nb % 16) {
       const uint32_t pitch = pitch_of(nb);
       q.scratch = p.scratch + part_bytes(plan, p.m, p.n);
-      const uint64_t count = (p.m + p.n) * (pitch / 4);
+      const uint64_t count = (p.m + p.n) * (pitch / 16);
       const uint32_t x = uint32_t((count < (1ull << 30) ? count + 255 : 1ull << 30) / 256);
-      k_mx_pitch<<<dim3(x, uint32_t(((count - 1) >> 30) + 1)), 256, 0, s>>>(q, nb, FastDiv(pitch / 4), count);
+      k_mx_pitch<<<dim3(x, uint32_t(((count - 1) >> 30) + 1)), 256, 0, s>>>(q, nb, pitch / 16, count);
       q.as = q.scratch;
       q.ws = q.scratch + p.m * pitch;
     }

@@ -308,7 +308,7 @@ def up(c, fmt):
 PRODUCTS = [(1, 1, 32), (1, 16, 128), (1, 100, 96), (2, 17, 160), (15, 33, 352), (16, 64, 512), (17, 300, 2016),
             (33, 31, 1056), (48, 130, 4096), (64, 128, 1024), (65, 1000, 224), (100, 257, 3104), (128, 128, 128),
             (129, 255, 640), (200, 513, 1120), (256, 256, 256), (257, 300, 2016), (513, 770, 416), (1000, 1030, 1184),
-            (1025, 2300, 160), (2049, 1700, 384), (3600, 3650, 288), (4096, 3800, 512)]
+            (1025, 2300, 160), (2049, 1700, 384), (3600, 3650, 288), (4096, 3800, 512), (4300, 4090, 160)]
 
 
 @pytest.mark.parametrize("fmts", ["fp8 fp8", "fp8 fp4", "fp4 fp8", "fp4 fp4"])
@@ -428,6 +428,16 @@ def test_product_takes_the_scratch_it_asks_for():
     assert bool((buf[need:] == 0x55).all())
     with pytest.raises(zn.ZnError):
         zn.mx_matmul(*args, scratch=buf[:need - 1])
+
+
+@pytest.mark.parametrize("m", [1, 20])
+def test_product_of_very_long_rows(m):
+    # rows past what a tile addresses; ones by ones, a sum of at most 24 bits
+    k, n = (1 << 21) + 32, 17
+    a = torch.full((m, k), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    w = torch.full((n, k // 2), 0x22, dtype=torch.uint8, device="cuda")
+    sa, sw = (torch.full((r, k // 32), 127, dtype=torch.uint8, device="cuda") for r in (m, n))
+    assert bool((zn.mx_matmul(a, sa, w, sw, dtype=torch.float32) == k).all())
 
 
 def test_product_shapes_and_empty_sides():
