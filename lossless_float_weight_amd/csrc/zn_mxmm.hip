@@ -838,6 +838,28 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
       q.as = q.scratch;
       q.ws = q.scratch + p.m * pitch;
     }
+    // A last round of large tiles that would leave half the CUs idle or more is
+    // made of smaller ones: as many columns of tiles as fill whole rounds first,
+    // the other columns after them (FP4 by FP4, 4096 x 14336 x 4096, 3.5 rounds:
+    // 142.6 us for 148.2; 8192 x 9000 x 2048 113 for 127).  FP8 by FP4 has its wide
+    // tiles for this.
+    if (plan.form == kLarge) {
+      const uint64_t mt = (p.m + 255) / 256, total = mt * ((p.n + 255) / 256), left = total % 256;
+      const uint64_t first = (total - left) / mt * 256;  // n
+      if (total > 256 && left != 0 && left <= 128 && first > 0) {
+        const Plan rest = plan_of(FA, FW, kFine, p.m, p.n - first, p.k);
+        if (rest.form != kFew && rest.form != kLarge && rest.pieces == 1) {
+          MxMatmulArgs a = q, b = q;
+          a.n = first;
+          b.n -= first;
+          b.w += first * nb * code_bytes<FW>();
+          b.ws += first * pitch_of(nb);
+          b.out += first * esize(OUT);
+          const hipError_t e = tiled_form<FA, FW, OUT, kFine>(kLarge, a, nb, plan.per, s);
+          return e != hipSuccess ? e : tiled_form<FA, FW, OUT, kFine>(rest.form, b, nb, rest.per, s);
+        }
+      }
+    }
     if (plan.pieces == 1) return tiled_form<FA, FW, OUT, kFine>(plan.form, q, nb, plan.per, s);
     q.out = p.scratch;
     q.out_stride = padded(p.n);
