@@ -260,12 +260,6 @@ __device__ __forceinline__ void copy16_of(uint32_t lds, const uint8_t *base, uin
   asm volatile("s_mov_b32 m0, %0\n\ts_mov_b64 exec, %3\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1"
                ::"s"(lds), "v"(off), "s"(base), "s"(lanes) : "memory");
 }
-__device__ __forceinline__ void copy4(uint32_t lds, const uint8_t *base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
-}
-__device__ __forceinline__ void copy1(uint32_t lds, const uint8_t *base, uint32_t off) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_ubyte %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory");
-}
 template <int N>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
@@ -370,10 +364,10 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
   const uint32_t ra = wave * T::kRowsA + lane, rw = weight_row<OUT>(wave * T::kRowsW + lane);
   const uint32_t osa = (ra < mr ? ra : mr - 1) * pitch, osw = (rw < nr ? rw : nr - 1) * pitch;
   const uint32_t lds0 = lds_offset(lds);
-  // A last step of fewer blocks: the absent pieces of the activations
-  // are copied from zeros, those of the weights repeat the row's last block
-  // and the scales are 1.  A NaN that this multiplies by zero is one that the
-  // row has anyway.
+  // A last step of fewer blocks: the absent pieces of the activations are
+  // copied from zeros, those of the weights repeat the row's last block and the
+  // scales are 1.  A NaN that this multiplies by zero is one that the row has
+  // anyway.
   const uint32_t steps = (blocks + 4 * S - 1) / (4 * S), rest = blocks % (4 * S);
   const uint32_t q0 = wave * 64 + lane;  // the piece is the same in all of a wave's copies
   const uint32_t pa0 = LA::piece(q0 / LA::kPieces, q0 % LA::kPieces), pw0 = LW::piece(q0 / LW::kPieces, q0 % LW::kPieces);
@@ -429,8 +423,8 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
     else
       return operand<FP4X2>(x, x);
   };
-  // the scales of 128 k, number t, for 16 rows from `row` on, of A then W: a dword of the
-  // step's four blocks, shifted to the lane group's at its use
+  // the scales of 128 k, number t, for 16 rows from `row` on, of A then W: a
+  // dword of its four blocks, shifted to the lane group's at its use
   const auto scale = [&](uint32_t t, uint32_t row) {
     return *reinterpret_cast<const uint32_t *>(lds + kBuf * T::kStage + ((t >> 2) % T::kQuads) * T::kQuad + 4 * (t & 3) + 16 * r + 16 * row);
   };
@@ -639,8 +633,8 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
     }
     return;
   }
-  // tiles at the edges: 16 m of a wave at a
-  // time through LDS of its own, then one n a lane
+  // tiles at the edges: 16 m of a wave at a time through LDS of its own, then
+  // one n a lane
   barrier();
   constexpr uint32_t kLine = 16 * TN + 4;  // floats: rows of a column fall in different banks
   static_assert(T::kWaves * 16 * kLine * 4 <= kBuf * T::kStage, "edge rows");
