@@ -91,12 +91,13 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
   return top >= 0x7F800000u ? 255u : uint32_t(e < 0 ? 0 : e);
 }
 
-// Eight values times 2^(127 - s), rounded to nearest even and saturated:
-// 8 bytes of E4M3 or 4 bytes of E2M1 pairs (in the low word).  A block with
-// an infinity or a NaN (s = 255) gets codes 0.
+// 2^(127 - s), exact: s is at most 252 when the maximum is finite in FP32.
+__device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
+
+// Eight values times inv, rounded to nearest even and saturated: 8 bytes of
+// E4M3 or 4 bytes of E2M1 pairs (in the low word).
 template <int FMT>
-__device__ __forceinline__ u32x2 mx_codes8(const float (&v)[8], uint32_t s) {
-  const float inv = __uint_as_float((254u - (s < 254u ? s : 254u)) << 23);  // 2^(127 - s), exact; s <= 252 when finite
+__device__ __forceinline__ u32x2 mx_codes8(const float (&v)[8], float inv) {
   u32x2 c = {0, 0};
   if constexpr (FMT == FP8) {
     float q[8];
@@ -117,7 +118,6 @@ __device__ __forceinline__ u32x2 mx_codes8(const float (&v)[8], uint32_t s) {
     w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6] * inv, v[7] * inv, 1.0f, 3);
     c[0] = w;
   }
-  if (s == 255u) c = u32x2{0, 0};
   return c;
 }
 

@@ -86,9 +86,7 @@ __device__ __forceinline__ uint32_t top8(const float (&v)[8]) {
 // tensor whose groups are numbered through all rows.  The four lanes of a
 // quad hold one block.
 template <int FMT>
-__device__ __forceinline__ void put_codes(uint8_t *codes, uint8_t *scales, uint64_t gi, const float (&v)[8], bool live) {
-  const uint32_t s = mx_scale_byte<FMT>(quad_max(top8(v)));
-  const u32x2 c = mx_codes8<FMT>(v, s);
+__device__ __forceinline__ void put_codes(uint8_t *codes, uint8_t *scales, uint64_t gi, u32x2 c, uint32_t s, bool live) {
   if (!live) return;
   if constexpr (FMT == FP8)
     *reinterpret_cast<u32x2 *>(codes + 8 * gi) = c;
@@ -114,7 +112,12 @@ __global__ __launch_bounds__(256) void k_mx_quantize(MxQuantArgs a, FastDiv gpr,
     load8<DT>(a.x + row * a.x_stride * esize(DT), k0, uint32_t(a.k), v[u]);
   }
 #pragma unroll
-  for (int u = 0; u < U; u++) put_codes<FMT>(a.codes, a.scales, first + 256u * u, v[u], first + 256u * u < groups);
+  for (int u = 0; u < U; u++) {
+    const uint32_t s = mx_scale_byte<FMT>(quad_max(top8(v[u])));
+    // a block with an infinity or a NaN gets codes 0
+    const u32x2 c = s == 255u ? u32x2{0, 0} : mx_codes8<FMT>(v[u], mx_inverse(s));
+    put_codes<FMT>(a.codes, a.scales, first + 256u * u, c, s, first + 256u * u < groups);
+  }
 }
 
 // ------------------------------------------------------------------- read --
@@ -171,12 +174,17 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
 // The squares are summed in 64 bits, so no finite row overflows or vanishes,
 // and 1 / sqrt is split into a power of two and a 24-bit fraction for the
 // same reason: h is scaled by the power exactly before it meets the fraction.
+// y then has three FP32 roundings, under 2^-22, and a code or a scale that
+// could come out otherwise within 2^-21 of it is computed again in 64 bits: the
+// result is the 64-bit formula's, and the second way is taken by about one
+// group in 10,000.
 // One pass over memory with the row in registers: 8192 x 4096 BF16 with the
-// addition, 236 MB, 38 us in a row (6.2 TB/s with what the 256 MB cache holds),
-// 2.8 us for one row.
+// addition, 236 MB, FULL us in a row (RATE TB/s with what the 256 MB cache
+// holds), ONE us for one row.
 struct RowScale {
   int e;
   float m;
+  double sum;
 };
 __device__ __forceinline__ RowScale row_scale(double sum, double over_k, float eps) {
   const double a = sum * over_k + double(eps);
@@ -188,6 +196,47 @@ __device__ __forceinline__ RowScale row_scale(double sum, double over_k, float e
   RowScale s;
   s.e = __builtin_amdgcn_frexp_exp(r);
   s.m = float(__builtin_amdgcn_frexp_mant(r));
+  s.sum = sum;
+  return s;
+}
+
+// A 64-bit value in FP32, inexact ones to the odd neighbour: a later rounding to
+// fewer bits gives what it would have given from 64.
+__device__ __forceinline__ float to_odd(double v) {
+  float f = float(v);
+  const double d = double(f);
+  if (d != v) {
+    uint32_t b = __float_as_uint(f);
+    if (__builtin_fabs(d) > __builtin_fabs(v)) b -= 1;
+    f = __uint_as_float(b | 1u);
+  }
+  return f;
+}
+
+// Codes and scale of a group from the formula in 64 bits; all four lanes of a
+// quad come here together.
+template <int FMT>
+__device__ __forceinline__ uint32_t exact8(const MxNormArgs &a, double sum, const float (&h)[8], const float (&w)[8], u32x2 &c) {
+  constexpr int emax = FMT == FP8 ? 8 : 2;
+  const double q = __builtin_sqrt(sum / double(a.k) + double(a.eps));
+  // y is computed twice, and one value at a time, for the registers' sake
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    const double y = double(h[i]) / q * double(w[i]);
+    const uint32_t b = uint32_t(__double_as_longlong(y) >> 52) & 0x7FFu;  // only the exponent of the largest matters
+    top = top > b ? top : b;
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  const int e = int(quad_max(top)) - 1023 + 127 - emax;
+  const uint32_t s = uint32_t(e < 0 ? 0 : e > 254 ? 254 : e);
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) {
+    v[i] = to_odd(__builtin_amdgcn_ldexp(double(h[i]) / q * double(w[i]), 127 - int(s)));
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  c = mx_codes8<FMT>(v, 1.0f);
   return s;
 }
 
@@ -223,12 +272,24 @@ __device__ __forceinline__ double squares8(const float (&h)[8]) {
 }
 
 template <int FMT>
-__device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, RowScale s, const float (&h)[8],
+__device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, const RowScale &r, const float (&h)[8],
                                       const float (&w)[8], bool live) {
   float y[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_ldexpf(h[i], s.e) * s.m * w[i];
-  put_codes<FMT>(a.codes, a.scales, gi, y, live);
+  for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_ldexpf(h[i], r.e) * r.m * w[i];
+  const uint32_t top = quad_max(top8(y));
+  uint32_t s = mx_scale_byte<FMT>(top);
+  u32x2 c = {0, 0};
+  if (s != 255u) {
+    const float inv = mx_inverse(s), d = 0x1p-21f;
+    c = mx_codes8<FMT>(y, inv * (1.0f - d));
+    const u32x2 above = mx_codes8<FMT>(y, inv * (1.0f + d));
+    // a code between two, a maximum within 8 steps of a power of two, or one
+    // too small for FP32's full precision
+    const bool unsure = c[0] != above[0] || c[1] != above[1] || ((top + 8) ^ (top - 8)) >> 23 != 0 || top < (27u << 23);
+    if (quad_max(unsure && top != 0)) s = exact8<FMT>(a, r.sum, h, w, c);
+  }
+  put_codes<FMT>(a.codes, a.scales, gi, c, s, live);
 }
 
 // The sum over a workgroup; `slot` alternates between rows so that one barrier
@@ -246,7 +307,7 @@ __device__ __forceinline__ double group_sum(double s, double (*part)[16], int sl
 // Rows of at most CH groups of 8 a lane stay in registers; a workgroup has as
 // many waves as its row needs.  kFour: rows of one wave, four to a workgroup.
 template <int DT, int FMT, int CH, bool kFour>
-__global__ __launch_bounds__(kFour ? 256 : 1024) void k_mx_norm(MxNormArgs a, uint32_t gpr) {
+__global__ __launch_bounds__(kFour ? 256 : 1024, CH == 1 ? 6 : 1) void k_mx_norm(MxNormArgs a, uint32_t gpr) {
   __shared__ double part[2][16];
   const uint32_t t = kFour ? threadIdx.x & 63 : threadIdx.x, team = kFour ? 64 : blockDim.x;
   float w[CH][8];

@@ -3,11 +3,10 @@
 What is exact is compared bit by bit: the quantiser, reading back, the stored
 sum of the norm, and products whose terms and sums are small whole numbers.
 The rest is held to bounds derived here:
-  * norm: y reaches the quantiser with three FP32 roundings (the fraction of
-    1/sqrt, two products) and the 64-bit row sum's, under 2^-22 relative in
-    all, and rounding is monotone: the code lies between those of
-    y (1 - 2^-22) and y (1 + 2^-22) under the scale that was chosen, and that
-    scale between theirs;
+  * norm: codes and scales are those of the formula in 64 bits, up to its own
+    roundings (sums of another order, under 2^-40 relative for these rows), and
+    rounding is monotone: the code lies between those of y (1 - 2^-40) and
+    y (1 + 2^-40) under the scale that was chosen, and that scale between theirs;
   * product: every FP32 addition of the K terms and partial sums rounds (or
     cuts) by at most 2^-23 of a partial sum, which is at most the sum of the
     terms' magnitudes S: K 2^-23 S, and the output's rounding, half a step.
@@ -207,7 +206,7 @@ def test_dequantize_lengths_and_outputs(shape):
 # -------------------------------------------------------------------- norm --
 def between(y, fmt, codes, scales):
     """Codes and scales of y within the bounds of the module's text."""
-    d = 2.0 ** -22
+    d = 2.0 ** -40
     s = raw(scales).reshape(len(y), -1)
     b = mx.blocks(y)
     with np.errstate(invalid="ignore", over="ignore"):
@@ -237,7 +236,7 @@ def test_norm(shape, t, add):
     r = rounded(rng.normal(0, 1, shape), TYPE[t])
     w = rounded(1 + 0.3 * rng.normal(0, 1, k), TYPE[t])
     h = (x.float() + r.float()).to(TYPE[t]) if add else x
-    y = mx.rms_norm(f64(h), f64(w), 1e-5)
+    y = mx.rms_norm(f64(h), f64(w), float(np.float32(1e-5)))
     for fmt in FMT:
         codes, scales, got = zn.mx_rms_norm(x.cuda(), w.cuda(), residual=r.cuda() if add else None, eps=1e-5, fmt=FMT[fmt])
         assert torch.equal(got.cpu(), h)
@@ -253,7 +252,7 @@ def test_norm_in_place_and_views(t, k):
     w = rounded(rng.normal(1, 0.1, k), TYPE[t]).cuda()
     for x in (big[::2, 8:8 + k], big[::2, 3:3 + k], big[:6, :k]):
         c, s, h = zn.mx_rms_norm(x, w, residual=r)
-        between(mx.rms_norm(f64(h), f64(w), 1e-5), "fp8", c, s)
+        between(mx.rms_norm(f64(h), f64(w), float(np.float32(1e-5))), "fp8", c, s)
         for into in ("x", "residual"):
             a, b = big.clone(), r.clone()
             xa = torch.as_strided(a, x.shape, x.stride(), x.storage_offset())
