@@ -95,14 +95,15 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t top) {
 __device__ __forceinline__ float mx_inverse(uint32_t s) { return __uint_as_float((254u - s) << 23); }
 
 // Eight values times inv, rounded to nearest even and saturated: 8 bytes of
-// E4M3 or 4 bytes of E2M1 pairs (in the low word).
-template <int FMT>
+// E4M3 or 4 bytes of E2M1 pairs (in the low word).  Without kClamp the values
+// are known to be under 464.
+template <int FMT, bool kClamp = true>
 __device__ __forceinline__ u32x2 mx_codes8(const float (&v)[8], float inv) {
   u32x2 c = {0, 0};
   if constexpr (FMT == FP8) {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) q[i] = __builtin_amdgcn_fmed3f(v[i] * inv, -448.0f, 448.0f);
+    for (int i = 0; i < 8; i++) q[i] = kClamp ? __builtin_amdgcn_fmed3f(v[i] * inv, -448.0f, 448.0f) : v[i] * inv;
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);

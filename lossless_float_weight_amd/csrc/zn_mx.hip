@@ -175,12 +175,11 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
 // and 1 / sqrt is split into a power of two and a 24-bit fraction for the
 // same reason: h is scaled by the power exactly before it meets the fraction.
 // y then has three FP32 roundings, under 2^-22, and a code or a scale that
-// could come out otherwise within 2^-21 of it is computed again in 64 bits: the
-// result is the 64-bit formula's, and the second way is taken by about one
-// group in 10,000.
+// could come out otherwise is computed again in 64 bits: the result is the
+// 64-bit formula's, and the second way is taken by one or two groups in 10,000.
 // One pass over memory with the row in registers: 8192 x 4096 BF16 with the
-// addition, 236 MB, FULL us in a row (RATE TB/s with what the 256 MB cache
-// holds), ONE us for one row.
+// addition, 236 MB, 43 us in a row (5.5 TB/s with what the 256 MB cache holds),
+// 3.1 us for one row; without the second look it was 38 and 2.8.
 struct RowScale {
   int e;
   float m;
@@ -194,8 +193,11 @@ __device__ __forceinline__ RowScale row_scale(double sum, double over_k, float e
   const double n = __builtin_fma(0.5 * r, t, r);
   r = (a > 0 && a < __builtin_inf()) ? n : r;  // 0 gives infinity, infinity gives 0, a NaN stays
   RowScale s;
-  s.e = __builtin_amdgcn_frexp_exp(r);
-  s.m = float(__builtin_amdgcn_frexp_mant(r));
+  // the power is kept apart only where FP32 could not carry it
+  const int e = __builtin_amdgcn_frexp_exp(r);
+  const bool far = e < -60 || e > 60;
+  s.e = far ? e : 0;
+  s.m = far ? float(__builtin_amdgcn_frexp_mant(r)) : float(r);
   s.sum = sum;
   return s;
 }
@@ -216,28 +218,25 @@ __device__ __forceinline__ float to_odd(double v) {
 // Codes and scale of a group from the formula in 64 bits; all four lanes of a
 // quad come here together.
 template <int FMT>
-__device__ __forceinline__ uint32_t exact8(const MxNormArgs &a, double sum, const float (&h)[8], const float (&w)[8], u32x2 &c) {
+__device__ __forceinline__ u32x2 exact8(const MxNormArgs &a, double sum, const float (&h)[8], const float (&w)[8], uint32_t &s) {
   constexpr int emax = FMT == FP8 ? 8 : 2;
-  const double q = __builtin_sqrt(sum / double(a.k) + double(a.eps));
-  // y is computed twice, and one value at a time, for the registers' sake
-  uint32_t top = 0;
+  const double q = __builtin_sqrt(sum / double(a.k) + double(a.eps)), over = 1.0 / q;
+  double y[8];
+  uint32_t top = 0;  // the exponent of the largest
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    const double y = double(h[i]) / q * double(w[i]);
-    const uint32_t b = uint32_t(__double_as_longlong(y) >> 52) & 0x7FFu;  // only the exponent of the largest matters
+    // h / q by its reciprocal and one correction
+    const double x = double(h[i]), t = x * over;
+    y[i] = __builtin_fma(__builtin_fma(-t, q, x), over, t) * double(w[i]);
+    const uint32_t b = uint32_t(__double_as_longlong(y[i]) >> 52) & 0x7FFu;
     top = top > b ? top : b;
-    __builtin_amdgcn_sched_barrier(0);
   }
   const int e = int(quad_max(top)) - 1023 + 127 - emax;
-  const uint32_t s = uint32_t(e < 0 ? 0 : e > 254 ? 254 : e);
+  s = uint32_t(e < 0 ? 0 : e > 254 ? 254 : e);
   float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; i++) {
-    v[i] = to_odd(__builtin_amdgcn_ldexp(double(h[i]) / q * double(w[i]), 127 - int(s)));
-    __builtin_amdgcn_sched_barrier(0);
-  }
-  c = mx_codes8<FMT>(v, 1.0f);
-  return s;
+  for (int i = 0; i < 8; i++) v[i] = to_odd(__builtin_amdgcn_ldexp(y[i], 127 - int(s)));
+  return mx_codes8<FMT>(v, 1.0f);
 }
 
 template <int DT>
@@ -275,19 +274,30 @@ template <int FMT>
 __device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, const RowScale &r, const float (&h)[8],
                                       const float (&w)[8], bool live) {
   float y[8];
+  if (r.e) {
 #pragma unroll
-  for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_ldexpf(h[i], r.e) * r.m * w[i];
+    for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_ldexpf(h[i], r.e) * r.m * w[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++) y[i] = h[i] * r.m * w[i];
+  }
   const uint32_t top = quad_max(top8(y));
   uint32_t s = mx_scale_byte<FMT>(top);
   u32x2 c = {0, 0};
   if (s != 255u) {
-    const float inv = mx_inverse(s), d = 0x1p-21f;
-    c = mx_codes8<FMT>(y, inv * (1.0f - d));
-    const u32x2 above = mx_codes8<FMT>(y, inv * (1.0f + d));
-    // a code between two, a maximum within 8 steps of a power of two, or one
-    // too small for FP32's full precision
-    const bool unsure = c[0] != above[0] || c[1] != above[1] || ((top + 8) ^ (top - 8)) >> 23 != 0 || top < (27u << 23);
-    if (quad_max(unsure && top != 0)) s = exact8<FMT>(a, r.sum, h, w, c);
+    const float inv = mx_inverse(s);
+    if constexpr (FMT == FP8) {  // saturated before it is scaled, once for both
+      const float most = 448.0f * mx_scale_value(s);
+#pragma unroll
+      for (int i = 0; i < 8; i++) y[i] = __builtin_amdgcn_fmed3f(y[i], -most, most);
+    }
+    // y and its product with the scale are off by at most 4 x 2^-24
+    c = mx_codes8<FMT, false>(y, inv * (1.0f - 5 * 0x1p-24f));
+    const u32x2 above = mx_codes8<FMT, false>(y, inv * (1.0f + 6 * 0x1p-24f));
+    // in doubt: a maximum within 8 steps of a power of two or too small for
+    // FP32's full precision, or a code between two
+    const bool scale = (((top + 8) ^ (top - 8)) >> 23 != 0 || top < (27u << 23)) && top != 0;
+    if (quad_max(scale || c[0] != above[0] || c[1] != above[1])) c = exact8<FMT>(a, r.sum, h, w, s);
   }
   put_codes<FMT>(a.codes, a.scales, gi, c, s, live);
 }
@@ -405,10 +415,10 @@ template <int DT, int FMT>
 hipError_t norm(const MxNormArgs &a, hipStream_t s) {
   const uint32_t gpr = uint32_t((a.k + kMxBlock - 1) / kMxBlock * 4);
   const uint32_t grid = uint32_t(a.rows < 4096 ? a.rows : 4096);
-  // One group of 8 a lane wherever 1024 lanes are enough: against two a lane it
-  // took, at 8192 x 4096 BF16 with the addition, 36.1 us for 37.7 (2.8 for 3.5
-  // on a single row), and at 4096 x 8192 38.9 for 42.2.  Waves as needed and no
-  // power of two of them: 613 x 5003 FP32 6.6 us for 7.2.
+  // One group of 8 a lane wherever 1024 lanes are enough: two a lane took, at
+  // 8192 x 4096 BF16 with the addition, 4% longer (a single row 25%), and at
+  // 4096 x 8192 8%.  Waves as needed and no power of two of them: 613 x 5003 FP32
+  // 8% shorter.
   if (gpr <= 64)
     k_mx_norm<DT, FMT, 1, true><<<uint32_t((a.rows + 3) / 4 < 4096 ? (a.rows + 3) / 4 : 4096), 256, 0, s>>>(a, gpr);
   else if (gpr <= 1024)
