@@ -47,7 +47,7 @@ hipError_t launch_mx_quantize(int in_dtype, int fmt, const MxQuantArgs &a, hipSt
 hipError_t launch_mx_dequantize(int fmt, int out_dtype, const MxDequantArgs &a, hipStream_t s);
 hipError_t launch_mx_norm(int dtype, int fmt, const MxNormArgs &a, hipStream_t s);
 uint64_t mx_matmul_scratch(int a_fmt, int w_fmt, uint64_t m, uint64_t n, uint64_t k);
-hipError_t launch_mx_matmul(int a_fmt, int w_fmt, int out_dtype, const MxMatmulArgs &a, hipStream_t s);
+hipError_t launch_mx_matmul(int a_fmt, int w_fmt, int out_dtype, bool fast, const MxMatmulArgs &a, hipStream_t s);
 
 // ------------------------------------------------------------ device side --
 

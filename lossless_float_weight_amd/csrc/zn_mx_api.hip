@@ -97,6 +97,16 @@ extern "C" zn_status zn_mx_matmul(zn_dtype a_fmt, const void *d_a, const void *d
                                   const void *d_w, const void *d_w_scales, uint64_t m, uint64_t n, uint64_t k,
                                   zn_dtype out_dtype, void *d_out, uint64_t out_stride, void *d_scratch,
                                   uint64_t scratch_bytes, hipStream_t stream) {
+  return zn_mx_matmul2(a_fmt, d_a, d_a_scales, w_fmt, d_w, d_w_scales, m, n, k, 0, out_dtype, d_out, out_stride,
+                       d_scratch, scratch_bytes, stream);
+}
+
+extern "C" zn_status zn_mx_matmul2(zn_dtype a_fmt, const void *d_a, const void *d_a_scales, zn_dtype w_fmt,
+                                   const void *d_w, const void *d_w_scales, uint64_t m, uint64_t n, uint64_t k,
+                                   uint32_t flags, zn_dtype out_dtype, void *d_out, uint64_t out_stride,
+                                   void *d_scratch, uint64_t scratch_bytes, hipStream_t stream) {
+  if (flags & ~uint32_t(ZN_MX_FAST_SUMS)) return ZN_ERR_ARG;
+  if (flags && out_dtype != ZN_BF16) return ZN_ERR_ARG;
   uint64_t need;
   const zn_status st = zn_mx_matmul_scratch_bytes(a_fmt, w_fmt, m, n, k, &need);
   if (st != ZN_OK) return st;
@@ -116,5 +126,5 @@ extern "C" zn_status zn_mx_matmul(zn_dtype a_fmt, const void *d_a, const void *d
   p.out = static_cast<uint8_t *>(d_out);
   p.out_stride = out_stride;
   p.scratch = static_cast<uint8_t *>(d_scratch);
-  return done(launch_mx_matmul(a_fmt, w_fmt, out_dtype, p, stream));
+  return done(launch_mx_matmul(a_fmt, w_fmt, out_dtype, flags & ZN_MX_FAST_SUMS, p, stream));
 }

@@ -78,6 +78,7 @@ def lib() -> C.CDLL:
         L.zn_mx_rms_norm.argtypes = [I, P, U64, P, U64, P, C.c_float, U64, U64, P, U64, I, P, P, P]
         L.zn_mx_matmul_scratch_bytes.argtypes = [I, I, U64, U64, U64, PU64]
         L.zn_mx_matmul.argtypes = [I, P, P, I, P, P, U64, U64, U64, I, P, U64, P, U64, P]
+        L.zn_mx_matmul2.argtypes = [I, P, P, I, P, P, U64, U64, U64, U32, I, P, U64, P, U64, P]
         for f in ("zn_setup", "zn_setup_transfer", "zn_plan_from_container", "zn_header_info",
                   "zn_tableset_info", "zn_compress_bound",
                   "zn_scratch_bytes", "zn_compress", "zn_decompress", "zn_decompress_noalloc",
@@ -85,7 +86,7 @@ def lib() -> C.CDLL:
                   "zn_tableset_load", "zn_tableset_lengths", "zn_tableset_map",
                   "zn_tableset_cost_history", "zn_debug_histograms", "zn_debug_code_lengths",
                   "zn_debug_kernel_events", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
-                  "zn_mx_matmul_scratch_bytes", "zn_mx_matmul"):
+                  "zn_mx_matmul_scratch_bytes", "zn_mx_matmul", "zn_mx_matmul2"):
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -402,6 +403,7 @@ def decompress_noalloc(ts: Tableset, blob: torch.Tensor, outs: Sequence[torch.Te
 # with one E8M0 scale byte (torch.float8_e8m0fnu, or the same as uint8) for
 # every 32 values; the last axis is the row, filled up to whole blocks.
 MX_BLOCK = 32
+MX_FAST_SUMS = 1
 _MX_FMT = {torch.float8_e4m3fn: FP8_E4M3, torch.uint8: FP4X2_E2M1}
 _MX_PLAIN = {torch.bfloat16: BF16, torch.float32: FP32}
 _MX_SCALE = (torch.float8_e8m0fnu, torch.uint8)
@@ -624,9 +626,11 @@ def mx_matmul_scratch_bytes(a_fmt: int, w_fmt: int, m: int, n: int, k: int) -> i
 
 def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor,
               dtype=torch.bfloat16, out: torch.Tensor | None = None, scratch: torch.Tensor | None = None,
-              stream=None) -> torch.Tensor:
+              stream=None, fast_sums: bool = False) -> torch.Tensor:
     """zn_mx_matmul: a [..., k] by the rows of w [n, k], both microscaled (FP8
-    or FP4 each), as BF16 or FP32 [..., n]."""
+    or FP4 each), as BF16 or FP32 [..., n], summed in FP32.  fast_sums
+    (zn_mx_matmul2 with ZN_MX_FAST_SUMS, BF16 only) adds FP8 products by the
+    scaled matrix instruction: faster, with fewer bits."""
     where = "mx_matmul"
     fa, k, lead = _mx_packed(where, "a", a, a_scales)
     fw, kw, wlead = _mx_packed(where, "w", w, w_scales)
@@ -635,13 +639,15 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     dev = _mx_device(where, stream, a, a_scales, w, w_scales, out, scratch)
     n = wlead[0]
     out, dt, m, stride = _mx_out(where, lead, n, dtype, out, dev, stream)
+    if fast_sums and dt != BF16:
+        raise ZnError(-1, f"{where}: fast_sums is for bfloat16 results, not {out.dtype}")
     need = mx_matmul_scratch_bytes(fa, fw, m, n, k)
     if scratch is None:
         scratch = _mx_new(torch.uint8, dev, stream, need) if need else None
     elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
         raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
-    _mx_call(where, dev, stream, lib().zn_mx_matmul, fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(),
-             w_scales.data_ptr(), m, n, k, dt, out.data_ptr(), stride,
+    _mx_call(where, dev, stream, lib().zn_mx_matmul2, fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(),
+             w_scales.data_ptr(), m, n, k, MX_FAST_SUMS if fast_sums else 0, dt, out.data_ptr(), stride,
              scratch.data_ptr() if scratch is not None else None, scratch.numel() if scratch is not None else 0)
     if stream is not None:
         _mx_use(stream, a, a_scales, w, w_scales, out, scratch)

@@ -1,0 +1,28 @@
+"""More refusals of the microscaled operators, on the CPU."""
+import os
+
+import pytest
+import torch
+
+from lossless_float_weight_amd import zn
+from test_mx_abi import ARG, CAPACITY, FP32, FP8, LIB, MATMUL, P, _with
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libzn.so not built")
+
+
+def matmul2(**change):
+    args = dict(MATMUL, **{k: v for k, v in change.items() if k != "flags"})
+    a = list(args.values())
+    return zn.lib().zn_mx_matmul2(*a[:9], change.get("flags", 0), *a[9:])
+
+
+def test_flags_of_the_product():
+    assert matmul2() == 0 and matmul2(flags=zn.MX_FAST_SUMS) == 0          # no rows: nothing is launched
+    assert matmul2(dtype=FP32) == 0
+    for bad in (dict(flags=2), dict(flags=1 << 31), dict(flags=3), dict(flags=1, dtype=FP32), dict(flags=1, dtype=FP8),
+                dict(flags=1, m=1, a=None), dict(flags=1, m=1, out=P + 1), dict(flags=1, k=48)):
+        assert matmul2(**bad) == ARG
+    need = zn.mx_matmul_scratch_bytes(zn.FP8_E4M3, zn.FP4X2_E2M1, 48, 4096, 14336)
+    size = dict(flags=1, m=48, n=4096, k=14336, stride=4096, scratch=P)
+    assert need > 0 and matmul2(**size, bytes=need - 1) == CAPACITY
+    assert zn.lib().zn_mx_matmul(*_with(MATMUL)) == 0
