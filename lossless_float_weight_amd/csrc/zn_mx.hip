@@ -223,9 +223,9 @@ __device__ __forceinline__ u32x2 exact8(const MxNormArgs &a, double sum, const f
   uint32_t top = 0;  // the exponent of the largest
 #pragma unroll
   for (int i = 0; i < 8; i++) {
-    // h / q by its reciprocal and one correction
+    // h / q by its reciprocal and one correction, which would make -0 a +0
     const double x = double(h[i]), t = x * over;
-    y[i] = __builtin_fma(__builtin_fma(-t, q, x), over, t) * double(w[i]);
+    y[i] = __builtin_copysign(__builtin_fma(__builtin_fma(-t, q, x), over, t), x) * double(w[i]);
     const uint32_t b = uint32_t(__double_as_longlong(y[i]) >> 52) & 0x7FFu;
     top = top > b ? top : b;
   }
