@@ -175,6 +175,11 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
 // y then has three FP32 roundings, under 2^-22, and a code or a scale that
 // could come out otherwise is computed again in 64 bits: the result is the
 // 64-bit formula's, and the second way is taken by one or two groups in 10,000.
+// So are blocks that FP32 cannot hold: |y| past 2^128, or h / rms under 2^-126,
+// where it has fewer bits, if that can matter.  It cannot where the block's
+// maximum is at least kLow = 2^-80 and |w| under kWide = 2^24: codes change at
+// multiples of 2^-98 then (2^-10 of a scale of at least 2^-88), and y has
+// passed 2^-122 before the weight there.
 // One pass over memory with the row in registers: 8192 x 4096 BF16 with the
 // addition, 236 MB, 41 us in a row (5.7 TB/s with what the 256 MB cache holds),
 // 3.1 us for one row; without the second look it was 38 and 2.8.
@@ -229,8 +234,10 @@ __device__ __forceinline__ u32x2 exact8(const MxNormArgs &a, double sum, const f
     const uint32_t b = uint32_t(__double_as_longlong(y[i]) >> 52) & 0x7FFu;
     top = top > b ? top : b;
   }
-  const int e = int(quad_max(top)) - 1023 + 127 - emax;
-  s = uint32_t(e < 0 ? 0 : e > 254 ? 254 : e);
+  top = quad_max(top);
+  const int e = int(top) - 1023 + 127 - emax;
+  s = top == 0x7FFu ? 255u : uint32_t(e < 0 ? 0 : e > 254 ? 254 : e);
+  if (s == 255u) return u32x2{0, 0};
   float v[8];
 #pragma unroll
   for (int i = 0; i < 8; i++) v[i] = to_odd(__builtin_amdgcn_ldexp(y[i], 127 - int(s)));
@@ -268,9 +275,12 @@ __device__ __forceinline__ double squares8(const float (&h)[8]) {
   return s;
 }
 
+constexpr uint32_t kLow = uint32_t(127 - 80) << 23, kWide = uint32_t(127 + 24) << 23;
+
+// `wide`: one of this lane's weights is kWide or more, an infinity or a NaN.
 template <int FMT>
 __device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, const RowScale &r, const float (&h)[8],
-                                      const float (&w)[8], bool live) {
+                                      const float (&w)[8], bool wide, bool live) {
   float y[8];
   if (r.e) {
 #pragma unroll
@@ -282,6 +292,7 @@ __device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, const Ro
   const uint32_t top = quad_max(top8(y));
   uint32_t s = mx_scale_byte<FMT>(top);
   u32x2 c = {0, 0};
+  bool again = true;
   if (s != 255u) {
     const float inv = mx_inverse(s);
     if constexpr (FMT == FP8) {  // saturated before it is scaled, once for both
@@ -292,11 +303,14 @@ __device__ __forceinline__ void norm8(const MxNormArgs &a, uint64_t gi, const Ro
     // y and its product with the scale are off by at most 4 x 2^-24
     c = mx_codes8<FMT, false>(y, inv * (1.0f - 5 * 0x1p-24f));
     const u32x2 above = mx_codes8<FMT, false>(y, inv * (1.0f + 6 * 0x1p-24f));
-    // in doubt: a maximum within 8 steps of a power of two or too small for
-    // FP32's full precision, or a code between two
-    const bool scale = (((top + 8) ^ (top - 8)) >> 23 != 0 || top < (27u << 23)) && top != 0;
-    if (quad_max(scale || c[0] != above[0] || c[1] != above[1])) c = exact8<FMT>(a, r.sum, h, w, s);
+    // in doubt: a maximum within 8 steps of a power of two or too small, a code
+    // between two, a wide weight; nothing but zeros only where h has no others
+    bool block = ((top + 8) ^ (top - 8)) >> 23 != 0 || top < kLow;
+    if (top == 0) block = top8(h) != 0;
+    again = quad_max(block || wide || c[0] != above[0] || c[1] != above[1]);
   }
+  // a row that holds an infinity or a NaN has only zeros and NaNs, as they are
+  if (again && r.sum < __builtin_inf()) c = exact8<FMT>(a, r.sum, h, w, s);
   put_codes<FMT>(a.codes, a.scales, gi, c, s, live);
 }
 
@@ -319,8 +333,12 @@ __global__ __launch_bounds__(kFour ? 256 : 1024, CH == 1 ? 6 : 1) void k_mx_norm
   __shared__ double part[2][16];
   const uint32_t t = kFour ? threadIdx.x & 63 : threadIdx.x, team = kFour ? 64 : blockDim.x;
   float w[CH][8];
+  bool wide = false;
 #pragma unroll
-  for (int c = 0; c < CH; c++) load8<DT>(a.w, (c * team + t) * 8, uint32_t(a.k), w[c]);
+  for (int c = 0; c < CH; c++) {
+    load8<DT>(a.w, (c * team + t) * 8, uint32_t(a.k), w[c]);
+    wide |= top8(w[c]) >= kWide;
+  }
   int slot = 0;
   const uint64_t step = uint64_t(gridDim.x) * (kFour ? 4 : 1);
   for (uint64_t row = uint64_t(blockIdx.x) * (kFour ? 4 : 1) + (kFour ? threadIdx.x >> 6 : 0); row < a.rows; row += step, slot ^= 1) {
@@ -335,14 +353,14 @@ __global__ __launch_bounds__(kFour ? 256 : 1024, CH == 1 ? 6 : 1) void k_mx_norm
 #pragma unroll
     for (int c = 0; c < CH; c++) {
       const uint32_t g = c * team + t;
-      norm8<FMT>(a, row * gpr + g, r, h[c], w[c], g < gpr);
+      norm8<FMT>(a, row * gpr + g, r, h[c], w[c], wide, g < gpr);
     }
   }
 }
 
 // Longer rows are read twice, the second time as they were stored.
 template <int DT, int FMT>
-__global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gpr) {
+__global__ __launch_bounds__(1024, 8) void k_mx_norm_long(MxNormArgs a, uint32_t gpr) {
   __shared__ double part[2][16];
   int slot = 0;
   for (uint64_t row = blockIdx.x; row < a.rows; row += gridDim.x, slot ^= 1) {
@@ -359,7 +377,7 @@ __global__ __launch_bounds__(1024) void k_mx_norm_long(MxNormArgs a, uint32_t gp
       float h[8], w[8];
       load8<DT>(src, g * 8, uint32_t(a.k), h);
       load8<DT>(a.w, g * 8, uint32_t(a.k), w);
-      norm8<FMT>(a, row * gpr + g, r, h, w, true);
+      norm8<FMT>(a, row * gpr + g, r, h, w, top8(w) >= kWide, true);
     }
   }
 }

@@ -65,3 +65,47 @@ def test_values_that_round_to_zero_keep_their_sign(k, fmt):
     y = mx.rms_norm(f64(x), f64(w), EPS)
     between(y, fmt, codes, scales)
     signs(y, fmt, codes, scales)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("k", [96, 512, 4096, 8224, 16416])
+def test_weights_that_bring_tiny_values_back(k, fmt):
+    # h / rms lies under FP32's normal numbers, or is zero there, and the weight makes y ordinary
+    rng = np.random.default_rng(k)
+    z = rng.normal(0, 1, (5, k))
+    x = z * np.exp2(np.array([-50.0, -80, -100, -38, -20]))[:, None]
+    x[:, 3] = 2.0 ** 100
+    x[4, 3] = 2.0 ** 90
+    x[:, 40:48] = -0.0
+    x = rounded(x, torch.float32)
+    for power in (12, 25, 60, 100):
+        w = rounded((1 + 0.3 * rng.random(k)) * np.where(np.arange(k) == 3, 1.0, 2.0 ** power), torch.float32)
+        codes, scales, _ = zn.mx_rms_norm(x.cuda(), w.cuda(), eps=0.0, fmt=FMT[fmt])
+        y = mx.rms_norm(f64(x), f64(w), 0.0)
+        between(y, fmt, codes, scales)
+        signs(y, fmt, codes, scales)
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+@pytest.mark.parametrize("k", [64, 4096, 8224, 16416])
+def test_values_past_fp32_have_finite_scales(k, fmt):
+    # |y| passes 2^128: the formula's scale is finite (at most 254) and so is the block
+    rng = np.random.default_rng(k)
+    x = rounded(rng.normal(0, 1, (4, k)), torch.float32)
+    x[1, 0] = 2.0 ** 40
+    x[2] = 0.0
+    x[3, k // 2] = float("inf")
+    for w in (np.full(k, 2.0 ** 127), rng.normal(0, 1, k) * 2.0 ** 126):
+        w = rounded(w, torch.float32)
+        codes, scales, _ = zn.mx_rms_norm(x.cuda(), w.cuda(), eps=1e-5, fmt=FMT[fmt])
+        y = mx.rms_norm(f64(x), f64(w), EPS)
+        assert np.abs(y[0]).max() > 2.0 ** 128
+        between(y, fmt, codes, scales)
+        signs(y, fmt, codes, scales)
+        # normal numbers past 4 are no FP32 weights any more: infinities, whose blocks are NaNs
+        dead = ~np.isfinite(mx.blocks(f64(w)[None])).all(2)[0]
+        assert ((raw(scales)[:3] == 255) == dead).all()
+    # an infinite weight is one, and a NaN is one
+    w[k // 3], w[k - 1] = float("inf"), float("nan")
+    codes, scales, _ = zn.mx_rms_norm(x.cuda(), w.cuda(), eps=1e-5, fmt=FMT[fmt])
+    assert (raw(scales)[:, k // 3 // 32] == 255).all() and (raw(scales)[:, -1] == 255).all()
