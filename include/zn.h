@@ -324,7 +324,10 @@ zn_status zn_mx_rms_norm(zn_dtype dtype, const void *d_x, uint64_t x_stride, con
  * Needs zn_mx_matmul_scratch_bytes() bytes of 16-byte aligned device scratch
  * (ZN_ERR_CAPACITY if it is less; 0 for many sizes, then d_scratch may be
  * NULL); calls that may run at the same time, and graphs that may replay at
- * the same time, need scratch of their own.
+ * the same time, need scratch of their own.  Scale bytes that start at no
+ * multiple of 16, k being one of 512 and m over 16, want (m + n) * k / 32
+ * bytes more: without them the product is made the way of few rows, several
+ * times slower, its sums in another order.
  *
  * zn_mx_matmul2 -- zn_mx_matmul with flags.  ZN_MX_FAST_SUMS, for ZN_BF16
  * results (ZN_ERR_ARG for ZN_FP32 and for unknown flags): products of an E4M3

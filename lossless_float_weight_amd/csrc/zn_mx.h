@@ -41,6 +41,7 @@ struct MxMatmulArgs {
   uint8_t *out;
   uint64_t out_stride;           // elements
   uint8_t *scratch;
+  uint64_t scratch_bytes;
 };
 
 hipError_t launch_mx_quantize(int in_dtype, int fmt, const MxQuantArgs &a, hipStream_t s);

@@ -126,5 +126,6 @@ extern "C" zn_status zn_mx_matmul2(zn_dtype a_fmt, const void *d_a, const void *
   p.out = static_cast<uint8_t *>(d_out);
   p.out_stride = out_stride;
   p.scratch = static_cast<uint8_t *>(d_scratch);
+  p.scratch_bytes = at16(d_scratch) ? scratch_bytes : 0;
   return done(launch_mx_matmul(a_fmt, w_fmt, out_dtype, flags & ZN_MX_FAST_SUMS, p, stream));
 }

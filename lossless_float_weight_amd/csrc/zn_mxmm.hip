@@ -667,9 +667,9 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
   }
 }
 
-// Scale rows on a pitch of 16 bytes, which the tiled form's copies need: where
-// the caller's are not, both sides are laid out in the scratch first, scale 1
-// after the row's end.
+// Scale rows on a pitch of 16 bytes and from such an address on, which the tiled
+// form's copies need: where the caller's are not, both sides are laid out in
+// the scratch first, scale 1 after the row's end.
 __host__ __device__ constexpr uint32_t pitch_of(uint32_t nb) { return (nb + 15) & ~15u; }
 __global__ __launch_bounds__(256) void k_mx_pitch(MxMatmulArgs p, uint32_t nb, uint32_t per_row, uint64_t count) {
   const uint64_t i = (uint64_t(blockIdx.y) << 30) + uint64_t(blockIdx.x) * 256 + threadIdx.x;
@@ -824,12 +824,13 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
   const uint32_t nb = uint32_t(p.k / kMxBlock);
   const Plan plan = plan_of(FA, FW, kFine, p.m, p.n, p.k);
   // scale rows that could be copied as they lie but for the first one's
-  // address have no room in the scratch: any m goes the way of few rows
+  // address are laid out as well, where the caller has given room for them
+  const uint32_t pitch = pitch_of(nb);
   const bool apart = nb % 16 == 0 && (uintptr_t(p.as) | uintptr_t(p.ws)) % 16;
-  if (plan.form != kFew && !apart) {
+  const bool room = !apart || p.scratch_bytes >= part_bytes(plan, p.m, p.n) + (p.m + p.n) * pitch;
+  if (plan.form != kFew && room) {
     MxMatmulArgs q = p;
-    if (nb % 16) {
-      const uint32_t pitch = pitch_of(nb);
+    if (nb % 16 || apart) {
       q.scratch = p.scratch + part_bytes(plan, p.m, p.n);
       const uint64_t count = (p.m + p.n) * (pitch / 16);
       const uint32_t x = uint32_t((count < (1ull << 30) ? count + 255 : 1ull << 30) / 256);
@@ -852,7 +853,7 @@ hipError_t matmul(const MxMatmulArgs &p, hipStream_t s) {
           a.n = first;
           b.n -= first;
           b.w += first * nb * code_bytes<FW>();
-          b.ws += first * pitch_of(nb);
+          b.ws += first * pitch;
           b.out += first * esize(OUT);
           const hipError_t e = tiled_form<FA, FW, OUT, kFine>(kLarge, a, nb, plan.per, s);
           return e != hipSuccess ? e : tiled_form<FA, FW, OUT, kFine>(rest.form, b, nb, rest.per, s);

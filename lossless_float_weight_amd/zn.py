@@ -642,12 +642,15 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     if fast_sums and dt != BF16:
         raise ZnError(-1, f"{where}: fast_sums is for bfloat16 results, not {out.dtype}")
     need = mx_matmul_scratch_bytes(fa, fw, m, n, k)
+    sa, sw = a_scales.data_ptr(), w_scales.data_ptr()
     if scratch is None:
+        if (sa | sw) % 16 and k % 512 == 0 and m > 16:
+            need += (m + n) * k // MX_BLOCK  # room to lay the scales out
         scratch = _mx_new(torch.uint8, dev, stream, need) if need else None
     elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
         raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
-    _mx_call(where, dev, stream, lib().zn_mx_matmul2, fa, a.data_ptr(), a_scales.data_ptr(), fw, w.data_ptr(),
-             w_scales.data_ptr(), m, n, k, MX_FAST_SUMS if fast_sums else 0, dt, out.data_ptr(), stride,
+    _mx_call(where, dev, stream, lib().zn_mx_matmul2, fa, a.data_ptr(), sa, fw, w.data_ptr(), sw,
+             m, n, k, MX_FAST_SUMS if fast_sums else 0, dt, out.data_ptr(), stride,
              scratch.data_ptr() if scratch is not None else None, scratch.numel() if scratch is not None else 0)
     if stream is not None:
         _mx_use(stream, a, a_scales, w, w_scales, out, scratch)

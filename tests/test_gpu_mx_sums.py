@@ -241,3 +241,32 @@ def test_fast_sums_are_for_bf16_results():
     for bad in (dict(dtype=torch.float32), dict(out=out)):
         with pytest.raises(zn.ZnError):
             zn.mx_matmul(*args, fast_sums=True, **bad)
+
+
+@pytest.mark.parametrize("fmts", PAIRS)
+@pytest.mark.parametrize("size", [(17, 40, 512), (40, 300, 8192), (300, 280, 1024), (1800, 1900, 512), (3600, 3650, 512)])
+def test_results_do_not_go_by_the_scales_address(size, fmts):
+    (m, n, k), (fa, fw) = size, fmts.split()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(m)
+    F = {"fp8": zn.FP8_E4M3, "fp4": zn.FP4X2_E2M1}
+    a, sa = zn.mx_quantize(torch.randn(m, k, device="cuda", generator=g), F[fa])
+    w, sw = zn.mx_quantize(torch.randn(n, k, device="cuda", generator=g), F[fw])
+
+    def moved(s, by):
+        b = torch.zeros(s.numel() + by, dtype=torch.uint8, device="cuda")
+        b[by:] = s.view(torch.uint8).view(-1)
+        return b[by:].view(s.shape)
+
+    for kw in ({"dtype": torch.float32}, {}, {"fast_sums": True}):
+        want = zn.mx_matmul(a, sa, w, sw, **kw)
+        for da, dw in ((1, 0), (0, 8), (3, 13)):
+            assert torch.equal(zn.mx_matmul(a, moved(sa, da), w, moved(sw, dw), **kw), want)
+    # scratch of the size asked for has no room to lay them out: right all the same
+    need = zn.mx_matmul_scratch_bytes(F[fa], F[fw], m, n, k)
+    scratch = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    wide = torch.randint(-3, 4, (n, k), device="cuda").float()
+    w, sw = zn.mx_quantize(wide, F[fw])
+    one, s1 = zn.mx_quantize(torch.ones(m, k, device="cuda"), F[fa])
+    got = zn.mx_matmul(one, moved(s1, 1), w, moved(sw, 5), dtype=torch.float32, scratch=scratch)
+    assert torch.equal(got, zn.mx_dequantize(w, sw, dtype=torch.float32).double().sum(1).float().expand(m, n))
