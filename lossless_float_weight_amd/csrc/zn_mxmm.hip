@@ -767,9 +767,9 @@ hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, 
 //    in 4 pieces, 28 in one; 128 x 4096 x 4096 10.0 in one, 11.1 in two.
 Plan plan_of(int a_fmt, int w_fmt, bool fine, uint64_t m, uint64_t n, uint64_t k) {
   const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
-  // offsets inside a tile stay below 2^31, and so do the tiles' numbers
-  if (m <= 16 || nb > (1u << 16) || m * n >= (1ull << 42)) return {kFew, steps, 1};
   const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
+  // offsets inside a tile stay below 2^31, and a grid's threads, 256 a tile, below 2^32
+  if (m <= 16 || nb > (1u << 16) || tiles(128, 128) >= (1ull << 24)) return {kFew, steps, 1};
   const uint64_t large = tiles(256, 256), t = tiles(64, 64);
   if (large >= 200 && !fine) {
     const uint64_t wide = tiles(128, 256), left = wide % 512;
@@ -793,15 +793,22 @@ uint64_t part_bytes(const Plan &plan, uint64_t m, uint64_t n) {
 template <int FA, int FW, int OUT, bool kFine, int MT, int NT, int KS>
 hipError_t few_form(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
   const uint64_t nt = (p.n + 16 * NT - 1) / (16 * NT), mt = (p.m + 16 * MT - 1) / (16 * MT);
-  for (uint64_t y = 0; y < mt; y += 65535) {  // the grid's limit
-    MxMatmulArgs q = p;
-    const uint64_t rows = y * 16 * MT;
-    q.a += rows * nb * code_bytes<FA>();
-    q.as += rows * nb;
-    q.out += rows * p.out_stride * esize(OUT);
-    q.m -= rows;
-    k_mx_few<FA, FW, OUT, kFine, MT, NT, KS><<<dim3(uint32_t(nt), uint32_t(mt - y < 65535 ? mt - y : 65535)), 64 * KS, 0, s>>>(q, nb);
-  }
+  // the grid's limits: 65535 along y, and fewer than 2^32 threads along x
+  const uint64_t most_x = 1ull << 22, most_y = 65535;
+  for (uint64_t y = 0; y < mt; y += most_y)
+    for (uint64_t x = 0; x < nt; x += most_x) {
+      MxMatmulArgs q = p;
+      const uint64_t rows = y * 16 * MT, first = x * 16 * NT;
+      q.a += rows * nb * code_bytes<FA>();
+      q.as += rows * nb;
+      q.w += first * nb * code_bytes<FW>();
+      q.ws += first * nb;
+      q.out += (rows * p.out_stride + first) * esize(OUT);
+      q.m -= rows;
+      q.n -= first;
+      k_mx_few<FA, FW, OUT, kFine, MT, NT, KS>
+          <<<dim3(uint32_t(nt - x < most_x ? nt - x : most_x), uint32_t(mt - y < most_y ? mt - y : most_y)), 64 * KS, 0, s>>>(q, nb);
+    }
   return hipGetLastError();
 }
 template <int FA, int FW, int OUT, bool kFine>

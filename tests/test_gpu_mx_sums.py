@@ -270,3 +270,22 @@ def test_results_do_not_go_by_the_scales_address(size, fmts):
     one, s1 = zn.mx_quantize(torch.ones(m, k, device="cuda"), F[fa])
     got = zn.mx_matmul(one, moved(s1, 1), w, moved(sw, 5), dtype=torch.float32, scratch=scratch)
     assert torch.equal(got, zn.mx_dequantize(w, sw, dtype=torch.float32).double().sum(1).float().expand(m, n))
+
+
+@pytest.mark.parametrize("m", [1, 9])
+def test_more_columns_than_a_grid_holds(m):
+    # 2^29 + 100 rows of one block: 64 of them to a workgroup of 512 threads pass 2^32 threads
+    n, at = (1 << 29) + 100, [0, 1, 63, 64, (1 << 28) - 1, 1 << 28, (1 << 28) + 77, (1 << 29) - 1, 1 << 29, (1 << 29) + 99]
+    w = torch.zeros(n, 16, dtype=torch.uint8, device="cuda")
+    sw = torch.full((n, 1), 127, dtype=torch.uint8, device="cuda")
+    a = torch.full((m, 32), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sa = torch.full((m, 1), 127, dtype=torch.uint8, device="cuda")
+    for i, r in enumerate(at):
+        w[r, :i + 1] = 0x22
+    want = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    for i, r in enumerate(at):
+        want[r] = 2 * (i + 1)
+    out = torch.full((m, n + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    zn.mx_matmul(a, sa, w, sw, out=out[:, :n])
+    for row in out:
+        assert torch.equal(row[:n], want) and bool((row[n:] == 7.0).all())

@@ -26,3 +26,10 @@ def test_flags_of_the_product():
     size = dict(flags=1, m=48, n=4096, k=14336, stride=4096, scratch=P)
     assert need > 0 and matmul2(**size, bytes=need - 1) == CAPACITY
     assert zn.lib().zn_mx_matmul(*_with(MATMUL)) == 0
+
+
+def test_products_of_more_tiles_than_a_grid_holds_need_no_scratch():
+    # 2^24 tiles of 256 threads would pass a grid: the way of few rows, which lays nothing out
+    for fa in (zn.FP8_E4M3, zn.FP4X2_E2M1):
+        assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 1, 32) == 0
+        assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 256, 32) == (17 + (1 << 31) - 256) * 16
