@@ -503,6 +503,16 @@ def _mx_use(stream, *tensors) -> None:
             t.record_stream(stream)
 
 
+def _mx_no_grad(where: str, **tensors) -> None:
+    """The operators have no gradient: a plain output whose graph would end
+    here, or a given one that autograd watches, is refused."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if t is not None and t.requires_grad:
+                raise ZnError(-1, f"{where}: {name} requires a gradient, which the operator has not "
+                                  "(pass .detach(), or call under torch.no_grad())")
+
+
 def _mx_codes(where, lead, k, fmt, codes, scales, dev, stream):
     """The output pair, given or made."""
     if fmt == FP8_E4M3:
@@ -564,6 +574,7 @@ def mx_dequantize(codes: torch.Tensor, scales: torch.Tensor, k: int | None = Non
     """zn_mx_dequantize: the values of the first k of every row (all stored
     ones when None), in BF16 or FP32."""
     where = "mx_dequantize"
+    _mx_no_grad(where, out=out)
     fmt, kp, lead = _mx_packed(where, "codes", codes, scales)
     if k is None:
         k = kp
@@ -583,8 +594,11 @@ def mx_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | 
                 residual_out: torch.Tensor | None = None, stream=None):
     """zn_mx_rms_norm: (codes, scales, h) of h = x + residual normed and
     quantised; h is stored in residual_out (x or residual itself is fine).
-    Without a residual h is x."""
+    Without a residual h is x.  No gradient: with a residual, an x or residual
+    that requires one is refused while gradients are recorded."""
     where = "mx_rms_norm"
+    if residual is not None:  # without one h is x itself
+        _mx_no_grad(where, x=x, residual=residual, residual_out=residual_out)
     dt = _mx_plain(where, "x", x.dtype)
     dev = _mx_device(where, stream, x, weight, residual, residual_out, codes, scales)
     rows, k, stride = _mx_rows(where, "x", x)
@@ -632,6 +646,7 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     (zn_mx_matmul2 with ZN_MX_FAST_SUMS, BF16 only) adds FP8 products by the
     scaled matrix instruction: faster, with fewer bits."""
     where = "mx_matmul"
+    _mx_no_grad(where, out=out)
     fa, k, lead = _mx_packed(where, "a", a, a_scales)
     fw, kw, wlead = _mx_packed(where, "w", w, w_scales)
     if len(wlead) != 1 or kw != k:

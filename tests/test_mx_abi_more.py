@@ -33,3 +33,33 @@ def test_products_of_more_tiles_than_a_grid_holds_need_no_scratch():
     for fa in (zn.FP8_E4M3, zn.FP4X2_E2M1):
         assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 1, 32) == 0
         assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 256, 32) == (17 + (1 << 31) - 256) * 16
+
+
+def test_a_sum_that_would_leave_the_graph_is_refused():
+    x, r, w = (torch.zeros(s, dtype=torch.bfloat16) for s in ((4, 64), (4, 64), (64,)))
+    g = torch.zeros(4, 64, dtype=torch.bfloat16, requires_grad=True)
+
+    def refused(f, *a, **k):
+        with pytest.raises(zn.ZnError, match="requires a gradient") as e:
+            f(*a, **k)
+        assert e.value.code == ARG
+
+    def passes(f, *a, **k):                     # as far as the device, which is the CPU here
+        with pytest.raises(zn.ZnError, match="not on a CUDA device"):
+            f(*a, **k)
+
+    refused(zn.mx_rms_norm, g, w, residual=r)
+    refused(zn.mx_rms_norm, x, w, residual=g)
+    refused(zn.mx_rms_norm, x, w, residual=g * 1)
+    refused(zn.mx_rms_norm, x, w, residual=r, residual_out=g)
+    c, s = torch.zeros(4, 64, dtype=torch.float8_e4m3fn), torch.zeros(4, 2, dtype=torch.float8_e8m0fnu)
+    refused(zn.mx_dequantize, c, s, out=g)
+    refused(zn.mx_matmul, c, s, c, s, out=g)
+    passes(zn.mx_rms_norm, g, w)                # h is x itself, with its graph
+    passes(zn.mx_rms_norm, x, w.clone().requires_grad_(), residual=r)
+    with torch.no_grad():
+        passes(zn.mx_rms_norm, g, w, residual=r)
+        passes(zn.mx_dequantize, c, s, out=g)
+        passes(zn.mx_matmul, c, s, c, s, out=g)
+    passes(zn.mx_rms_norm, g.detach(), w, residual=r)
+    passes(zn.mx_quantize, g)                   # codes have no derivative
