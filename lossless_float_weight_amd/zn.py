@@ -422,13 +422,23 @@ def _mx_device(where: str, stream, first: torch.Tensor, *others) -> torch.device
     return first.device
 
 
+def _torch_c(name: str, public):
+    """A function of torch's own module that saves microseconds a call, or the
+    public one where this torch has none of the name."""
+    return getattr(torch._C, name, None) or public
+
+
+_current_device = _torch_c("_cuda_getDevice", lambda: torch.cuda.current_device())
+_current_raw_stream = _torch_c("_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 def _mx_call(where: str, dev: torch.device, stream, function, *args) -> None:
     """The library call on the tensors' device and the stream (its current one when None)."""
-    if torch._C._cuda_getDevice() != dev.index:
+    if _current_device() != dev.index:
         with torch.cuda.device(dev):
             return _mx_call(where, dev, stream, function, *args)
     # the handle alone: making a Stream object takes longer than the launch
-    raw = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev.index)
+    raw = stream.cuda_stream if stream is not None else _current_raw_stream(dev.index)
     rc = function(*args, raw)
     if rc:
         raise ZnError(rc, where)

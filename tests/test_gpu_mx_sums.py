@@ -289,3 +289,17 @@ def test_more_columns_than_a_grid_holds(m):
     zn.mx_matmul(a, sa, w, sw, out=out[:, :n])
     for row in out:
         assert torch.equal(row[:n], want) and bool((row[n:] == 7.0).all())
+
+
+def test_public_ways_to_the_device_and_stream(monkeypatch):
+    (a, sa), (w, sw) = whole(20, 64, "fp8", 1), whole(5, 64, "fp4", 2)
+    args = on_gpu(a, sa, "fp8", w, sw, "fp4")
+    want = zn.mx_matmul(*args)
+    monkeypatch.setattr(zn, "_current_device", torch.cuda.current_device)
+    monkeypatch.setattr(zn, "_current_raw_stream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = zn.mx_matmul(*args)
+    side.synchronize()
+    assert torch.equal(got, want)

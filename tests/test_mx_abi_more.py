@@ -63,3 +63,8 @@ def test_a_sum_that_would_leave_the_graph_is_refused():
         passes(zn.mx_matmul, c, s, c, s, out=g)
     passes(zn.mx_rms_norm, g.detach(), w, residual=r)
     passes(zn.mx_quantize, g)                   # codes have no derivative
+
+
+def test_torch_without_the_short_ways():
+    assert zn._torch_c("_no_such_function", len) is len
+    assert callable(zn._torch_c("_cuda_getDevice", None) or len)
