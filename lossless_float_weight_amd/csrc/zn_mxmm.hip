@@ -244,7 +244,9 @@ __global__ __launch_bounds__(64 * KS) void k_mx_few(MxMatmulArgs p, uint32_t nb)
 // A copy's end is waited for with vmcnt by the wave that issued it, then by
 // all at the barrier that ends a step.  The base's two scalar registers may
 // come from vector instructions (uniform), which takes 5 wait states before a
-// memory instruction that the compiler does not see: s_nop 4.
+// memory instruction that the compiler does not see: s_nop 4.  m0 cannot be
+// declared (the compiler reserves it, and sets it where it uses it); nothing
+// else in these kernels does.  The build refuses a form whose registers spill.
 __device__ __forceinline__ uint64_t uniform(uint64_t v) {
   return uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v)))) |
          (uint64_t(uint32_t(__builtin_amdgcn_readfirstlane(int(v >> 32)))) << 32);
@@ -740,7 +742,7 @@ hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, 
   // FP32 results of FP8 need registers for both sides in BF16
   if constexpr (kFine) {
     if (f == kMiddle) return tiled<FA, FW, OUT, true, 4, 4, 2, 2, 1, 2>(p, nb, per, s);
-    return tiled<FA, FW, OUT, true, 2, 2, 2, 2, 1, k88 ? 3 : 2>(p, nb, per, s);
+    return tiled<FA, FW, OUT, true, 2, 2, 2, 2, 1, k88 && OUT == FP32 ? 3 : 2>(p, nb, per, s);
   } else {
     if (f == kSmall) return tiled<FA, FW, OUT, false, 2, 2, 2, 2, k88 ? 1 : 2, k88 ? 3 : 2>(p, nb, per, s);
     if (f == kSmall3) return tiled<FA, FW, OUT, false, 2, 2, 2, 2, k88 ? 1 : 2, 3>(p, nb, per, s);
