@@ -753,17 +753,24 @@ hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, 
   }
 }
 
-// Which form, and how many pieces of k.  Times at m x n x k, FP8 by FP4:
+// Which form, and how many pieces of k.  Times at m x n x k, FP8 by FP4 with fast
+// sums, where nothing else is said:
+//  - no tile twice as tall as the rows: 48 x 28672 x 4096 15.9 us in 64 x 64 tiles,
+//    27.1 in 128 x 128 (with FP32 sums 25.9 and 38.2); 100 x 28672 x 4096 28.2
+//    in 128 x 128, 47.5 in 128 x 256, 67.9 in 256 x 256.
 //  - 256 x 256 tiles from about a CU each: 1024 x 14336 x 4096 50 us, 63 with
 //    128 x 128; 128 x 128 then, 1024 x 4096 x 4096 24 us, 35 with 256 x 256,
-//    and 64 x 64 below, 512 x 4096 x 4096 16 us, 23 with 128 x 128.
+//    and 64 x 64 below, 512 x 4096 x 4096 14 us, 23 with 128 x 128.  FP32 sums
+//    of FP8 have 128 x 128 tiles at most and meet the smaller ones at the same
+//    place: 512 x 4096 x 4096 24 us in 64 x 64, 33 in 128 x 128; 700 rows 38
+//    either way; 1024 46 and 35.
 //  - two workgroups of 128 x 256 to a CU are 7% slower than one of 256 x 256
 //    (8192 x 28672 x 4096 802 us for 750) but end less raggedly: where the
 //    last round of large tiles would leave many CUs idle they are taken
 //    (4096 x 14336 x 4096, 3.5 rounds: 189 us for 197).
 //  - three 64 x 64 workgroups to a CU, with fewer steps copied ahead, where
-//    two would need a second round: 600 x 4096 x 4096 19.5 us for 22.4, but
-//    512 x 4096 x 4096, one round, 16.9 for 15.3.
+//    two would need a second round: 600 x 4096 x 4096 19.7 us for 22.0, but
+//    512 x 4096 x 4096, one round, 14.7 for 14.0.
 //  - pieces of k only where there are fewer tiles than CUs and a piece saves
 //    more than 20 steps, about the time of joining them: 48 x 4096 x 14336 14 us
 //    in 4 pieces, 28 in one; 128 x 4096 x 4096 10.0 in one, 11.1 in two.
@@ -773,12 +780,12 @@ Plan plan_of(int a_fmt, int w_fmt, bool fine, uint64_t m, uint64_t n, uint64_t k
   // offsets inside a tile stay below 2^31, and a grid's threads, 256 a tile, below 2^32
   if (m <= 16 || nb > (1u << 16) || tiles(128, 128) >= (1ull << 24)) return {kFew, steps, 1};
   const uint64_t large = tiles(256, 256), t = tiles(64, 64);
-  if (large >= 200 && !fine) {
+  if (large >= 200 && m > 128 && !fine) {
     const uint64_t wide = tiles(128, 256), left = wide % 512;
     const uint64_t rounds = 100 * ((large + 255) / 256), wide_rounds = 107 * (wide / 512) + (left == 0 ? 0 : left <= 256 ? 59 : 107);
     return {a_fmt == FP8 && w_fmt == FP4X2 && wide_rounds < rounds ? kWide : kLarge, steps, 1};
   }
-  if (tiles(128, 128) >= 200) return {kMiddle, steps, 1};
+  if (tiles(128, 128) >= 200 && m > 64) return {kMiddle, steps, 1};
   if (t > 512) return {kSmall3, steps, 1};
   if (t > 256) return {kSmall, steps, 1};
   const uint32_t pieces = uint32_t(256 / t);

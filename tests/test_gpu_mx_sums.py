@@ -303,3 +303,16 @@ def test_public_ways_to_the_device_and_stream(monkeypatch):
         got = zn.mx_matmul(*args)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("fmts", PAIRS)
+@pytest.mark.parametrize("size", [(17, 60000, 96), (48, 28672, 1056), (64, 26000, 160), (65, 26000, 96), (100, 52000, 544),
+                                  (128, 60000, 96), (129, 52000, 96)])
+def test_few_rows_by_many_columns(size, fmts):
+    (m, n, k), (fa, fw) = size, fmts.split()
+    (a, sa), (w, sw) = whole(m, k, fa, m + k), whole(n, k, fw, n + k + 1)
+    want = mx.values(a, sa, fa).astype(np.float32) @ mx.values(w, sw, fw).astype(np.float32).T
+    args = on_gpu(a, sa, fa, w, sw, fw)
+    np.testing.assert_array_equal(zn.mx_matmul(*args, dtype=torch.float32).cpu().numpy(), want)
+    for fast in (False, True):
+        assert torch.equal(zn.mx_matmul(*args, fast_sums=fast).cpu(), rounded(want, torch.bfloat16))
