@@ -824,13 +824,20 @@ template <int FA, int FW, int OUT, bool kFine>
 hipError_t few(const MxMatmulArgs &p, uint32_t nb, hipStream_t s) {
   if (p.m > 16) return few_form<FA, FW, OUT, kFine, 4, 1, 8>(p, nb, s);  // what the tiled form cannot address
   // Weight tiles of a wave: more of them share the activations' loads, fewer
-  // leave more workgroups.  FP8 by FP4, in us with 1, 2, 4 tiles:
-  //   1 x 28672 x 4096   13.6 14.3 13.1     16 x 28672 x 4096  23.8 19.8 15.7
-  //   1 x 14336 x 4096    8.8  8.0  8.3     16 x 14336 x 4096  14.8 11.1  9.2
-  //   1 x  4096 x 4096    3.6  5.2  7.6     16 x  4096 x 14336 12.6 15.9 22.7
-  //   1 x  6144 x 4096    5.1  5.3          16 x  6144 x 4096   8.0  6.6
+  // leave more workgroups.  In us with 1, 2, 4 tiles, FP32 sums of FP8 by FP4,
+  // FP8 by FP8, fast sums of FP8 by FP4, and FP4 by FP4:
+  //   1 x   4096 x  4096   4.0  5.2  7.8    5.1  7.1 10.8    3.9  5.0  7.4    3.7  4.8  7.1
+  //   1 x  14336 x  4096   9.0  8.4 10.0   13.7 12.6 14.8    8.6  8.2  8.3    7.9  8.1  7.7
+  //   1 x  28672 x  4096  14.4 16.0 16.2   21.9 22.0 27.7   14.0 14.5 13.4   12.4 14.5 16.0
+  //   1 x 128256 x  4096  55.3 53.8 60.5  100.4 95.6 114.1  55.4 52.7 47.4   47.4 51.5 51.6
+  //  16 x   6144 x  4096   8.6  6.7  8.9   10.8  8.7 12.3    8.4  6.6  8.8    6.6  5.7  7.9
+  //  16 x  14336 x  4096  15.2 11.2  9.7   18.9 15.1 15.5   14.7 11.0  9.1   11.2  9.2  8.2
+  //  16 x  28672 x  4096  24.4 19.7 17.7   30.7 26.8 28.0   24.3 20.2 16.1   18.3 16.7 15.0
+  //  16 x   4096 x 14336  12.8 16.0 27.5   16.3 22.1 41.2   12.6 16.0 22.8    9.5 13.0 20.1
+  // FP4 by FP8 goes like FP8 by FP8.  Up to 4 rows four tiles pay for fast sums alone.
   const uint64_t nt = (p.n + 15) / 16;
-  if (nt >= 1536 || (p.m > 4 && nt >= 768)) return few_form<FA, FW, OUT, kFine, 1, 4, 8>(p, nb, s);
+  constexpr bool kFour = !kFine && (FA == FP8 || FW == FP8);
+  if ((kFour && nt >= 1536) || (p.m > 4 && nt >= 768)) return few_form<FA, FW, OUT, kFine, 1, 4, 8>(p, nb, s);
   if (nt >= (p.m > 4 ? 384 : 512)) return few_form<FA, FW, OUT, kFine, 1, 2, 8>(p, nb, s);
   return few_form<FA, FW, OUT, kFine, 1, 1, 8>(p, nb, s);
 }
