@@ -777,8 +777,9 @@ hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, 
 Plan plan_of(int a_fmt, int w_fmt, bool fine, uint64_t m, uint64_t n, uint64_t k) {
   const uint32_t nb = uint32_t(k / kMxBlock), steps = (nb + 3) / 4;
   const auto tiles = [&](uint64_t bm, uint64_t bn) { return ((m + bm - 1) / bm) * ((n + bn - 1) / bn); };
-  // offsets inside a tile stay below 2^31, and a grid's threads, 256 a tile, below 2^32
-  if (m <= 16 || nb > (1u << 16) || tiles(128, 128) >= (1ull << 24)) return {kFew, steps, 1};
+  // offsets inside a tile stay below 2^31, and a grid's threads, 256 a tile, below
+  // 2^32 (many tiles are of 64 x 64 only up to 64 rows)
+  if (m <= 16 || nb > (1u << 16) || (m <= 64 ? tiles(64, 64) : tiles(128, 128)) >= (1ull << 24)) return {kFew, steps, 1};
   const uint64_t large = tiles(256, 256), t = tiles(64, 64);
   if (large >= 200 && m > 128 && !fine) {
     const uint64_t wide = tiles(128, 256), left = wide % 512;

@@ -32,7 +32,10 @@ def test_products_of_more_tiles_than_a_grid_holds_need_no_scratch():
     # 2^24 tiles of 256 threads would pass a grid: the way of few rows, which lays nothing out
     for fa in (zn.FP8_E4M3, zn.FP4X2_E2M1):
         assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 1, 32) == 0
-        assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, 17, (1 << 31) - 256, 32) == (17 + (1 << 31) - 256) * 16
+        for m, n in ((17, 1 << 30), (64, (1 << 30) - 63), (65, (1 << 31) - 127)):
+            assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, m, n, 32) == 0
+        for m, n in ((17, (1 << 30) - 64), (64, (1 << 30) - 64), (65, (1 << 31) - 128)):
+            assert zn.mx_matmul_scratch_bytes(fa, zn.FP4X2_E2M1, m, n, 32) == (m + n) * 16
 
 
 def test_a_sum_that_would_leave_the_graph_is_refused():
