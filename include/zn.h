@@ -274,8 +274,8 @@ const char *zn_status_str(zn_status s);
  * A row of k values is stored as kp = 32 * ceil(k / 32) codes (kp bytes of
  * E4M3, kp / 2 bytes of E2M1 pairs), zero past k, and kp / 32 scale bytes;
  * rows follow each other without gaps.  Codes must be 16-byte aligned; scale
- * bytes and plain rows may lie anywhere (plain elements at their own size;
- * 16-byte aligned rows take wide loads).  Plain rows are `*_stride` elements
+ * bytes and plain rows may lie anywhere (plain elements at their own size).
+ * Plain rows are `*_stride` elements
  * apart; an input's stride may be 0 (one row read many times), an output's is
  * at least the row (ZN_ERR_ARG).  k is 1 .. 2^30, rows at most 2^31 - 1; rows
  * = 0 does nothing.
@@ -283,7 +283,7 @@ const char *zn_status_str(zn_status s);
  * The calls launch on the caller's stream for the current device, which has
  * to be the memory's, allocate nothing and may be captured into a graph.
  * Outputs must not overlap inputs except where stated.  Results do not depend
- * on the launch: the same inputs give the same bits. */
+ * on the launch: the same inputs give the same bits.  There are no gradients. */
 
 /* zn_mx_quantize -- plain rows (ZN_BF16 or ZN_FP32) to codes and scales:
  * s = clamp(floor(log2 max|x|) + 127 - emax, 0, 254) over the block, emax 8
@@ -306,8 +306,9 @@ zn_status zn_mx_dequantize(zn_dtype fmt, const void *d_codes, const void *d_scal
  *   y = h * weight / sqrt(mean(h^2) + eps), quantised as zn_mx_quantize does.
  * d_residual and d_residual_out are both NULL for h = x (nothing is stored
  * then).  x, residual, weight (k values) and the stored sum share one dtype.
- * d_residual_out may be d_x or d_residual itself, with its stride.  The mean
- * is summed in 64 bits: no finite row overflows.  eps is finite and >= 0. */
+ * d_residual_out may be d_x or d_residual itself, with its stride.  Codes and
+ * scales are those of the formula in 64 bits: no finite row or weight overflows
+ * or vanishes on the way.  eps is finite and >= 0. */
 zn_status zn_mx_rms_norm(zn_dtype dtype, const void *d_x, uint64_t x_stride, const void *d_residual,
                          uint64_t residual_stride, const void *d_weight, float eps, uint64_t rows, uint64_t k,
                          void *d_residual_out, uint64_t residual_out_stride, zn_dtype fmt, void *d_codes,
@@ -319,8 +320,8 @@ zn_status zn_mx_rms_norm(zn_dtype dtype, const void *d_x, uint64_t x_stride, con
  * Row m of the output starts at element m * out_stride.
  * Where a side is E4M3 both are multiplied as zn_mx_dequantize gives them in
  * ZN_BF16, which holds every value that zn_mx_quantize can have stored but
- * those under 2^-133; scale bytes above 246 (E4M3) or 252 (E2M1) pass
- * BF16's range and give infinities.
+ * those under 2^-133; scale bytes above 246 (E4M3) or 252 (E2M1) may pass
+ * BF16's range and give infinities, and NaNs beside zeros.
  * Needs zn_mx_matmul_scratch_bytes() bytes of 16-byte aligned device scratch
  * (ZN_ERR_CAPACITY if it is less; 0 for many sizes, then d_scratch may be
  * NULL); calls that may run at the same time, and graphs that may replay at

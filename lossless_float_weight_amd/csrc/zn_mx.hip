@@ -181,8 +181,9 @@ __global__ __launch_bounds__(256) void k_mx_dequantize(MxDequantArgs a, FastDiv 
 // multiples of 2^-98 then (2^-10 of a scale of at least 2^-88), and y has
 // passed 2^-122 before the weight there.
 // One pass over memory with the row in registers: 8192 x 4096 BF16 with the
-// addition, 236 MB, 41 us in a row (5.7 TB/s with what the 256 MB cache holds),
-// 3.1 us for one row; without the second look it was 38 and 2.8.
+// addition, 236 MB, 40 us in a row (5.9 TB/s with what the 256 MB cache holds),
+// 3.1 us for one row; without the second look it was 38 and 2.8, and 613 x 5003
+// FP32 6.6 for 7.5: its registers leave six waves a SIMD where eight would fit.
 struct RowScale {
   int e;
   float m;

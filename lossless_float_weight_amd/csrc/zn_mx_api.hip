@@ -12,7 +12,8 @@ namespace {
 bool plain(int dt) { return dt == ZN_BF16 || dt == ZN_FP32; }
 bool coded(int dt) { return dt == ZN_FP8_E4M3 || dt == ZN_FP4X2_E2M1; }
 bool good_rows(uint64_t rows, uint64_t k) { return rows <= kMxMaxRows && k >= 1 && k <= kMxMaxK; }
-// a row pitch in elements: rows must not run into each other when written
+// a row pitch in elements, whose products with rows stay in 64 bits; that rows do
+// not run into each other is asked where they are written
 bool good_stride(uint64_t stride) { return stride <= (1ull << 40); }
 // elements are read and written whole
 bool at(const void *p, int dt) { return p && uintptr_t(p) % (dt == ZN_FP32 ? 4 : 2) == 0; }

@@ -25,9 +25,10 @@
 // which is exact for every value of BF16's range, and use
 // v_mfma_f32_16x16x32_bf16, which adds in FP32 throughout: half the rate of the
 // scaled instruction, and one conversion for two values that a wave takes in.
-// 8192 x 28672 x 4096 FP8 by FP4 takes 1.51 ms (1.28 PFLOP/s; a large BF16 product
-// of the library's reaches 1.38), with ZN_MX_FAST_SUMS 0.74 ms; one row of
-// 14336 x 4096, bound by memory, 8.7 us either way.
+// 8192 x 28672 x 4096 FP8 by FP4 takes 1.51 to 1.65 ms, by the clock that the power
+// leaves (1.17 to 1.28 PFLOP/s; a large BF16 product of the library's reaches
+// 1.38), with ZN_MX_FAST_SUMS 0.73 to 0.78 ms; one row of 14336 x 4096, bound by
+// memory, 8.3 and 7.9 us.
 #include "zn_mx.h"
 
 namespace zn {
@@ -520,8 +521,8 @@ __global__ __launch_bounds__(64 * WM * WN, G) void k_mx_tiled(
     // products run the next step's are read.  A step waits once: its operands
     // have been read by all waves (the copies of step t + kBuf may follow) and
     // the copies of the next have landed.  256 x 4096 x 4096 took 8.2 us for 9.5
-    // in 4 bits and 13.1 for 13.6 in FP8; FP8 by FP4, 10.4 for 10.3, is bounded
-    // by the copies (24 KB a step and CU, about 25 bytes a cycle) either way.
+    // in 4 bits and 13.1 for 13.6 in FP8; FP8 by FP4 (with fast sums, 393 KB copied
+    // to LDS by every CU) 10.4 for 10.3.
     copy_quad(T::kQuads - 1, 0);
 #pragma unroll
     for (int t = 0; t < kBuf; t++) {
@@ -739,7 +740,7 @@ struct Plan {
 template <int FA, int FW, int OUT, bool kFine>
 hipError_t tiled_form(Form f, const MxMatmulArgs &p, uint32_t nb, uint32_t per, hipStream_t s) {
   constexpr bool k44 = FA == FP4X2 && FW == FP4X2, k88 = FA == FP8 && FW == FP8, k84 = FA == FP8 && FW == FP4X2;
-  // FP32 results of FP8 need registers for both sides in BF16
+  // FP32 sums of FP8 need registers for both sides in BF16
   if constexpr (kFine) {
     if (f == kMiddle) return tiled<FA, FW, OUT, true, 4, 4, 2, 2, 1, 2>(p, nb, per, s);
     return tiled<FA, FW, OUT, true, 2, 2, 2, 2, 1, k88 && OUT == FP32 ? 3 : 2>(p, nb, per, s);
