@@ -316,3 +316,37 @@ def test_few_rows_by_many_columns(size, fmts):
     np.testing.assert_array_equal(zn.mx_matmul(*args, dtype=torch.float32).cpu().numpy(), want)
     for fast in (False, True):
         assert torch.equal(zn.mx_matmul(*args, fast_sums=fast).cpu(), rounded(want, torch.bfloat16))
+
+
+@pytest.mark.parametrize("fast", [True, False])
+@pytest.mark.parametrize("size", [(3, 28700, 512), (40, 300, 8192), (300, 640, 1024), (1800, 1900, 544)])
+def test_captured_with_new_operands_and_scales_at_any_address(size, fast):
+    (m, n, k), pad = size, 5
+    g = torch.Generator(device="cuda")
+    g.manual_seed(k)
+    w, sw = zn.mx_quantize(torch.randn(n, k, device="cuda", generator=g), zn.FP4X2_E2M1)
+    a, sa = zn.mx_quantize(torch.randn(m, k, device="cuda", generator=g))
+    room = torch.zeros(pad + sa.numel(), dtype=torch.uint8, device="cuda")
+    moved = room[pad:].view(sa.shape)
+    moved.copy_(sa.view(torch.uint8))
+    zn.mx_matmul(a, moved, w, sw, fast_sums=fast)
+    graphs = []
+    for _ in range(2):
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = zn.mx_matmul(a, moved, w, sw, fast_sums=fast)
+        graphs.append((graph, out))
+    side = torch.cuda.Stream()
+    for step in range(4):
+        x, s = zn.mx_quantize(torch.randn(m, k, device="cuda", generator=g))
+        want = zn.mx_matmul(x, s, w, sw, fast_sums=fast)
+        a.copy_(x)
+        moved.copy_(s.view(torch.uint8))
+        torch.cuda.synchronize()
+        graphs[0][0].replay()               # both at once, each with scratch of its own
+        with torch.cuda.stream(side):
+            graphs[1][0].replay()
+        torch.cuda.synchronize()
+        for _, out in graphs:
+            assert torch.equal(out, want)
