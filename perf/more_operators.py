@@ -190,7 +190,7 @@ def _tables(state):
     need = torch.where(fits, want - have, 0)
     upto = need.cumsum(0)
     served = fits & ((need == 0) | (upto <= left))
-    taken = torch.where(served, upto, 0).amax()
+    taken = torch.where(served & (need > 0), upto, 0).amax()
     first = (upto - need).unsqueeze(1) + column - have.unsqueeze(1)
     new = served.unsqueeze(1) & (column >= have.unsqueeze(1)) & (column < want.unsqueeze(1))
     table = torch.where(new, free[(left - 1 - first).clamp(0, free.numel() - 1)], table)
