@@ -351,6 +351,139 @@ zn_status zn_mx_matmul2(zn_dtype a_fmt, const void *d_a, const void *d_a_scales,
                         zn_dtype out_dtype, void *d_out, uint64_t out_stride, void *d_scratch,
                         uint64_t scratch_bytes, hipStream_t stream);
 
+/* ---- a key-value cache in 4 bits ----
+ * Keys and values of earlier tokens as E2M1 pairs, in pages that requests share
+ * out among them.  A page holds page_size tokens; every row (page, head,
+ * place) is head_dim values, stored like a row of zn_mx_quantize in
+ * ZN_FP4X2_E2M1: head_dim / 2 bytes of codes and head_dim / 32 scale bytes, so
+ * pages are tensors that an FP4 plan compresses and zn_mx_dequantize reads.
+ * Tokens are placed by slots, slot = page * page_size + place.
+ *
+ * A request's row of the block table (int32) names its pages in order: its
+ * token at position i lies in page table[i / page_size], place i % page_size.
+ * Lengths, new tokens, starts, slots and tables are int32 arrays on the
+ * device; what they hold is checked there, since the host does not see it: no
+ * entry leads to an access outside the arrays and the pages.
+ *
+ * As with the microscaled operators the calls launch on the caller's stream
+ * for the current device, allocate nothing, may be captured into a graph, give
+ * the same bits for the same inputs, and have no gradients.  Outputs must not
+ * overlap inputs except where stated. */
+
+/* The cache.  Strides are in blocks of 32 values (16 bytes of codes, one scale
+ * byte) and the same for all four arrays; a row's blocks are consecutive.  The
+ * codes are 16-byte aligned.  head_dim is a multiple of 32 up to 256,
+ * page_size a power of two from 16 to 65536, kv_heads at most 65535, n_pages *
+ * page_size below 2^31, strides at most 2^40. */
+typedef struct zn_mx_cache {
+  void *k, *k_scales, *v, *v_scales;
+  uint64_t n_pages;
+  uint32_t page_size, kv_heads, head_dim, reserved;   /* reserved: 0 */
+  uint64_t page_stride, head_stride, place_stride;
+} zn_mx_cache;
+
+/* zn_kv_extend -- pages and slots for a step's new tokens.  Request b has
+ * d_lens[b] tokens and gets d_add[b] more (values below 0 count as 0).  Free
+ * pages are a stack, d_free[0 .. *d_n_free): in the order of the requests the
+ * pages that they need come off its end and are entered in their table rows.
+ *   A request is served if its tokens fit in `width` pages, if they end within
+ *   the step's `tokens`, and if it needs no page or the stack holds what it and
+ *   all requests before it need (those that do not fit need none).  One that is
+ *   not served keeps its length and its pages, and its tokens get slot -1.
+ *   d_new_lens[batch]: the lengths after the step.
+ *   d_starts[batch + 1]: where each request's new tokens begin in the step (the
+ *     sums of d_add, at most 2^31 - 1).
+ *   d_slots, d_positions [tokens]: slot and position of every new token; -1 and
+ *     0 for tokens of requests that were not served and behind the last one.  A
+ *     token whose page is not in [0, n_pages) gets slot -1.
+ *   d_n_left: pages left on the stack.
+ * d_new_lens and d_n_left must not be d_lens and d_n_free themselves
+ * (ZN_ERR_ARG).  batch is at most 8192, tokens, free_cap and width * page_size at
+ * most 2^31 - 1, page_size a power of two up to 65536; d_n_free counts as at most
+ * free_cap. */
+zn_status zn_kv_extend(const int32_t *d_lens, const int32_t *d_add, uint32_t batch, int32_t *d_table,
+                       uint64_t table_stride, uint32_t width, const int32_t *d_free, uint64_t free_cap,
+                       const int32_t *d_n_free, uint32_t page_size, uint64_t n_pages, uint64_t tokens,
+                       int32_t *d_new_lens, int32_t *d_starts, int32_t *d_slots, int32_t *d_positions,
+                       int32_t *d_n_left, hipStream_t stream);
+
+/* zn_kv_release -- the pages of requests that are done (d_done[b] != 0, bytes)
+ * go back onto the stack, request after request, and their length becomes 0;
+ * other lengths are copied.  Table rows stay as they are.  Pages past free_cap
+ * are dropped.  Limits as for zn_kv_extend. */
+zn_status zn_kv_release(const int32_t *d_lens, const uint8_t *d_done, uint32_t batch, const int32_t *d_table,
+                        uint64_t table_stride, uint32_t width, int32_t *d_free, uint64_t free_cap,
+                        const int32_t *d_n_free, uint32_t page_size, int32_t *d_new_lens, int32_t *d_n_left,
+                        hipStream_t stream);
+
+/* zn_mx_kv_write -- rows of keys and values (ZN_BF16 or ZN_FP32), quantised as
+ * zn_mx_quantize does, into the cache.  Element d of token t's head h is at t *
+ * token_stride + h * head_stride + d.  Tokens whose slot is negative or past
+ * the last page are left out.  Slots of a call are distinct: of two tokens with
+ * one slot, either one's blocks of 32 values are left there. */
+zn_status zn_mx_kv_write(zn_dtype dtype, const void *d_k, uint64_t k_token_stride, uint64_t k_head_stride,
+                         const void *d_v, uint64_t v_token_stride, uint64_t v_head_stride, const int32_t *d_slots,
+                         uint64_t tokens, const zn_mx_cache *cache, hipStream_t stream);
+
+/* zn_mx_kv_read -- the values at the slots as ZN_BF16 or ZN_FP32 (rounded as by
+ * zn_mx_dequantize), dense [tokens][kv_heads][head_dim]; zeros for tokens whose
+ * slot is negative or past the last page. */
+zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64_t tokens, zn_dtype dtype,
+                        void *d_k, void *d_v, hipStream_t stream);
+
+/* zn_mx_attention -- attention of queries over the cache.  q, out: ZN_BF16 or
+ * ZN_FP32 [tokens][heads][head_dim] (strides in elements, a row dense); heads
+ * is a multiple of kv_heads, and query head h reads head h / (heads / kv_heads).
+ * Request b has d_lens[b] tokens in the cache, and its queries are rows
+ * d_starts[b] .. d_starts[b+1] - 1; with d_starts = NULL it has one, row b, and
+ * tokens must be batch.  The last of a request's n queries stands at position
+ * lens - 1, query i at p = lens - n + i:
+ *   causal != 0: it sees the keys at 0 .. p, with window > 0 only the last
+ *   `window` of them (p - window + 1 .. p);
+ *   causal == 0: it sees all keys; window must be 0 then.
+ * out = sum of softmax(scale * q . k) v over the keys seen, and d_lse (NULL, or
+ * FP32 [tokens][heads]) the natural logarithm of the sum of exp(scale * q . k).
+ * A query that sees no key (an empty request, or more queries than keys) gives
+ * zeros and -infinity.  Rows behind the last request are left as they were.
+ * Keys that a query does not see have no effect on it, whatever they hold.
+ *   Values of keys and values are taken as stored; products, sums, maxima and
+ * exponentials are FP32 (BF16 queries: the weights keep 16 bits before they
+ * meet the values; FP32: 24), and the result is rounded once.  Weights are at
+ * most 1: n keys whose values pass 2^127 / n may give infinities and NaNs.  A
+ * scale byte over 252, which the write makes only (255) of infinities and NaNs,
+ * is a NaN.
+ *   Bad arrays: starts are clamped to [0, tokens], and a request that ends before
+ * it starts has no queries (rows that starts out of order name twice, or any row
+ * beside them, may be left as they were); a length that passes the table's width
+ * * page_size, and a page outside [0, n_pages), turn the queries that see them
+ * into NaNs.
+ *   max_new: the most queries of one request, as far as the caller knows (0 if
+ * not).  It chooses between kernels and has no effect on what is computed but
+ * the order of sums.
+ * scale is finite and > 0, batch at most 8192, window at most 2^31 - 1, tokens *
+ * heads / kv_heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
+ * 16-byte aligned device scratch (ZN_ERR_CAPACITY if it is less; 0 for some
+ * sizes, then d_scratch may be NULL); calls that may run at the same time, and
+ * graphs that may replay at the same time, need scratch of their own. */
+typedef struct zn_mx_attention_args {
+  zn_dtype dtype;                       /* of q and out */
+  uint32_t heads, batch;
+  uint64_t tokens, max_new;
+  const void *q;
+  uint64_t q_token_stride, q_head_stride;
+  void *out;
+  uint64_t out_token_stride, out_head_stride;
+  float *lse;
+  const int32_t *table, *lens, *starts;
+  uint64_t table_stride;
+  uint32_t width;
+  float scale;
+  uint32_t causal, window;
+} zn_mx_attention_args;
+zn_status zn_mx_attention_scratch_bytes(const zn_mx_cache *cache, const zn_mx_attention_args *args, uint64_t *bytes);
+zn_status zn_mx_attention(const zn_mx_cache *cache, const zn_mx_attention_args *args, void *d_scratch,
+                          uint64_t scratch_bytes, hipStream_t stream);
+
 /* ---- single steps, for parity tests of each stage (asynchronous) ----
  * zn_debug_histograms: order-0 histograms of every coded stream of every
  *   chunk of the plan: d_hist[n_chunks][n_coded][256] u32.

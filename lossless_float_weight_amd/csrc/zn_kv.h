@@ -1,0 +1,65 @@
+// zn_kv.h -- the key-value cache in 4 bits: arguments of the kernels that fill
+// its block tables, write and read its rows and attend over it, and their
+// launch interface.
+#pragma once
+#include "zn_mx.h"
+
+namespace zn {
+
+constexpr uint32_t kKvMaxBatch = 8192;         // requests of a step
+constexpr uint32_t kKvMaxPage = 65536;         // tokens of a page (at least 16, a power of two)
+constexpr uint32_t kKvMaxDim = 256;
+
+// Where the cache's rows lie: block i of row (page, head, place) is block
+// page * page_stride + head * head_stride + place * place_stride + i.
+struct KvCache {
+  uint8_t *k, *ks, *v, *vs;
+  uint32_t n_pages, shift;                     // page_size = 1 << shift
+  uint32_t heads, blocks;                      // of keys; of a row
+  uint64_t page_stride, head_stride, place_stride;
+};
+
+struct KvStepArgs {
+  const int32_t *lens, *add;                   // add: NULL for a release
+  const uint8_t *done;
+  uint32_t batch, width, shift;
+  int32_t *table;
+  uint64_t table_stride;
+  int32_t *free;
+  uint32_t free_cap, n_pages, tokens;
+  const int32_t *n_free;
+  int32_t *new_lens, *starts, *slots, *positions, *n_left;
+};
+hipError_t launch_kv_extend(const KvStepArgs &a, hipStream_t s);
+hipError_t launch_kv_release(const KvStepArgs &a, hipStream_t s);
+
+struct KvRowsArgs {
+  KvCache c;
+  const uint8_t *k, *v;                        // write: plain rows
+  uint64_t k_token, k_head, v_token, v_head;   // strides, elements
+  uint8_t *k_out, *v_out;                      // read: dense rows
+  const int32_t *slots;
+  uint64_t tokens;
+};
+hipError_t launch_kv_write(int dtype, const KvRowsArgs &a, hipStream_t s);
+hipError_t launch_kv_read(int dtype, const KvRowsArgs &a, hipStream_t s);
+
+struct AttnArgs {
+  KvCache c;
+  const uint8_t *q;
+  uint64_t q_token, q_head;                    // strides, elements
+  uint8_t *out;
+  uint64_t out_token, out_head;
+  float *lse;
+  const int32_t *table, *lens, *starts;        // starts: NULL for one query a request
+  uint64_t table_stride;
+  uint32_t width, batch, tokens, heads, group; // group: query heads of a key head
+  float scale;
+  uint32_t causal, window, max_new;
+  uint8_t *scratch;
+};
+// Bytes of scratch, by the sizes alone.
+uint64_t attention_scratch(int dtype, const AttnArgs &a);
+hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s);
+
+}  // namespace zn

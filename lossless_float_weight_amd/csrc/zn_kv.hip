@@ -1,0 +1,365 @@
+// zn_kv.hip -- the key-value cache's bookkeeping (pages of a step's new tokens,
+// their slots, pages that come back) and its rows (written and read by slots).
+#include "zn_kv.h"
+
+namespace zn {
+namespace {
+
+// ------------------------------------------------------------------ tables --
+constexpr int kStepThreads = 256;
+constexpr uint32_t kMost = 0x7FFFFFFFu;
+
+__device__ __forceinline__ uint32_t at_least_0(int32_t v) { return v < 0 ? 0u : uint32_t(v); }
+__device__ __forceinline__ uint32_t clip(uint64_t v) { return v > kMost ? kMost : uint32_t(v); }
+
+// Exclusive prefix sums of a and b over the workgroup's threads, and the sums.
+__device__ __forceinline__ void scan2(uint64_t &a, uint64_t &b, uint64_t &sum_a, uint64_t &sum_b) {
+  __shared__ uint64_t part[2][kStepThreads / 64];
+  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint64_t x = a, y = b;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint64_t p = __shfl_up(x, d), q = __shfl_up(y, d);
+    if (lane >= uint32_t(d)) {
+      x += p;
+      y += q;
+    }
+  }
+  if (lane == 63) {
+    part[0][wave] = x;
+    part[1][wave] = y;
+  }
+  __syncthreads();
+  sum_a = sum_b = 0;
+  a = x - a;
+  b = y - b;
+#pragma unroll
+  for (uint32_t w = 0; w < kStepThreads / 64; w++) {
+    if (w < wave) {
+      a += part[0][w];
+      b += part[1][w];
+    }
+    sum_a += part[0][w];
+    sum_b += part[1][w];
+  }
+}
+
+// The last i in [0, n) whose first[i] (without its top bit) is at most v; first
+// rises, and first[0] <= v.
+__device__ __forceinline__ uint32_t owner(const uint32_t *first, uint32_t n, uint32_t v) {
+  uint32_t lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if ((first[mid] & kMost) <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Bookkeeping is bound by latency (64 requests' step moves 4 KB): one launch, in
+// which every workgroup makes the sums over the requests for itself (a load and
+// a scan) and then does its share of pages and tokens by a search in the sums.
+// A thread takes `per` requests in a row.
+//
+// LDS, both batch + 1 long: first[b], the pages before request b's, with the top
+// bit set if b is served; begin[b], the tokens before its.
+template <bool EXTEND>
+__global__ __launch_bounds__(kStepThreads) void k_kv_step(KvStepArgs a) {
+  extern __shared__ uint32_t lds[];
+  uint32_t *first = lds, *begin = lds + a.batch + 1;
+  const uint32_t per = (a.batch + kStepThreads - 1) / kStepThreads;
+  const uint32_t b0 = threadIdx.x * per;
+  const uint32_t round = (1u << a.shift) - 1;
+  const uint32_t n_free = min(at_least_0(*a.n_free), a.free_cap);
+
+  // pages and tokens of this thread's requests, then of all before them
+  uint64_t pages = 0, tokens = 0, all_pages, all_tokens;
+  if constexpr (EXTEND) {
+    for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) tokens += at_least_0(a.add[b0 + i]);
+    uint64_t none = 0, no_sum;
+    scan2(tokens, none, all_tokens, no_sum);
+    __syncthreads();
+  }
+  uint64_t at_token = tokens;
+  for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) {
+    const uint32_t b = b0 + i;
+    const uint64_t len = at_least_0(a.lens[b]);
+    if constexpr (EXTEND) {
+      const uint64_t more = at_least_0(a.add[b]);
+      at_token += more;
+      const uint64_t want = (len + more + round) >> a.shift;
+      if (want <= a.width && at_token <= a.tokens) pages += want - ((len + round) >> a.shift);
+    } else {
+      const uint64_t have = (len + round) >> a.shift;
+      if (a.done[b]) pages += have < a.width ? have : a.width;
+    }
+  }
+  uint64_t none = 0, no_sum;
+  scan2(pages, none, all_pages, no_sum);
+
+  // what each request gets
+  uint64_t at_page = pages;
+  at_token = tokens;
+  uint32_t taken = 0;
+  for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) {
+    const uint32_t b = b0 + i;
+    const uint64_t len = at_least_0(a.lens[b]);
+    if constexpr (EXTEND) {
+      const uint64_t more = at_least_0(a.add[b]);
+      const uint64_t want = (len + more + round) >> a.shift;
+      const bool fits = want <= a.width && at_token + more <= a.tokens;
+      const uint64_t need = fits ? want - ((len + round) >> a.shift) : 0;
+      const bool served = fits && (need == 0 || at_page + need <= n_free);
+      first[b] = clip(at_page) | (served ? 0x80000000u : 0u);
+      begin[b] = clip(at_token);
+      if (served && need) taken = uint32_t(at_page + need);
+      if (blockIdx.x == 0) {
+        a.new_lens[b] = int32_t(served ? len + more : len);
+        a.starts[b] = int32_t(begin[b]);
+      }
+      at_page += need;
+      at_token += more;
+    } else {
+      const uint64_t have = (len + round) >> a.shift;
+      first[b] = clip(at_page);
+      if (a.done[b]) at_page += have < a.width ? have : a.width;
+      if (blockIdx.x == 0) a.new_lens[b] = a.done[b] ? 0 : int32_t(len);
+    }
+  }
+  const uint32_t id = blockIdx.x * kStepThreads + threadIdx.x, step = gridDim.x * kStepThreads;
+  if constexpr (EXTEND) {
+    __shared__ uint32_t most;
+    if (threadIdx.x == 0) most = 0;
+    if (threadIdx.x == 0) begin[a.batch] = clip(all_tokens);
+    __syncthreads();
+    if (taken) atomicMax(&most, taken);
+    __syncthreads();
+    taken = most;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      a.starts[a.batch] = int32_t(clip(all_tokens));
+      *a.n_left = int32_t(n_free - taken);
+    }
+    // pages: the i-th one taken is the i-th from the stack's end
+    for (uint32_t i = id; i < taken; i += step) {
+      const uint32_t b = owner(first, a.batch, i);
+      const uint32_t have = (at_least_0(a.lens[b]) + round) >> a.shift;
+      a.table[b * a.table_stride + have + i - (first[b] & kMost)] = a.free[n_free - 1 - i];
+    }
+    // tokens; a page that this step enters is looked up on the stack
+    for (uint64_t t = id; t < a.tokens; t += step) {
+      int32_t slot = -1, position = 0;
+      if (t < begin[a.batch]) {
+        const uint32_t b = owner(begin, a.batch, uint32_t(t));
+        if (first[b] >> 31) {
+          const uint32_t len = at_least_0(a.lens[b]), have = (len + round) >> a.shift;
+          const uint32_t p = len + uint32_t(t) - begin[b], at = p >> a.shift;
+          const int32_t page =
+              at < have ? a.table[b * a.table_stride + at] : a.free[n_free - 1 - ((first[b] & kMost) + at - have)];
+          position = int32_t(p);
+          if (page >= 0 && uint32_t(page) < a.n_pages) slot = int32_t((uint32_t(page) << a.shift) | (p & round));
+        }
+      }
+      a.slots[t] = slot;
+      a.positions[t] = position;
+    }
+  } else {
+    __syncthreads();
+    const uint32_t room = a.free_cap - n_free;
+    const uint32_t back = all_pages < room ? uint32_t(all_pages) : room;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_left = int32_t(n_free + back);
+    for (uint32_t i = id; i < back; i += step) {
+      const uint32_t b = owner(first, a.batch, i);
+      a.free[n_free + i] = a.table[b * a.table_stride + i - first[b]];
+    }
+  }
+}
+
+template <bool EXTEND>
+hipError_t step(const KvStepArgs &a, uint64_t work, hipStream_t s) {
+  // four pieces of work a thread; more workgroups only repeat the sums
+  const uint64_t grid = (work + 4 * kStepThreads - 1) / (4 * kStepThreads);
+  const uint32_t lds = (2 * a.batch + 2) * sizeof(uint32_t);
+  if (lds > 48 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_step<EXTEND>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
+    if (e != hipSuccess) return e;
+  }
+  k_kv_step<EXTEND><<<uint32_t(grid < 1 ? 1 : grid > 256 ? 256 : grid), kStepThreads, lds, s>>>(a);
+  return hipGetLastError();
+}
+
+// -------------------------------------------------------------------- rows --
+// Eight consecutive elements of a dense row, at their own alignment.
+template <int DT>
+__device__ __forceinline__ void take8(const uint8_t *p, float (&v)[8]) {
+  if constexpr (DT == BF16) {
+    const u32x4 w = *reinterpret_cast<const u32x4_any *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[2 * i] = bf16_lo(w[i]);
+      v[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+    const f32x4 x = *reinterpret_cast<const f32x4_any *>(p), y = *reinterpret_cast<const f32x4_any *>(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[i] = x[i];
+      v[4 + i] = y[i];
+    }
+  }
+}
+
+// Group g of 8 values -> token, head and place within the row; the blocks of one
+// row lie on neighbouring lanes, a block on one quad.
+struct RowMap {
+  FastDiv per_row, heads;  // groups of a row; heads
+  __device__ __forceinline__ void at(uint32_t g, uint32_t &t, uint32_t &h, uint32_t &in_row) const {
+    const uint32_t row = per_row.div(g);
+    in_row = g - row * per_row.d;
+    t = heads.div(row);
+    h = row - t * heads.d;
+  }
+};
+
+__device__ __forceinline__ bool slot_at(const KvCache &c, int32_t slot, uint32_t h, uint64_t &block) {
+  if (slot < 0 || (uint32_t(slot) >> c.shift) >= c.n_pages) return false;
+  const uint32_t page = uint32_t(slot) >> c.shift, place = uint32_t(slot) & ((1u << c.shift) - 1);
+  block = page * c.page_stride + h * c.head_stride + place * c.place_stride;
+  return true;
+}
+
+// Quantises as k_mx_quantize does: a lane takes 8 values, a quad shares out a
+// block's maximum.  Keys and values are the grid's y = 0 and 1.
+template <int DT, int U>
+__global__ __launch_bounds__(256) void k_kv_write(KvRowsArgs a, RowMap m, uint32_t groups) {
+  const bool keys = blockIdx.y == 0;
+  const uint8_t *x = keys ? a.k : a.v;
+  uint8_t *codes = keys ? a.c.k : a.c.v, *scales = keys ? a.c.ks : a.c.vs;
+  const uint64_t ts = keys ? a.k_token : a.v_token, hs = keys ? a.k_head : a.v_head;
+  const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+  float v[U][8];
+  uint64_t block[U];
+  uint32_t r[U];
+  bool live[U];
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    uint32_t t, h;
+    m.at(g < groups ? g : 0, t, h, r[u]);
+    live[u] = g < groups && slot_at(a.c, a.slots[t], h, block[u]);
+    take8<DT>(x + (t * ts + h * hs + r[u] * 8) * esize(DT), v[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const uint32_t b = __float_as_uint(v[u][i]) & 0x7FFFFFFFu;
+      top = b > top ? b : top;
+    }
+    const uint32_t s = mx_scale_byte<FP4X2>(quad_max(top));
+    const u32x2 c = s == 255u ? u32x2{0, 0} : mx_codes8<FP4X2>(v[u], mx_inverse(s));
+    if (!live[u]) continue;
+    const uint64_t b = block[u] + (r[u] >> 2);
+    *reinterpret_cast<uint32_t *>(codes + b * 16 + (r[u] & 3) * 4) = c[0];
+    if ((r[u] & 3) == 0) scales[b] = uint8_t(s);
+  }
+}
+
+template <int DT, int U>
+__global__ __launch_bounds__(256) void k_kv_read(KvRowsArgs a, RowMap m, uint32_t groups) {
+  const bool keys = blockIdx.y == 0;
+  const uint8_t *codes = keys ? a.c.k : a.c.v, *scales = keys ? a.c.ks : a.c.vs;
+  uint8_t *out = keys ? a.k_out : a.v_out;
+  const uint32_t first = blockIdx.x * (256u * U) + threadIdx.x;
+  uint32_t w[U], s[U];
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    uint32_t t, h, r;
+    uint64_t block;
+    m.at(g < groups ? g : 0, t, h, r);
+    w[u] = s[u] = 0;
+    if (g < groups && slot_at(a.c, a.slots[t], h, block)) {
+      w[u] = *reinterpret_cast<const uint32_t *>(codes + (block + (r >> 2)) * 16 + (r & 3) * 4);
+      s[u] = scales[block + (r >> 2)];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; u++) {
+    const uint32_t g = first + 256u * u;
+    if (g >= groups) continue;
+    const float f = mx_scale_value(s[u]);
+    const f32x2 p0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 0), p1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 1);
+    const f32x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 2), p3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[u], 1.0f, 3);
+    const f32x4 lo = {p0[0] * f, p0[1] * f, p1[0] * f, p1[1] * f}, hi = {p2[0] * f, p2[1] * f, p3[0] * f, p3[1] * f};
+    if constexpr (DT == BF16) {
+      const u32x4 o = {f32_bf16x2(lo[0], lo[1]), f32_bf16x2(lo[2], lo[3]), f32_bf16x2(hi[0], hi[1]), f32_bf16x2(hi[2], hi[3])};
+      *reinterpret_cast<u32x4_any *>(out + uint64_t(g) * 16) = o;
+    } else {
+      *reinterpret_cast<f32x4_any *>(out + uint64_t(g) * 32) = lo;
+      *reinterpret_cast<f32x4_any *>(out + uint64_t(g) * 32 + 16) = hi;
+    }
+  }
+}
+
+// Calls f(first token, tokens) for pieces whose groups of 8 stay below 2^31.
+template <class F>
+hipError_t by_tokens(const KvRowsArgs &a, F f) {
+  const uint64_t most = 0x7FFF0000u / (uint64_t(a.c.heads) * a.c.blocks * 4);
+  for (uint64_t t = 0; t < a.tokens; t += most) {
+    const hipError_t e = f(t, a.tokens - t < most ? a.tokens - t : most);
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <int DT>
+hipError_t write_rows(const KvRowsArgs &a, hipStream_t s) {
+  constexpr int U = 2;
+  const uint32_t per_row = a.c.blocks * 4;
+  return by_tokens(a, [&](uint64_t t0, uint64_t tokens) {
+    KvRowsArgs p = a;
+    p.k += t0 * a.k_token * esize(DT);
+    p.v += t0 * a.v_token * esize(DT);
+    p.slots += t0;
+    const uint32_t groups = uint32_t(tokens * a.c.heads * per_row);
+    k_kv_write<DT, U><<<dim3((groups + 256 * U - 1) / (256 * U), 2), 256, 0, s>>>(
+        p, RowMap{FastDiv(per_row), FastDiv(a.c.heads)}, groups);
+    return hipGetLastError();
+  });
+}
+
+template <int DT>
+hipError_t read_rows(const KvRowsArgs &a, hipStream_t s) {
+  constexpr int U = 2;
+  const uint32_t per_row = a.c.blocks * 4;
+  return by_tokens(a, [&](uint64_t t0, uint64_t tokens) {
+    KvRowsArgs p = a;
+    const uint64_t skip = t0 * a.c.heads * per_row * 8 * esize(DT);
+    p.k_out += skip;
+    p.v_out += skip;
+    p.slots += t0;
+    const uint32_t groups = uint32_t(tokens * a.c.heads * per_row);
+    k_kv_read<DT, U><<<dim3((groups + 256 * U - 1) / (256 * U), 2), 256, 0, s>>>(
+        p, RowMap{FastDiv(per_row), FastDiv(a.c.heads)}, groups);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace
+
+hipError_t launch_kv_extend(const KvStepArgs &a, hipStream_t s) { return step<true>(a, a.tokens, s); }
+hipError_t launch_kv_release(const KvStepArgs &a, hipStream_t s) {
+  return step<false>(a, uint64_t(a.batch) * a.width / 8, s);
+}
+hipError_t launch_kv_write(int dtype, const KvRowsArgs &a, hipStream_t s) {
+  return dtype == BF16 ? write_rows<BF16>(a, s) : write_rows<FP32>(a, s);
+}
+hipError_t launch_kv_read(int dtype, const KvRowsArgs &a, hipStream_t s) {
+  return dtype == BF16 ? read_rows<BF16>(a, s) : read_rows<FP32>(a, s);
+}
+
+}  // namespace zn

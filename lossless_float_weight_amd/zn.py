@@ -11,7 +11,8 @@ import ctypes as C
 import functools
 import math
 import os
-from typing import Sequence
+import struct
+from typing import NamedTuple, Sequence
 
 import torch
 
@@ -79,6 +80,12 @@ def lib() -> C.CDLL:
         L.zn_mx_matmul_scratch_bytes.argtypes = [I, I, U64, U64, U64, PU64]
         L.zn_mx_matmul.argtypes = [I, P, P, I, P, P, U64, U64, U64, I, P, U64, P, U64, P]
         L.zn_mx_matmul2.argtypes = [I, P, P, I, P, P, U64, U64, U64, U32, I, P, U64, P, U64, P]
+        L.zn_kv_extend.argtypes = [P, P, U32, P, U64, U32, P, U64, P, U32, U64, U64, P, P, P, P, P, P]
+        L.zn_kv_release.argtypes = [P, P, U32, P, U64, U32, P, U64, P, U32, P, P, P]
+        L.zn_mx_kv_write.argtypes = [I, P, U64, U64, P, U64, U64, P, U64, P, P]
+        L.zn_mx_kv_read.argtypes = [P, P, U64, I, P, P, P]
+        L.zn_mx_attention_scratch_bytes.argtypes = [P, P, PU64]
+        L.zn_mx_attention.argtypes = [P, P, P, U64, P]
         for f in ("zn_setup", "zn_setup_transfer", "zn_plan_from_container", "zn_header_info",
                   "zn_tableset_info", "zn_compress_bound",
                   "zn_scratch_bytes", "zn_compress", "zn_decompress", "zn_decompress_noalloc",
@@ -86,7 +93,9 @@ def lib() -> C.CDLL:
                   "zn_tableset_load", "zn_tableset_lengths", "zn_tableset_map",
                   "zn_tableset_cost_history", "zn_debug_histograms", "zn_debug_code_lengths",
                   "zn_debug_kernel_events", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
-                  "zn_mx_matmul_scratch_bytes", "zn_mx_matmul", "zn_mx_matmul2"):
+                  "zn_mx_matmul_scratch_bytes", "zn_mx_matmul", "zn_mx_matmul2", "zn_kv_extend",
+                  "zn_kv_release", "zn_mx_kv_write", "zn_mx_kv_read", "zn_mx_attention_scratch_bytes",
+                  "zn_mx_attention"):
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -680,6 +689,293 @@ def mx_matmul(a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor, w_scales
     if stream is not None:
         _mx_use(stream, a, a_scales, w, w_scales, out, scratch)
     return out
+
+
+# ------------------------------------------------------- key-value cache --
+# Keys and values in 4 bits, in pages that requests share out among them.
+class MxCache(NamedTuple):
+    """zn_mx_cache: codes uint8 [pages, kv_heads, page_size, head_dim / 2] and
+    scales float8_e8m0fnu (or uint8) [pages, kv_heads, page_size, head_dim / 32]
+    of keys and values.  Any strides that agree between the four, rows dense."""
+    k: torch.Tensor
+    k_scales: torch.Tensor
+    v: torch.Tensor
+    v_scales: torch.Tensor
+
+
+class KvStep(NamedTuple):
+    """What zn_kv_extend makes of a step."""
+    lens: torch.Tensor
+    starts: torch.Tensor
+    slots: torch.Tensor
+    positions: torch.Tensor
+    n_free: torch.Tensor
+
+
+_CACHE_ARGS = struct.Struct("@4PQ4I3Q")                # zn_mx_cache
+_ATTENTION_ARGS = struct.Struct("@iII2QP2QP2Q4PQIfII")  # zn_mx_attention_args
+
+
+def mx_kv_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int, device="cuda") -> MxCache:
+    """An empty cache (all codes and scales 0)."""
+    if head_dim % MX_BLOCK or not MX_BLOCK <= head_dim <= 256:
+        raise ZnError(-1, f"mx_kv_cache: head_dim is {head_dim}, wanted a multiple of 32 up to 256")
+    if not 16 <= page_size <= 65536 or page_size & (page_size - 1):
+        raise ZnError(-1, f"mx_kv_cache: page_size is {page_size}, wanted a power of two from 16 to 65536")
+    if n_pages < 1 or n_pages * page_size >= 1 << 31 or not 1 <= kv_heads <= 65535:
+        raise ZnError(-1, f"mx_kv_cache: {n_pages} pages of {page_size} tokens and {kv_heads} heads")
+    lead = (n_pages, kv_heads, page_size)
+    k, v = (torch.zeros(*lead, head_dim // 2, dtype=torch.uint8, device=device) for _ in range(2))
+    ks, vs = (torch.zeros(*lead, head_dim // MX_BLOCK, dtype=torch.uint8, device=device).view(torch.float8_e8m0fnu)
+              for _ in range(2))
+    return MxCache(k, ks, v, vs)
+
+
+@functools.lru_cache(maxsize=1024)
+def _kv_layout(where, shape, kst, sshape, ksst, vshape, vst, vsshape, vsst):
+    """(n_pages, page_size, kv_heads, head_dim, strides in blocks) of a cache's shapes and strides, checked."""
+    if len(shape) != 4 or shape[3] == 0 or shape[3] % 16 or shape[3] > 128:
+        raise ZnError(-1, f"{where}: the cache's keys are {tuple(shape)}, wanted [pages, kv_heads, page_size, "
+                          "head_dim / 2] with head_dim a multiple of 32 up to 256")
+    blocks = shape[3] // 16
+    if vshape != shape or sshape != (*shape[:3], blocks) or vsshape != sshape:
+        raise ZnError(-1, f"{where}: the cache's keys are {tuple(shape)}, its values {tuple(vshape)}, their scales "
+                          f"{tuple(sshape)} and {tuple(vsshape)}")
+    if min(shape) < 1 or not 16 <= shape[2] <= 65536 or shape[2] & (shape[2] - 1) or shape[0] * shape[2] >= 1 << 31:
+        raise ZnError(-1, f"{where}: a cache of {shape[0]} pages with {shape[1]} heads of {shape[2]} tokens")
+    strides = []
+    for i in range(3):
+        if shape[i] == 1:   # never stepped
+            strides.append(blocks)
+            continue
+        st = kst[i] // 16
+        if kst[i] % 16 or st < blocks or vst[i] != kst[i] or ksst[i] != st or vsst[i] != st:
+            raise ZnError(-1, f"{where}: the cache's strides do not agree: {kst}, {ksst}, {vst}, {vsst}")
+        strides.append(st)
+    if kst[3] != 1 or vst[3] != 1 or (blocks > 1 and (ksst[3] != 1 or vsst[3] != 1)):
+        raise ZnError(-1, f"{where}: the cache's rows are not dense")
+    # rows must not share bytes: each axis steps past the ones inside it
+    inner = blocks
+    for st, n in sorted((st, n) for st, n in zip(strides, shape) if n > 1):
+        if st < inner:
+            raise ZnError(-1, f"{where}: the cache's rows overlap (strides {kst})")
+        inner = st * n
+    return shape[0], shape[2], shape[1], blocks * MX_BLOCK, tuple(strides)
+
+
+def _kv_cache(where: str, cache):
+    """(zn_mx_cache as bytes, its layout) of four tensors, checked."""
+    k, ks, v, vs = cache
+    if k.dtype != torch.uint8 or v.dtype != torch.uint8 or ks.dtype not in _MX_SCALE or vs.dtype not in _MX_SCALE:
+        raise ZnError(-1, f"{where}: the cache is {k.dtype}, {ks.dtype}, {v.dtype}, {vs.dtype}, wanted uint8 codes "
+                          "and float8_e8m0fnu scales")
+    lay = _kv_layout(where, k.shape, k.stride(), ks.shape, ks.stride(), v.shape, v.stride(), vs.shape, vs.stride())
+    return _CACHE_ARGS.pack(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), *lay[:4], 0, *lay[4]), lay
+
+
+def _kv_ints(where: str, name: str, t: torch.Tensor, shape) -> None:
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+        raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted dense int32 {tuple(shape)}")
+
+
+def _kv_table(where: str, table: torch.Tensor, batch: int):
+    """(row stride, width) of a block table."""
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch:
+        raise ZnError(-1, f"{where}: table is {table.dtype} {tuple(table.shape)}, wanted int32 rows of {batch} requests")
+    width = table.shape[1]
+    if (width > 1 and table.stride(1) != 1) or (batch > 1 and table.stride(0) < width):
+        raise ZnError(-1, f"{where}: table is not made of dense rows (pass .contiguous())")
+    return (table.stride(0) if batch > 1 else width), width
+
+
+def _kv_page(where: str, page_size: int) -> None:
+    if not 1 <= page_size <= 65536 or page_size & (page_size - 1):
+        raise ZnError(-1, f"{where}: page_size is {page_size}, wanted a power of two up to 65536")
+
+
+def _kv_rows(where: str, name: str, t: torch.Tensor, shape, dtype):
+    """(token stride, head stride) of [tokens, heads, head_dim] whose rows are dense."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted {dtype} {tuple(shape)}")
+    st = t.stride()
+    if st[2] != 1 or st[0] < 0 or st[1] < 0:
+        raise ZnError(-1, f"{where}: {name}'s rows are not dense (pass .contiguous())")
+    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
+
+
+def kv_extend(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: torch.Tensor, n_free: torch.Tensor,
+              page_size: int, n_pages: int, tokens: int, out: KvStep | None = None, stream=None) -> KvStep:
+    """zn_kv_extend: pages from the stack free[:n_free] for add[b] new tokens of
+    every request, entered in the table; (lens, starts, slots, positions,
+    n_free) after the step.  A request that is not served keeps its length and
+    its tokens get slot -1.  tokens: length of slots and positions."""
+    where = "kv_extend"
+    dev = _mx_device(where, stream, lens, add, table, free, n_free, *(out or ()))
+    batch = lens.numel()
+    _kv_ints(where, "lens", lens, (batch,))
+    _kv_ints(where, "add", add, (batch,))
+    _kv_ints(where, "free", free, (free.numel(),))
+    _kv_ints(where, "n_free", n_free, (1,))
+    stride, width = _kv_table(where, table, batch)
+    _kv_page(where, page_size)
+    if not 0 <= tokens < 1 << 31 or n_pages < 0 or n_pages * page_size >= 1 << 31:
+        raise ZnError(-1, f"{where}: {tokens} tokens, {n_pages} pages of {page_size}")
+    shapes = (batch,), (batch + 1,), (tokens,), (tokens,), (1,)
+    if out is None:
+        made = _mx_new(torch.int32, dev, stream, 2 * batch + 2 + 2 * tokens)
+        out = KvStep(*made.split([batch, batch + 1, tokens, tokens, 1]))
+    else:
+        out = KvStep(*out)
+        for name, t, shape in zip(KvStep._fields, out, shapes):
+            _kv_ints(where, "out." + name, t, shape)
+    _mx_call(where, dev, stream, lib().zn_kv_extend, lens.data_ptr(), add.data_ptr(), batch, table.data_ptr(), stride,
+             width, free.data_ptr(), free.numel(), n_free.data_ptr(), page_size, n_pages, tokens, out[0].data_ptr(),
+             out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr())
+    if stream is not None:
+        _mx_use(stream, lens, add, table, free, n_free, *out)
+    return out
+
+
+def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free: torch.Tensor, n_free: torch.Tensor,
+               page_size: int, out=None, stream=None):
+    """zn_kv_release: the pages of requests that are done (bool or uint8) go
+    back onto the stack; (lens, n_free) after that."""
+    where = "kv_release"
+    dev = _mx_device(where, stream, lens, done, table, free, n_free, *(out or ()))
+    batch = lens.numel()
+    _kv_ints(where, "lens", lens, (batch,))
+    if done.dtype not in (torch.bool, torch.uint8) or done.shape != (batch,) or not done.is_contiguous():
+        raise ZnError(-1, f"{where}: done is {done.dtype} {tuple(done.shape)}, wanted dense bool {(batch,)}")
+    _kv_ints(where, "free", free, (free.numel(),))
+    _kv_ints(where, "n_free", n_free, (1,))
+    stride, width = _kv_table(where, table, batch)
+    _kv_page(where, page_size)
+    if out is None:
+        made = _mx_new(torch.int32, dev, stream, batch + 1)
+        out = made[:batch], made[batch:]
+    else:
+        out = tuple(out)
+        _kv_ints(where, "out's lens", out[0], (batch,))
+        _kv_ints(where, "out's n_free", out[1], (1,))
+    _mx_call(where, dev, stream, lib().zn_kv_release, lens.data_ptr(), done.data_ptr(), batch, table.data_ptr(), stride,
+             width, free.data_ptr(), free.numel(), n_free.data_ptr(), page_size, out[0].data_ptr(), out[1].data_ptr())
+    if stream is not None:
+        _mx_use(stream, lens, done, table, free, n_free, *out)
+    return out
+
+
+def mx_kv_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, stream=None) -> None:
+    """zn_mx_kv_write: rows of k and v [tokens, kv_heads, head_dim] (BF16 or
+    FP32) quantised into the cache at slots [tokens]; a token whose slot is
+    negative or past the last page is left out."""
+    where = "mx_kv_write"
+    dt = _mx_plain(where, "k", k.dtype)
+    dev = _mx_device(where, stream, k, v, slots, *cache)
+    c, (_, _, heads, dim, _) = _kv_cache(where, cache)
+    tokens = slots.numel()
+    _kv_ints(where, "slots", slots, (tokens,))
+    kt, kh = _kv_rows(where, "k", k, (tokens, heads, dim), k.dtype)
+    vt, vh = _kv_rows(where, "v", v, (tokens, heads, dim), k.dtype)
+    _mx_call(where, dev, stream, lib().zn_mx_kv_write, dt, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
+             slots.data_ptr(), tokens, c)
+    if stream is not None:
+        _mx_use(stream, k, v, slots, *cache)
+
+
+def mx_kv_read(cache, slots: torch.Tensor, dtype=torch.bfloat16, out=None, stream=None):
+    """zn_mx_kv_read: (k, v) [tokens, kv_heads, head_dim] at slots [tokens], in
+    BF16 or FP32; zeros where a slot is negative or past the last page."""
+    where = "mx_kv_read"
+    dev = _mx_device(where, stream, slots, *cache, *(out or ()))
+    c, (_, _, heads, dim, _) = _kv_cache(where, cache)
+    tokens = slots.numel()
+    _kv_ints(where, "slots", slots, (tokens,))
+    if out is None:
+        _mx_plain(where, "dtype", dtype)
+        out = tuple(_mx_new(dtype, dev, stream, tokens, heads, dim) for _ in range(2))
+    else:
+        k, v = out = tuple(out)
+        _mx_no_grad(where, k=k, v=v)
+        dtype = k.dtype
+        for name, t in (("k", k), ("v", v)):
+            _mx_given(where, name, t, (tokens, heads, dim), (dtype,))
+    _mx_call(where, dev, stream, lib().zn_mx_kv_read, c, slots.data_ptr(), tokens, _mx_plain(where, "out", dtype),
+             out[0].data_ptr(), out[1].data_ptr())
+    if stream is not None:
+        _mx_use(stream, slots, *cache, *out)
+    return out
+
+
+@functools.lru_cache(maxsize=4096)
+def _attention_scratch(dt, heads, batch, tokens, max_new, width, causal, window, with_starts, lay) -> int:
+    """zn_mx_attention_scratch_bytes, which goes by sizes alone."""
+    c = _CACHE_ARGS.pack(0, 0, 0, 0, *lay[:4], 0, *lay[4])
+    g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, 0, 0, 0, 0, 0, 0, 0, 0, 0, with_starts, width, width,
+                             1.0, causal, window)
+    b = C.c_uint64()
+    _check(lib().zn_mx_attention_scratch_bytes(c, g, C.byref(b)), "mx_attention")
+    return b.value
+
+
+def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None = None,
+                 max_new: int = 0, causal: bool = True, window: int = 0, scale: float | None = None,
+                 out: torch.Tensor | None = None, lse: bool | torch.Tensor = False,
+                 scratch: torch.Tensor | None = None, stream=None):
+    """zn_mx_attention: queries q [tokens, heads, head_dim] (BF16 or FP32) over
+    the cache.  Request b has lens[b] keys in the pages of table[b]; its queries
+    are q[starts[b]:starts[b + 1]], the last of them at position lens[b] - 1, or
+    the one row q[b] without starts.  scale is 1 / sqrt(head_dim) when None.
+    max_new: the most queries of one request, if known; it only helps to choose
+    kernels.  With lse (True, or an FP32 tensor [tokens, heads]) the result is
+    (out, logarithm of the sums of the weights).  No gradient: a q that requires
+    one is refused while gradients are recorded."""
+    where = "mx_attention"
+    given = lse if isinstance(lse, torch.Tensor) else None
+    _mx_no_grad(where, q=q, out=out, lse=given)
+    dt = _mx_plain(where, "q", q.dtype)
+    dev = _mx_device(where, stream, q, table, lens, starts, out, given, scratch, *cache)
+    c, lay = _kv_cache(where, cache)
+    if q.dim() != 3 or q.shape[2] != lay[3] or q.shape[1] == 0 or q.shape[1] % lay[2]:
+        raise ZnError(-1, f"{where}: q is {tuple(q.shape)}, wanted [tokens, a multiple of {lay[2]} heads, {lay[3]}]")
+    tokens, heads, dim = q.shape
+    qt, qh = _kv_rows(where, "q", q, q.shape, q.dtype)
+    batch = lens.numel()
+    _kv_ints(where, "lens", lens, (batch,))
+    stride, width = _kv_table(where, table, batch)
+    if starts is not None:
+        _kv_ints(where, "starts", starts, (batch + 1,))
+    elif tokens != batch:
+        raise ZnError(-1, f"{where}: {tokens} queries for {batch} requests need starts")
+    if window < 0 or window >= 1 << 31 or (window and not causal):
+        raise ZnError(-1, f"{where}: window is {window}" + ("" if causal else ", and causal is False"))
+    if scale is None:
+        scale = 1.0 / math.sqrt(dim)
+    elif not (math.isfinite(scale) and scale > 0):
+        raise ZnError(-1, f"{where}: scale is {scale}")
+    max_new = min(max(int(max_new), 0), tokens)
+    need = _attention_scratch(dt, heads, batch, tokens, max_new, width, bool(causal), window, starts is not None, lay)
+    if out is None:
+        out, ot, oh = _mx_new(q.dtype, dev, stream, tokens, heads, dim), heads * dim, dim
+    else:
+        ot, oh = _kv_rows(where, "out", out, q.shape, q.dtype)
+        if (tokens > 1 and ot < dim) or (heads > 1 and oh < dim):
+            raise ZnError(-1, f"{where}: out's rows overlap")
+    if given is not None:
+        _mx_given(where, "lse", given, (tokens, heads), (torch.float32,))
+    elif lse:
+        given = _mx_new(torch.float32, dev, stream, tokens, heads)
+    if scratch is None:
+        scratch = _mx_new(torch.uint8, dev, stream, need) if need else None
+    elif scratch.dtype != torch.uint8 or not scratch.is_contiguous() or scratch.numel() < need:
+        raise ZnError(-1, f"{where}: scratch must be a contiguous uint8 tensor of at least {need} bytes")
+    g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
+                             given.data_ptr() if given is not None else 0, table.data_ptr(), lens.data_ptr(),
+                             starts.data_ptr() if starts is not None else 0, stride, width, scale, bool(causal), window)
+    _mx_call(where, dev, stream, lib().zn_mx_attention, c, g, scratch.data_ptr() if scratch is not None else None,
+             scratch.numel() if scratch is not None else 0)
+    if stream is not None:
+        _mx_use(stream, q, table, lens, starts, out, given, scratch, *cache)
+    return out if given is None else (out, given)
 
 
 def debug_histograms(ts: Tableset, tensors: Sequence[torch.Tensor], stream=None) -> torch.Tensor:
