@@ -38,10 +38,14 @@ __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// The largest of the four lanes l % 16 + 16 j (NaNs lose).
+// The largest of the four lanes l % 16 + 16 j (NaNs lose), by exchanges of 16 and
+// 32 lanes: two registers that hold the same come out with both halves in each.
 __device__ __forceinline__ float max_j(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  const uint32_t w = __float_as_uint(x);
+  const auto p = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+  const uint32_t y = __float_as_uint(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+  const auto q = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return fmaxf(__uint_as_float(q[0]), __uint_as_float(q[1]));
 }
 __device__ __forceinline__ float sum_j(float x) {
   x += __shfl_xor(x, 16);
@@ -94,6 +98,21 @@ __device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&out)[N]) {
       }
     }
   }
+}
+
+// Eight keys of one value from LDS: 4 rows from `p`, 4 from `p + next`, where this
+// lane's address is its part of a row (4 values of a row a lane, 4 lanes a row).
+union Turned {
+  s16x4 half[2];
+  bf16x8 all;
+  uint16_t bits[8];
+};
+__device__ __forceinline__ Turned turned(const uint8_t *p, int next) {
+  typedef __attribute__((address_space(3))) s16x4 lds16;
+  Turned t;
+  t.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p));
+  t.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p + next));
+  return t;
 }
 
 // A request of the call: its queries and the keys that any of them sees.
@@ -263,20 +282,22 @@ struct Rows16 {
 };
 
 template <int DT, int NB>
-__global__ __launch_bounds__(64 * kWaves) void k_attend(AttnArgs a, Plan plan, Parts out, FastDiv per_group, float c) {
+__global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_attend(AttnArgs a, Plan plan, Parts out, FastDiv per_group, float c) {
   using R = Rows16<DT, NB>;
   constexpr int D = 32 * NB;
   constexpr int kPad = D + 4;   // floats of a row where the waves join
   constexpr int kShared = kWaves * (R::kLds > 64 * kPad ? R::kLds : 64 * kPad);
   __shared__ __attribute__((aligned(16))) uint8_t lds[kShared];
   __shared__ float2 ml_of[kWaves][16];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t n = lane & 15, j = lane >> 4;
   const uint32_t head = blockIdx.y;
 
   Item it;
   if (!find_item<64 * kWaves>(a, plan, 16, blockIdx.x, it, blockIdx.x + blockIdx.y == 0 ? out.meta : nullptr)) return;
   it.b = __builtin_amdgcn_readfirstlane(it.b);
+  it.from = __builtin_amdgcn_readfirstlane(it.from);
+  it.to = __builtin_amdgcn_readfirstlane(it.to);
   const Request rq = request(a, it.b);
   // this lane's row
   const uint32_t row = it.group * 16 + n;
@@ -343,36 +364,99 @@ __global__ __launch_bounds__(64 * kWaves) void k_attend(AttnArgs a, Plan plan, P
   const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
   const int32_t *pages = a.table + it.b * a.table_stride;
   const uint32_t mask = (1u << a.c.shift) - 1;
+  const uint32_t place = uint32_t(a.c.place_stride);
+  const uint32_t last = a.c.n_pages;
 
-  for (uint32_t t = it.from + wave; t < it.to; t += kWaves) {
-    const uint32_t key0 = rq.lo + t * kTile;
-    if (key0 >= high || key0 + kTile <= low) continue;
-    // the page of each 16 keys, and where its rows begin; a place outside any page
-    // is taken from page 0 and counts as a NaN
+  // Codes and scale bytes of a tile on their way.  Both are asked for as soon as
+  // the registers of the tile before are free: a tile's keys before the values of
+  // the one before are used, its values before its scores are computed.
+  constexpr int kBytes = (NB % 4 == 0 ? NB / 4 : NB < 3 ? 1 : NB == 7 ? 3 : 2);   // blocks that a lane's quarter touches
+  constexpr int kUnits = (NB + 1) / 2;                                            // blocks of 32 keys' values a lane
+  uint32_t kw[4][NB], kb[4][kBytes];
+  u32x4 vw[2][kUnits];
+  uint32_t vb[2][kUnits];
+  // The page of each 16 keys; a place outside any page is taken from page 0 and
+  // counts as a NaN.
+  struct Where {
     uint64_t base[4];
-    bool gone[4];
+    uint32_t gone;
+  };
+  auto where = [&](uint32_t key0) {
+    Where w;
+    w.gone = 0;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
       const uint32_t key = key0 + 16 * g;
-      const int32_t page = key < rq.len ? pages[key >> a.c.shift] : 0;
-      gone[g] = uint32_t(page) >= a.c.n_pages;
-      base[g] = (gone[g] ? 0 : uint32_t(page)) * a.c.page_stride + (key & mask) * a.c.place_stride;
+      uint32_t page = key < rq.len ? uint32_t(pages[key >> a.c.shift]) : 0;
+      if (page >= last) {
+        page = 0;
+        w.gone |= 1u << g;
+      }
+      w.base[g] = page * a.c.page_stride + (key & mask) * uint64_t(place);
     }
+    return w;
+  };
+  auto ask_keys = [&](const Where &w) {
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      const u32_any *p = reinterpret_cast<const u32_any *>(kc + w.base[g] * 16 + (n * place * 16 + 4 * NB * j));
+#pragma unroll
+      for (int st = 0; st < NB; st++) kw[g][st] = p[st];
+      const uint8_t *q = ksc + w.base[g];
+#pragma unroll
+      for (int i = 0; i < kBytes; i++) kb[g][i] = q[n * place + min(NB * j / 4 + i, uint32_t(NB - 1))];
+    }
+  };
+  auto ask_values = [&](const Where &w) {
+#pragma unroll
+    for (int h = 0; h < 2; h++)
+#pragma unroll
+      for (int u = 0; u < kUnits; u++) {
+        const uint32_t unit = min(lane + 64 * u, uint32_t(32 * NB - 1));
+        const uint32_t key = unit / NB, off = (key & 15) * place + unit % NB;
+        const uint64_t base = key < 16 ? w.base[2 * h] : w.base[2 * h + 1];
+        vw[h][u] = *reinterpret_cast<const u32x4 *>(vc + base * 16 + off * 16);
+        vb[h][u] = *(vsc + base + off);
+      }
+  };
+
+  // this wave's tiles that some row sees
+  uint32_t t = it.from + wave, end = it.to;
+  if (high > rq.lo) end = min(end, (high - rq.lo + kTile - 1) / kTile);
+  else end = 0;
+  if (low > rq.lo + t * kTile) {
+    const uint32_t skip = ((low - rq.lo) / kTile - t + kWaves - 1) / kWaves;   // low >= rq.lo + t * kTile
+    t += skip * kWaves;
+  }
+  Where w = {};
+  if (t < end) {
+    w = where(rq.lo + t * kTile);
+    ask_keys(w);
+    ask_values(w);
+  }
+  for (; t < end; t += kWaves) {
+    const uint32_t key0 = rq.lo + t * kTile;
     // scores
     f32x4 s[4];
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-      const uint64_t at = base[g] + n * a.c.place_stride;
-      const u32_any *w = reinterpret_cast<const u32_any *>(kc + at * 16 + 4 * NB * j);
       f32x4 acc = {0, 0, 0, 0};
 #pragma unroll
       for (int st = 0; st < NB; st++) {
-        const uint32_t byte = ksc[at + (NB * j + st) / 4];
-        const bf16x8 k = values8(w[st], scale_of(gone[g] ? 255u : byte));
+        uint32_t byte = kb[g][0];
+#pragma unroll
+        for (int i = 1; i < kBytes; i++)
+          if ((NB * j + st) / 4 - NB * j / 4 == i) byte = kb[g][i];
+        const bf16x8 k = values8(kw[g][st], scale_of(w.gone >> g & 1 ? 255u : byte));
 #pragma unroll
         for (int p = R::QP - 1; p >= 0; p--) acc = mfma(k, r.q[st][p], acc);
       }
       s[g] = acc;
+    }
+    const bool more = t + kWaves < end;
+    if (more) {
+      w = where(key0 + kWaves * kTile);
+      ask_keys(w);
     }
     // keys that the row does not see
     if (key0 < low_all || key0 + kTile > high_all) {
@@ -397,73 +481,76 @@ __global__ __launch_bounds__(64 * kWaves) void k_attend(AttnArgs a, Plan plan, P
       r.m = m;
     }
     const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
+    // values of 32 keys to LDS
+    const bool cut = key0 < low || key0 + kTile > high;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; i++) {
-        w[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * h + i / 4][i & 3], c, -m));
-        r.l += w[i];
-      }
-      bf16x8 wp[R::WP];
-      pieces<R::WP>(w, wp);
-      // values of 32 keys to LDS
       bool nan = false;
 #pragma unroll
-      for (int u = 0; u < (NB + 1) / 2; u++) {
+      for (int u = 0; u < kUnits; u++) {
         const uint32_t unit = lane + 64 * u;
         if (NB % 2 == 0 || unit < 32 * NB) {
           const uint32_t key = unit / NB, blk = unit % NB;
-          const uint64_t at = (key < 16 ? base[2 * h] : base[2 * h + 1]) + (key & 15) * a.c.place_stride + blk;
-          u32x4 w4 = *reinterpret_cast<const u32x4 *>(vc + at * 16);
-          uint32_t byte = vsc[at];
           // no row sees a key outside [low, high)
-          if (key0 + 32 * h + key - low >= high - low) {
-            w4 = u32x4{0, 0, 0, 0};
-            byte = 127;
+          if (cut && key0 + 32 * h + key - low >= high - low) {
+            vw[h][u] = u32x4{0, 0, 0, 0};
+            vb[h][u] = 127;
           }
-          nan |= byte > 252;
-          const float f = scale_of(byte);
+          nan |= vb[h][u] > 252;
+          const float f = scale_of(vb[h][u]);
           uint8_t *p = mine + key * R::kPitch + blk * 64;
 #pragma unroll
-          for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + 16 * i) = values8(w4[i], f);
+          for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + 16 * i) = values8(vw[h][u][i], f);
         }
       }
       const bool any_nan = __any(nan);
       lds_in_order();
+      if (h == 1 && more) ask_values(w);
+      bf16x8 wp[R::WP];
+      {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * h + i / 4][i & 3], c, -m));
+          r.l += x[i];
+        }
+        pieces<R::WP>(x, wp);
+      }
       // and back, 4 keys of one value at a time
       const uint8_t *from = mine + (4 * j + n / 4) * R::kPitch + (n & 3) * 8;
-#pragma unroll
-      for (int d = 0; d < 2 * NB; d++) {
-        typedef __attribute__((address_space(3))) s16x4 lds16;
+      if (__builtin_expect(any_nan, 0)) {
+        // A NaN would meet the weight 0 of rows that do not see its key.  It is left
+        // out here, and rows that see one are found by a product of their own.
         union {
-          s16x4 half[2];
-          bf16x8 all;
           uint16_t bits[8];
-        } v;
-        v.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(from + 32 * d));
-        v.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(from + 32 * d + 16 * R::kPitch));
-        if (any_nan) {
-          // A NaN would meet the weight 0 of rows that do not see its key.  It is
-          // left out here, and rows that see one are found by a product of their own.
-          union {
-            uint16_t bits[8];
-            bf16x8 all;
-          } bad, seen;
+          bf16x8 all;
+        } seen;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          seen.bits[i] = key0 + 32 * h + 16 * (i / 4) + 4 * j + (i & 3) - first < count ? 0x3F80 : 0;
+#pragma unroll
+        for (int d = 0; d < 2 * NB; d++) {
+          Turned v = turned(from + 32 * d, 16 * R::kPitch), bad;
 #pragma unroll
           for (int i = 0; i < 8; i++) {
             const bool is = (v.bits[i] & 0x7FFF) > 0x7F80;
             bad.bits[i] = is ? 0x3F80 : 0;
             v.bits[i] = is ? 0 : v.bits[i];
-            seen.bits[i] = key0 + 32 * h + 16 * (i / 4) + 4 * j + (i & 3) - first < count ? 0x3F80 : 0;
           }
           const f32x4 hit = mfma(bad.all, seen.all, f32x4{0, 0, 0, 0});
 #pragma unroll
           for (int i = 0; i < 4; i++)
             if (hit[i] > 0.0f) r.o[d][i] = __builtin_nanf("");
-        }
 #pragma unroll
-        for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v.all, wp[p], r.o[d]);
+          for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v.all, wp[p], r.o[d]);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < 2 * NB; d++) {
+          const Turned v = turned(from + 32 * d, 16 * R::kPitch);
+#pragma unroll
+          for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v.all, wp[p], r.o[d]);
+        }
       }
       lds_in_order();
     }
