@@ -21,13 +21,16 @@
 // lie, and reads them back through ds_read_b64_tr_b16, 4 keys of 16 values at a
 // time.  Rows are 32 bytes apart modulo 64, so eight of them fill the banks.
 // Codes become BF16 exactly: 2 significant bits and BF16's range.
+#include <algorithm>
+
 #include "zn_kv.h"
 
 namespace zn {
 namespace {
 
 constexpr int kTile = 64;       // keys a wave takes at a time
-constexpr int kWaves = 4;       // of a workgroup, which share out its keys
+constexpr int kWaves = 4;       // of a workgroup
+constexpr uint32_t kLeast = 2;  // tiles that a wave takes at least
 constexpr float kRise = 8.0f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -142,114 +145,83 @@ __device__ __forceinline__ Request request(const AttnArgs &a, uint32_t b) {
   return r;
 }
 
-// How the work is shared out.  Rows go in groups of ROWS (a power of two), the
-// keys of a group in pieces of `piece` tiles, so that a head's items, (request,
-// rows, piece), come to about `items`: with tiles t_b and row groups g_b,
-//   sum g_b ceil(t_b / piece) <= sum g_b t_b / piece + sum g_b <= items + sum g_b.
-// Every workgroup finds its own item from the lengths (two sums over the
-// requests); the host knows the bound alone.
-struct Plan {
-  uint32_t items;      // wanted of a head
-  uint32_t least;      // tiles of a piece at least
-};
-struct Item {
-  uint32_t b, group, piece, pieces, first;   // first: item number of the request's first
-  uint32_t from, to;                         // tiles of keys
-};
+// Values that are the same in all lanes, known to be so.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return uint64_t(uniform(uint32_t(v >> 32))) << 32 | uniform(uint32_t(v));
+}
+__device__ __forceinline__ Request uniform(const Request &r) {
+  return Request{uniform(r.start), uniform(r.n), uniform(r.len), uniform(r.lo), uniform(r.tiles), uniform(uint32_t(r.bad)) != 0};
+}
 
-template <int THREADS>
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t &sum) {
-  __shared__ uint32_t part[THREADS / 64];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t x = v;
+// How the work is shared out.  Rows of a request go in groups of `rows`, and the
+// tiles of all groups of all requests, one after the other (a group without any
+// counts as one), are cut into equal shares, one for each of a head's `takers`,
+// whatever the requests' lengths are.  A group that lies in several shares is left
+// in pieces and joined by a second launch: its first piece in slot 2 f + 1 of its
+// first taker f, the others in slots 2 i, so that no taker has two of a kind.
+// Every taker finds its place by itself, with a sum over the requests.
+// Groups are counted in 32 bits: the host keeps tokens * group + batch below 2^30.
+struct Plan {
+  uint32_t takers;     // of a head
+  uint32_t least;      // tiles of a share at least
+};
+struct Shares {
+  uint64_t total, each;
+};
+__device__ __forceinline__ uint32_t groups_of(const AttnArgs &a, const Request &r, uint32_t rows) {
+  return (r.n * a.group + rows - 1) / rows;
+}
+__device__ __forceinline__ uint64_t tiles_of(const AttnArgs &a, const Request &r, uint32_t rows) {
+  return uint64_t(groups_of(a, r, rows)) * max(r.tiles, 1u);
+}
+
+// The request of tile `taker * each` and the tiles before it, by one wave: a lane
+// sums batch / 64 requests in a row.
+__device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, uint32_t rows, uint32_t taker,
+                                           Shares &sh, uint32_t &b, uint64_t &before) {
+  const uint32_t lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
+  uint64_t mine = 0;
+  for (uint32_t i = 0; i < per; i++)
+    if (lane * per + i < a.batch) mine += tiles_of(a, request(a, lane * per + i), rows);
+  uint64_t upto = mine;
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
-    const uint32_t p = __shfl_up(x, d);
-    if (lane >= uint32_t(d)) x += p;
+    const uint64_t p = __shfl_up(upto, d);
+    if (lane >= uint32_t(d)) upto += p;
   }
-  __syncthreads();
-  if (lane == 63) part[wave] = x;
-  __syncthreads();
-  uint32_t before = 0;
-  sum = 0;
-#pragma unroll
-  for (uint32_t w = 0; w < THREADS / 64; w++) {
-    if (w < wave) before += part[w];
-    sum += part[w];
+  sh.total = __shfl(upto, 63);
+  sh.each = (sh.total + plan.takers - 1) / plan.takers;
+  if (sh.each < plan.least) sh.each = plan.least;
+  const uint64_t want = taker * sh.each;
+  if (want >= sh.total) return false;
+  const uint32_t owner = __popcll(__ballot(upto <= want));
+  before = __shfl(upto - mine, int(owner));
+  b = owner * per;
+  for (;; b++) {
+    const uint64_t t = tiles_of(a, request(a, b), rows);
+    if (want < before + t) return true;
+    before += t;
   }
-  return x - v + before;
 }
 
-// Row groups and items are counted in 32 bits: the host keeps tokens * group +
-// batch below 2^30, and starts in order then keep every count there.  Starts out
-// of order may wrap the counts: an item found is one of its request all the same.
-template <int THREADS>
-__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint32_t rows, uint32_t want, Item &it,
-                                          uint2 *meta) {
-  __shared__ unsigned long long total;
-  __shared__ Item found;
-  if (threadIdx.x == 0) {
-    total = 0;
-    found.pieces = 0;
-  }
-  __syncthreads();
-  uint64_t mine = 0;
-  for (uint32_t b = threadIdx.x; b < a.batch; b += THREADS) {
-    const Request r = request(a, b);
-    mine += uint64_t((r.n * a.group + rows - 1) / rows) * r.tiles;
-  }
-  if (mine) atomicAdd(&total, (unsigned long long)mine);
-  __syncthreads();
-  const uint64_t each = (total + plan.items - 1) / plan.items;
-  const uint32_t piece = each < plan.least ? plan.least : uint32_t(each);
-  uint32_t done = 0;
-  for (uint32_t b0 = 0; b0 < a.batch; b0 += THREADS) {
-    const uint32_t b = b0 + threadIdx.x;
-    Request r = {};
-    uint32_t groups = 0, pieces = 0;
-    if (b < a.batch) {
-      r = request(a, b);
-      groups = (r.n * a.group + rows - 1) / rows;
-      pieces = (r.tiles + piece - 1) / piece;
-      pieces = pieces ? pieces : 1;
-    }
-    uint32_t sum;
-    const uint32_t first = done + block_scan<THREADS>(groups * pieces, sum);
-    if (meta && b < a.batch) meta[b] = make_uint2(first, pieces);
-    if (want >= first && want - first < groups * pieces) {
-      const uint32_t i = want - first;
-      found.b = b;
-      found.group = i / pieces;
-      found.piece = i - found.group * pieces;
-      found.pieces = pieces;
-      found.first = first;
-      found.from = found.piece * piece;
-      found.to = min(r.tiles, found.from + piece);
-    }
-    done += sum;
-    if (done > want && !meta) break;
-  }
-  __syncthreads();
-  it = found;
-  return it.pieces != 0;
-}
-
-// ---------------------------------------------------------------- few rows --
-// Scratch: where each request's items begin and how many pieces it has; then
-// per item and key head 16 rows of sums, and their (m, l).
+// Scratch: the shares' size; the tiles before each request's; then per head and
+// slot `rows` rows of sums, and their (m, l).
 struct Parts {
-  uint2 *meta;
+  uint64_t *each, *before;
   float2 *ml;
   float *sums;
-  uint32_t items;   // of a key head
+  uint32_t slots;   // of a key head
 };
-__host__ __device__ __forceinline__ Parts parts(uint8_t *scratch, uint32_t batch, uint32_t kv_heads, uint32_t items) {
+__host__ __device__ __forceinline__ Parts parts(uint8_t *scratch, uint32_t batch, uint32_t kv_heads, uint32_t slots,
+                                                uint32_t rows) {
   Parts p;
-  p.meta = reinterpret_cast<uint2 *>(scratch);
-  const uint64_t head = (uint64_t(batch) * 8 + 255) / 256 * 256;
+  p.each = reinterpret_cast<uint64_t *>(scratch);
+  p.before = p.each + 1;
+  const uint64_t head = (uint64_t(batch) * 8 + 8 + 255) / 256 * 256;
   p.ml = reinterpret_cast<float2 *>(scratch + head);
-  p.sums = reinterpret_cast<float *>(scratch + head + uint64_t(kv_heads) * items * 16 * 8);
-  p.items = items;
+  p.sums = reinterpret_cast<float *>(scratch + head + uint64_t(kv_heads) * slots * rows * 8);
+  p.slots = slots;
   return p;
 }
 
@@ -282,25 +254,39 @@ struct Rows16 {
 };
 
 template <int DT, int NB>
-__global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_attend(AttnArgs a, Plan plan, Parts out, FastDiv per_group, float c) {
+constexpr int kResident = DT == BF16 && NB <= 2 ? 3 : DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
+
+template <int DT, int NB>
+__global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(AttnArgs a, Plan plan, Parts out,
+                                                                        FastDiv per_group, float c) {
   using R = Rows16<DT, NB>;
   constexpr int D = 32 * NB;
-  constexpr int kPad = D + 4;   // floats of a row where the waves join
-  constexpr int kShared = kWaves * (R::kLds > 64 * kPad ? R::kLds : 64 * kPad);
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kShared];
-  __shared__ float2 ml_of[kWaves][16];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * R::kLds];
   const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t n = lane & 15, j = lane >> 4;
-  const uint32_t head = blockIdx.y;
+  const uint32_t head = blockIdx.y, taker = blockIdx.x * kWaves + wave;
 
-  Item it;
-  if (!find_item<64 * kWaves>(a, plan, 16, blockIdx.x, it, blockIdx.x + blockIdx.y == 0 ? out.meta : nullptr)) return;
-  it.b = __builtin_amdgcn_readfirstlane(it.b);
-  it.from = __builtin_amdgcn_readfirstlane(it.from);
-  it.to = __builtin_amdgcn_readfirstlane(it.to);
-  const Request rq = request(a, it.b);
+  Shares share;
+  uint32_t b;
+  uint64_t before;
+  if (taker >= plan.takers || !find_start(a, plan, 16, taker, share, b, before)) return;
+  share.each = uniform(share.each);
+  b = uniform(b);
+  before = uniform(before);
+  uint64_t at_tile = taker * share.each;
+  const uint64_t end_tile = min(at_tile + share.each, uniform(share.total));
+  if (taker == 0 && head == 0 && out.each && lane == 0) *out.each = share.each;
+  // group after group, request after request
+  while (at_tile < end_tile) {
+  const Request rq = uniform(request(a, b));
+  const uint32_t whole = max(rq.tiles, 1u);
+  const uint32_t groups = groups_of(a, rq, 16);
+  const uint32_t grp = groups > 1 ? uint32_t((at_tile - before) / whole) : 0;
+  const uint32_t from = uint32_t(at_tile - before - uint64_t(grp) * whole);
+  const uint32_t to = uint32_t(min(uint64_t(whole), from + (end_tile - at_tile)));
+  if (out.before && at_tile == before && head == 0 && lane == 0) out.before[b] = before;
   // this lane's row
-  const uint32_t row = it.group * 16 + n;
+  const uint32_t row = grp * 16 + n;
   const bool live = row < rq.n * a.group;
   const uint32_t token = live ? per_group.div(row) : 0;
   const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
@@ -325,10 +311,10 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
     low_all = max(low_all, uint32_t(__shfl_xor(int(low_all), d)));
     high_all = min(high_all, uint32_t(__shfl_xor(int(high_all), d)));
   }
-  low = __builtin_amdgcn_readfirstlane(low);
-  high = __builtin_amdgcn_readfirstlane(high);
-  low_all = __builtin_amdgcn_readfirstlane(low_all);
-  high_all = __builtin_amdgcn_readfirstlane(high_all);
+  low = uniform(low);
+  high = uniform(high);
+  low_all = uniform(low_all);
+  high_all = uniform(high_all);
 
   R r;
 #pragma unroll
@@ -362,7 +348,7 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
   uint8_t *mine = lds + wave * R::kLds;
   const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
   const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
-  const int32_t *pages = a.table + it.b * a.table_stride;
+  const int32_t *pages = a.table + b * a.table_stride;
   const uint32_t mask = (1u << a.c.shift) - 1;
   const uint32_t place = uint32_t(a.c.place_stride);
   const uint32_t last = a.c.n_pages;
@@ -375,24 +361,27 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
   uint32_t kw[4][NB], kb[4][kBytes];
   u32x4 vw[2][kUnits];
   uint32_t vb[2][kUnits];
-  // The page of each 16 keys; a place outside any page is taken from page 0 and
-  // counts as a NaN.
+  // The page of each 16 keys of a tile, lane g % 4 that of 16 g; asked for a tile
+  // ahead of the codes.  Behind the last key it is the last one's.
+  auto ask_pages = [&](uint32_t key0) {
+    return uint32_t(pages[min(key0 + 16 * (lane & 3), rq.len - 1) >> a.c.shift]);
+  };
+  // A place outside any page is taken from page 0 and counts as a NaN.
   struct Where {
     uint64_t base[4];
     uint32_t gone;
   };
-  auto where = [&](uint32_t key0) {
+  auto where = [&](uint32_t key0, uint32_t asked) {
     Where w;
     w.gone = 0;
 #pragma unroll
     for (int g = 0; g < 4; g++) {
-      const uint32_t key = key0 + 16 * g;
-      uint32_t page = key < rq.len ? uint32_t(pages[key >> a.c.shift]) : 0;
+      uint32_t page = __builtin_amdgcn_readlane(asked, g);
       if (page >= last) {
         page = 0;
         w.gone |= 1u << g;
       }
-      w.base[g] = page * a.c.page_stride + (key & mask) * uint64_t(place);
+      w.base[g] = page * a.c.page_stride + ((key0 + 16 * g) & mask) * uint64_t(place);
     }
     return w;
   };
@@ -420,21 +409,20 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
       }
   };
 
-  // this wave's tiles that some row sees
-  uint32_t t = it.from + wave, end = it.to;
-  if (high > rq.lo) end = min(end, (high - rq.lo + kTile - 1) / kTile);
-  else end = 0;
-  if (low > rq.lo + t * kTile) {
-    const uint32_t skip = ((low - rq.lo) / kTile - t + kWaves - 1) / kWaves;   // low >= rq.lo + t * kTile
-    t += skip * kWaves;
-  }
+  // the tiles that some row sees
+  uint32_t t = from, end = min(to, rq.tiles);
+  end = high > rq.lo ? min(end, (high - rq.lo + kTile - 1) / kTile) : 0;
+  if (low > rq.lo) t = max(t, (low - rq.lo) / kTile);
   Where w = {};
+  uint32_t asked = 0;
   if (t < end) {
-    w = where(rq.lo + t * kTile);
+    asked = ask_pages(rq.lo + t * kTile);
+    w = where(rq.lo + t * kTile, asked);
+    asked = ask_pages(rq.lo + (t + 1) * kTile);
     ask_keys(w);
     ask_values(w);
   }
-  for (; t < end; t += kWaves) {
+  for (; t < end; t++) {
     const uint32_t key0 = rq.lo + t * kTile;
     // scores
     f32x4 s[4];
@@ -453,9 +441,10 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
       }
       s[g] = acc;
     }
-    const bool more = t + kWaves < end;
+    const bool more = t + 1 < end;
     if (more) {
-      w = where(key0 + kWaves * kTile);
+      w = where(key0 + kTile, asked);
+      asked = ask_pages(key0 + 2 * kTile);
       ask_keys(w);
     }
     // keys that the row does not see
@@ -556,54 +545,45 @@ __global__ __launch_bounds__(64 * kWaves, DT == BF16 && NB <= 4 ? 2 : 1) void k_
     }
   }
 
-  // the waves' sums join
   r.l = sum_j(r.l);
   if (rq.bad) r.l = __builtin_nanf("");
-  if (j == 0) ml_of[wave][n] = make_float2(r.m, r.l);
-  __syncthreads();
-  float *joined = reinterpret_cast<float *>(lds);
+  if (live) {
+    if (to - from == whole) {
+      const uint64_t y = rq.start + token;
+      const float f = over(r.l);
+      uint8_t *p = a.out + (y * a.out_token + qh * a.out_head + 4 * j) * esize(DT);
 #pragma unroll
-  for (int d = 0; d < 2 * NB; d++)
-    *reinterpret_cast<f32x4 *>(joined + (wave * 16 + n) * kPad + 16 * d + 4 * j) = r.o[d];
-  __syncthreads();
-  for (uint32_t i = threadIdx.x; i < 16 * D / 4; i += 64 * kWaves) {
-    const uint32_t rr = i / (D / 4), col = (i % (D / 4)) * 4;
-    const uint32_t rw = it.group * 16 + rr;
-    if (rw >= rq.n * a.group) continue;
-    float top = ml_of[0][rr].x;
-#pragma unroll
-    for (int w = 1; w < kWaves; w++) top = fmaxf(top, ml_of[w][rr].x);
-    float l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kWaves; w++) {
-      const float2 ml = ml_of[w][rr];
-      const float f = ml.x == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
-      l += ml.y * f;
-      o += *reinterpret_cast<const f32x4 *>(joined + (w * 16 + rr) * kPad + col) * f;
-    }
-    if (it.pieces == 1) {
-      const uint32_t tk = per_group.div(rw), h = head * a.group + rw - tk * a.group;
-      const uint64_t y = rq.start + tk;
-      const float f = over(l);
-      store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * f);
-      if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
+      for (int d = 0; d < 2 * NB; d++) store4<DT>(p + 16 * d * esize(DT), r.o[d] * f);
+      if (a.lse && j == 0) a.lse[y * a.heads + qh] = log_sum(r.m, r.l);
     } else {
-      const uint64_t p = (uint64_t(head) * out.items + blockIdx.x) * 16 + rr;
-      *reinterpret_cast<f32x4 *>(out.sums + p * D + col) = o;
-      if (col == 0) out.ml[p] = make_float2(top, l);
+      const uint64_t p = (uint64_t(head) * out.slots + 2 * taker + (from == 0)) * 16 + n;
+#pragma unroll
+      for (int d = 0; d < 2 * NB; d++) *reinterpret_cast<f32x4 *>(out.sums + p * D + 16 * d + 4 * j) = r.o[d];
+      if (j == 0) out.ml[p] = make_float2(r.m, r.l);
     }
+  }
+  at_tile += to - from;
+  if (at_tile == before + uint64_t(groups) * whole) {
+    before = at_tile;
+    do b++;
+    while (at_tile < end_tile && uniform(request(a, b)).n == 0);
+  }
   }
 }
 
-// Joins the pieces of a row, in their order: a wave a row, four values a lane.
+// Joins the pieces of a row: a workgroup a row, four values a lane; its lanes make
+// 256 / (D / 4) teams that take every so manieth piece in order, and their sums are
+// added in order.
 template <int DT, int NB>
 __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group) {
-  constexpr int D = 32 * NB;
-  const uint32_t lane = threadIdx.x & 63;
+  constexpr int D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
+  __shared__ float tops[4];
+  __shared__ __attribute__((aligned(16))) float sums[kTeams][D + 4];
+  __shared__ float weights[kTeams];
   const uint32_t head = blockIdx.y;
   // the rows' groups of 16, numbered with gaps: request b's from starts[b] group / 16 + b
-  const uint32_t slot = blockIdx.x;
+  const uint32_t rows = a.starts ? 16 : min(16u, a.group);   // of a group, at most
+  const uint32_t slot = blockIdx.x / rows, rr = blockIdx.x - slot * rows;
   uint32_t b;
   if (a.starts) {
     uint32_t lo = 0, hi = a.batch;
@@ -622,92 +602,127 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
   }
   const Request rq = request(a, b);
   const uint32_t group = a.starts ? slot - (rq.start * a.group / 16 + b) : slot % ((a.group + 15) / 16);
-  const uint2 meta = in.meta[b];
-  if (meta.y <= 1 || group >= (rq.n * a.group + 15) / 16) return;
-  // starts out of order: items past the grid were not made
-  if (meta.x >= in.items || uint64_t(group + 1) * meta.y > in.items - meta.x) return;
-  for (uint32_t rr = threadIdx.x >> 6; rr < 16; rr += 4) {
-    const uint32_t row = group * 16 + rr;
-    if (row >= rq.n * a.group) return;
-    const uint64_t p0 = uint64_t(head) * in.items + meta.x + group * meta.y;
-    float top = -__builtin_inff();
-    for (uint32_t i = lane; i < meta.y; i += 64) top = fmaxf(top, in.ml[(p0 + i) * 16 + rr].x);
+  const uint32_t row = group * 16 + rr;
+  if (group >= groups_of(a, rq, 16) || row >= rq.n * a.group) return;
+  const uint64_t whole = max(rq.tiles, 1u), at = in.before[b] + group * whole, each = *in.each;
+  const uint64_t f = at / each, pieces = (at + whole - 1) / each - f + 1;
+  if (pieces <= 1) return;
+  if (pieces > in.slots || 2 * f > in.slots - pieces) return;   // starts out of order: not all tiles had a taker
+  const uint32_t count = uint32_t(pieces);
+  const uint64_t p0 = uint64_t(head) * in.slots + 2 * f;
+  // a row's piece i
+  auto piece = [&](uint32_t i) { return (p0 + (i ? 2 * i : 1)) * 16 + rr; };
+
+  float top = -__builtin_inff();
+  for (uint32_t i = threadIdx.x; i < count; i += 256) top = fmaxf(top, in.ml[piece(i)].x);
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+
+  const uint32_t team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  if (team < kTeams) {
     float l = 0.0f;
     f32x4 o = {0, 0, 0, 0};
-    for (uint32_t i = 0; i < meta.y; i++) {
-      const uint64_t p = (p0 + i) * 16 + rr;
+#pragma unroll 4
+    for (uint32_t i = team; i < count; i += kTeams) {
+      const uint64_t p = piece(i);
       const float2 ml = in.ml[p];
       const float f = ml.x == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
       l += ml.y * f;
-      if (lane < D / 4) o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + 4 * lane) * f;
+      o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
     }
-    const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
-    const uint64_t y = rq.start + tk;
-    if (lane < D / 4) store4<DT>(a.out + (y * a.out_token + h * a.out_head + 4 * lane) * esize(DT), o * over(l));
-    if (a.lse && lane == 0) a.lse[y * a.heads + h] = log_sum(top, l);
+    *reinterpret_cast<f32x4 *>(&sums[team][col]) = o;
+    if (col == 0) weights[team] = l;
   }
+  __syncthreads();
+  if (threadIdx.x >= kLanes) return;
+  float l = 0.0f;
+  f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < kTeams; i++) {
+    l += weights[i];
+    o += *reinterpret_cast<const f32x4 *>(&sums[i][col]);
+  }
+  const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
+  const uint64_t y = rq.start + tk;
+  store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
+  if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
 }
 
 // ------------------------------------------------------------------ launch --
+// The takers fill the chip once, so that they all run at the same time.
+template <int DT, int NB>
+Plan few_plan(const AttnArgs &a) {
+  constexpr uint32_t kSimds = 1024;
+  const uint32_t n = kSimds * kResident<DT, NB> / a.c.heads;
+  return Plan{n ? n : 1, kLeast};
+}
 struct Sizes {
-  Plan plan;
-  uint32_t groups, items;  // row groups of 16 and items of a key head, at most
+  uint32_t groups;         // row groups of a key head, at most
   bool split;              // some request may be cut into pieces
 };
-Sizes sizes(const AttnArgs &a) {
+Sizes sizes(const AttnArgs &a, uint32_t rows, uint32_t least) {
   Sizes s;
-  s.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / 16 + a.batch) : a.batch * ((a.group + 15) / 16);
-  const uint32_t want = 1024 / a.c.heads;
-  s.plan.items = want ? want : 1;
-  s.plan.least = 4;
-  const uint64_t longest = (uint64_t(a.width) << a.c.shift) / kTile + 1;
-  s.split = longest > s.plan.least;
-  s.items = s.groups + (s.split ? s.plan.items : 0);
+  s.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / rows + a.batch) : a.batch * ((a.group + rows - 1) / rows);
+  // a share never ends inside a request that is all there is
+  s.split = (uint64_t(a.width) << a.c.shift) > uint64_t(least) * kTile || s.groups > 1;
   return s;
 }
 
 template <int DT, int NB>
-hipError_t attend(const AttnArgs &a, hipStream_t s) {
-  const Sizes z = sizes(a);
-  const Parts p = parts(a.scratch, a.batch, a.c.heads, z.items);
-  const float c = float(double(a.scale) * 1.4426950408889634);
-  const FastDiv per_group(a.group);
-  Parts q = p;
-  if (!z.split) q.meta = nullptr;
-  k_attend<DT, NB><<<dim3(z.items, a.c.heads), 64 * kWaves, 0, s>>>(a, z.plan, q, per_group, c);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !z.split) return e;
-  k_join<DT, NB><<<dim3(z.groups, a.c.heads), 256, 0, s>>>(a, p, per_group);
-  return hipGetLastError();
-}
+struct Few {
+  static uint64_t scratch(const AttnArgs &a) {
+    const Plan plan = few_plan<DT, NB>(a);
+    if (!sizes(a, 16, plan.least).split) return 0;
+    const Parts p = parts(nullptr, a.batch, a.c.heads, 2 * plan.takers, 16);
+    return reinterpret_cast<uint64_t>(p.sums) + uint64_t(a.c.heads) * 2 * plan.takers * 16 * NB * 32 * 4;
+  }
+  static hipError_t run(const AttnArgs &a, hipStream_t s) {
+    const Plan plan = few_plan<DT, NB>(a);
+    const Sizes z = sizes(a, 16, plan.least);
+    Parts p = {};
+    if (z.split) p = parts(a.scratch, a.batch, a.c.heads, 2 * plan.takers, 16);
+    const FastDiv per_group(a.group);
+    // no more takers than the table's width gives tiles to
+    const uint64_t tiles = uint64_t(z.groups) * (((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile + 1);
+    const uint64_t busy = std::min<uint64_t>(plan.takers, (tiles + plan.least - 1) / plan.least);
+    k_attend<DT, NB><<<dim3(uint32_t((busy + kWaves - 1) / kWaves), a.c.heads), 64 * kWaves, 0, s>>>(
+        a, plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !z.split) return e;
+    const uint32_t rows = a.starts || a.group > 16 ? 16 : a.group;
+    k_join<DT, NB><<<dim3(z.groups * rows, a.c.heads), 256, 0, s>>>(a, p, per_group);
+    return hipGetLastError();
+  }
+};
 
-template <int DT>
-hipError_t by_blocks(const AttnArgs &a, hipStream_t s) {
-  switch (a.c.blocks) {
-    case 1: return attend<DT, 1>(a, s);
-    case 2: return attend<DT, 2>(a, s);
-    case 3: return attend<DT, 3>(a, s);
-    case 4: return attend<DT, 4>(a, s);
-    case 5: return attend<DT, 5>(a, s);
-    case 6: return attend<DT, 6>(a, s);
-    case 7: return attend<DT, 7>(a, s);
-    default: return attend<DT, 8>(a, s);
+// f of the kernels for the call's type and head size.
+template <int DT, class F>
+auto by_blocks(uint32_t blocks, F f) {
+  switch (blocks) {
+    case 1: return f(Few<DT, 1>());
+    case 2: return f(Few<DT, 2>());
+    case 3: return f(Few<DT, 3>());
+    case 4: return f(Few<DT, 4>());
+    case 5: return f(Few<DT, 5>());
+    case 6: return f(Few<DT, 6>());
+    case 7: return f(Few<DT, 7>());
+    default: return f(Few<DT, 8>());
   }
 }
 
 }  // namespace
 
 uint64_t attention_scratch(int dtype, const AttnArgs &a) {
-  const Sizes z = sizes(a);
-  if (!z.split) return 0;
-  const Parts p = parts(nullptr, a.batch, a.c.heads, z.items);
-  return reinterpret_cast<uint64_t>(p.sums) + uint64_t(a.c.heads) * z.items * 16 * a.c.blocks * 32 * 4;
+  auto f = [&](auto k) { return k.scratch(a); };
+  return dtype == BF16 ? by_blocks<BF16>(a.c.blocks, f) : by_blocks<FP32>(a.c.blocks, f);
 }
 
 hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s) {
-  return dtype == BF16 ? by_blocks<BF16>(a, s) : by_blocks<FP32>(a, s);
+  auto f = [&](auto k) { return k.run(a, s); };
+  return dtype == BF16 ? by_blocks<BF16>(a.c.blocks, f) : by_blocks<FP32>(a.c.blocks, f);
 }
 
 }  // namespace zn

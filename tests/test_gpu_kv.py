@@ -393,16 +393,19 @@ def test_attention_checks_what_the_device_holds():
     # lengths past the table, and below 0
     out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32([table.shape[1] * 16 + 1, -7, 200]), lse=True)
     assert out[0].isnan().all() and lse[0].isnan().all()
-    assert (out[1] == 0).all() and (lse[1] == -torch.inf).all() and torch.equal(out[2], want[2])
+    assert (out[1] == 0).all() and (lse[1] == -torch.inf).all()
+    # (the order of a request's sums goes by all lengths: the same result, not the same bits)
+    check_attention(q[2:], c, table[2:], lens[2:], None, 16, out[2:], lse[2:])
     out = zn.mx_attention(q, c, i32(table.tolist()), i32([2 ** 31 - 1, -2 ** 31, 200]))
-    assert out[0].isnan().all() and (out[1] == 0).all() and torch.equal(out[2], want[2])
+    assert out[0].isnan().all() and (out[1] == 0).all()
+    check_attention(q[2:], c, table[2:], lens[2:], None, 16, out[2:])
     # a table without columns
     out = zn.mx_attention(q, c, torch.zeros(3, 0, dtype=torch.int32, device="cuda"), i32([0, 0, 0]))
     assert (out == 0).all()
     # starts outside the queries, and a request that ends before it starts
     out = torch.full_like(q, 7.0)
     zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32([-5, 1, 1, 9]), out=out)
-    assert torch.equal(out[0], want[0])
+    check_attention(q, c, table, lens, [0, 1, 1, 3], 16, out)
     zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32([2, -1, 3, 1]), out=out)
     torch.cuda.synchronize()
 
