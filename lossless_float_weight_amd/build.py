@@ -12,7 +12,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libzn.so")
 SOURCES = ["zn_api.hip", "zn_encode.hip", "zn_decode.hip", "zn_setup.hip", "zn_mx_api.hip", "zn_mx.hip", "zn_mxmm.hip",
-           "zn_kv_api.hip", "zn_kv.hip", "zn_attn.hip"]
+           "zn_kv_api.hip", "zn_kv.hip", "zn_attn.hip", "zn_attn_tall.hip"]
 ARCH = os.environ.get("ZN_OFFLOAD_ARCH", "gfx950")
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          # packed FP32 instructions are kept out of every kernel

@@ -1,0 +1,240 @@
+// zn_attn.h -- attention over the key-value cache in 4 bits: what its kernels
+// share.  Codes become BF16 exactly (2 significant bits and BF16's range) and are
+// multiplied by the BF16 matrix instructions, which add in FP32.
+#pragma once
+#include "zn_kv.h"
+
+namespace zn {
+
+constexpr uint32_t kTile = 64;  // keys that a wave takes at a time
+// The weights' bound m rises to this much (as a power of two) above a score that
+// passes it.
+constexpr float kRise = 8.0f;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
+
+// A wave's own LDS operations run in order; the compiler keeps it.
+__device__ __forceinline__ void lds_in_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Eight codes under a scale (a float's exponent field: 0 is 2^-127, 255 a NaN).
+__device__ __forceinline__ bf16x8 values8(uint32_t w, float s) {
+  union {
+    bf16x2 p[4];
+    bf16x8 all;
+  } o;
+  o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
+  o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
+  o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
+  o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
+  return o.all;
+}
+// Bytes over 252 would leave BF16's range: NaNs, like 255.
+__device__ __forceinline__ float scale_of(uint32_t s) {
+  return __uint_as_float(s > 252u ? 0x7FC00000u : s << 23);
+}
+
+// Eight FP32 values as N BF16 pieces whose sum they are (up to 2^-(8 N) of them).
+template <int N>
+__device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&out)[N]) {
+  float rest[8];
+#pragma unroll
+  for (int i = 0; i < 8; i++) rest[i] = x[i];
+#pragma unroll
+  for (int n = 0; n < N; n++) {
+    union {
+      uint32_t w[4];
+      bf16x8 all;
+    } o;
+#pragma unroll
+    for (int i = 0; i < 4; i++) o.w[i] = f32_bf16x2(rest[2 * i], rest[2 * i + 1]);
+    out[n] = o.all;
+    if (n + 1 < N) {
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        rest[2 * i] -= bf16_lo(o.w[i]);
+        rest[2 * i + 1] -= bf16_hi(o.w[i]);
+      }
+    }
+  }
+}
+
+// Eight keys of one value from LDS: 4 rows from `p`, 4 from `p + next`, where this
+// lane's address is its part of a row (4 values of a row a lane, 4 lanes a row).
+__device__ __forceinline__ bf16x8 turned(const uint8_t *p, int next) {
+  typedef __attribute__((address_space(3))) s16x4 lds16;
+  union {
+    s16x4 half[2];
+    bf16x8 all;
+  } t;
+  t.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p));
+  t.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p + next));
+  return t.all;
+}
+
+// A request of the call: its queries and the keys that any of them sees.
+struct Request {
+  uint32_t start, n, len;    // first query, queries, keys in the cache
+  uint32_t lo, tiles;        // tiles of keys from lo (a multiple of kTile) to len
+  bool bad;                  // longer than its table
+};
+__device__ __forceinline__ Request request(const AttnArgs &a, uint32_t b) {
+  Request r;
+  if (a.starts) {
+    const int32_t s = a.starts[b], e = a.starts[b + 1];
+    const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens), to = e < 0 ? 0 : min(uint32_t(e), a.tokens);
+    r.start = from;
+    r.n = to > from ? to - from : 0;
+  } else {
+    r.start = b;
+    r.n = 1;
+  }
+  const int32_t len = a.lens[b];
+  r.len = len < 0 ? 0 : uint32_t(len);
+  r.bad = r.len > (uint64_t(a.width) << a.c.shift);
+  if (r.bad) r.len = 0;
+  const uint32_t back = r.n + a.window - 1;   // keys before the end that the first query's window reaches
+  r.lo = a.window && r.len > back ? (r.len - back) / kTile * kTile : 0;
+  r.tiles = r.n ? (r.len - r.lo + kTile - 1) / kTile : 0;
+  return r;
+}
+
+// Keys that query `token` of a request sees: first + 0 .. count - 1.
+struct Span {
+  uint32_t first, count;
+};
+__device__ __forceinline__ Span span(const AttnArgs &a, const Request &r, uint32_t token, bool live) {
+  const int64_t at = int64_t(r.len) - r.n + token;   // its position
+  const int64_t end = a.causal ? at + 1 : int64_t(r.len);
+  const int64_t begin = a.window && end > a.window ? end - a.window : 0;
+  return live && end > begin ? Span{uint32_t(begin), uint32_t(end - begin)} : Span{0, 0};
+}
+
+// Eight consecutive values of a row of q.
+template <int DT>
+__device__ __forceinline__ void take_row8(const uint8_t *p, float (&x)[8]) {
+  if constexpr (DT == BF16) {
+    const u32x4 w = *reinterpret_cast<const u32x4_any *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+  } else {
+    const f32x4 y = *reinterpret_cast<const f32x4_any *>(p), z = *reinterpret_cast<const f32x4_any *>(p + 16);
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      x[i] = y[i];
+      x[4 + i] = z[i];
+    }
+  }
+}
+
+// Values that are the same in all lanes, known to be so.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint64_t uniform(uint64_t v) {
+  return uint64_t(uniform(uint32_t(v >> 32))) << 32 | uniform(uint32_t(v));
+}
+__device__ __forceinline__ Request uniform(const Request &r) {
+  return Request{uniform(r.start), uniform(r.n), uniform(r.len), uniform(r.lo), uniform(r.tiles), uniform(uint32_t(r.bad)) != 0};
+}
+
+__device__ __forceinline__ uint32_t groups_of(const AttnArgs &a, const Request &r, uint32_t rows) {
+  return (r.n * a.group + rows - 1) / rows;
+}
+
+// Scratch: how the work was shared out (`each`, and `before` of every request);
+// then per head and slot `rows` rows of (m, l), and of sums.
+struct Parts {
+  uint64_t *each, *before;
+  float2 *ml;
+  float *sums;
+  uint32_t slots;   // of a key head
+};
+__host__ __device__ __forceinline__ Parts parts(uint8_t *scratch, uint32_t batch, uint32_t kv_heads, uint32_t slots,
+                                                uint32_t rows) {
+  Parts p;
+  p.each = reinterpret_cast<uint64_t *>(scratch);
+  p.before = p.each + 1;
+  const uint64_t head = (uint64_t(batch) * 8 + 8 + 255) / 256 * 256;
+  p.ml = reinterpret_cast<float2 *>(scratch + head);
+  p.sums = reinterpret_cast<float *>(scratch + head + uint64_t(kv_heads) * slots * rows * 8);
+  p.slots = slots;
+  return p;
+}
+
+template <int DT>
+__device__ __forceinline__ void store4(uint8_t *p, f32x4 v) {
+  if constexpr (DT == BF16) {
+    *reinterpret_cast<u32x2_any *>(p) = u32x2{f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
+  } else {
+    *reinterpret_cast<f32x4_any *>(p) = v;
+  }
+}
+
+// Result of a row from its sums, weight and bound.
+__device__ __forceinline__ float over(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+}
+
+// NaNs among a tile's values would meet the weight 0 of rows that do not see their
+// key, so such a block goes in as zeros, and the rows that see it are marked: bit i
+// for block i of the values.  For the seldom tile that has some; a lane reads the
+// scale bytes of one key, at `scales`.
+template <int NB>
+__device__ __attribute__((noinline)) uint32_t marked(const uint8_t *scales, uint32_t key0, uint32_t first, uint32_t count) {
+  uint32_t mine = 0, bad = 0;
+  for (int i = 0; i < NB; i++) mine |= uint32_t(scales[i] > 252) << i;
+  for (uint64_t left = __ballot(mine != 0); left; left &= left - 1) {
+    const int k = __builtin_ctzll(left);
+    if (key0 + k - first < count) bad |= __builtin_amdgcn_readlane(mine, k);
+  }
+  return bad;
+}
+
+// A piece's share of a row: 2^(its bound - the largest one).
+__device__ __forceinline__ float share(float m, float top) {
+  return m == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+}
+// The last request b with before[b] <= v (before rises from 0).
+__device__ __forceinline__ uint32_t holder(const uint64_t *before, uint32_t batch, uint64_t v) {
+  uint32_t lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const uint32_t mid = (lo + hi) >> 1;
+    if (before[mid] <= v)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// f of the kernels K<type, blocks of 32 values of a head>, for the call's.
+template <template <int, int> class K, int DT, class F>
+auto by_blocks(uint32_t blocks, F f) {
+  switch (blocks) {
+    case 1: return f(K<DT, 1>());
+    case 2: return f(K<DT, 2>());
+    case 3: return f(K<DT, 3>());
+    case 4: return f(K<DT, 4>());
+    case 5: return f(K<DT, 5>());
+    case 6: return f(K<DT, 6>());
+    case 7: return f(K<DT, 7>());
+    default: return f(K<DT, 8>());
+  }
+}
+template <template <int, int> class K, class F>
+auto by_kind(int dtype, uint32_t blocks, F f) {
+  return dtype == BF16 ? by_blocks<K, BF16>(blocks, f) : by_blocks<K, FP32>(blocks, f);
+}
+
+// zn_attn_tall.hip
+uint64_t attention_tall_scratch(int dtype, const AttnArgs &a);
+hipError_t launch_attention_tall(int dtype, const AttnArgs &a, hipStream_t s);
+
+}  // namespace zn

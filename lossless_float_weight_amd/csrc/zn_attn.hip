@@ -23,19 +23,13 @@
 // Codes become BF16 exactly: 2 significant bits and BF16's range.
 #include <algorithm>
 
-#include "zn_kv.h"
+#include "zn_attn.h"
 
 namespace zn {
 namespace {
 
-constexpr int kTile = 64;       // keys a wave takes at a time
 constexpr int kWaves = 4;       // of a workgroup
 constexpr uint32_t kLeast = 2;  // tiles that a wave takes at least
-constexpr float kRise = 8.0f;
-
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -55,105 +49,6 @@ __device__ __forceinline__ float sum_j(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// A wave's own LDS operations run in order; the compiler keeps it.
-__device__ __forceinline__ void lds_in_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
-// Eight codes under a scale (a float's exponent field: 0 is 2^-127, 255 a NaN).
-__device__ __forceinline__ bf16x8 values8(uint32_t w, float s) {
-  union {
-    bf16x2 p[4];
-    bf16x8 all;
-  } o;
-  o.p[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0);
-  o.p[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1);
-  o.p[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2);
-  o.p[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3);
-  return o.all;
-}
-// Bytes over 252 would leave BF16's range: NaNs, like 255.
-__device__ __forceinline__ float scale_of(uint32_t s) {
-  return __uint_as_float(s > 252u ? 0x7FC00000u : s << 23);
-}
-
-// Eight FP32 values as N BF16 pieces whose sum they are (up to 2^-(8 N) of them).
-template <int N>
-__device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&out)[N]) {
-  float rest[8];
-#pragma unroll
-  for (int i = 0; i < 8; i++) rest[i] = x[i];
-#pragma unroll
-  for (int n = 0; n < N; n++) {
-    union {
-      uint32_t w[4];
-      bf16x8 all;
-    } o;
-#pragma unroll
-    for (int i = 0; i < 4; i++) o.w[i] = f32_bf16x2(rest[2 * i], rest[2 * i + 1]);
-    out[n] = o.all;
-    if (n + 1 < N) {
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        rest[2 * i] -= bf16_lo(o.w[i]);
-        rest[2 * i + 1] -= bf16_hi(o.w[i]);
-      }
-    }
-  }
-}
-
-// Eight keys of one value from LDS: 4 rows from `p`, 4 from `p + next`, where this
-// lane's address is its part of a row (4 values of a row a lane, 4 lanes a row).
-union Turned {
-  s16x4 half[2];
-  bf16x8 all;
-  uint16_t bits[8];
-};
-__device__ __forceinline__ Turned turned(const uint8_t *p, int next) {
-  typedef __attribute__((address_space(3))) s16x4 lds16;
-  Turned t;
-  t.half[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p));
-  t.half[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds16 *)(p + next));
-  return t;
-}
-
-// A request of the call: its queries and the keys that any of them sees.
-struct Request {
-  uint32_t start, n, len;    // first query, queries, keys in the cache
-  uint32_t lo, tiles;        // tiles of keys from lo (a multiple of kTile) to len
-  bool bad;                  // longer than its table
-};
-__device__ __forceinline__ Request request(const AttnArgs &a, uint32_t b) {
-  Request r;
-  if (a.starts) {
-    const int32_t s = a.starts[b], e = a.starts[b + 1];
-    const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens), to = e < 0 ? 0 : min(uint32_t(e), a.tokens);
-    r.start = from;
-    r.n = to > from ? to - from : 0;
-  } else {
-    r.start = b;
-    r.n = 1;
-  }
-  const int32_t len = a.lens[b];
-  r.len = len < 0 ? 0 : uint32_t(len);
-  r.bad = r.len > (uint64_t(a.width) << a.c.shift);
-  if (r.bad) r.len = 0;
-  const uint32_t back = r.n + a.window - 1;   // keys before the end that the first query's window reaches
-  r.lo = a.window && r.len > back ? (r.len - back) / kTile * kTile : 0;
-  r.tiles = r.n ? (r.len - r.lo + kTile - 1) / kTile : 0;
-  return r;
-}
-
-// Values that are the same in all lanes, known to be so.
-__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
-__device__ __forceinline__ uint64_t uniform(uint64_t v) {
-  return uint64_t(uniform(uint32_t(v >> 32))) << 32 | uniform(uint32_t(v));
-}
-__device__ __forceinline__ Request uniform(const Request &r) {
-  return Request{uniform(r.start), uniform(r.n), uniform(r.len), uniform(r.lo), uniform(r.tiles), uniform(uint32_t(r.bad)) != 0};
-}
-
 // How the work is shared out.  Rows of a request go in groups of `rows`, and the
 // tiles of all groups of all requests, one after the other (a group without any
 // counts as one), are cut into equal shares, one for each of a head's `takers`,
@@ -169,9 +64,6 @@ struct Plan {
 struct Shares {
   uint64_t total, each;
 };
-__device__ __forceinline__ uint32_t groups_of(const AttnArgs &a, const Request &r, uint32_t rows) {
-  return (r.n * a.group + rows - 1) / rows;
-}
 __device__ __forceinline__ uint64_t tiles_of(const AttnArgs &a, const Request &r, uint32_t rows) {
   return uint64_t(groups_of(a, r, rows)) * max(r.tiles, 1u);
 }
@@ -179,7 +71,7 @@ __device__ __forceinline__ uint64_t tiles_of(const AttnArgs &a, const Request &r
 // The request of tile `taker * each` and the tiles before it, by one wave: a lane
 // sums batch / 64 requests in a row.
 __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, uint32_t rows, uint32_t taker,
-                                           Shares &sh, uint32_t &b, uint64_t &before) {
+                                           Shares &sh, uint32_t &b, uint64_t &before, uint64_t *tell_each, uint64_t *tell_before) {
   const uint32_t lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
   uint64_t mine = 0;
   for (uint32_t i = 0; i < per; i++)
@@ -193,6 +85,15 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
   sh.total = __shfl(upto, 63);
   sh.each = (sh.total + plan.takers - 1) / plan.takers;
   if (sh.each < plan.least) sh.each = plan.least;
+  if (tell_each) {
+    uint64_t at = upto - mine;
+    for (uint32_t i = 0; i < per; i++)
+      if (lane * per + i < a.batch) {
+        tell_before[lane * per + i] = at;
+        at += tiles_of(a, request(a, lane * per + i), rows);
+      }
+    if (lane == 0) *tell_each = sh.each;
+  }
   const uint64_t want = taker * sh.each;
   if (want >= sh.total) return false;
   const uint32_t owner = __popcll(__ballot(upto <= want));
@@ -203,41 +104,6 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
     if (want < before + t) return true;
     before += t;
   }
-}
-
-// Scratch: the shares' size; the tiles before each request's; then per head and
-// slot `rows` rows of sums, and their (m, l).
-struct Parts {
-  uint64_t *each, *before;
-  float2 *ml;
-  float *sums;
-  uint32_t slots;   // of a key head
-};
-__host__ __device__ __forceinline__ Parts parts(uint8_t *scratch, uint32_t batch, uint32_t kv_heads, uint32_t slots,
-                                                uint32_t rows) {
-  Parts p;
-  p.each = reinterpret_cast<uint64_t *>(scratch);
-  p.before = p.each + 1;
-  const uint64_t head = (uint64_t(batch) * 8 + 8 + 255) / 256 * 256;
-  p.ml = reinterpret_cast<float2 *>(scratch + head);
-  p.sums = reinterpret_cast<float *>(scratch + head + uint64_t(kv_heads) * slots * rows * 8);
-  p.slots = slots;
-  return p;
-}
-
-template <int DT>
-__device__ __forceinline__ void store4(uint8_t *p, f32x4 v) {
-  if constexpr (DT == BF16) {
-    *reinterpret_cast<u32x2_any *>(p) = u32x2{f32_bf16x2(v[0], v[1]), f32_bf16x2(v[2], v[3])};
-  } else {
-    *reinterpret_cast<f32x4_any *>(p) = v;
-  }
-}
-
-// Result of a row from its sums, weight and bound.
-__device__ __forceinline__ float over(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
-__device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.6931471805599453f;
 }
 
 // One wave's tiles: sums o (values 16 d + 4 j + i of row l % 16), bound m and this
@@ -266,16 +132,17 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
   const uint32_t n = lane & 15, j = lane >> 4;
   const uint32_t head = blockIdx.y, taker = blockIdx.x * kWaves + wave;
 
-  Shares share;
+  Shares sh;
   uint32_t b;
   uint64_t before;
-  if (taker >= plan.takers || !find_start(a, plan, 16, taker, share, b, before)) return;
-  share.each = uniform(share.each);
+  if (taker >= plan.takers || !find_start(a, plan, 16, taker, sh, b, before,
+                                            taker + head ? nullptr : out.each, out.before))
+    return;
+  sh.each = uniform(sh.each);
   b = uniform(b);
   before = uniform(before);
-  uint64_t at_tile = taker * share.each;
-  const uint64_t end_tile = min(at_tile + share.each, uniform(share.total));
-  if (taker == 0 && head == 0 && out.each && lane == 0) *out.each = share.each;
+  uint64_t at_tile = taker * sh.each;
+  const uint64_t end_tile = min(at_tile + sh.each, uniform(sh.total));
   // group after group, request after request
   while (at_tile < end_tile) {
   const Request rq = uniform(request(a, b));
@@ -284,23 +151,13 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
   const uint32_t grp = groups > 1 ? uint32_t((at_tile - before) / whole) : 0;
   const uint32_t from = uint32_t(at_tile - before - uint64_t(grp) * whole);
   const uint32_t to = uint32_t(min(uint64_t(whole), from + (end_tile - at_tile)));
-  if (out.before && at_tile == before && head == 0 && lane == 0) out.before[b] = before;
   // this lane's row
   const uint32_t row = grp * 16 + n;
   const bool live = row < rq.n * a.group;
   const uint32_t token = live ? per_group.div(row) : 0;
   const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
-  // keys that it sees: first + 0 .. count - 1
-  uint32_t first = 0, count = 0;
-  if (live) {
-    const int64_t at = int64_t(rq.len) - rq.n + token;   // its position
-    const int64_t end = a.causal ? at + 1 : int64_t(rq.len);
-    const int64_t begin = a.window && end > a.window ? end - a.window : 0;
-    if (end > begin) {
-      first = uint32_t(begin);
-      count = uint32_t(end - begin);
-    }
-  }
+  const Span sees = span(a, rq, token, live);
+  const uint32_t first = sees.first, count = sees.count;
   // tiles that some row of the wave sees, and those that all see whole
   uint32_t low = count ? first : ~0u, high = count ? first + count : 0;
   uint32_t low_all = live ? first : 0, high_all = live ? first + count : ~0u;
@@ -320,30 +177,14 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
 #pragma unroll
   for (int s = 0; s < NB; s++) {
     float x[8] = {};
-    if (live) {
-      const uint8_t *p = a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (NB * j + s)) * esize(DT);
-      if constexpr (DT == BF16) {
-        const u32x4 w = *reinterpret_cast<const u32x4_any *>(p);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          x[2 * i] = bf16_lo(w[i]);
-          x[2 * i + 1] = bf16_hi(w[i]);
-        }
-      } else {
-        const f32x4 y = *reinterpret_cast<const f32x4_any *>(p), z = *reinterpret_cast<const f32x4_any *>(p + 16);
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          x[i] = y[i];
-          x[4 + i] = z[i];
-        }
-      }
-    }
+    if (live) take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (NB * j + s)) * esize(DT), x);
     pieces<R::QP>(x, r.q[s]);
   }
 #pragma unroll
   for (int d = 0; d < 2 * NB; d++) r.o[d] = f32x4{0, 0, 0, 0};
   r.m = -__builtin_inff();
   r.l = 0.0f;
+  uint32_t marks = 0;   // blocks of values that have a NaN for this row
 
   uint8_t *mine = lds + wave * R::kLds;
   const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
@@ -442,6 +283,7 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
       s[g] = acc;
     }
     const bool more = t + 1 < end;
+    const uint64_t here[4] = {w.base[0], w.base[1], w.base[2], w.base[3]};
     if (more) {
       w = where(key0 + kTile, asked);
       asked = ask_pages(key0 + 2 * kTile);
@@ -472,9 +314,9 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
     const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
     // values of 32 keys to LDS
     const bool cut = key0 < low || key0 + kTile > high;
+    bool nan = false;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
-      bool nan = false;
 #pragma unroll
       for (int u = 0; u < kUnits; u++) {
         const uint32_t unit = lane + 64 * u;
@@ -485,14 +327,17 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
             vw[h][u] = u32x4{0, 0, 0, 0};
             vb[h][u] = 127;
           }
-          nan |= vb[h][u] > 252;
-          const float f = scale_of(vb[h][u]);
+          if (vb[h][u] > 252) {
+            nan = true;
+            vw[h][u] = u32x4{0, 0, 0, 0};
+            vb[h][u] = 127;
+          }
+          const float f = __uint_as_float(vb[h][u] << 23);
           uint8_t *p = mine + key * R::kPitch + blk * 64;
 #pragma unroll
           for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + 16 * i) = values8(vw[h][u][i], f);
         }
       }
-      const bool any_nan = __any(nan);
       lds_in_order();
       if (h == 1 && more) ask_values(w);
       bf16x8 wp[R::WP];
@@ -507,46 +352,25 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
       }
       // and back, 4 keys of one value at a time
       const uint8_t *from = mine + (4 * j + n / 4) * R::kPitch + (n & 3) * 8;
-      if (__builtin_expect(any_nan, 0)) {
-        // A NaN would meet the weight 0 of rows that do not see its key.  It is left
-        // out here, and rows that see one are found by a product of their own.
-        union {
-          uint16_t bits[8];
-          bf16x8 all;
-        } seen;
 #pragma unroll
-        for (int i = 0; i < 8; i++)
-          seen.bits[i] = key0 + 32 * h + 16 * (i / 4) + 4 * j + (i & 3) - first < count ? 0x3F80 : 0;
+      for (int d = 0; d < 2 * NB; d++) {
+        const bf16x8 v = turned(from + 32 * d, 16 * R::kPitch);
 #pragma unroll
-        for (int d = 0; d < 2 * NB; d++) {
-          Turned v = turned(from + 32 * d, 16 * R::kPitch), bad;
-#pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const bool is = (v.bits[i] & 0x7FFF) > 0x7F80;
-            bad.bits[i] = is ? 0x3F80 : 0;
-            v.bits[i] = is ? 0 : v.bits[i];
-          }
-          const f32x4 hit = mfma(bad.all, seen.all, f32x4{0, 0, 0, 0});
-#pragma unroll
-          for (int i = 0; i < 4; i++)
-            if (hit[i] > 0.0f) r.o[d][i] = __builtin_nanf("");
-#pragma unroll
-          for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v.all, wp[p], r.o[d]);
-        }
-      } else {
-#pragma unroll
-        for (int d = 0; d < 2 * NB; d++) {
-          const Turned v = turned(from + 32 * d, 16 * R::kPitch);
-#pragma unroll
-          for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v.all, wp[p], r.o[d]);
-        }
+        for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v, wp[p], r.o[d]);
       }
       lds_in_order();
+    }
+    if (__builtin_expect(__any(nan), 0)) {
+      const uint64_t at = (lane < 32 ? lane < 16 ? here[0] : here[1] : lane < 48 ? here[2] : here[3]) + (lane & 15) * place;
+      marks |= marked<NB>(vsc + at, key0, first, count);
     }
   }
 
   r.l = sum_j(r.l);
   if (rq.bad) r.l = __builtin_nanf("");
+#pragma unroll
+  for (int d = 0; d < 2 * NB; d++)
+    if (marks >> d / 2 & 1) r.o[d] = f32x4{} + __builtin_nanf("");
   if (live) {
     if (to - from == whole) {
       const uint64_t y = rq.start + token;
@@ -575,37 +399,58 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
 // 256 / (D / 4) teams that take every so manieth piece in order, and their sums are
 // added in order.
 template <int DT, int NB>
-__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group) {
+__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group, bool by_edges) {
   constexpr int D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
   __shared__ float tops[4];
   __shared__ __attribute__((aligned(16))) float sums[kTeams][D + 4];
   __shared__ float weights[kTeams];
   const uint32_t head = blockIdx.y;
-  // the rows' groups of 16, numbered with gaps: request b's from starts[b] group / 16 + b
   const uint32_t rows = a.starts ? 16 : min(16u, a.group);   // of a group, at most
-  const uint32_t slot = blockIdx.x / rows, rr = blockIdx.x - slot * rows;
-  uint32_t b;
-  if (a.starts) {
-    uint32_t lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const uint32_t mid = (lo + hi) >> 1;
-      const int32_t s = a.starts[mid];
-      const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens);
-      if (from * a.group / 16 + mid <= slot)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
+  const uint32_t x = blockIdx.x / rows, rr = blockIdx.x - x * rows;
+  const uint64_t each = *in.each;
+  uint32_t b, group;
+  uint64_t at;     // the group's first tile
+  if (by_edges) {
+    // the group that edge x + 1 lies in, if that is its first one
+    const uint64_t edge = (x + 1) * each;
+    b = uniform(holder(in.before, a.batch, edge));
+    const Request r = uniform(request(a, b));
+    const uint32_t whole = max(r.tiles, 1u);
+    const uint64_t g = (edge - in.before[b]) / whole;
+    if (g >= groups_of(a, r, 16)) return;
+    group = uint32_t(g);
+    at = in.before[b] + g * whole;
+    if (at == edge || at / each != x) return;
   } else {
-    b = slot / ((a.group + 15) / 16);
+    // groups numbered with gaps: request b's from starts[b] group / 16 + b
+    if (a.starts) {
+      uint32_t lo = 0, hi = a.batch;
+      while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) >> 1;
+        const int32_t s = a.starts[mid];
+        const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens);
+        if (from * a.group / 16 + mid <= x)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      b = lo;
+      const int32_t s = a.starts[b];
+      group = x - ((s < 0 ? 0 : min(uint32_t(s), a.tokens)) * a.group / 16 + b);
+    } else {
+      b = x / ((a.group + 15) / 16);
+      group = x % ((a.group + 15) / 16);
+    }
+    b = uniform(b);
+    group = uniform(group);
+    const Request r = uniform(request(a, b));
+    if (group >= groups_of(a, r, 16)) return;
+    at = in.before[b] + uint64_t(group) * max(r.tiles, 1u);
   }
-  const Request rq = request(a, b);
-  const uint32_t group = a.starts ? slot - (rq.start * a.group / 16 + b) : slot % ((a.group + 15) / 16);
+  const Request rq = uniform(request(a, b));
   const uint32_t row = group * 16 + rr;
-  if (group >= groups_of(a, rq, 16) || row >= rq.n * a.group) return;
-  const uint64_t whole = max(rq.tiles, 1u), at = in.before[b] + group * whole, each = *in.each;
-  const uint64_t f = at / each, pieces = (at + whole - 1) / each - f + 1;
+  if (row >= rq.n * a.group) return;
+  const uint64_t f = at / each, pieces = (at + max(rq.tiles, 1u) - 1) / each - f + 1;
   if (pieces <= 1) return;
   if (pieces > in.slots || 2 * f > in.slots - pieces) return;   // starts out of order: not all tiles had a taker
   const uint32_t count = uint32_t(pieces);
@@ -629,7 +474,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
     for (uint32_t i = team; i < count; i += kTeams) {
       const uint64_t p = piece(i);
       const float2 ml = in.ml[p];
-      const float f = ml.x == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
+      const float f = share(ml.x, top);
       l += ml.y * f;
       o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
     }
@@ -691,38 +536,32 @@ struct Few {
     k_attend<DT, NB><<<dim3(uint32_t((busy + kWaves - 1) / kWaves), a.c.heads), 64 * kWaves, 0, s>>>(
         a, plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !z.split) return e;
+    if (e != hipSuccess || !z.split || plan.takers == 1) return e;
     const uint32_t rows = a.starts || a.group > 16 ? 16 : a.group;
-    k_join<DT, NB><<<dim3(z.groups * rows, a.c.heads), 256, 0, s>>>(a, p, per_group);
+    // a workgroup for each row of every group, or of every group that an edge between two shares can lie in
+    const bool by_edges = plan.takers - 1 < z.groups;
+    k_join<DT, NB><<<dim3((by_edges ? plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, by_edges);
     return hipGetLastError();
   }
 };
 
-// f of the kernels for the call's type and head size.
-template <int DT, class F>
-auto by_blocks(uint32_t blocks, F f) {
-  switch (blocks) {
-    case 1: return f(Few<DT, 1>());
-    case 2: return f(Few<DT, 2>());
-    case 3: return f(Few<DT, 3>());
-    case 4: return f(Few<DT, 4>());
-    case 5: return f(Few<DT, 5>());
-    case 6: return f(Few<DT, 6>());
-    case 7: return f(Few<DT, 7>());
-    default: return f(Few<DT, 8>());
-  }
+// Sixteen rows a request or fewer, as far as the sizes tell, are taken by single
+// waves, more by workgroups for 128.
+bool few(const AttnArgs &a) {
+  const uint64_t most = !a.starts ? 1 : a.max_new ? a.max_new : (uint64_t(a.tokens) + a.batch - 1) / a.batch;
+  return most * a.group <= 16;
 }
 
 }  // namespace
 
 uint64_t attention_scratch(int dtype, const AttnArgs &a) {
-  auto f = [&](auto k) { return k.scratch(a); };
-  return dtype == BF16 ? by_blocks<BF16>(a.c.blocks, f) : by_blocks<FP32>(a.c.blocks, f);
+  if (!few(a)) return attention_tall_scratch(dtype, a);
+  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.scratch(a); });
 }
 
 hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s) {
-  auto f = [&](auto k) { return k.run(a, s); };
-  return dtype == BF16 ? by_blocks<BF16>(a.c.blocks, f) : by_blocks<FP32>(a.c.blocks, f);
+  if (!few(a)) return launch_attention_tall(dtype, a, s);
+  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.run(a, s); });
 }
 
 }  // namespace zn

@@ -1,0 +1,485 @@
+// zn_attn_tall.hip -- attention over the key-value cache in 4 bits for requests
+// with many rows (a request's queries times the query heads of a key head): the
+// method of zn_attn.hip with a workgroup of four waves for 128 rows.
+//
+// A wave takes 32 rows and 64 keys at a time with v_mfma_f32_32x32x16_bf16, keys
+// and values as the first operand: scores come out with a lane holding row l % 32
+// and keys 8 b + 4 h + i of each 32 (h = l / 32, b, i = 0 .. 3), which is the
+// second operand's layout for the product with the values; a row's maximum is one
+// exchange away.  Every wave reads the keys' codes itself (half a row a lane,
+// straight from memory, the next tile's while this one is used) and converts them;
+// the values are converted once, by all four waves, into one of two tiles in LDS
+// while the other one is used: one barrier a tile.
+#include <algorithm>
+
+#include "zn_attn.h"
+
+namespace zn {
+namespace {
+
+constexpr uint32_t kRows = 128;     // of a workgroup
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kLeast = 4;      // tiles of a piece at least
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+// The larger of lanes l and l + 32 (NaNs lose).
+__device__ __forceinline__ float max_h(float x) {
+  const uint32_t w = __float_as_uint(x);
+  const auto p = __builtin_amdgcn_permlane32_swap(w, w, false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// How the work is shared out.  Rows of a request go in groups of 128, and the keys
+// of a group in pieces of `piece` tiles, so many that a head's items, (request,
+// rows, piece), come to about `items` where the rows alone give fewer: with tiles
+// t_b and groups g_b, sum g_b ceil(t_b / piece) <= items + sum g_b.  Requests of
+// several pieces have t_b > piece, so at most 2 `items` items are pieces to be
+// joined; they are numbered apart.  Items go from the last to the first: the last
+// rows of a prompt see the most keys.  Every wave finds its item by itself, with
+// two sums over the requests; the host knows the bounds alone.
+struct Plan {
+  uint32_t items;
+};
+struct Item {
+  uint32_t b, group, piece, pieces;
+  uint64_t slot;      // where a piece goes
+  uint64_t tiles;     // of a piece
+};
+
+__device__ __forceinline__ uint64_t scan(uint64_t v, uint32_t lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint64_t p = __shfl_up(v, d);
+    if (lane >= uint32_t(d)) v += p;
+  }
+  return v;
+}
+
+__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint64_t *before, Item &it) {
+  const uint32_t lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
+  uint64_t mine = 0;
+  for (uint32_t i = 0; i < per; i++)
+    if (lane * per + i < a.batch) {
+      const Request r = request(a, lane * per + i);
+      mine += uint64_t(groups_of(a, r, kRows)) * max(r.tiles, 1u);
+    }
+  const uint64_t total = __shfl(scan(mine, lane), 63);
+  uint64_t piece = (total + plan.items - 1) / plan.items;
+  it.tiles = piece = piece < kLeast ? kLeast : piece;
+  uint64_t items = 0, parts = 0;
+  for (uint32_t i = 0; i < per; i++)
+    if (lane * per + i < a.batch) {
+      const Request r = request(a, lane * per + i);
+      const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
+      items += g * p;
+      if (p > 1) parts += g * p;
+    }
+  const uint64_t upto = scan(items, lane), parts_upto = scan(parts, lane), all = __shfl(upto, 63);
+  if (blockIdx.x >= all) return false;
+  // the requests' numbers of pieces for the join
+  if (before && threadIdx.x < 64) {
+    uint64_t at = parts_upto - parts;
+    for (uint32_t i = 0; i < per; i++)
+      if (lane * per + i < a.batch) {
+        before[lane * per + i] = at;
+        const Request r = request(a, lane * per + i);
+        const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
+        if (p > 1) at += g * p;
+      }
+  }
+  const uint64_t want = all - 1 - blockIdx.x;
+  const uint32_t owner = __popcll(__ballot(upto <= want));
+  uint64_t first = __shfl(upto - items, int(owner)), slot = __shfl(parts_upto - parts, int(owner));
+  for (uint32_t b = owner * per;; b++) {
+    const Request r = request(a, b);
+    const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
+    if (want < first + g * p) {
+      const uint32_t i = uint32_t(want - first);
+      it.b = uniform(b);
+      it.pieces = uniform(uint32_t(p));
+      it.group = uniform(i / it.pieces);
+      it.piece = uniform(i - it.group * it.pieces);
+      it.slot = uniform(slot + i);
+      it.tiles = uniform(piece);
+      return true;
+    }
+    first += g * p;
+    if (p > 1) slot += g * p;
+  }
+}
+
+template <int DT, int NB>
+constexpr int kResident = DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
+
+template <int DT, int NB>
+__global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(AttnArgs a, Plan plan, Parts out,
+                                                                            FastDiv per_group, float c) {
+  constexpr int QP = DT == BF16 ? 1 : 3;                  // pieces of a query
+  constexpr int WP = DT == BF16 ? 2 : 3;                  // pieces of a weight
+  constexpr int D = 32 * NB, kSteps = 2 * NB;             // steps of 8 values a lane
+  constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64);     // bytes of a key's values in LDS: 64 modulo 128
+  constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's values a thread
+  constexpr int kBytes = (NB + 1) / 2;                    // blocks that half a key touches
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kTile * kPitch];
+  __shared__ uint32_t nans[3];                            // a tile has a NaN: this one, the next, the one after
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t n = lane & 31, h = lane >> 5;
+  const uint32_t head = blockIdx.y;
+
+  Item it;
+  if (!find_item(a, plan, blockIdx.x + blockIdx.y == 0 ? out.before : nullptr, it)) return;
+  if (out.each && blockIdx.x + blockIdx.y + threadIdx.x == 0) *out.each = it.tiles;
+  const Request rq = uniform(request(a, it.b));
+  // this lane's row, and the keys that it sees: first + 0 .. count - 1
+  const uint32_t row = it.group * kRows + wave * 32 + n;
+  const bool live = row < rq.n * a.group;
+  const uint32_t token = live ? per_group.div(row) : 0;
+  const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
+  const Span sees = span(a, rq, token, live);
+  // tiles that some row of the wave sees, and those that all see whole
+  uint32_t low = sees.count ? sees.first : ~0u, high = sees.count ? sees.first + sees.count : 0;
+  uint32_t low_all = live ? sees.first : 0, high_all = live ? sees.first + sees.count : ~0u;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    low = min(low, uint32_t(__shfl_xor(int(low), d)));
+    high = max(high, uint32_t(__shfl_xor(int(high), d)));
+    low_all = max(low_all, uint32_t(__shfl_xor(int(low_all), d)));
+    high_all = min(high_all, uint32_t(__shfl_xor(int(high_all), d)));
+  }
+  low = uniform(low);
+  high = uniform(high);
+  low_all = uniform(low_all);
+  high_all = uniform(high_all);
+  // keys that some row of the workgroup sees: its first and its last live row's
+  const uint32_t last_row = min(it.group * kRows + kRows, rq.n * a.group) - 1;
+  const Span s0 = span(a, rq, uniform(per_group.div(it.group * kRows)), true);
+  const Span s1 = span(a, rq, uniform(per_group.div(last_row)), true);
+  const uint32_t wg_high = s1.first + s1.count, wg_low = s0.count ? s0.first : 0;
+
+  bf16x8 q[kSteps][QP];
+#pragma unroll
+  for (int s = 0; s < kSteps; s++) {
+    float x[8] = {};
+    if (live)
+      take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (kSteps * h + s)) * esize(DT), x);
+    pieces<QP>(x, q[s]);
+  }
+  f32x16 o[NB] = {};
+  float m = -__builtin_inff(), l = 0.0f;
+  uint32_t marks = 0;   // blocks of values that have a NaN for this row
+
+  const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
+  const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
+  const int32_t *pages = a.table + it.b * a.table_stride;
+  const uint32_t mask = (1u << a.c.shift) - 1, place = uint32_t(a.c.place_stride);
+
+  uint32_t t = uint32_t(min(it.piece * it.tiles, uint64_t(rq.tiles)));
+  uint32_t end = uint32_t(min((it.piece + 1) * it.tiles, uint64_t(rq.tiles)));
+  end = wg_high > rq.lo ? min(end, (wg_high - rq.lo + kTile - 1) / kTile) : 0;
+  if (wg_low > rq.lo) t = max(t, (wg_low - rq.lo) / kTile);
+
+  // The page of each 16 keys of a tile, lane g % 4 that of 16 g; behind the last
+  // key it is the last one's.  A place outside any page is taken from page 0 and
+  // counts as a NaN.
+  auto ask_pages = [&](uint32_t key0) {
+    return uint32_t(pages[min(key0 + 16 * (lane & 3), rq.len - 1) >> a.c.shift]);
+  };
+  struct Where {
+    uint64_t base[4];
+    uint32_t gone;
+  };
+  auto where = [&](uint32_t key0, uint32_t asked) {
+    Where w;
+    w.gone = 0;
+#pragma unroll
+    for (int g = 0; g < 4; g++) {
+      uint32_t page = __builtin_amdgcn_readlane(asked, g);
+      if (page >= a.c.n_pages) {
+        page = 0;
+        w.gone |= 1u << g;
+      }
+      w.base[g] = page * a.c.page_stride + ((key0 + 16 * g) & mask) * uint64_t(place);
+    }
+    return w;
+  };
+  uint32_t kw[2][kSteps], kb[2][kBytes];
+  auto ask_keys = [&](const Where &w) {
+#pragma unroll
+    for (int g = 0; g < 2; g++) {
+      const uint64_t base = (n < 16 ? w.base[2 * g] : w.base[2 * g + 1]) + (n & 15) * place;
+      const u32_any *p = reinterpret_cast<const u32_any *>(kc + base * 16 + 4 * kSteps * h);
+#pragma unroll
+      for (int s = 0; s < kSteps; s++) kw[g][s] = p[s];
+#pragma unroll
+      for (int i = 0; i < kBytes; i++) kb[g][i] = ksc[base + min(kSteps * h / 4 + i, uint32_t(NB - 1))];
+    }
+  };
+  u32x4 vw[kUnits];
+  uint32_t vb[kUnits];
+  auto ask_values = [&](const Where &w) {
+#pragma unroll
+    for (int u = 0; u < kUnits; u++) {
+      const uint32_t unit = min(threadIdx.x + kThreads * u, kTile * NB - 1);
+      const uint32_t key = unit / NB;
+      const uint64_t lo = key < 16 ? w.base[0] : w.base[1], hi = key < 48 ? w.base[2] : w.base[3];
+      const uint64_t base = (key < 32 ? lo : hi) + (key & 15) * place + unit % NB;
+      vw[u] = *reinterpret_cast<const u32x4 *>(vc + base * 16);
+      vb[u] = vsc[base];
+    }
+  };
+  // A thread's blocks of values to LDS.  Its four 16 bytes go in an order of its own,
+  // so that neighbouring lanes, 64 bytes apart, meet different banks.
+  auto put_values = [&](uint32_t key0, uint32_t buf, uint32_t flag) {
+    const bool cut = key0 < wg_low || key0 + kTile > wg_high;
+#pragma unroll
+    for (int u = 0; u < kUnits; u++) {
+      const uint32_t unit = threadIdx.x + kThreads * u;
+      if ((kTile * NB) % kThreads == 0 || unit < kTile * NB) {
+        const uint32_t key = unit / NB;
+        // no row sees a key outside [wg_low, wg_high)
+        if (cut && key0 + key - wg_low >= wg_high - wg_low) {
+          vw[u] = u32x4{0, 0, 0, 0};
+          vb[u] = 127;
+        }
+        if (vb[u] > 252) {
+          nans[flag] = 1;
+          vw[u] = u32x4{0, 0, 0, 0};
+          vb[u] = 127;
+        }
+        const float f = __uint_as_float(vb[u] << 23);
+        uint8_t *p = lds[buf] + key * kPitch + unit % NB * 64;
+        const bool one = unit & 1, two = unit & 2;
+        const u32x4 x = {one ? vw[u][1] : vw[u][0], one ? vw[u][0] : vw[u][1], one ? vw[u][3] : vw[u][2],
+                         one ? vw[u][2] : vw[u][3]};
+        const u32x4 y = {two ? x[2] : x[0], two ? x[3] : x[1], two ? x[0] : x[2], two ? x[1] : x[3]};
+        const uint32_t turn = (unit & 3) * 16;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + (16 * i ^ turn)) = values8(y[i], f);
+      }
+    }
+  };
+
+  if (threadIdx.x < 3) nans[threadIdx.x] = 0;
+  __syncthreads();
+  Where w = {};
+  uint32_t asked = 0;
+  if (t < end) {
+    const uint32_t key0 = rq.lo + t * kTile;
+    asked = ask_pages(key0);
+    w = where(key0, asked);
+    asked = ask_pages(key0 + kTile);
+    ask_values(w);
+    ask_keys(w);
+    put_values(key0, t & 1, 0);
+  }
+  __syncthreads();
+  for (uint32_t flag = 0; t < end; t++) {
+    const uint32_t next = flag == 2 ? 0 : flag + 1;
+    if (threadIdx.x == 0) nans[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
+    const uint32_t key0 = rq.lo + t * kTile, buf = t & 1;
+    const bool more = t + 1 < end;
+    const bool busy = key0 < high && key0 + kTile > low;   // some row of this wave sees the tile
+    const uint64_t here[4] = {w.base[0], w.base[1], w.base[2], w.base[3]};
+    f32x16 s[2];
+    if (busy) {
+#pragma unroll
+      for (int g = 0; g < 2; g++) {
+        f32x16 acc = {};
+        const uint32_t gone = (n < 16 ? w.gone >> (2 * g) : w.gone >> (2 * g + 1)) & 1;
+#pragma unroll
+        for (int st = 0; st < kSteps; st++) {
+          uint32_t byte = kb[g][0];
+#pragma unroll
+          for (int i = 1; i < kBytes; i++)
+            if ((kSteps * h + st) / 4 - kSteps * h / 4 == i) byte = kb[g][i];
+          const bf16x8 k = values8(kw[g][st], scale_of(gone ? 255u : byte));
+#pragma unroll
+          for (int p = QP - 1; p >= 0; p--) acc = mfma(k, q[st][p], acc);
+        }
+        s[g] = acc;
+      }
+    }
+    if (more) {
+      w = where(key0 + kTile, asked);
+      asked = ask_pages(key0 + 2 * kTile);
+      ask_values(w);
+      ask_keys(w);
+    }
+    if (busy) {
+      // keys that the row does not see
+      if (key0 < low_all || key0 + kTile > high_all) {
+#pragma unroll
+        for (int g = 0; g < 2; g++)
+#pragma unroll
+          for (int i = 0; i < 16; i++)
+            if (key0 + 32 * g + 8 * (i / 4) + 4 * h + i % 4 - sees.first >= sees.count) s[g][i] = -__builtin_inff();
+      }
+      float top = -__builtin_inff();
+#pragma unroll
+      for (int g = 0; g < 2; g++)
+#pragma unroll
+        for (int i = 0; i < 16; i++) top = fmaxf(top, s[g][i]);
+      top = max_h(top) * c;
+      if (__any(top > m)) {
+        const float up = top > m ? top + kRise : m;
+        const float f = up > m ? __builtin_amdgcn_exp2f(m - up) : 1.0f;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < NB; d++) o[d] *= f;
+        m = up;
+      }
+      const float bound = m == -__builtin_inff() ? 0.0f : m;
+      // 16 keys of 32 values at a time
+      const uint8_t *from = lds[buf] + (4 * h + (lane & 15) / 4) * kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+      if (__builtin_expect(uniform(nans[flag]), 0)) {
+        const uint64_t at = (lane < 32 ? lane < 16 ? here[0] : here[1] : lane < 48 ? here[2] : here[3]) + (lane & 15) * place;
+        marks |= marked<NB>(vsc + at, key0, sees.first, sees.count);
+      }
+#pragma unroll
+      for (int g = 0; g < 4; g++) {
+        bf16x8 wp[WP];
+        {
+          float x[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, -bound));
+            l += x[i];
+          }
+          pieces<WP>(x, wp);
+        }
+        const uint8_t *rows = from + 16 * g * kPitch;
+#pragma unroll
+        for (int d = 0; d < NB; d++) {
+          const bf16x8 v = turned(rows + 64 * d, 8 * kPitch);
+#pragma unroll
+          for (int p = WP - 1; p >= 0; p--) o[d] = mfma(v, wp[p], o[d]);
+        }
+      }
+    }
+    if (more) put_values(key0 + kTile, buf ^ 1, next);
+    flag = next;
+    __syncthreads();
+  }
+
+  l += __shfl_xor(l, 32);
+  if (rq.bad) l = __builtin_nanf("");
+  if (!live) return;
+#pragma unroll
+  for (int d = 0; d < NB; d++)
+    if (marks >> d & 1) o[d] = f32x16{} + __builtin_nanf("");
+  if (it.pieces == 1) {
+    const uint64_t y = rq.start + token;
+    const float f = over(l);
+    uint8_t *p = a.out + (y * a.out_token + qh * a.out_head + 4 * h) * esize(DT);
+#pragma unroll
+    for (int d = 0; d < NB; d++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        store4<DT>(p + (32 * d + 8 * i) * esize(DT), f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * f);
+    if (a.lse && h == 0) a.lse[y * a.heads + qh] = log_sum(m, l);
+  } else if (it.slot < out.slots) {   // starts out of order can make more pieces than there is room for
+    const uint64_t p = (uint64_t(head) * out.slots + it.slot) * kRows + wave * 32 + n;
+#pragma unroll
+    for (int d = 0; d < NB; d++)
+#pragma unroll
+      for (int i = 0; i < 4; i++)
+        *reinterpret_cast<f32x4 *>(out.sums + p * D + 32 * d + 8 * i + 4 * h) =
+            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+    if (h == 0) out.ml[p] = make_float2(m, l);
+  }
+}
+
+// Joins the pieces of a group, in their order: four workgroups a group, a team of
+// D / 4 lanes a row.  Groups are named by their first piece's slot.
+template <int DT, int NB>
+__global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv per_group) {
+  constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
+  const uint32_t head = blockIdx.y, slot = blockIdx.x >> 2;
+  const uint32_t b = uniform(holder(in.before, a.batch, slot));
+  const Request rq = uniform(request(a, b));
+  const uint64_t piece = *in.each, count = (max(rq.tiles, 1u) + piece - 1) / piece;
+  const uint64_t rel = slot - in.before[b];
+  // (the last: starts out of order can make more pieces than there is room for)
+  if (count <= 1 || rel % count || rel / count >= groups_of(a, rq, kRows) || slot + count > in.slots) return;
+  const uint32_t team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  const uint32_t end = min((blockIdx.x & 3) * 32 + 32, rq.n * a.group - uint32_t(rel / count) * kRows);
+  if (team >= kTeams) return;
+  for (uint32_t r = (blockIdx.x & 3) * 32 + team; r < end; r += kTeams) {
+    const uint64_t p0 = (uint64_t(head) * in.slots + slot) * kRows + r;
+    float top = -__builtin_inff();
+#pragma unroll 4
+    for (uint32_t i = 0; i < count; i++) top = fmaxf(top, in.ml[p0 + i * uint64_t(kRows)].x);
+    float l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (uint32_t i = 0; i < count; i++) {
+      const uint64_t p = p0 + i * uint64_t(kRows);
+      const float2 ml = in.ml[p];
+      const float f = share(ml.x, top);
+      l += ml.y * f;
+      o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
+    }
+    const uint32_t row = uint32_t(rel / count) * kRows + r, tk = per_group.div(row);
+    const uint32_t h = head * a.group + row - tk * a.group;
+    const uint64_t y = rq.start + tk;
+    store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
+    if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
+  }
+}
+
+// ------------------------------------------------------------------ launch --
+template <int DT, int NB>
+struct Tall {
+  struct Sizes {
+    Plan plan;
+    uint32_t groups;   // row groups of a key head, at most
+    uint32_t items;    // and their pieces
+    uint32_t slots;    // for pieces to be joined; 0: none
+  };
+  static Sizes sizes(const AttnArgs &a) {
+    Sizes z;
+    z.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / kRows + a.batch) : a.batch * ((a.group + kRows - 1) / kRows);
+    // two workgroups a resident wave of each SIMD, one after the other
+    const uint32_t want = 512 * kResident<DT, NB> / a.c.heads;
+    z.plan.items = want ? want : 1;
+    const uint64_t longest = ((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile + 1;
+    const uint64_t most = uint64_t(z.groups) * ((longest + kLeast - 1) / kLeast);
+    z.items = uint32_t(std::min<uint64_t>(most, uint64_t(z.groups) + z.plan.items));
+    z.slots = longest <= kLeast ? 0 : uint32_t(std::min<uint64_t>(most, 2 * uint64_t(z.plan.items)));
+    return z;
+  }
+  static uint64_t scratch(const AttnArgs &a) {
+    const Sizes z = sizes(a);
+    if (!z.slots) return 0;
+    const Parts p = parts(nullptr, a.batch, a.c.heads, z.slots, kRows);
+    return reinterpret_cast<uint64_t>(p.sums) + uint64_t(a.c.heads) * z.slots * kRows * NB * 32 * 4;
+  }
+  static hipError_t run(const AttnArgs &a, hipStream_t s) {
+    const Sizes z = sizes(a);
+    Parts p = {};
+    if (z.slots) p = parts(a.scratch, a.batch, a.c.heads, z.slots, kRows);
+    const FastDiv per_group(a.group);
+    k_attend_tall<DT, NB><<<dim3(z.items, a.c.heads), kThreads, 0, s>>>(
+        a, z.plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !z.slots) return e;
+    k_join_tall<DT, NB><<<dim3(z.slots * 4, a.c.heads), 256, 0, s>>>(a, p, per_group);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+uint64_t attention_tall_scratch(int dtype, const AttnArgs &a) {
+  return by_kind<Tall>(dtype, a.c.blocks, [&](auto k) { return k.scratch(a); });
+}
+hipError_t launch_attention_tall(int dtype, const AttnArgs &a, hipStream_t s) {
+  return by_kind<Tall>(dtype, a.c.blocks, [&](auto k) { return k.run(a, s); });
+}
+
+}  // namespace zn

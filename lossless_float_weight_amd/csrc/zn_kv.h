@@ -55,7 +55,8 @@ struct AttnArgs {
   uint64_t table_stride;
   uint32_t width, batch, tokens, heads, group; // group: query heads of a key head
   float scale;
-  uint32_t causal, window, max_new;
+  uint32_t causal, window;
+  uint32_t max_new;                            // 0: not known
   uint8_t *scratch;
 };
 // Bytes of scratch, by the sizes alone.

@@ -87,7 +87,7 @@ bool attention_of(const zn_mx_cache *cache, const zn_mx_attention_args *g, bool 
   a->scale = g->scale;
   a->causal = g->causal != 0;
   a->window = g->window;
-  a->max_new = uint32_t(g->max_new && g->max_new < g->tokens ? g->max_new : g->tokens);
+  a->max_new = uint32_t(g->max_new < g->tokens ? g->max_new : g->tokens);
   return true;
 }
 
