@@ -373,8 +373,9 @@ zn_status zn_mx_matmul2(zn_dtype a_fmt, const void *d_a, const void *d_a_scales,
 /* The cache.  Strides are in blocks of 32 values (16 bytes of codes, one scale
  * byte) and the same for all four arrays; a row's blocks are consecutive.  The
  * codes are 16-byte aligned.  head_dim is a multiple of 32 up to 256,
- * page_size a power of two from 16 to 65536, kv_heads at most 65535, n_pages *
- * page_size below 2^31, strides at most 2^40. */
+ * page_size a power of two from 16 to 65536, kv_heads at most 1024, n_pages *
+ * page_size below 2^31; page_stride is below 2^32, head_stride at most 2^40 and
+ * place_stride at most 2^20. */
 typedef struct zn_mx_cache {
   void *k, *k_scales, *v, *v_scales;
   uint64_t n_pages;
@@ -461,7 +462,7 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * not).  It chooses between kernels and has no effect on what is computed but
  * the order of sums.
  * scale is finite and > 0, batch at most 8192, window at most 2^31 - 1, tokens *
- * heads / kv_heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
+ * heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
  * 16-byte aligned device scratch (ZN_ERR_CAPACITY if it is less; 0 for some
  * sizes, then d_scratch may be NULL); calls that may run at the same time, and
  * graphs that may replay at the same time, need scratch of their own. */

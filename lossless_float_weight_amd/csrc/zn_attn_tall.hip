@@ -6,10 +6,10 @@
 // and values as the first operand: scores come out with a lane holding row l % 32
 // and keys 8 b + 4 h + i of each 32 (h = l / 32, b, i = 0 .. 3), which is the
 // second operand's layout for the product with the values; a row's maximum is one
-// exchange away.  Every wave reads the keys' codes itself (half a row a lane,
-// straight from memory, the next tile's while this one is used) and converts them;
-// the values are converted once, by all four waves, into one of two tiles in LDS
-// while the other one is used: one barrier a tile.
+// exchange away.  A conversion of two codes takes as long as an exponential (8
+// cycles of a SIMD, where other instructions take 2), so a tile is converted once,
+// by all four waves, into one of two places in LDS while the other is used: one
+// barrier a tile.
 #include <algorithm>
 
 #include "zn_attn.h"
@@ -39,9 +39,12 @@ __device__ __forceinline__ float max_h(float x) {
 // rows, piece), come to about `items` where the rows alone give fewer: with tiles
 // t_b and groups g_b, sum g_b ceil(t_b / piece) <= items + sum g_b.  Requests of
 // several pieces have t_b > piece, so at most 2 `items` items are pieces to be
-// joined; they are numbered apart.  Items go from the last to the first: the last
-// rows of a prompt see the most keys.  Every wave finds its item by itself, with
-// two sums over the requests; the host knows the bounds alone.
+// joined; they are numbered apart.  Items go from the last to the first, all heads'
+// of one number together: the last rows of a prompt see the most keys, and long
+// items at the end would leave the others waiting (head after head, 8192 rows of 8
+// heads took 950 us for 730).  Neighbouring workgroups run on different dies, so
+// eight heads keep to one die's cache each.  Every wave finds its item by itself,
+// with two sums over the requests; the host knows the bounds alone.
 struct Plan {
   uint32_t items;
 };
@@ -60,7 +63,7 @@ __device__ __forceinline__ uint64_t scan(uint64_t v, uint32_t lane) {
   return v;
 }
 
-__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint64_t *before, Item &it) {
+__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint32_t number, uint64_t *before, Item &it) {
   const uint32_t lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
   uint64_t mine = 0;
   for (uint32_t i = 0; i < per; i++)
@@ -80,7 +83,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       if (p > 1) parts += g * p;
     }
   const uint64_t upto = scan(items, lane), parts_upto = scan(parts, lane), all = __shfl(upto, 63);
-  if (blockIdx.x >= all) return false;
+  if (number >= all) return false;
   // the requests' numbers of pieces for the join
   if (before && threadIdx.x < 64) {
     uint64_t at = parts_upto - parts;
@@ -92,7 +95,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
         if (p > 1) at += g * p;
       }
   }
-  const uint64_t want = all - 1 - blockIdx.x;
+  const uint64_t want = all - 1 - number;
   const uint32_t owner = __popcll(__ballot(upto <= want));
   uint64_t first = __shfl(upto - items, int(owner)), slot = __shfl(parts_upto - parts, int(owner));
   for (uint32_t b = owner * per;; b++) {
@@ -122,18 +125,19 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   constexpr int QP = DT == BF16 ? 1 : 3;                  // pieces of a query
   constexpr int WP = DT == BF16 ? 2 : 3;                  // pieces of a weight
   constexpr int D = 32 * NB, kSteps = 2 * NB;             // steps of 8 values a lane
-  constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64);     // bytes of a key's values in LDS: 64 modulo 128
-  constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's values a thread
-  constexpr int kBytes = (NB + 1) / 2;                    // blocks that half a key touches
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2][kTile * kPitch];
+  // bytes of a key's values in LDS: 64 modulo 128, so that four keys' parts fill the
+  // banks; and of its keys, 16 modulo 32, for rows of 16 bytes a lane
+  constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64), kKeyPitch = 64 * NB + 16;
+  constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's keys, and values, a thread
+  __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][kTile * kPitch], lds_k[2][kTile * kKeyPitch];
   __shared__ uint32_t nans[3];                            // a tile has a NaN: this one, the next, the one after
   const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const uint32_t n = lane & 31, h = lane >> 5;
-  const uint32_t head = blockIdx.y;
+  const uint32_t number = blockIdx.x / a.c.heads, head = blockIdx.x - number * a.c.heads;
 
   Item it;
-  if (!find_item(a, plan, blockIdx.x + blockIdx.y == 0 ? out.before : nullptr, it)) return;
-  if (out.each && blockIdx.x + blockIdx.y + threadIdx.x == 0) *out.each = it.tiles;
+  if (!find_item(a, plan, number, blockIdx.x == 0 ? out.before : nullptr, it)) return;
+  if (out.each && blockIdx.x + threadIdx.x == 0) *out.each = it.tiles;
   const Request rq = uniform(request(a, it.b));
   // this lane's row, and the keys that it sees: first + 0 .. count - 1
   const uint32_t row = it.group * kRows + wave * 32 + n;
@@ -166,7 +170,7 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   for (int s = 0; s < kSteps; s++) {
     float x[8] = {};
     if (live)
-      take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (kSteps * h + s)) * esize(DT), x);
+      take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 16 * s + 8 * h) * esize(DT), x);
     pieces<QP>(x, q[s]);
   }
   f32x16 o[NB] = {};
@@ -183,64 +187,49 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   end = wg_high > rq.lo ? min(end, (wg_high - rq.lo + kTile - 1) / kTile) : 0;
   if (wg_low > rq.lo) t = max(t, (wg_low - rq.lo) / kTile);
 
-  // The page of each 16 keys of a tile, lane g % 4 that of 16 g; behind the last
-  // key it is the last one's.  A place outside any page is taken from page 0 and
-  // counts as a NaN.
+  // A thread's blocks are `unit % NB` of the keys unit / NB of a tile.  Their pages are
+  // asked for a tile ahead of the codes (behind the last key, the last one's).  A place
+  // outside any page is taken from page 0 and counts as a NaN.
+  const uint32_t page_stride = uint32_t(a.c.page_stride);
+  uint32_t page[kUnits];
   auto ask_pages = [&](uint32_t key0) {
-    return uint32_t(pages[min(key0 + 16 * (lane & 3), rq.len - 1) >> a.c.shift]);
-  };
-  struct Where {
-    uint64_t base[4];
-    uint32_t gone;
-  };
-  auto where = [&](uint32_t key0, uint32_t asked) {
-    Where w;
-    w.gone = 0;
 #pragma unroll
-    for (int g = 0; g < 4; g++) {
-      uint32_t page = __builtin_amdgcn_readlane(asked, g);
-      if (page >= a.c.n_pages) {
-        page = 0;
-        w.gone |= 1u << g;
-      }
-      w.base[g] = page * a.c.page_stride + ((key0 + 16 * g) & mask) * uint64_t(place);
-    }
-    return w;
-  };
-  uint32_t kw[2][kSteps], kb[2][kBytes];
-  auto ask_keys = [&](const Where &w) {
-#pragma unroll
-    for (int g = 0; g < 2; g++) {
-      const uint64_t base = (n < 16 ? w.base[2 * g] : w.base[2 * g + 1]) + (n & 15) * place;
-      const u32_any *p = reinterpret_cast<const u32_any *>(kc + base * 16 + 4 * kSteps * h);
-#pragma unroll
-      for (int s = 0; s < kSteps; s++) kw[g][s] = p[s];
-#pragma unroll
-      for (int i = 0; i < kBytes; i++) kb[g][i] = ksc[base + min(kSteps * h / 4 + i, uint32_t(NB - 1))];
+    for (int u = 0; u < kUnits; u++) {
+      const uint32_t key = min(threadIdx.x + kThreads * u, kTile * NB - 1) / NB;
+      page[u] = uint32_t(pages[min(key0 + key, rq.len - 1) >> a.c.shift]);
     }
   };
-  u32x4 vw[kUnits];
-  uint32_t vb[kUnits];
-  auto ask_values = [&](const Where &w) {
+  auto block_of = [&](uint32_t page, uint32_t key) {
+    return uint64_t(page < a.c.n_pages ? page : 0) * page_stride + uint64_t(key & mask) * place;
+  };
+  u32x4 kw[kUnits], vw[kUnits];
+  uint32_t kb[kUnits], vb[kUnits];
+  bool gone[kUnits];
+  auto ask = [&](uint32_t key0) {
 #pragma unroll
     for (int u = 0; u < kUnits; u++) {
       const uint32_t unit = min(threadIdx.x + kThreads * u, kTile * NB - 1);
-      const uint32_t key = unit / NB;
-      const uint64_t lo = key < 16 ? w.base[0] : w.base[1], hi = key < 48 ? w.base[2] : w.base[3];
-      const uint64_t base = (key < 32 ? lo : hi) + (key & 15) * place + unit % NB;
-      vw[u] = *reinterpret_cast<const u32x4 *>(vc + base * 16);
-      vb[u] = vsc[base];
+      const uint64_t block = block_of(page[u], key0 + unit / NB) + unit % NB;
+      gone[u] = page[u] >= a.c.n_pages;
+      kw[u] = *reinterpret_cast<const u32x4 *>(kc + block * 16);
+      kb[u] = ksc[block];
+      vw[u] = *reinterpret_cast<const u32x4 *>(vc + block * 16);
+      vb[u] = vsc[block];
     }
   };
-  // A thread's blocks of values to LDS.  Its four 16 bytes go in an order of its own,
-  // so that neighbouring lanes, 64 bytes apart, meet different banks.
-  auto put_values = [&](uint32_t key0, uint32_t buf, uint32_t flag) {
+  // A thread's blocks to LDS.  Those of values go 16 bytes at a time in an order of
+  // the lane's own, so that neighbouring lanes, 64 bytes apart, meet different banks.
+  auto put = [&](uint32_t key0, uint32_t buf, uint32_t flag) {
     const bool cut = key0 < wg_low || key0 + kTile > wg_high;
 #pragma unroll
     for (int u = 0; u < kUnits; u++) {
       const uint32_t unit = threadIdx.x + kThreads * u;
       if ((kTile * NB) % kThreads == 0 || unit < kTile * NB) {
         const uint32_t key = unit / NB;
+        const float fk = scale_of(gone[u] ? 255u : kb[u]);
+        uint8_t *pk = lds_k[buf] + key * kKeyPitch + unit % NB * 64;
+#pragma unroll
+        for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(pk + 16 * i) = values8(kw[u][i], fk);
         // no row sees a key outside [wg_low, wg_high)
         if (cut && key0 + key - wg_low >= wg_high - wg_low) {
           vw[u] = u32x4{0, 0, 0, 0};
@@ -251,31 +240,27 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
           vw[u] = u32x4{0, 0, 0, 0};
           vb[u] = 127;
         }
-        const float f = __uint_as_float(vb[u] << 23);
-        uint8_t *p = lds[buf] + key * kPitch + unit % NB * 64;
+        const float fv = __uint_as_float(vb[u] << 23);
+        uint8_t *pv = lds_v[buf] + key * kPitch + unit % NB * 64;
         const bool one = unit & 1, two = unit & 2;
         const u32x4 x = {one ? vw[u][1] : vw[u][0], one ? vw[u][0] : vw[u][1], one ? vw[u][3] : vw[u][2],
                          one ? vw[u][2] : vw[u][3]};
         const u32x4 y = {two ? x[2] : x[0], two ? x[3] : x[1], two ? x[0] : x[2], two ? x[1] : x[3]};
         const uint32_t turn = (unit & 3) * 16;
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + (16 * i ^ turn)) = values8(y[i], f);
+        for (uint32_t i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(pv + (16 * i ^ turn)) = values8(y[i], fv);
       }
     }
   };
 
   if (threadIdx.x < 3) nans[threadIdx.x] = 0;
   __syncthreads();
-  Where w = {};
-  uint32_t asked = 0;
   if (t < end) {
     const uint32_t key0 = rq.lo + t * kTile;
-    asked = ask_pages(key0);
-    w = where(key0, asked);
-    asked = ask_pages(key0 + kTile);
-    ask_values(w);
-    ask_keys(w);
-    put_values(key0, t & 1, 0);
+    ask_pages(key0);
+    ask(key0);
+    ask_pages(key0 + kTile);
+    put(key0, t & 1, 0);
   }
   __syncthreads();
   for (uint32_t flag = 0; t < end; t++) {
@@ -283,32 +268,23 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
     if (threadIdx.x == 0) nans[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
     const uint32_t key0 = rq.lo + t * kTile, buf = t & 1;
     const bool more = t + 1 < end;
+    if (more) {
+      ask(key0 + kTile);
+      ask_pages(key0 + 2 * kTile);
+    }
     const bool busy = key0 < high && key0 + kTile > low;   // some row of this wave sees the tile
-    const uint64_t here[4] = {w.base[0], w.base[1], w.base[2], w.base[3]};
     f32x16 s[2];
     if (busy) {
+      const uint8_t *rows = lds_k[buf] + n * kKeyPitch + 16 * h;
+      s[0] = s[1] = f32x16{};
 #pragma unroll
-      for (int g = 0; g < 2; g++) {
-        f32x16 acc = {};
-        const uint32_t gone = (n < 16 ? w.gone >> (2 * g) : w.gone >> (2 * g + 1)) & 1;
+      for (int st = 0; st < kSteps; st++)
 #pragma unroll
-        for (int st = 0; st < kSteps; st++) {
-          uint32_t byte = kb[g][0];
+        for (int g = 0; g < 2; g++) {
+          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(rows + 32 * g * kKeyPitch + 32 * st);
 #pragma unroll
-          for (int i = 1; i < kBytes; i++)
-            if ((kSteps * h + st) / 4 - kSteps * h / 4 == i) byte = kb[g][i];
-          const bf16x8 k = values8(kw[g][st], scale_of(gone ? 255u : byte));
-#pragma unroll
-          for (int p = QP - 1; p >= 0; p--) acc = mfma(k, q[st][p], acc);
+          for (int p = QP - 1; p >= 0; p--) s[g] = mfma(k, q[st][p], s[g]);
         }
-        s[g] = acc;
-      }
-    }
-    if (more) {
-      w = where(key0 + kTile, asked);
-      asked = ask_pages(key0 + 2 * kTile);
-      ask_values(w);
-      ask_keys(w);
     }
     if (busy) {
       // keys that the row does not see
@@ -335,33 +311,35 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
       }
       const float bound = m == -__builtin_inff() ? 0.0f : m;
       // 16 keys of 32 values at a time
-      const uint8_t *from = lds[buf] + (4 * h + (lane & 15) / 4) * kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+      const uint8_t *from = lds_v[buf] + (4 * h + (lane & 15) / 4) * kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
       if (__builtin_expect(uniform(nans[flag]), 0)) {
-        const uint64_t at = (lane < 32 ? lane < 16 ? here[0] : here[1] : lane < 48 ? here[2] : here[3]) + (lane & 15) * place;
-        marks |= marked<NB>(vsc + at, key0, sees.first, sees.count);
+        const uint32_t key = min(key0 + lane, rq.len - 1);
+        marks |= marked<NB>(vsc + block_of(pages[key >> a.c.shift], key), key0, sees.first, sees.count);
       }
+      // The weights of the next 16 keys are made while the matrix unit takes these.
+      bf16x8 wp[2][WP], v[NB];
+      auto weigh = [&](int g) {
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, -bound));
+          l += x[i];
+        }
+        pieces<WP>(x, wp[g & 1]);
+      };
+      weigh(0);
 #pragma unroll
       for (int g = 0; g < 4; g++) {
-        bf16x8 wp[WP];
-        {
-          float x[8];
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, -bound));
-            l += x[i];
-          }
-          pieces<WP>(x, wp);
-        }
-        const uint8_t *rows = from + 16 * g * kPitch;
+        for (int d = 0; d < NB; d++) v[d] = turned(from + 16 * g * kPitch + 64 * d, 8 * kPitch);
+        if (g < 3) weigh(g + 1);
 #pragma unroll
-        for (int d = 0; d < NB; d++) {
-          const bf16x8 v = turned(rows + 64 * d, 8 * kPitch);
+        for (int p = WP - 1; p >= 0; p--)
 #pragma unroll
-          for (int p = WP - 1; p >= 0; p--) o[d] = mfma(v, wp[p], o[d]);
-        }
+          for (int d = 0; d < NB; d++) o[d] = mfma(v[d], wp[g & 1][p], o[d]);
       }
     }
-    if (more) put_values(key0 + kTile, buf ^ 1, next);
+    if (more) put(key0 + kTile, buf ^ 1, next);
     flag = next;
     __syncthreads();
   }
@@ -444,8 +422,8 @@ struct Tall {
   static Sizes sizes(const AttnArgs &a) {
     Sizes z;
     z.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / kRows + a.batch) : a.batch * ((a.group + kRows - 1) / kRows);
-    // two workgroups a resident wave of each SIMD, one after the other
-    const uint32_t want = 512 * kResident<DT, NB> / a.c.heads;
+    // as many as run at the same time
+    const uint32_t want = 256 * kResident<DT, NB> / a.c.heads;
     z.plan.items = want ? want : 1;
     const uint64_t longest = ((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile + 1;
     const uint64_t most = uint64_t(z.groups) * ((longest + kLeast - 1) / kLeast);
@@ -464,7 +442,7 @@ struct Tall {
     Parts p = {};
     if (z.slots) p = parts(a.scratch, a.batch, a.c.heads, z.slots, kRows);
     const FastDiv per_group(a.group);
-    k_attend_tall<DT, NB><<<dim3(z.items, a.c.heads), kThreads, 0, s>>>(
+    k_attend_tall<DT, NB><<<z.items * a.c.heads, kThreads, 0, s>>>(
         a, z.plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !z.slots) return e;

@@ -9,6 +9,9 @@ namespace zn {
 constexpr uint32_t kKvMaxBatch = 8192;         // requests of a step
 constexpr uint32_t kKvMaxPage = 65536;         // tokens of a page (at least 16, a power of two)
 constexpr uint32_t kKvMaxDim = 256;
+constexpr uint32_t kKvMaxHeads = 1024;         // of keys
+// strides in blocks, for products and offsets of 32 bits
+constexpr uint64_t kKvMaxPageStride = 0xFFFFFFFFull, kKvMaxPlaceStride = 1ull << 20;
 
 // Where the cache's rows lie: block i of row (page, head, place) is block
 // page * page_stride + head * head_stride + place * place_stride + i.

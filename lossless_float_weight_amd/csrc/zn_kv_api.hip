@@ -26,9 +26,9 @@ zn_status done(hipError_t e) { return e == hipSuccess ? ZN_OK : ZN_ERR_HIP; }
 bool good_cache(const zn_mx_cache *c, bool used, KvCache *out) {
   if (!c || c->reserved || !power(c->page_size, 16, kKvMaxPage)) return false;
   if (c->head_dim < kMxBlock || c->head_dim > kKvMaxDim || c->head_dim % kMxBlock) return false;
-  if (c->kv_heads < 1 || c->kv_heads > 65535) return false;
+  if (c->kv_heads < 1 || c->kv_heads > kKvMaxHeads) return false;
   if (c->n_pages < 1 || c->n_pages > kMost / c->page_size) return false;
-  if (c->page_stride > kMostStride || c->head_stride > kMostStride || c->place_stride > kMostStride) return false;
+  if (c->page_stride > kKvMaxPageStride || c->head_stride > kMostStride || c->place_stride > kKvMaxPlaceStride) return false;
   if (used && (!at16(c->k) || !c->k_scales || !at16(c->v) || !c->v_scales)) return false;
   out->k = static_cast<uint8_t *>(c->k);
   out->ks = static_cast<uint8_t *>(c->k_scales);
@@ -61,7 +61,8 @@ bool attention_of(const zn_mx_cache *cache, const zn_mx_attention_args *g, bool 
   if (!g || !good_cache(cache, used, &a->c) || !plain(g->dtype)) return false;
   if (g->heads < 1 || g->heads % a->c.heads || g->batch > kKvMaxBatch) return false;
   const uint64_t group = g->heads / a->c.heads;
-  if (g->tokens > (1ull << 29) / group) return false;
+  // workgroups of 256 threads, one for 128 rows and one more for every request and key head, fit a grid
+  if (g->tokens > (1ull << 29) / g->heads) return false;
   if (uint64_t(g->width) * cache->page_size > kMost || g->window > kMost || (g->window && !g->causal)) return false;
   if (!(g->scale > 0.0f) || !isfinite(g->scale)) return false;
   if (!g->starts && g->tokens != g->batch) return false;

@@ -722,7 +722,7 @@ def mx_kv_cache(n_pages: int, kv_heads: int, page_size: int, head_dim: int, devi
         raise ZnError(-1, f"mx_kv_cache: head_dim is {head_dim}, wanted a multiple of 32 up to 256")
     if not 16 <= page_size <= 65536 or page_size & (page_size - 1):
         raise ZnError(-1, f"mx_kv_cache: page_size is {page_size}, wanted a power of two from 16 to 65536")
-    if n_pages < 1 or n_pages * page_size >= 1 << 31 or not 1 <= kv_heads <= 65535:
+    if n_pages < 1 or n_pages * page_size >= 1 << 31 or not 1 <= kv_heads <= 1024:
         raise ZnError(-1, f"mx_kv_cache: {n_pages} pages of {page_size} tokens and {kv_heads} heads")
     lead = (n_pages, kv_heads, page_size)
     k, v = (torch.zeros(*lead, head_dim // 2, dtype=torch.uint8, device=device) for _ in range(2))

@@ -23,8 +23,8 @@ CACHE = dict(k=P, ks=P, v=P, vs=P, n_pages=8, page_size=16, kv_heads=2, head_dim
              head_stride=32, place_stride=2)
 BAD_CACHES = [
     dict(page_size=8), dict(page_size=24), dict(page_size=131072), dict(n_pages=0), dict(n_pages=1 << 27),
-    dict(kv_heads=0), dict(kv_heads=65536), dict(head_dim=0), dict(head_dim=48), dict(head_dim=288), dict(reserved=1),
-    dict(page_stride=FAR), dict(head_stride=FAR), dict(place_stride=FAR)]
+    dict(kv_heads=0), dict(kv_heads=1025), dict(head_dim=0), dict(head_dim=48), dict(head_dim=288), dict(reserved=1),
+    dict(page_stride=FAR), dict(head_stride=FAR), dict(place_stride=(1 << 20) + 1), dict(page_stride=1 << 32)]
 BAD_ADDRESSES = [dict(k=0), dict(k=P + 8), dict(v=0), dict(v=P + 4), dict(ks=0), dict(vs=0)]
 
 
@@ -95,7 +95,7 @@ def attend(scratch=None, nbytes=0, c=None, **change):
 
 @pytest.mark.parametrize("bad", [
     dict(dtype=FP8), dict(heads=0), dict(heads=3), dict(batch=8193, tokens=8193), dict(tokens=1), dict(batch=1),
-    dict(tokens=(1 << 28) + 1, starts=P), dict(qt=FAR), dict(qh=FAR), dict(ot=FAR), dict(oh=FAR), dict(ts=FAR),
+    dict(tokens=(1 << 27) + 1, starts=P), dict(qt=FAR), dict(qh=FAR), dict(ot=FAR), dict(oh=FAR), dict(ts=FAR),
     dict(batch=2, tokens=2, ts=7), dict(width=1 << 27, ts=1 << 27), dict(scale=0.0), dict(scale=-1.0),
     dict(scale=math.nan), dict(scale=math.inf), dict(window=1 << 31), dict(window=4, causal=0)])
 def test_attention_refuses(bad):
@@ -181,7 +181,7 @@ def test_binding_refuses_caches():
                 (k.transpose(2, 3), ks, v, vs), (near[0], both[1][:, 0, :2], near[0], near[1])):
         _raises(zn._kv_cache, "t", bad)
     for bad in ((0, 2, 16, 64), (1 << 27, 2, 16, 64), (4, 0, 16, 64), (4, 2, 8, 64), (4, 2, 24, 64), (4, 2, 16, 48),
-                (4, 2, 16, 0), (4, 2, 16, 288), (4, 70000, 16, 64)):
+                (4, 2, 16, 0), (4, 2, 16, 288), (4, 1025, 16, 64)):
         _raises(zn.mx_kv_cache, *bad, device="cpu")
 
 
