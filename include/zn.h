@@ -448,8 +448,9 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * zeros and -infinity.  Rows behind the last request are left as they were.
  * Keys that a query does not see have no effect on it, whatever they hold.
  *   Values of keys and values are taken as stored; products, sums, maxima and
- * exponentials are FP32 (BF16 queries: the weights keep 16 bits before they
- * meet the values; FP32: 24), and the result is rounded once.  Weights are at
+ * exponentials are FP32 (before they meet the values the weights are rounded: beside
+ * BF16 queries to 11 bits, or 16 for few rows a request, beside FP32 to 24), and the
+ * result is rounded once.  Weights are at
  * most 1: n keys whose values pass 2^127 / n may give infinities and NaNs.  A
  * scale byte over 252, which the write makes only (255) of infinities and NaNs,
  * is a NaN.

@@ -134,6 +134,18 @@ __device__ __forceinline__ void take_row8(const uint8_t *p, float (&x)[8]) {
   }
 }
 
+// The same as the matrix instruction's pieces.
+template <int DT, int N>
+__device__ __forceinline__ void take_query8(const uint8_t *p, bool live, bf16x8 (&out)[N]) {
+  if constexpr (DT == BF16) {
+    out[0] = __builtin_bit_cast(bf16x8, live ? u32x4(*reinterpret_cast<const u32x4_any *>(p)) : u32x4{0, 0, 0, 0});
+  } else {
+    float x[8] = {};
+    if (live) take_row8<DT>(p, x);
+    pieces<N>(x, out);
+  }
+}
+
 // Values that are the same in all lanes, known to be so.
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ uint64_t uniform(uint64_t v) {
@@ -147,10 +159,10 @@ __device__ __forceinline__ uint32_t groups_of(const AttnArgs &a, const Request &
   return (r.n * a.group + rows - 1) / rows;
 }
 
-// Scratch: how the work was shared out (`each`, and `before` of every request);
+// Scratch: how the work was shared out (`each`, `all`, and `before` of every request);
 // then per head and slot `rows` rows of (m, l), and of sums.
 struct Parts {
-  uint64_t *each, *before;
+  uint64_t *each, *all, *before;
   float2 *ml;
   float *sums;
   uint32_t slots;   // of a key head
@@ -159,8 +171,9 @@ __host__ __device__ __forceinline__ Parts parts(uint8_t *scratch, uint32_t batch
                                                 uint32_t rows) {
   Parts p;
   p.each = reinterpret_cast<uint64_t *>(scratch);
-  p.before = p.each + 1;
-  const uint64_t head = (uint64_t(batch) * 8 + 8 + 255) / 256 * 256;
+  p.all = p.each + 1;
+  p.before = p.each + 2;
+  const uint64_t head = (uint64_t(batch) * 8 + 16 + 255) / 256 * 256;
   p.ml = reinterpret_cast<float2 *>(scratch + head);
   p.sums = reinterpret_cast<float *>(scratch + head + uint64_t(kv_heads) * slots * rows * 8);
   p.slots = slots;
@@ -201,17 +214,44 @@ __device__ __attribute__((noinline)) uint32_t marked(const uint8_t *scales, uint
 __device__ __forceinline__ float share(float m, float top) {
   return m == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 }
-// The last request b with before[b] <= v (before rises from 0).
+// The last request b with before[b] <= v (before rises from 0), by one wave: 64
+// places a step.
 __device__ __forceinline__ uint32_t holder(const uint64_t *before, uint32_t batch, uint64_t v) {
-  uint32_t lo = 0, hi = batch;
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) >> 1;
-    if (before[mid] <= v)
-      lo = mid;
-    else
-      hi = mid;
+  const uint32_t lane = threadIdx.x & 63;
+  uint32_t lo = 0;
+  for (uint32_t n = batch; n > 1;) {
+    const uint32_t step = (n + 63) / 64, i = lane * step;
+    const uint64_t at = before[lo + min(i, n - 1)];
+    const uint32_t last = __popcll(__ballot(i < n && at <= v)) - 1;   // place 0 always
+    lo += last * step;
+    n = min(step, n - last * step);
   }
   return lo;
+}
+
+// Sums of v over the lanes up to this one.  32 bits where the sum surely fits.
+__device__ __forceinline__ uint32_t scan32(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false);   // a lane down, within 16
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false);   // the last of 16 to the next 16
+  v += __builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false);   // the last of 32 to the next 32
+  return v;
+}
+__device__ __forceinline__ uint64_t scan(uint64_t v) {
+  if (!__any((v >> 25) != 0)) return scan32(uint32_t(v));
+#pragma unroll 1
+  for (int d = 1; d < 64; d *= 2) {
+    const uint64_t p = __shfl_up(v, d);
+    if ((threadIdx.x & 63) >= uint32_t(d)) v += p;
+  }
+  return v;
+}
+// v of a lane that all know.
+__device__ __forceinline__ uint64_t of_lane(uint64_t v, uint32_t lane) {
+  return uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(v >> 32), lane))) << 32 |
+         uint32_t(__builtin_amdgcn_readlane(uint32_t(v), lane));
 }
 
 // f of the kernels K<type, blocks of 32 values of a head>, for the call's.

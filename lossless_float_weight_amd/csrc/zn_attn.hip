@@ -29,7 +29,7 @@ namespace zn {
 namespace {
 
 constexpr int kWaves = 4;       // of a workgroup
-constexpr uint32_t kLeast = 2;  // tiles that a wave takes at least
+constexpr uint32_t kLeast = 1;  // tiles that a wave takes at least
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -76,13 +76,8 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
   uint64_t mine = 0;
   for (uint32_t i = 0; i < per; i++)
     if (lane * per + i < a.batch) mine += tiles_of(a, request(a, lane * per + i), rows);
-  uint64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t p = __shfl_up(upto, d);
-    if (lane >= uint32_t(d)) upto += p;
-  }
-  sh.total = __shfl(upto, 63);
+  const uint64_t upto = scan(mine);
+  sh.total = of_lane(upto, 63);
   sh.each = (sh.total + plan.takers - 1) / plan.takers;
   if (sh.each < plan.least) sh.each = plan.least;
   if (tell_each) {
@@ -96,8 +91,8 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
   }
   const uint64_t want = taker * sh.each;
   if (want >= sh.total) return false;
-  const uint32_t owner = __popcll(__ballot(upto <= want));
-  before = __shfl(upto - mine, int(owner));
+  const uint32_t owner = uniform(uint32_t(__popcll(__ballot(upto <= want))));
+  before = of_lane(upto - mine, owner);
   b = owner * per;
   for (;; b++) {
     const uint64_t t = tiles_of(a, request(a, b), rows);
@@ -174,12 +169,6 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
   high_all = uniform(high_all);
 
   R r;
-#pragma unroll
-  for (int s = 0; s < NB; s++) {
-    float x[8] = {};
-    if (live) take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (NB * j + s)) * esize(DT), x);
-    pieces<R::QP>(x, r.q[s]);
-  }
 #pragma unroll
   for (int d = 0; d < 2 * NB; d++) r.o[d] = f32x4{0, 0, 0, 0};
   r.m = -__builtin_inff();
@@ -258,6 +247,11 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
   uint32_t asked = 0;
   if (t < end) {
     asked = ask_pages(rq.lo + t * kTile);
+  }
+#pragma unroll
+  for (int s = 0; s < NB; s++)
+    take_query8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (NB * j + s)) * esize(DT), live, r.q[s]);
+  if (t < end) {
     w = where(rq.lo + t * kTile, asked);
     asked = ask_pages(rq.lo + (t + 1) * kTile);
     ask_keys(w);

@@ -22,9 +22,29 @@ constexpr uint32_t kThreads = 256;
 constexpr uint32_t kLeast = 4;      // tiles of a piece at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ f32x16 mfma(bf16x8 a, bf16x8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16 mfma_half(bf16x8 a, bf16x8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+// Eight values, or eight codes under a scale, in FP16.
+__device__ __forceinline__ u32x4 half8(const float (&x)[8]) {
+  u32x4 w;
+#pragma unroll
+  for (int i = 0; i < 4; i++)
+    w[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * i], x[2 * i + 1]}, f16x2));
+  return w;
+}
+__device__ __forceinline__ u32x4 halves8(uint32_t w, float s) {
+  return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2)),
+               __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3))};
 }
 
 // The larger of lanes l and l + 32 (NaNs lose).
@@ -54,16 +74,8 @@ struct Item {
   uint64_t tiles;     // of a piece
 };
 
-__device__ __forceinline__ uint64_t scan(uint64_t v, uint32_t lane) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t p = __shfl_up(v, d);
-    if (lane >= uint32_t(d)) v += p;
-  }
-  return v;
-}
-
-__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint32_t number, uint64_t *before, Item &it) {
+__device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, uint32_t number, bool tell, uint64_t *each,
+                                          uint64_t *whole, uint64_t *before, Item &it) {
   const uint32_t lane = threadIdx.x & 63, per = (a.batch + 63) / 64;
   uint64_t mine = 0;
   for (uint32_t i = 0; i < per; i++)
@@ -71,7 +83,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       const Request r = request(a, lane * per + i);
       mine += uint64_t(groups_of(a, r, kRows)) * max(r.tiles, 1u);
     }
-  const uint64_t total = __shfl(scan(mine, lane), 63);
+  const uint64_t total = of_lane(scan(mine), 63);
   uint64_t piece = (total + plan.items - 1) / plan.items;
   it.tiles = piece = piece < kLeast ? kLeast : piece;
   uint64_t items = 0, parts = 0;
@@ -82,10 +94,10 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       items += g * p;
       if (p > 1) parts += g * p;
     }
-  const uint64_t upto = scan(items, lane), parts_upto = scan(parts, lane), all = __shfl(upto, 63);
+  const uint64_t upto = scan(items), parts_upto = scan(parts), all = of_lane(upto, 63);
   if (number >= all) return false;
   // the requests' numbers of pieces for the join
-  if (before && threadIdx.x < 64) {
+  if (tell && threadIdx.x < 64) {
     uint64_t at = parts_upto - parts;
     for (uint32_t i = 0; i < per; i++)
       if (lane * per + i < a.batch) {
@@ -94,10 +106,14 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
         const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
         if (p > 1) at += g * p;
       }
+    if (lane == 63) {
+      *each = piece;
+      *whole = parts_upto;
+    }
   }
   const uint64_t want = all - 1 - number;
-  const uint32_t owner = __popcll(__ballot(upto <= want));
-  uint64_t first = __shfl(upto - items, int(owner)), slot = __shfl(parts_upto - parts, int(owner));
+  const uint32_t owner = uniform(uint32_t(__popcll(__ballot(upto <= want))));
+  uint64_t first = of_lane(upto - items, owner), slot = of_lane(parts_upto - parts, owner);
   for (uint32_t b = owner * per;; b++) {
     const Request r = request(a, b);
     const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
@@ -120,81 +136,70 @@ template <int DT, int NB>
 constexpr int kResident = DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
 
 template <int DT, int NB>
-__global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(AttnArgs a, Plan plan, Parts out,
-                                                                            FastDiv per_group, float c) {
-  constexpr int QP = DT == BF16 ? 1 : 3;                  // pieces of a query
-  constexpr int WP = DT == BF16 ? 2 : 3;                  // pieces of a weight
-  constexpr int D = 32 * NB, kSteps = 2 * NB;             // steps of 8 values a lane
+struct Shape {
+  static constexpr int QP = DT == BF16 ? 1 : 3;                  // pieces of a query
+  static constexpr int kSteps = 2 * NB;                          // of 16 values of a key
   // bytes of a key's values in LDS: 64 modulo 128, so that four keys' parts fill the
   // banks; and of its keys, 16 modulo 32, for rows of 16 bytes a lane
-  constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64), kKeyPitch = 64 * NB + 16;
-  constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's keys, and values, a thread
-  __shared__ __attribute__((aligned(16))) uint8_t lds_v[2][kTile * kPitch], lds_k[2][kTile * kKeyPitch];
-  __shared__ uint32_t nans[3];                            // a tile has a NaN: this one, the next, the one after
-  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const uint32_t n = lane & 31, h = lane >> 5;
-  const uint32_t number = blockIdx.x / a.c.heads, head = blockIdx.x - number * a.c.heads;
+  static constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64), kKeyPitch = 64 * NB + 16;
+  static constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's keys, and values, a thread
+  struct Lds {
+    __attribute__((aligned(16))) uint8_t v[2][kTile * kPitch], k[2][kTile * kKeyPitch];
+    uint32_t odd[3];     // a tile has a NaN (1), scales out of reach (2): this one, the next, the one after
+    uint32_t top;        // the largest scale byte of the first tile
+  };
+};
 
-  Item it;
-  if (!find_item(a, plan, number, blockIdx.x == 0 ? out.before : nullptr, it)) return;
-  if (out.each && blockIdx.x + threadIdx.x == 0) *out.each = it.tiles;
-  const Request rq = uniform(request(a, it.b));
-  // this lane's row, and the keys that it sees: first + 0 .. count - 1
-  const uint32_t row = it.group * kRows + wave * 32 + n;
-  const bool live = row < rq.n * a.group;
-  const uint32_t token = live ? per_group.div(row) : 0;
-  const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
-  const Span sees = span(a, rq, token, live);
-  // tiles that some row of the wave sees, and those that all see whole
-  uint32_t low = sees.count ? sees.first : ~0u, high = sees.count ? sees.first + sees.count : 0;
-  uint32_t low_all = live ? sees.first : 0, high_all = live ? sees.first + sees.count : ~0u;
-#pragma unroll
-  for (int d = 1; d < 32; d *= 2) {
-    low = min(low, uint32_t(__shfl_xor(int(low), d)));
-    high = max(high, uint32_t(__shfl_xor(int(high), d)));
-    low_all = max(low_all, uint32_t(__shfl_xor(int(low_all), d)));
-    high_all = min(high_all, uint32_t(__shfl_xor(int(high_all), d)));
-  }
-  low = uniform(low);
-  high = uniform(high);
-  low_all = uniform(low_all);
-  high_all = uniform(high_all);
-  // keys that some row of the workgroup sees: its first and its last live row's
-  const uint32_t last_row = min(it.group * kRows + kRows, rq.n * a.group) - 1;
-  const Span s0 = span(a, rq, uniform(per_group.div(it.group * kRows)), true);
-  const Span s1 = span(a, rq, uniform(per_group.div(last_row)), true);
-  const uint32_t wg_high = s1.first + s1.count, wg_low = s0.count ? s0.first : 0;
+// What a wave has of its rows.
+template <int DT, int NB>
+struct Rows32 {
+  bf16x8 q[2 * NB][Shape<DT, NB>::QP];
+  Span sees;                                   // this lane's row
+  uint32_t low, high, low_all, high_all;       // keys that some row of the wave sees, and that all see
+  uint32_t wg_low, wg_high;                    // that some row of the workgroup sees
+  f32x16 o[NB];                                // sums, times 2^(127 - unit)
+  float m, l;
+  uint32_t marks;                              // blocks of values that have a NaN for this row
+  uint32_t unit;
+};
 
-  bf16x8 q[kSteps][QP];
-#pragma unroll
-  for (int s = 0; s < kSteps; s++) {
-    float x[8] = {};
-    if (live)
-      take_row8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 16 * s + 8 * h) * esize(DT), x);
-    pieces<QP>(x, q[s]);
-  }
-  f32x16 o[NB] = {};
-  float m = -__builtin_inff(), l = 0.0f;
-  uint32_t marks = 0;   // blocks of values that have a NaN for this row
-
+// The product with the values is one of two.
+//   HALF, beside BF16 queries: weights and values in FP16, one product.  Weights go up
+// to 2^15 and keep 11 bits down to 2^-14 (beside a largest one of 2^7 or more), the
+// values are held relative to a scale of the first tile and are exact while the tiles'
+// scales lie within 2^-23 and 2^12 of it (FP4 times that is FP16).  A tile with others
+// ends it, false is returned, and the rows are taken again the other way.
+//   Otherwise weights in BF16 pieces (two beside BF16 queries, three beside FP32),
+// a product each, and values in BF16, exact whatever their scales.
+// The first takes two thirds of the matrix instructions and three quarters of the
+// others: 8192 queries of 32 heads 790 -> 650 us.
+template <int DT, int NB, bool HALF>
+__device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq, const int32_t *pages, uint32_t head,
+                                           uint32_t t, uint32_t end, float c, typename Shape<DT, NB>::Lds &lds,
+                                           Rows32<DT, NB> &r) {
+  using S = Shape<DT, NB>;
+  constexpr int WP = HALF ? 1 : DT == BF16 ? 2 : 3;      // pieces of a weight
+  constexpr float kTop = HALF ? 15.0f : 0.0f;            // weights stay under 2^kTop
+  constexpr int kBelow = 23, kAbove = 12;                // scales that HALF takes
+  const uint32_t lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
   const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
   const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
-  const int32_t *pages = a.table + it.b * a.table_stride;
-  const uint32_t mask = (1u << a.c.shift) - 1, place = uint32_t(a.c.place_stride);
-
-  uint32_t t = uint32_t(min(it.piece * it.tiles, uint64_t(rq.tiles)));
-  uint32_t end = uint32_t(min((it.piece + 1) * it.tiles, uint64_t(rq.tiles)));
-  end = wg_high > rq.lo ? min(end, (wg_high - rq.lo + kTile - 1) / kTile) : 0;
-  if (wg_low > rq.lo) t = max(t, (wg_low - rq.lo) / kTile);
+  const uint32_t mask = (1u << a.c.shift) - 1, place = uint32_t(a.c.place_stride), page_stride = uint32_t(a.c.page_stride);
+  const uint32_t wg_low = r.wg_low, wg_high = r.wg_high;
+#pragma unroll
+  for (int d = 0; d < NB; d++) r.o[d] = f32x16{};
+  r.m = -__builtin_inff();
+  r.l = 0.0f;
+  r.marks = 0;
+  r.unit = 127;
 
   // A thread's blocks are `unit % NB` of the keys unit / NB of a tile.  Their pages are
   // asked for a tile ahead of the codes (behind the last key, the last one's).  A place
   // outside any page is taken from page 0 and counts as a NaN.
-  const uint32_t page_stride = uint32_t(a.c.page_stride);
-  uint32_t page[kUnits];
+  uint32_t page[S::kUnits];
   auto ask_pages = [&](uint32_t key0) {
 #pragma unroll
-    for (int u = 0; u < kUnits; u++) {
+    for (int u = 0; u < S::kUnits; u++) {
       const uint32_t key = min(threadIdx.x + kThreads * u, kTile * NB - 1) / NB;
       page[u] = uint32_t(pages[min(key0 + key, rq.len - 1) >> a.c.shift]);
     }
@@ -202,12 +207,12 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   auto block_of = [&](uint32_t page, uint32_t key) {
     return uint64_t(page < a.c.n_pages ? page : 0) * page_stride + uint64_t(key & mask) * place;
   };
-  u32x4 kw[kUnits], vw[kUnits];
-  uint32_t kb[kUnits], vb[kUnits];
-  bool gone[kUnits];
+  u32x4 kw[S::kUnits], vw[S::kUnits];
+  uint32_t kb[S::kUnits], vb[S::kUnits];
+  bool gone[S::kUnits];
   auto ask = [&](uint32_t key0) {
 #pragma unroll
-    for (int u = 0; u < kUnits; u++) {
+    for (int u = 0; u < S::kUnits; u++) {
       const uint32_t unit = min(threadIdx.x + kThreads * u, kTile * NB - 1);
       const uint64_t block = block_of(page[u], key0 + unit / NB) + unit % NB;
       gone[u] = page[u] >= a.c.n_pages;
@@ -217,83 +222,106 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
       vb[u] = vsc[block];
     }
   };
+  // Whether a thread's block of values counts for scales: no row sees a key outside
+  // [wg_low, wg_high), NaNs are marked, and zeros have any scale.
+  auto counts = [&](uint32_t key0, int u) {
+    const uint32_t unit = threadIdx.x + kThreads * u;
+    return unit < kTile * NB && key0 + unit / NB - wg_low < wg_high - wg_low && vb[u] <= 252 &&
+           ((vw[u][0] | vw[u][1] | vw[u][2] | vw[u][3]) & 0x77777777u) != 0;
+  };
   // A thread's blocks to LDS.  Those of values go 16 bytes at a time in an order of
   // the lane's own, so that neighbouring lanes, 64 bytes apart, meet different banks.
   auto put = [&](uint32_t key0, uint32_t buf, uint32_t flag) {
     const bool cut = key0 < wg_low || key0 + kTile > wg_high;
 #pragma unroll
-    for (int u = 0; u < kUnits; u++) {
+    for (int u = 0; u < S::kUnits; u++) {
       const uint32_t unit = threadIdx.x + kThreads * u;
       if ((kTile * NB) % kThreads == 0 || unit < kTile * NB) {
         const uint32_t key = unit / NB;
         const float fk = scale_of(gone[u] ? 255u : kb[u]);
-        uint8_t *pk = lds_k[buf] + key * kKeyPitch + unit % NB * 64;
+        uint8_t *pk = lds.k[buf] + key * S::kKeyPitch + unit % NB * 64;
 #pragma unroll
         for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(pk + 16 * i) = values8(kw[u][i], fk);
-        // no row sees a key outside [wg_low, wg_high)
         if (cut && key0 + key - wg_low >= wg_high - wg_low) {
           vw[u] = u32x4{0, 0, 0, 0};
-          vb[u] = 127;
+          vb[u] = r.unit;
         }
         if (vb[u] > 252) {
-          nans[flag] = 1;
+          atomicOr(&lds.odd[flag], 1u);
           vw[u] = u32x4{0, 0, 0, 0};
-          vb[u] = 127;
+          vb[u] = r.unit;
         }
-        const float fv = __uint_as_float(vb[u] << 23);
-        uint8_t *pv = lds_v[buf] + key * kPitch + unit % NB * 64;
+        if (HALF && vb[u] + kBelow - r.unit > kBelow + kAbove) {
+          if (counts(key0, u)) atomicOr(&lds.odd[flag], 2u);
+          vb[u] = r.unit;
+        }
+        const float fv = __uint_as_float((HALF ? vb[u] + 127 - r.unit : vb[u]) << 23);
+        uint8_t *pv = lds.v[buf] + key * S::kPitch + unit % NB * 64;
         const bool one = unit & 1, two = unit & 2;
         const u32x4 x = {one ? vw[u][1] : vw[u][0], one ? vw[u][0] : vw[u][1], one ? vw[u][3] : vw[u][2],
                          one ? vw[u][2] : vw[u][3]};
         const u32x4 y = {two ? x[2] : x[0], two ? x[3] : x[1], two ? x[0] : x[2], two ? x[1] : x[3]};
         const uint32_t turn = (unit & 3) * 16;
 #pragma unroll
-        for (uint32_t i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(pv + (16 * i ^ turn)) = values8(y[i], fv);
+        for (uint32_t i = 0; i < 4; i++)
+          *reinterpret_cast<u32x4 *>(pv + (16 * i ^ turn)) =
+              HALF ? halves8(y[i], fv) : __builtin_bit_cast(u32x4, values8(y[i], fv));
       }
     }
   };
 
-  if (threadIdx.x < 3) nans[threadIdx.x] = 0;
+  if (threadIdx.x < 3) lds.odd[threadIdx.x] = 0;
+  if (HALF && threadIdx.x == 3) lds.top = 0;
   __syncthreads();
   if (t < end) {
     const uint32_t key0 = rq.lo + t * kTile;
     ask_pages(key0);
     ask(key0);
     ask_pages(key0 + kTile);
+    if constexpr (HALF) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < S::kUnits; u++)
+        if (counts(key0, u)) top = max(top, vb[u] + 1);
+#pragma unroll
+      for (int d = 1; d < 64; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
+      if (lane == 0) atomicMax(&lds.top, top);
+      __syncthreads();
+      top = uniform(lds.top);
+      r.unit = top ? top - 1 : 127;
+    }
     put(key0, t & 1, 0);
   }
   __syncthreads();
   for (uint32_t flag = 0; t < end; t++) {
     const uint32_t next = flag == 2 ? 0 : flag + 1;
-    if (threadIdx.x == 0) nans[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
+    if (threadIdx.x == 0) lds.odd[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
     const uint32_t key0 = rq.lo + t * kTile, buf = t & 1;
+    const uint32_t odd = uniform(lds.odd[flag]);
+    if (HALF && __builtin_expect(odd & 2, 0)) return false;
     const bool more = t + 1 < end;
     if (more) {
       ask(key0 + kTile);
       ask_pages(key0 + 2 * kTile);
     }
-    const bool busy = key0 < high && key0 + kTile > low;   // some row of this wave sees the tile
-    f32x16 s[2];
-    if (busy) {
-      const uint8_t *rows = lds_k[buf] + n * kKeyPitch + 16 * h;
-      s[0] = s[1] = f32x16{};
+    if (key0 < r.high && key0 + kTile > r.low) {   // some row of this wave sees the tile
+      f32x16 s[2] = {};
+      const uint8_t *keys = lds.k[buf] + n * S::kKeyPitch + 16 * h;
 #pragma unroll
-      for (int st = 0; st < kSteps; st++)
+      for (int st = 0; st < S::kSteps; st++)
 #pragma unroll
         for (int g = 0; g < 2; g++) {
-          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(rows + 32 * g * kKeyPitch + 32 * st);
+          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(keys + 32 * g * S::kKeyPitch + 32 * st);
 #pragma unroll
-          for (int p = QP - 1; p >= 0; p--) s[g] = mfma(k, q[st][p], s[g]);
+          for (int p = S::QP - 1; p >= 0; p--) s[g] = mfma(k, r.q[st][p], s[g]);
         }
-    }
-    if (busy) {
       // keys that the row does not see
-      if (key0 < low_all || key0 + kTile > high_all) {
+      if (key0 < r.low_all || key0 + kTile > r.high_all) {
 #pragma unroll
         for (int g = 0; g < 2; g++)
 #pragma unroll
           for (int i = 0; i < 16; i++)
-            if (key0 + 32 * g + 8 * (i / 4) + 4 * h + i % 4 - sees.first >= sees.count) s[g][i] = -__builtin_inff();
+            if (key0 + 32 * g + 8 * (i / 4) + 4 * h + i % 4 - r.sees.first >= r.sees.count) s[g][i] = -__builtin_inff();
       }
       float top = -__builtin_inff();
 #pragma unroll
@@ -301,55 +329,124 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
 #pragma unroll
         for (int i = 0; i < 16; i++) top = fmaxf(top, s[g][i]);
       top = max_h(top) * c;
-      if (__any(top > m)) {
-        const float up = top > m ? top + kRise : m;
-        const float f = up > m ? __builtin_amdgcn_exp2f(m - up) : 1.0f;
-        l *= f;
+      if (__any(top > r.m + kTop)) {
+        const float up = top > r.m + kTop ? top + (kRise - kTop) : r.m;
+        const float f = up > r.m ? __builtin_amdgcn_exp2f(r.m - up) : 1.0f;
+        r.l *= f;
 #pragma unroll
-        for (int d = 0; d < NB; d++) o[d] *= f;
-        m = up;
+        for (int d = 0; d < NB; d++) r.o[d] *= f;
+        r.m = up;
       }
-      const float bound = m == -__builtin_inff() ? 0.0f : m;
-      // 16 keys of 32 values at a time
-      const uint8_t *from = lds_v[buf] + (4 * h + (lane & 15) / 4) * kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
-      if (__builtin_expect(uniform(nans[flag]), 0)) {
+      const float bound = r.m == -__builtin_inff() ? 0.0f : r.m;
+      // 16 keys of 32 values at a time; the weights of the next 16 keys are made while
+      // the matrix unit takes these
+      const uint8_t *from = lds.v[buf] + (4 * h + (lane & 15) / 4) * S::kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
+      if (__builtin_expect(odd & 1, 0)) {
         const uint32_t key = min(key0 + lane, rq.len - 1);
-        marks |= marked<NB>(vsc + block_of(pages[key >> a.c.shift], key), key0, sees.first, sees.count);
+        r.marks |= marked<NB>(vsc + block_of(pages[key >> a.c.shift], key), key0, r.sees.first, r.sees.count);
       }
-      // The weights of the next 16 keys are made while the matrix unit takes these.
       bf16x8 wp[2][WP], v[NB];
       auto weigh = [&](int g) {
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
           x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, -bound));
-          l += x[i];
+          r.l += x[i];
         }
-        pieces<WP>(x, wp[g & 1]);
+        if constexpr (HALF)
+          wp[g & 1][0] = __builtin_bit_cast(bf16x8, half8(x));
+        else
+          pieces<WP>(x, wp[g & 1]);
       };
       weigh(0);
 #pragma unroll
       for (int g = 0; g < 4; g++) {
 #pragma unroll
-        for (int d = 0; d < NB; d++) v[d] = turned(from + 16 * g * kPitch + 64 * d, 8 * kPitch);
+        for (int d = 0; d < NB; d++) v[d] = turned(from + 16 * g * S::kPitch + 64 * d, 8 * S::kPitch);
         if (g < 3) weigh(g + 1);
 #pragma unroll
         for (int p = WP - 1; p >= 0; p--)
 #pragma unroll
-          for (int d = 0; d < NB; d++) o[d] = mfma(v[d], wp[g & 1][p], o[d]);
+          for (int d = 0; d < NB; d++) r.o[d] = HALF ? mfma_half(v[d], wp[g & 1][p], r.o[d]) : mfma(v[d], wp[g & 1][p], r.o[d]);
       }
     }
     if (more) put(key0 + kTile, buf ^ 1, next);
     flag = next;
     __syncthreads();
   }
+  if constexpr (HALF) {   // weights under 1 again, as the other way leaves them
+    constexpr float kDown = 0x1p-15f;
+    r.m += kTop;
+    r.l *= kDown;
+#pragma unroll
+    for (int d = 0; d < NB; d++) r.o[d] *= kDown;
+  }
+  return true;
+}
 
+template <int DT, int NB>
+__global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(AttnArgs a, Plan plan, Parts out,
+                                                                            FastDiv per_group, float c) {
+  constexpr int D = 32 * NB;
+  __shared__ typename Shape<DT, NB>::Lds lds;
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t n = lane & 31, h = lane >> 5;
+  const uint32_t number = blockIdx.x / a.c.heads, head = blockIdx.x - number * a.c.heads;
+
+  Item it;
+  if (!find_item(a, plan, number, blockIdx.x == 0 && out.each, out.each, out.all, out.before, it)) return;
+  const Request rq = uniform(request(a, it.b));
+  // this lane's row
+  const uint32_t row = it.group * kRows + wave * 32 + n;
+  const bool live = row < rq.n * a.group;
+  const uint32_t token = live ? per_group.div(row) : 0;
+  const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
+  Rows32<DT, NB> r;
+  const Span sees = r.sees = span(a, rq, token, live);
+  r.low = sees.count ? sees.first : ~0u;
+  r.high = sees.count ? sees.first + sees.count : 0;
+  r.low_all = live ? sees.first : 0;
+  r.high_all = live ? sees.first + sees.count : ~0u;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    r.low = min(r.low, uint32_t(__shfl_xor(int(r.low), d)));
+    r.high = max(r.high, uint32_t(__shfl_xor(int(r.high), d)));
+    r.low_all = max(r.low_all, uint32_t(__shfl_xor(int(r.low_all), d)));
+    r.high_all = min(r.high_all, uint32_t(__shfl_xor(int(r.high_all), d)));
+  }
+  r.low = uniform(r.low);
+  r.high = uniform(r.high);
+  r.low_all = uniform(r.low_all);
+  r.high_all = uniform(r.high_all);
+  // the workgroup's first and last row have the first and the last key
+  const uint32_t last_row = min(it.group * kRows + kRows, rq.n * a.group) - 1;
+  const Span s0 = span(a, rq, uniform(per_group.div(it.group * kRows)), true);
+  const Span s1 = span(a, rq, uniform(per_group.div(last_row)), true);
+  r.wg_high = s1.first + s1.count;
+  r.wg_low = s0.count ? s0.first : 0;
+#pragma unroll
+  for (int s = 0; s < 2 * NB; s++) {
+    take_query8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 16 * s + 8 * h) * esize(DT), live, r.q[s]);
+  }
+
+  const int32_t *pages = a.table + it.b * a.table_stride;
+  uint32_t t = uint32_t(min(it.piece * it.tiles, uint64_t(rq.tiles)));
+  uint32_t end = uint32_t(min((it.piece + 1) * it.tiles, uint64_t(rq.tiles)));
+  end = r.wg_high > rq.lo ? min(end, (r.wg_high - rq.lo + kTile - 1) / kTile) : 0;
+  if (r.wg_low > rq.lo) t = max(t, (r.wg_low - rq.lo) / kTile);
+  if (DT != BF16 || !take_tiles<DT, NB, DT == BF16>(a, rq, pages, head, t, end, c, lds, r)) {
+    __syncthreads();
+    take_tiles<DT, NB, false>(a, rq, pages, head, t, end, c, lds, r);
+  }
+
+  float l = r.l;
   l += __shfl_xor(l, 32);
   if (rq.bad) l = __builtin_nanf("");
   if (!live) return;
 #pragma unroll
   for (int d = 0; d < NB; d++)
-    if (marks >> d & 1) o[d] = f32x16{} + __builtin_nanf("");
+    if (r.marks >> d & 1) r.o[d] = f32x16{} + __builtin_nanf("");
+  const int unit = int(r.unit) - 127;
   if (it.pieces == 1) {
     const uint64_t y = rq.start + token;
     const float f = over(l);
@@ -357,37 +454,48 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
 #pragma unroll
     for (int d = 0; d < NB; d++)
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        store4<DT>(p + (32 * d + 8 * i) * esize(DT), f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]} * f);
-    if (a.lse && h == 0) a.lse[y * a.heads + qh] = log_sum(m, l);
+      for (int i = 0; i < 4; i++) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = __builtin_ldexpf(r.o[d][4 * i + e] * f, unit);
+        store4<DT>(p + (32 * d + 8 * i) * esize(DT), v);
+      }
+    if (a.lse && h == 0) a.lse[y * a.heads + qh] = log_sum(r.m, l);
   } else if (it.slot < out.slots) {   // starts out of order can make more pieces than there is room for
     const uint64_t p = (uint64_t(head) * out.slots + it.slot) * kRows + wave * 32 + n;
 #pragma unroll
     for (int d = 0; d < NB; d++)
 #pragma unroll
-      for (int i = 0; i < 4; i++)
-        *reinterpret_cast<f32x4 *>(out.sums + p * D + 32 * d + 8 * i + 4 * h) =
-            f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-    if (h == 0) out.ml[p] = make_float2(m, l);
+      for (int i = 0; i < 4; i++) {
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; e++) v[e] = __builtin_ldexpf(r.o[d][4 * i + e], unit);
+        *reinterpret_cast<f32x4 *>(out.sums + p * D + 32 * d + 8 * i + 4 * h) = v;
+      }
+    if (h == 0) out.ml[p] = make_float2(r.m, l);
   }
 }
 
-// Joins the pieces of a group, in their order: four workgroups a group, a team of
-// D / 4 lanes a row.  Groups are named by their first piece's slot.
+// Joins the pieces of a group, in their order: a team of D / 4 lanes a row, and as
+// many rows a workgroup as it has teams.  Groups are named by their first piece's
+// slot; the workgroups go through those there are.
 template <int DT, int NB>
 __global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv per_group) {
-  constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
-  const uint32_t head = blockIdx.y, slot = blockIdx.x >> 2;
-  const uint32_t b = uniform(holder(in.before, a.batch, slot));
-  const Request rq = uniform(request(a, b));
-  const uint64_t piece = *in.each, count = (max(rq.tiles, 1u) + piece - 1) / piece;
-  const uint64_t rel = slot - in.before[b];
-  // (the last: starts out of order can make more pieces than there is room for)
-  if (count <= 1 || rel % count || rel / count >= groups_of(a, rq, kRows) || slot + count > in.slots) return;
-  const uint32_t team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
-  const uint32_t end = min((blockIdx.x & 3) * 32 + 32, rq.n * a.group - uint32_t(rel / count) * kRows);
-  if (team >= kTeams) return;
-  for (uint32_t r = (blockIdx.x & 3) * 32 + team; r < end; r += kTeams) {
+  constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes, kShares = (kRows + kTeams - 1) / kTeams;
+  const uint32_t head = blockIdx.y, team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  const uint64_t all = min(*in.all, uint64_t(in.slots)) * kShares, piece = *in.each;
+  for (uint64_t x = blockIdx.x; x < all; x += gridDim.x) {
+    const uint32_t slot = uint32_t(x / kShares);
+    const uint32_t b = uniform(holder(in.before, a.batch, slot));
+    const Request rq = uniform(request(a, b));
+    const uint64_t count = (max(rq.tiles, 1u) + piece - 1) / piece, rel = slot - in.before[b];
+    const uint32_t r = uint32_t(x - uint64_t(slot) * kShares) * kTeams + team;
+    const uint64_t group = rel / count, row64 = group * kRows + r;
+    // (the last: starts out of order can make more pieces than there is room for)
+    if (count <= 1 || rel % count || team >= kTeams || r >= kRows || row64 >= uint64_t(rq.n) * a.group ||
+        slot + count > in.slots)
+      continue;
+    const uint32_t row = uint32_t(row64);
     const uint64_t p0 = (uint64_t(head) * in.slots + slot) * kRows + r;
     float top = -__builtin_inff();
 #pragma unroll 4
@@ -402,8 +510,7 @@ __global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv
       l += ml.y * f;
       o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
     }
-    const uint32_t row = uint32_t(rel / count) * kRows + r, tk = per_group.div(row);
-    const uint32_t h = head * a.group + row - tk * a.group;
+    const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
     const uint64_t y = rq.start + tk;
     store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
     if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
@@ -446,7 +553,8 @@ struct Tall {
         a, z.plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !z.slots) return e;
-    k_join_tall<DT, NB><<<dim3(z.slots * 4, a.c.heads), 256, 0, s>>>(a, p, per_group);
+    const uint32_t shares = (kRows * NB * 8 + 255) / 256 + 1, most = 4096 / a.c.heads + 1;
+    k_join_tall<DT, NB><<<dim3(std::min(z.slots * shares, most), a.c.heads), 256, 0, s>>>(a, p, per_group);
     return hipGetLastError();
   }
 };

@@ -63,13 +63,14 @@ def check_attention(q, c, table, lens, starts, page, got, got_lse=None, causal=T
       * the score: dim FP32 additions, each within 2^-23 of a partial sum of
         scale |q|.|k|, and three roundings (scale, its product with log2 e, the
         multiply-add) within 2^-24 of at most that sum and the largest score's;
-      * the exponential, 2^-22, and the weight's bits: 2^-17 beside BF16 queries
-        (two BF16 pieces), 2^-24 beside FP32;
+      * the exponential, 2^-22, and the weight's bits: beside BF16 queries 2^-11
+        (FP16, or two BF16 pieces, 2^-17), 2^-24 beside FP32;
     the sums over n keys add n 2^-23 each, joining pieces and dividing 8 roundings
     of 2^-24, and the result half a step of its type.  What FP32 cannot hold: a
     weight under 2^-126 may vanish, whole or in its last piece, the largest being at
     least 2^-8, so n 2^-118 max|v| are added for sum w|v| and as much for the sum of
-    weights; the result's step is at least 2^-133; and sums past FP32's range, which
+    weights; an FP16 weight under 2^-14 is off by up to 2^-25 where the row's largest
+    is 2^7 or more, n 2^-32 max|v| in all; the result's step is at least 2^-133; and sums past FP32's range, which
     weights up to 1 reach where n max|v| does, give infinities and NaNs."""
     k, v = values(c)
     x = f64(q)
@@ -77,11 +78,12 @@ def check_attention(q, c, table, lens, starts, page, got, got_lse=None, causal=T
     dim = x.shape[2]
     sc = 1 / np.sqrt(dim) if scale is None else scale
     top = sc * np.abs(x).sum(2) * np.nanmax(np.abs(k))         # at least scale |q|.|k| of any key
-    d = top * (dim * 2.0 ** -23 + 6 * 2.0 ** -24) + 2.0 ** -22 + (2.0 ** -17 if q.dtype == torch.bfloat16 else 2.0 ** -24)
+    d = top * (dim * 2.0 ** -23 + 6 * 2.0 ** -24) + 2.0 ** -22 + (2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -24)
     n = max(max(lens), 1)
     mine = (size != -1)                                        # rows that some request has
     bound = (2 * d[..., None] + 2 * n * 2.0 ** -23 + 8 * 2.0 ** -24) * size + torch.finfo(q.dtype).eps / 2 * np.abs(out)
-    bound = bound + 2 * n * 2.0 ** -118 * np.nanmax(np.abs(v)) + 2.0 ** -134
+    least = 2.0 ** -32 if q.dtype == torch.bfloat16 else 2.0 ** -118
+    bound = bound + 2 * n * least * np.nanmax(np.abs(v)) + 2.0 ** -134
     y = f64(got)
     nan = np.isnan(out)
     if n * np.nanmax(np.abs(v)) >= 2.0 ** 127:

@@ -354,6 +354,49 @@ def test_what_a_query_does_not_see_has_no_effect(t):
             u.copy_(old)
 
 
+@pytest.mark.parametrize("kind", ["near", "far", "rising", "zeros first", "one far block", "far where nobody looks"])
+def test_values_of_many_sizes(kind):
+    # values whose scales leave FP16's reach of the first tile's are taken another way
+    lens, new = [300, 90], [200, 90]
+    q, c, table, starts = attend_case(lens, new, 4, 2, 64, 16, "bf16", 9)
+    vs, rng = c.v_scales.view(torch.uint8), np.random.default_rng(2)
+    where = torch.zeros(c.v.shape[0], 16, dtype=torch.long, device="cuda")     # the position of each place
+    for row, n in zip(table, lens):
+        for p in range(n):
+            where[row[p // 16], p % 16] = p
+    pos = where[:, None, :, None].expand(vs.shape)
+    if kind == "near":        # as far as it reaches: 12 above and 23 below the first tile's largest
+        vs.copy_(torch.where(pos < 64, 127, torch.from_numpy(rng.integers(104, 140, vs.shape)).cuda()))
+    elif kind == "far":
+        vs.copy_(torch.from_numpy(rng.integers(60, 200, vs.shape)))
+    elif kind == "rising":
+        vs.copy_(100 + pos // 8)
+    elif kind == "zeros first":
+        c.v.mul_(where[:, None, :, None] >= 64)
+        vs.copy_(torch.where(pos < 64, 0, 150))
+    elif kind == "one far block":
+        vs[table[0][250 // 16], 1, 250 % 16, 1] = 90
+    else:                     # pages that no request's length reaches, and a key of zeros
+        used = torch.zeros(c.v.shape[0], 16, dtype=torch.bool, device="cuda")
+        for row, n in zip(table, lens):
+            for p in range(n):
+                used[row[p // 16], p % 16] = True
+        vs.masked_fill_(~used[:, None, :, None], 200)
+        c.v[table[0][200 // 16], :, 200 % 16] = 0x80 | 0x08
+        vs[table[0][200 // 16], :, 200 % 16] = 0
+    for mask in (dict(), dict(window=70), dict(causal=False)):
+        out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts), lse=True, **mask)
+        check_attention(q, c, table, lens, starts, 16, out, lse, **mask)
+
+
+def test_values_of_many_sizes_in_pieces():
+    lens, new = [5000], [20]
+    q, c, table, starts = attend_case(lens, new, 4, 2, 64, 64, "bf16", 9)
+    c.v_scales.view(torch.uint8)[table[0][70], 0, 5, 0] = 60       # one piece the other way, the others not
+    out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts), lse=True)
+    check_attention(q, c, table, lens, starts, 64, out, lse)
+
+
 def test_scale_bytes_at_the_ends():
     q, c, table, starts = attend_case([90], None, 2, 1, 64, 16, "bf16", 4)
     vs = c.v_scales.view(torch.uint8)
