@@ -133,7 +133,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
 }
 
 template <int DT, int NB>
-constexpr int kResident = DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
+constexpr int kResident = DT == BF16 ? NB == 1 ? 4 : NB == 2 ? 3 : NB <= 4 ? 2 : 1 : NB <= 2 ? 2 : 1;   // waves a SIMD
 
 template <int DT, int NB>
 struct Shape {
@@ -142,7 +142,9 @@ struct Shape {
   // bytes of a key's values in LDS: 64 modulo 128, so that four keys' parts fill the
   // banks; and of its keys, 16 modulo 32, for rows of 16 bytes a lane
   static constexpr int kPitch = 64 * NB + (NB % 2 ? 0 : 64), kKeyPitch = 64 * NB + 16;
-  static constexpr int kUnits = (NB + 3) / 4;                    // blocks of a tile's keys, and values, a thread
+  // blocks of a tile that a thread converts, of 64 NB of keys and then as many of values
+  static constexpr uint32_t kBlocks = kTile * NB;
+  static constexpr int kUnits = int((2 * kBlocks + kThreads - 1) / kThreads);
   struct Lds {
     __attribute__((aligned(16))) uint8_t v[2][kTile * kPitch], k[2][kTile * kKeyPitch];
     uint32_t odd[3];     // a tile has a NaN (1), scales out of reach (2): this one, the next, the one after
@@ -153,7 +155,7 @@ struct Shape {
 // What a wave has of its rows.
 template <int DT, int NB>
 struct Rows32 {
-  bf16x8 q[2 * NB][Shape<DT, NB>::QP];
+  bf16x8 q[2 * NB][DT == BF16 ? 1 : 3];
   Span sees;                                   // this lane's row
   uint32_t low, high, low_all, high_all;       // keys that some row of the wave sees, and that all see
   uint32_t wg_low, wg_high;                    // that some row of the workgroup sees
@@ -193,41 +195,44 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
   r.marks = 0;
   r.unit = 127;
 
-  // A thread's blocks are `unit % NB` of the keys unit / NB of a tile.  Their pages are
-  // asked for a tile ahead of the codes (behind the last key, the last one's).  A place
-  // outside any page is taken from page 0 and counts as a NaN.
+  // A thread's unit u is block `number % NB` of key number / NB of a tile, of its keys
+  // or of its values, the same for a whole wave.  Pages are asked for a tile ahead of
+  // the codes (behind the last key, the last one's).  A place outside any page is
+  // taken from page 0 and counts as a NaN.
+  const uint32_t wave = uniform(threadIdx.x >> 6);
+  auto is_key = [&](int u) {
+    return kThreads * (u + 1) <= S::kBlocks || (kThreads * u < S::kBlocks && kThreads * u + 64 * wave < S::kBlocks);
+  };
+  auto number = [&](int u) {
+    const uint32_t x = min(threadIdx.x + kThreads * u, 2 * S::kBlocks - 1);
+    return x < S::kBlocks ? x : x - S::kBlocks;
+  };
+  auto is_unit = [&](int u) { return kThreads * (u + 1) <= 2 * S::kBlocks || kThreads * u + 64 * wave < 2 * S::kBlocks; };
   uint32_t page[S::kUnits];
   auto ask_pages = [&](uint32_t key0) {
 #pragma unroll
-    for (int u = 0; u < S::kUnits; u++) {
-      const uint32_t key = min(threadIdx.x + kThreads * u, kTile * NB - 1) / NB;
-      page[u] = uint32_t(pages[min(key0 + key, rq.len - 1) >> a.c.shift]);
-    }
+    for (int u = 0; u < S::kUnits; u++) page[u] = uint32_t(pages[min(key0 + number(u) / NB, rq.len - 1) >> a.c.shift]);
   };
   auto block_of = [&](uint32_t page, uint32_t key) {
     return uint64_t(page < a.c.n_pages ? page : 0) * page_stride + uint64_t(key & mask) * place;
   };
-  u32x4 kw[S::kUnits], vw[S::kUnits];
-  uint32_t kb[S::kUnits], vb[S::kUnits];
+  u32x4 code[S::kUnits];
+  uint32_t byte[S::kUnits];
   bool gone[S::kUnits];
   auto ask = [&](uint32_t key0) {
 #pragma unroll
     for (int u = 0; u < S::kUnits; u++) {
-      const uint32_t unit = min(threadIdx.x + kThreads * u, kTile * NB - 1);
-      const uint64_t block = block_of(page[u], key0 + unit / NB) + unit % NB;
+      const uint64_t block = block_of(page[u], key0 + number(u) / NB) + number(u) % NB;
       gone[u] = page[u] >= a.c.n_pages;
-      kw[u] = *reinterpret_cast<const u32x4 *>(kc + block * 16);
-      kb[u] = ksc[block];
-      vw[u] = *reinterpret_cast<const u32x4 *>(vc + block * 16);
-      vb[u] = vsc[block];
+      code[u] = *reinterpret_cast<const u32x4 *>((is_key(u) ? kc : vc) + block * 16);
+      byte[u] = (is_key(u) ? ksc : vsc)[block];
     }
   };
   // Whether a thread's block of values counts for scales: no row sees a key outside
   // [wg_low, wg_high), NaNs are marked, and zeros have any scale.
   auto counts = [&](uint32_t key0, int u) {
-    const uint32_t unit = threadIdx.x + kThreads * u;
-    return unit < kTile * NB && key0 + unit / NB - wg_low < wg_high - wg_low && vb[u] <= 252 &&
-           ((vw[u][0] | vw[u][1] | vw[u][2] | vw[u][3]) & 0x77777777u) != 0;
+    return is_unit(u) && !is_key(u) && key0 + number(u) / NB - wg_low < wg_high - wg_low && byte[u] <= 252 &&
+           ((code[u][0] | code[u][1] | code[u][2] | code[u][3]) & 0x77777777u) != 0;
   };
   // A thread's blocks to LDS.  Those of values go 16 bytes at a time in an order of
   // the lane's own, so that neighbouring lanes, 64 bytes apart, meet different banks.
@@ -235,38 +240,40 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
     const bool cut = key0 < wg_low || key0 + kTile > wg_high;
 #pragma unroll
     for (int u = 0; u < S::kUnits; u++) {
-      const uint32_t unit = threadIdx.x + kThreads * u;
-      if ((kTile * NB) % kThreads == 0 || unit < kTile * NB) {
-        const uint32_t key = unit / NB;
-        const float fk = scale_of(gone[u] ? 255u : kb[u]);
-        uint8_t *pk = lds.k[buf] + key * S::kKeyPitch + unit % NB * 64;
+      if (!is_unit(u)) continue;
+      const uint32_t key = number(u) / NB, blk = number(u) % NB;
+      if (is_key(u)) {
+        const float f = scale_of(gone[u] ? 255u : byte[u]);
+        uint8_t *p = lds.k[buf] + key * S::kKeyPitch + blk * 64;
 #pragma unroll
-        for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(pk + 16 * i) = values8(kw[u][i], fk);
-        if (cut && key0 + key - wg_low >= wg_high - wg_low) {
-          vw[u] = u32x4{0, 0, 0, 0};
-          vb[u] = r.unit;
-        }
-        if (vb[u] > 252) {
-          atomicOr(&lds.odd[flag], 1u);
-          vw[u] = u32x4{0, 0, 0, 0};
-          vb[u] = r.unit;
-        }
-        if (HALF && vb[u] + kBelow - r.unit > kBelow + kAbove) {
-          if (counts(key0, u)) atomicOr(&lds.odd[flag], 2u);
-          vb[u] = r.unit;
-        }
-        const float fv = __uint_as_float((HALF ? vb[u] + 127 - r.unit : vb[u]) << 23);
-        uint8_t *pv = lds.v[buf] + key * S::kPitch + unit % NB * 64;
-        const bool one = unit & 1, two = unit & 2;
-        const u32x4 x = {one ? vw[u][1] : vw[u][0], one ? vw[u][0] : vw[u][1], one ? vw[u][3] : vw[u][2],
-                         one ? vw[u][2] : vw[u][3]};
-        const u32x4 y = {two ? x[2] : x[0], two ? x[3] : x[1], two ? x[0] : x[2], two ? x[1] : x[3]};
-        const uint32_t turn = (unit & 3) * 16;
-#pragma unroll
-        for (uint32_t i = 0; i < 4; i++)
-          *reinterpret_cast<u32x4 *>(pv + (16 * i ^ turn)) =
-              HALF ? halves8(y[i], fv) : __builtin_bit_cast(u32x4, values8(y[i], fv));
+        for (int i = 0; i < 4; i++) *reinterpret_cast<bf16x8 *>(p + 16 * i) = values8(code[u][i], f);
+        continue;
       }
+      if (cut && key0 + key - wg_low >= wg_high - wg_low) {
+        code[u] = u32x4{0, 0, 0, 0};
+        byte[u] = r.unit;
+      }
+      // seldom: a NaN, or a scale out of reach
+      const bool bad = byte[u] > 252 || (HALF && byte[u] + kBelow - r.unit > kBelow + kAbove);
+      if (__builtin_expect(__any(bad), 0)) {
+        if (byte[u] > 252) {
+          atomicOr(&lds.odd[flag], 1u);
+          code[u] = u32x4{0, 0, 0, 0};
+        }
+        if (HALF && bad && counts(key0, u)) atomicOr(&lds.odd[flag], 2u);
+        if (bad) byte[u] = r.unit;
+      }
+      const float f = __uint_as_float((HALF ? byte[u] + 127 - r.unit : byte[u]) << 23);
+      uint8_t *p = lds.v[buf] + key * S::kPitch + blk * 64;
+      const bool one = threadIdx.x & 1, two = threadIdx.x & 2;
+      const u32x4 x = {one ? code[u][1] : code[u][0], one ? code[u][0] : code[u][1], one ? code[u][3] : code[u][2],
+                       one ? code[u][2] : code[u][3]};
+      const u32x4 y = {two ? x[2] : x[0], two ? x[3] : x[1], two ? x[0] : x[2], two ? x[1] : x[3]};
+      const uint32_t turn = (threadIdx.x & 3) * 16;
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++)
+        *reinterpret_cast<u32x4 *>(p + (16 * i ^ turn)) =
+            HALF ? halves8(y[i], f) : __builtin_bit_cast(u32x4, values8(y[i], f));
     }
   };
 
@@ -282,7 +289,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
       uint32_t top = 0;
 #pragma unroll
       for (int u = 0; u < S::kUnits; u++)
-        if (counts(key0, u)) top = max(top, vb[u] + 1);
+        if (counts(key0, u)) top = max(top, byte[u] + 1);
 #pragma unroll
       for (int d = 1; d < 64; d *= 2) top = max(top, uint32_t(__shfl_xor(int(top), d)));
       if (lane == 0) atomicMax(&lds.top, top);
@@ -386,7 +393,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
 
 template <int DT, int NB>
 __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(AttnArgs a, Plan plan, Parts out,
-                                                                            FastDiv per_group, float c) {
+                                                                          FastDiv per_group, float c) {
   constexpr int D = 32 * NB;
   __shared__ typename Shape<DT, NB>::Lds lds;
   const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);

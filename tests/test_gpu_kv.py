@@ -258,6 +258,14 @@ def test_attention_of_long_caches(lens, new, mask, t):
     run_attention(lens, new, 4, 1, 64, 64, t, 3, **mask)
 
 
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 256])
+@pytest.mark.parametrize("lens,new", [([700, 150, 0], [300, 150, 0]), ([257, 5, 900], [257, 5, 256])])
+def test_attention_of_many_rows(lens, new, dim):
+    # 512 rows a request on average and more
+    run_attention(lens, new, 8, 2, dim, 32, "bf16", dim)
+    run_attention(lens, new, 4, 1, dim, 16, "bf16", dim, window=100)
+
+
 @pytest.mark.parametrize("batch", [64, 65, 300, 700])
 def test_attention_of_many_requests(batch):
     rng = np.random.default_rng(batch)
@@ -387,6 +395,21 @@ def test_values_of_many_sizes(kind):
     for mask in (dict(), dict(window=70), dict(causal=False)):
         out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts), lse=True, **mask)
         check_attention(q, c, table, lens, starts, 16, out, lse, **mask)
+
+
+def test_nans_among_the_largest_values():
+    # a NaN's byte lies within reach of the largest scales
+    lens, new = [100], [80]
+    q, c, table, starts = attend_case(lens, new, 4, 1, 64, 16, "bf16", 9)
+    vs = c.v_scales.view(torch.uint8)
+    vs.fill_(240)
+    want = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts))
+    for byte in (253, 254, 255):
+        vs[table[0][50 // 16], 0, 50 % 16, 1] = byte
+        out = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts))
+        nan = torch.zeros_like(out, dtype=torch.bool)
+        nan[30:, :, 32:] = True                                # queries at 20 .. 99
+        assert torch.equal(out.isnan(), nan) and torch.equal(out[~nan], want[~nan])
 
 
 def test_values_of_many_sizes_in_pieces():
