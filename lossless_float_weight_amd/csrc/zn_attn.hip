@@ -29,7 +29,7 @@ namespace zn {
 namespace {
 
 constexpr int kWaves = 4;       // of a workgroup
-constexpr uint32_t kLeast = 1;  // tiles that a wave takes at least
+constexpr uint32_t kShort = 16;  // tiles of a short cache
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -59,7 +59,6 @@ __device__ __forceinline__ float sum_j(float x) {
 // Groups are counted in 32 bits: the host keeps tokens * group + batch below 2^30.
 struct Plan {
   uint32_t takers;     // of a head
-  uint32_t least;      // tiles of a share at least
 };
 struct Shares {
   uint64_t total, each;
@@ -79,7 +78,6 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
   const uint64_t upto = scan(mine);
   sh.total = of_lane(upto, 63);
   sh.each = (sh.total + plan.takers - 1) / plan.takers;
-  if (sh.each < plan.least) sh.each = plan.least;
   if (tell_each) {
     uint64_t at = upto - mine;
     for (uint32_t i = 0; i < per; i++)
@@ -101,8 +99,8 @@ __device__ __forceinline__ bool find_start(const AttnArgs &a, const Plan &plan, 
   }
 }
 
-// One wave's tiles: sums o (values 16 d + 4 j + i of row l % 16), bound m and this
-// lane's share of the weights l.
+// What a wave has of a group of rows: sums o (values 16 d + 4 j + i of row l % 16),
+// bound m and this lane's share of the weights l.
 template <int DT, int NB>
 struct Rows16 {
   static constexpr int QP = DT == BF16 ? 1 : 3;   // pieces of a query
@@ -112,50 +110,24 @@ struct Rows16 {
   bf16x8 q[NB][QP];
   f32x4 o[2 * NB];
   float m, l;
+  uint32_t marks;                                 // blocks of values that have a NaN for this row
+  bool live;
+  uint32_t token, qh;
+  Span sees;
+  uint32_t low, high, low_all, high_all;          // keys that some row sees, and that all see
 };
 
 template <int DT, int NB>
-constexpr int kResident = DT == BF16 && NB <= 2 ? 3 : DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
-
-template <int DT, int NB>
-__global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(AttnArgs a, Plan plan, Parts out,
-                                                                        FastDiv per_group, float c) {
-  using R = Rows16<DT, NB>;
-  constexpr int D = 32 * NB;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * R::kLds];
-  const uint32_t lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const uint32_t n = lane & 15, j = lane >> 4;
-  const uint32_t head = blockIdx.y, taker = blockIdx.x * kWaves + wave;
-
-  Shares sh;
-  uint32_t b;
-  uint64_t before;
-  if (taker >= plan.takers || !find_start(a, plan, 16, taker, sh, b, before,
-                                            taker + head ? nullptr : out.each, out.before))
-    return;
-  sh.each = uniform(sh.each);
-  b = uniform(b);
-  before = uniform(before);
-  uint64_t at_tile = taker * sh.each;
-  const uint64_t end_tile = min(at_tile + sh.each, uniform(sh.total));
-  // group after group, request after request
-  while (at_tile < end_tile) {
-  const Request rq = uniform(request(a, b));
-  const uint32_t whole = max(rq.tiles, 1u);
-  const uint32_t groups = groups_of(a, rq, 16);
-  const uint32_t grp = groups > 1 ? uint32_t((at_tile - before) / whole) : 0;
-  const uint32_t from = uint32_t(at_tile - before - uint64_t(grp) * whole);
-  const uint32_t to = uint32_t(min(uint64_t(whole), from + (end_tile - at_tile)));
-  // this lane's row
-  const uint32_t row = grp * 16 + n;
-  const bool live = row < rq.n * a.group;
-  const uint32_t token = live ? per_group.div(row) : 0;
-  const uint32_t qh = head * a.group + (live ? row - token * a.group : 0);
-  const Span sees = span(a, rq, token, live);
-  const uint32_t first = sees.first, count = sees.count;
-  // tiles that some row of the wave sees, and those that all see whole
+__device__ __forceinline__ void set_rows(const AttnArgs &a, const Request &rq, uint32_t group, uint32_t head,
+                                         const FastDiv &per_group, Rows16<DT, NB> &r) {
+  const uint32_t row = group * 16 + (threadIdx.x & 15);
+  r.live = row < rq.n * a.group;
+  r.token = r.live ? per_group.div(row) : 0;
+  r.qh = head * a.group + (r.live ? row - r.token * a.group : 0);
+  r.sees = span(a, rq, r.token, r.live);
+  const uint32_t first = r.sees.first, count = r.sees.count;
   uint32_t low = count ? first : ~0u, high = count ? first + count : 0;
-  uint32_t low_all = live ? first : 0, high_all = live ? first + count : ~0u;
+  uint32_t low_all = r.live ? first : 0, high_all = r.live ? first + count : ~0u;
 #pragma unroll
   for (int d = 1; d < 16; d *= 2) {
     low = min(low, uint32_t(__shfl_xor(int(low), d)));
@@ -163,22 +135,27 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
     low_all = max(low_all, uint32_t(__shfl_xor(int(low_all), d)));
     high_all = min(high_all, uint32_t(__shfl_xor(int(high_all), d)));
   }
-  low = uniform(low);
-  high = uniform(high);
-  low_all = uniform(low_all);
-  high_all = uniform(high_all);
-
-  R r;
+  r.low = uniform(low);
+  r.high = uniform(high);
+  r.low_all = uniform(low_all);
+  r.high_all = uniform(high_all);
 #pragma unroll
   for (int d = 0; d < 2 * NB; d++) r.o[d] = f32x4{0, 0, 0, 0};
   r.m = -__builtin_inff();
   r.l = 0.0f;
-  uint32_t marks = 0;   // blocks of values that have a NaN for this row
+  r.marks = 0;
+}
 
-  uint8_t *mine = lds + wave * R::kLds;
+// One wave's tiles: t, t + STEP .. of those from `from` to `to` that some row sees.
+template <int DT, int NB, int STEP>
+__device__ __forceinline__ void take_tiles(const AttnArgs &a, const Request &rq, const int32_t *pages, uint32_t head,
+                                           uint32_t from, uint32_t to, uint32_t offset, float c, uint8_t *mine,
+                                           Rows16<DT, NB> &r) {
+  using R = Rows16<DT, NB>;
+  const uint32_t lane = threadIdx.x & 63, n = lane & 15, j = lane >> 4;
+  const uint32_t first = r.sees.first, count = r.sees.count;
   const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
   const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
-  const int32_t *pages = a.table + b * a.table_stride;
   const uint32_t mask = (1u << a.c.shift) - 1;
   const uint32_t place = uint32_t(a.c.place_stride);
   const uint32_t last = a.c.n_pages;
@@ -239,25 +216,23 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
       }
   };
 
-  // the tiles that some row sees
   uint32_t t = from, end = min(to, rq.tiles);
-  end = high > rq.lo ? min(end, (high - rq.lo + kTile - 1) / kTile) : 0;
-  if (low > rq.lo) t = max(t, (low - rq.lo) / kTile);
+  end = r.high > rq.lo ? min(end, (r.high - rq.lo + kTile - 1) / kTile) : 0;
+  if (r.low > rq.lo) t = max(t, (r.low - rq.lo) / kTile);
+  t += offset;
   Where w = {};
   uint32_t asked = 0;
-  if (t < end) {
-    asked = ask_pages(rq.lo + t * kTile);
-  }
+  if (t < end) asked = ask_pages(rq.lo + t * kTile);
 #pragma unroll
   for (int s = 0; s < NB; s++)
-    take_query8<DT>(a.q + ((rq.start + token) * a.q_token + qh * a.q_head + 8 * (NB * j + s)) * esize(DT), live, r.q[s]);
+    take_query8<DT>(a.q + ((rq.start + r.token) * a.q_token + r.qh * a.q_head + 8 * (NB * j + s)) * esize(DT), r.live, r.q[s]);
   if (t < end) {
     w = where(rq.lo + t * kTile, asked);
-    asked = ask_pages(rq.lo + (t + 1) * kTile);
+    asked = ask_pages(rq.lo + (t + STEP) * kTile);
     ask_keys(w);
     ask_values(w);
   }
-  for (; t < end; t++) {
+  for (; t < end; t += STEP) {
     const uint32_t key0 = rq.lo + t * kTile;
     // scores
     f32x4 s[4];
@@ -276,15 +251,15 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
       }
       s[g] = acc;
     }
-    const bool more = t + 1 < end;
+    const bool more = t + STEP < end;
     const uint64_t here[4] = {w.base[0], w.base[1], w.base[2], w.base[3]};
     if (more) {
-      w = where(key0 + kTile, asked);
-      asked = ask_pages(key0 + 2 * kTile);
+      w = where(key0 + STEP * kTile, asked);
+      asked = ask_pages(key0 + 2 * STEP * kTile);
       ask_keys(w);
     }
     // keys that the row does not see
-    if (key0 < low_all || key0 + kTile > high_all) {
+    if (key0 < r.low_all || key0 + kTile > r.high_all) {
 #pragma unroll
       for (int g = 0; g < 4; g++)
 #pragma unroll
@@ -307,7 +282,7 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
     }
     const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
     // values of 32 keys to LDS
-    const bool cut = key0 < low || key0 + kTile > high;
+    const bool cut = key0 < r.low || key0 + kTile > r.high;
     bool nan = false;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -317,7 +292,7 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
         if (NB % 2 == 0 || unit < 32 * NB) {
           const uint32_t key = unit / NB, blk = unit % NB;
           // no row sees a key outside [low, high)
-          if (cut && key0 + 32 * h + key - low >= high - low) {
+          if (cut && key0 + 32 * h + key - r.low >= r.high - r.low) {
             vw[h][u] = u32x4{0, 0, 0, 0};
             vb[h][u] = 127;
           }
@@ -345,10 +320,10 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
         pieces<R::WP>(x, wp);
       }
       // and back, 4 keys of one value at a time
-      const uint8_t *from = mine + (4 * j + n / 4) * R::kPitch + (n & 3) * 8;
+      const uint8_t *parts = mine + (4 * j + n / 4) * R::kPitch + (n & 3) * 8;
 #pragma unroll
       for (int d = 0; d < 2 * NB; d++) {
-        const bf16x8 v = turned(from + 32 * d, 16 * R::kPitch);
+        const bf16x8 v = turned(parts + 32 * d, 16 * R::kPitch);
 #pragma unroll
         for (int p = R::WP - 1; p >= 0; p--) r.o[d] = mfma(v, wp[p], r.o[d]);
       }
@@ -356,36 +331,151 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
     }
     if (__builtin_expect(__any(nan), 0)) {
       const uint64_t at = (lane < 32 ? lane < 16 ? here[0] : here[1] : lane < 48 ? here[2] : here[3]) + (lane & 15) * place;
-      marks |= marked<NB>(vsc + at, key0, first, count);
+      r.marks |= marked<NB>(vsc + at, key0, first, count);
     }
   }
-
   r.l = sum_j(r.l);
   if (rq.bad) r.l = __builtin_nanf("");
 #pragma unroll
   for (int d = 0; d < 2 * NB; d++)
-    if (marks >> d / 2 & 1) r.o[d] = f32x4{} + __builtin_nanf("");
-  if (live) {
-    if (to - from == whole) {
-      const uint64_t y = rq.start + token;
-      const float f = over(r.l);
-      uint8_t *p = a.out + (y * a.out_token + qh * a.out_head + 4 * j) * esize(DT);
+    if (r.marks >> d / 2 & 1) r.o[d] = f32x4{} + __builtin_nanf("");
+}
+
+template <int DT, int NB>
+constexpr int kResident = DT == BF16 && NB <= 2 ? 3 : DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
+
+// A row's result from its sums over all keys.
+template <int DT>
+__device__ __forceinline__ void put_row(const AttnArgs &a, const Request &rq, uint32_t token, uint32_t qh, uint32_t col,
+                                        f32x4 o, float m, float l) {
+  const uint64_t y = rq.start + token;
+  store4<DT>(a.out + (y * a.out_token + qh * a.out_head + col) * esize(DT), o * over(l));
+  if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l);
+}
+
+template <int DT, int NB>
+__global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(AttnArgs a, Plan plan, Parts out,
+                                                                        FastDiv per_group, float c) {
+  using R = Rows16<DT, NB>;
+  constexpr int D = 32 * NB;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kWaves * R::kLds];
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t n = lane & 15, j = lane >> 4;
+  const uint32_t head = blockIdx.y, taker = blockIdx.x * kWaves + wave;
+
+  Shares sh;
+  uint32_t b;
+  uint64_t before;
+  if (taker >= plan.takers || !find_start(a, plan, 16, taker, sh, b, before,
+                                            taker + head ? nullptr : out.each, out.before))
+    return;
+  sh.each = uniform(sh.each);
+  b = uniform(b);
+  before = uniform(before);
+  uint64_t at_tile = taker * sh.each;
+  const uint64_t end_tile = min(at_tile + sh.each, uniform(sh.total));
+  // group after group, request after request
+  while (at_tile < end_tile) {
+    const Request rq = uniform(request(a, b));
+    const uint32_t whole = max(rq.tiles, 1u);
+    const uint32_t groups = groups_of(a, rq, 16);
+    const uint32_t group = groups > 1 ? uint32_t((at_tile - before) / whole) : 0;
+    const uint32_t from = uint32_t(at_tile - before - uint64_t(group) * whole);
+    const uint32_t to = uint32_t(min(uint64_t(whole), from + (end_tile - at_tile)));
+    R r;
+    set_rows(a, rq, group, head, per_group, r);
+    take_tiles<DT, NB, 1>(a, rq, a.table + b * a.table_stride, head, from, to, 0, c, lds + wave * R::kLds, r);
+    if (r.live) {
+      if (to - from == whole) {
 #pragma unroll
-      for (int d = 0; d < 2 * NB; d++) store4<DT>(p + 16 * d * esize(DT), r.o[d] * f);
-      if (a.lse && j == 0) a.lse[y * a.heads + qh] = log_sum(r.m, r.l);
-    } else {
-      const uint64_t p = (uint64_t(head) * out.slots + 2 * taker + (from == 0)) * 16 + n;
+        for (int d = 0; d < 2 * NB; d++) put_row<DT>(a, rq, r.token, r.qh, 16 * d + 4 * j, r.o[d], r.m, r.l);
+      } else {
+        const uint64_t p = (uint64_t(head) * out.slots + 2 * taker + (from == 0)) * 16 + n;
 #pragma unroll
-      for (int d = 0; d < 2 * NB; d++) *reinterpret_cast<f32x4 *>(out.sums + p * D + 16 * d + 4 * j) = r.o[d];
-      if (j == 0) out.ml[p] = make_float2(r.m, r.l);
+        for (int d = 0; d < 2 * NB; d++) *reinterpret_cast<f32x4 *>(out.sums + p * D + 16 * d + 4 * j) = r.o[d];
+        if (j == 0) out.ml[p] = make_float2(r.m, r.l);
+      }
+    }
+    at_tile += to - from;
+    if (at_tile == before + uint64_t(groups) * whole) {
+      before = at_tile;
+      do b++;
+      while (at_tile < end_tile && uniform(request(a, b)).n == 0);
     }
   }
-  at_tile += to - from;
-  if (at_tile == before + uint64_t(groups) * whole) {
-    before = at_tile;
-    do b++;
-    while (at_tile < end_tile && uniform(request(a, b)).n == 0);
+}
+
+// Group x of all requests' groups of 16 rows, numbered with gaps where requests have
+// starts: request b's from starts[b] group / 16 + b on.
+__device__ __forceinline__ void group_at(const AttnArgs &a, uint32_t x, uint32_t &b, uint32_t &group) {
+  if (a.starts) {
+    uint32_t lo = 0, hi = a.batch;
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) >> 1;
+      const int32_t s = a.starts[mid];
+      const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens);
+      if (from * a.group / 16 + mid <= x)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    b = lo;
+    const int32_t s = a.starts[b];
+    group = x - ((s < 0 ? 0 : min(uint32_t(s), a.tokens)) * a.group / 16 + b);
+  } else {
+    b = x / ((a.group + 15) / 16);
+    group = x % ((a.group + 15) / 16);
   }
+  b = uniform(b);
+  group = uniform(group);
+}
+
+// Short caches: a workgroup for each group of rows, whose waves take turns at its
+// tiles and join their sums in LDS; no second launch.
+template <int DT, int NB>
+constexpr int kShortWaves = kResident<DT, NB> >= 2 ? 8 : 4;
+
+template <int DT, int NB>
+__global__ __launch_bounds__((64 * kShortWaves<DT, NB>)) void k_attend_short(AttnArgs a, FastDiv per_group, float c) {
+  using R = Rows16<DT, NB>;
+  constexpr int D = 32 * NB, W = kShortWaves<DT, NB>, kPad = D + 4;
+  constexpr int kShared = R::kLds > 16 * kPad * 4 ? R::kLds : 16 * kPad * 4;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[W * kShared];
+  __shared__ float2 ml_of[W][16];
+  const uint32_t lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const uint32_t n = lane & 15, j = lane >> 4;
+  const uint32_t head = blockIdx.y;
+  uint32_t b, group;
+  group_at(a, blockIdx.x, b, group);
+  const Request rq = uniform(request(a, b));
+  if (group >= groups_of(a, rq, 16)) return;
+  R r;
+  set_rows(a, rq, group, head, per_group, r);
+  take_tiles<DT, NB, W>(a, rq, a.table + b * a.table_stride, head, 0, rq.tiles, wave, c, lds + wave * R::kLds, r);
+  if (j == 0) ml_of[wave][n] = make_float2(r.m, r.l);
+  __syncthreads();   // the sums lie where the values did
+  float *sums = reinterpret_cast<float *>(lds);
+#pragma unroll
+  for (int d = 0; d < 2 * NB; d++)
+    *reinterpret_cast<f32x4 *>(sums + (wave * 16 + n) * kPad + 16 * d + 4 * j) = r.o[d];
+  __syncthreads();
+  const uint32_t rows = min(16u, rq.n * a.group - group * 16);
+  for (uint32_t i = threadIdx.x; i < rows * (D / 4); i += 64 * W) {
+    const uint32_t rr = i / (D / 4), col = i % (D / 4) * 4;
+    float top = ml_of[0][rr].x;
+#pragma unroll
+    for (int w = 1; w < W; w++) top = fmaxf(top, ml_of[w][rr].x);
+    float l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < W; w++) {
+      const float2 ml = ml_of[w][rr];
+      const float f = share(ml.x, top);
+      l += ml.y * f;
+      o += *reinterpret_cast<const f32x4 *>(sums + (w * 16 + rr) * kPad + col) * f;
+    }
+    const uint32_t row = group * 16 + rr, token = per_group.div(row);
+    put_row<DT>(a, rq, token, head * a.group + row - token * a.group, col, o, top, l);
   }
 }
 
@@ -416,27 +506,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
     at = in.before[b] + g * whole;
     if (at == edge || at / each != x) return;
   } else {
-    // groups numbered with gaps: request b's from starts[b] group / 16 + b
-    if (a.starts) {
-      uint32_t lo = 0, hi = a.batch;
-      while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) >> 1;
-        const int32_t s = a.starts[mid];
-        const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens);
-        if (from * a.group / 16 + mid <= x)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      b = lo;
-      const int32_t s = a.starts[b];
-      group = x - ((s < 0 ? 0 : min(uint32_t(s), a.tokens)) * a.group / 16 + b);
-    } else {
-      b = x / ((a.group + 15) / 16);
-      group = x % ((a.group + 15) / 16);
-    }
-    b = uniform(b);
-    group = uniform(group);
+    group_at(a, x, b, group);
     const Request r = uniform(request(a, b));
     if (group >= groups_of(a, r, 16)) return;
     at = in.before[b] + uint64_t(group) * max(r.tiles, 1u);
@@ -484,57 +554,60 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
     l += weights[i];
     o += *reinterpret_cast<const f32x4 *>(&sums[i][col]);
   }
-  const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
-  const uint64_t y = rq.start + tk;
-  store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
-  if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
+  const uint32_t token = per_group.div(row);
+  put_row<DT>(a, rq, token, head * a.group + row - token * a.group, col, o, top, l);
 }
 
 // ------------------------------------------------------------------ launch --
-// The takers fill the chip once, so that they all run at the same time.
-template <int DT, int NB>
-Plan few_plan(const AttnArgs &a) {
-  constexpr uint32_t kSimds = 1024;
-  const uint32_t n = kSimds * kResident<DT, NB> / a.c.heads;
-  return Plan{n ? n : 1, kLeast};
-}
-struct Sizes {
-  uint32_t groups;         // row groups of a key head, at most
-  bool split;              // some request may be cut into pieces
-};
-Sizes sizes(const AttnArgs &a, uint32_t rows, uint32_t least) {
-  Sizes s;
-  s.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / rows + a.batch) : a.batch * ((a.group + rows - 1) / rows);
-  // a share never ends inside a request that is all there is
-  s.split = (uint64_t(a.width) << a.c.shift) > uint64_t(least) * kTile || s.groups > 1;
-  return s;
-}
-
 template <int DT, int NB>
 struct Few {
+  struct Sizes {
+    Plan plan;
+    uint32_t groups;       // row groups of a key head, at most
+    bool brief;            // taken by k_attend_short
+    bool split;            // some group may be cut into pieces
+  };
+  static Sizes sizes(const AttnArgs &a) {
+    Sizes z;
+    z.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / 16 + a.batch) : a.batch * ((a.group + 15) / 16);
+    const uint64_t tiles = ((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile;
+    // One launch for two where the waves of a workgroup have two tiles each: 8 requests
+    // of 500 or 1000 keys (8 key heads of 128 values) take 6.8 and 9.4 us for 10.7 and
+    // 11.3, of 2000 14.0 for 13.9; 64 of 100 or 1000 10.4 and 20.0 for 13.3 and 22.5.
+    // Where workgroups wait for each other, shares win: 256 of 100 or 1000 keys 37 and
+    // 64 us for 25 and 53, but not for heads of 64 values (17 and 31 for 22 and 39),
+    // of which more run at a time.
+    z.brief = tiles <= kShort && uint64_t(z.groups) * a.c.heads <= (NB <= 2 ? 1u << 20 : 1024u);
+    // the takers fill the chip once, so that they all run at the same time; no more
+    // of them than tiles (one more a group where a window begins inside one)
+    const uint64_t n = std::min<uint64_t>(1024 * kResident<DT, NB> / a.c.heads, z.groups * (tiles + 1));
+    z.plan.takers = n ? uint32_t(n) : 1;
+    z.split = !z.brief && z.plan.takers > 1;
+    return z;
+  }
   static uint64_t scratch(const AttnArgs &a) {
-    const Plan plan = few_plan<DT, NB>(a);
-    if (!sizes(a, 16, plan.least).split) return 0;
-    const Parts p = parts(nullptr, a.batch, a.c.heads, 2 * plan.takers, 16);
-    return reinterpret_cast<uint64_t>(p.sums) + uint64_t(a.c.heads) * 2 * plan.takers * 16 * NB * 32 * 4;
+    const Sizes z = sizes(a);
+    if (!z.split) return 0;
+    const Parts p = parts(nullptr, a.batch, a.c.heads, 2 * z.plan.takers, 16);
+    return reinterpret_cast<uint64_t>(p.sums) + uint64_t(a.c.heads) * 2 * z.plan.takers * 16 * NB * 32 * 4;
   }
   static hipError_t run(const AttnArgs &a, hipStream_t s) {
-    const Plan plan = few_plan<DT, NB>(a);
-    const Sizes z = sizes(a, 16, plan.least);
-    Parts p = {};
-    if (z.split) p = parts(a.scratch, a.batch, a.c.heads, 2 * plan.takers, 16);
+    const Sizes z = sizes(a);
     const FastDiv per_group(a.group);
-    // no more takers than the table's width gives tiles to
-    const uint64_t tiles = uint64_t(z.groups) * (((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile + 1);
-    const uint64_t busy = std::min<uint64_t>(plan.takers, (tiles + plan.least - 1) / plan.least);
-    k_attend<DT, NB><<<dim3(uint32_t((busy + kWaves - 1) / kWaves), a.c.heads), 64 * kWaves, 0, s>>>(
-        a, plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
+    const float c = float(double(a.scale) * 1.4426950408889634);
+    if (z.brief) {
+      k_attend_short<DT, NB><<<dim3(z.groups, a.c.heads), 64 * kShortWaves<DT, NB>, 0, s>>>(a, per_group, c);
+      return hipGetLastError();
+    }
+    Parts p = {};
+    if (z.split) p = parts(a.scratch, a.batch, a.c.heads, 2 * z.plan.takers, 16);
+    k_attend<DT, NB><<<dim3((z.plan.takers + kWaves - 1) / kWaves, a.c.heads), 64 * kWaves, 0, s>>>(a, z.plan, p, per_group, c);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !z.split || plan.takers == 1) return e;
+    if (e != hipSuccess || !z.split) return e;
     const uint32_t rows = a.starts || a.group > 16 ? 16 : a.group;
     // a workgroup for each row of every group, or of every group that an edge between two shares can lie in
-    const bool by_edges = plan.takers - 1 < z.groups;
-    k_join<DT, NB><<<dim3((by_edges ? plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, by_edges);
+    const bool by_edges = z.plan.takers - 1 < z.groups;
+    k_join<DT, NB><<<dim3((by_edges ? z.plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, by_edges);
     return hipGetLastError();
   }
 };
