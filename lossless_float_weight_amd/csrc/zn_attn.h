@@ -229,31 +229,6 @@ __device__ __forceinline__ uint32_t holder(const uint64_t *before, uint32_t batc
   return lo;
 }
 
-// Sums of v over the lanes up to this one.  32 bits where the sum surely fits.
-__device__ __forceinline__ uint32_t scan32(uint32_t v) {
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x111, 0xF, 0xF, false);   // a lane down, within 16
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x112, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x114, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x118, 0xF, 0xF, false);
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x142, 0xA, 0xF, false);   // the last of 16 to the next 16
-  v += __builtin_amdgcn_update_dpp(0, int(v), 0x143, 0xC, 0xF, false);   // the last of 32 to the next 32
-  return v;
-}
-__device__ __forceinline__ uint64_t scan(uint64_t v) {
-  if (!__any((v >> 25) != 0)) return scan32(uint32_t(v));
-#pragma unroll 1
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t p = __shfl_up(v, d);
-    if ((threadIdx.x & 63) >= uint32_t(d)) v += p;
-  }
-  return v;
-}
-// v of a lane that all know.
-__device__ __forceinline__ uint64_t of_lane(uint64_t v, uint32_t lane) {
-  return uint64_t(uint32_t(__builtin_amdgcn_readlane(uint32_t(v >> 32), lane))) << 32 |
-         uint32_t(__builtin_amdgcn_readlane(uint32_t(v), lane));
-}
-
 // f of the kernels K<type, blocks of 32 values of a head>, for the call's.
 template <template <int, int> class K, int DT, class F>
 auto by_blocks(uint32_t blocks, F f) {

@@ -12,36 +12,22 @@ constexpr uint32_t kMost = 0x7FFFFFFFu;
 __device__ __forceinline__ uint32_t at_least_0(int32_t v) { return v < 0 ? 0u : uint32_t(v); }
 __device__ __forceinline__ uint32_t clip(uint64_t v) { return v > kMost ? kMost : uint32_t(v); }
 
-// Exclusive prefix sums of a and b over the workgroup's threads, and the sums.
-__device__ __forceinline__ void scan2(uint64_t &a, uint64_t &b, uint64_t &sum_a, uint64_t &sum_b) {
-  __shared__ uint64_t part[2][kStepThreads / 64];
-  const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint64_t x = a, y = b;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint64_t p = __shfl_up(x, d), q = __shfl_up(y, d);
-    if (lane >= uint32_t(d)) {
-      x += p;
-      y += q;
-    }
-  }
-  if (lane == 63) {
-    part[0][wave] = x;
-    part[1][wave] = y;
-  }
+// The sum of v over the workgroup's threads before this one, and over all.
+__device__ __forceinline__ uint64_t before(uint64_t v, uint64_t &sum) {
+  __shared__ uint64_t part[kStepThreads / 64];
+  const uint32_t wave = threadIdx.x >> 6;
+  const uint64_t x = scan(v);
   __syncthreads();
-  sum_a = sum_b = 0;
-  a = x - a;
-  b = y - b;
+  if ((threadIdx.x & 63) == 63) part[wave] = x;
+  __syncthreads();
+  uint64_t at = x - v;
+  sum = 0;
 #pragma unroll
   for (uint32_t w = 0; w < kStepThreads / 64; w++) {
-    if (w < wave) {
-      a += part[0][w];
-      b += part[1][w];
-    }
-    sum_a += part[0][w];
-    sum_b += part[1][w];
+    if (w < wave) at += part[w];
+    sum += part[w];
   }
+  return at;
 }
 
 // The last i in [0, n) whose first[i] (without its top bit) is at most v; first
@@ -63,109 +49,107 @@ __device__ __forceinline__ uint32_t owner(const uint32_t *first, uint32_t n, uin
 // a scan) and then does its share of pages and tokens by a search in the sums.
 // A thread takes `per` requests in a row.
 //
-// LDS, both batch + 1 long: first[b], the pages before request b's, with the top
-// bit set if b is served; begin[b], the tokens before its.
+// LDS, a word each for every request: len; first, the pages before its own, with the
+// top bit set if it is served; and begin, the tokens before its own, one more.
 template <bool EXTEND>
 __global__ __launch_bounds__(kStepThreads) void k_kv_step(KvStepArgs a) {
   extern __shared__ uint32_t lds[];
-  uint32_t *first = lds, *begin = lds + a.batch + 1;
+  uint32_t *len = lds, *first = lds + a.batch, *begin = lds + 2 * a.batch;
+  __shared__ uint32_t most;
   const uint32_t per = (a.batch + kStepThreads - 1) / kStepThreads;
-  const uint32_t b0 = threadIdx.x * per;
+  const uint32_t b0 = min(threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
   const uint32_t round = (1u << a.shift) - 1;
   const uint32_t n_free = min(at_least_0(*a.n_free), a.free_cap);
+  auto pages_of = [&](uint64_t tokens) { return (tokens + round) >> a.shift; };
+  if (threadIdx.x == 0) most = 0;
 
-  // pages and tokens of this thread's requests, then of all before them
-  uint64_t pages = 0, tokens = 0, all_pages, all_tokens;
-  if constexpr (EXTEND) {
-    for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) tokens += at_least_0(a.add[b0 + i]);
-    uint64_t none = 0, no_sum;
-    scan2(tokens, none, all_tokens, no_sum);
-    __syncthreads();
+  // tokens, then pages, of this thread's requests and of all before them
+  uint64_t tokens = 0, all_tokens = 0;
+  for (uint32_t b = b0; b < b1; b++) {
+    len[b] = at_least_0(a.lens[b]);
+    if constexpr (EXTEND) tokens += begin[b] = at_least_0(a.add[b]);   // for now
   }
-  uint64_t at_token = tokens;
-  for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) {
-    const uint32_t b = b0 + i;
-    const uint64_t len = at_least_0(a.lens[b]);
+  if constexpr (EXTEND) tokens = before(tokens, all_tokens);
+  uint64_t pages = 0, all_pages, at_token = tokens;
+  // what request b asks for
+  auto wants = [&](uint32_t b, bool &fits) -> uint64_t {
     if constexpr (EXTEND) {
-      const uint64_t more = at_least_0(a.add[b]);
-      at_token += more;
-      const uint64_t want = (len + more + round) >> a.shift;
-      if (want <= a.width && at_token <= a.tokens) pages += want - ((len + round) >> a.shift);
+      const uint64_t want = pages_of(uint64_t(len[b]) + begin[b]);
+      at_token += begin[b];
+      fits = want <= a.width && at_token <= a.tokens;
+      return fits ? want - pages_of(len[b]) : 0;
     } else {
-      const uint64_t have = (len + round) >> a.shift;
-      if (a.done[b]) pages += have < a.width ? have : a.width;
+      fits = a.done[b] != 0;
+      return fits ? min(pages_of(len[b]), uint64_t(a.width)) : 0;
     }
-  }
-  uint64_t none = 0, no_sum;
-  scan2(pages, none, all_pages, no_sum);
-
-  // what each request gets
-  uint64_t at_page = pages;
+  };
+  bool fits;
+  for (uint32_t b = b0; b < b1; b++) pages += wants(b, fits);
+  uint64_t at_page = before(pages, all_pages);
   at_token = tokens;
   uint32_t taken = 0;
-  for (uint32_t i = 0; i < per && b0 + i < a.batch; i++) {
-    const uint32_t b = b0 + i;
-    const uint64_t len = at_least_0(a.lens[b]);
+  for (uint32_t b = b0; b < b1; b++) {
+    const uint64_t need = wants(b, fits);
     if constexpr (EXTEND) {
-      const uint64_t more = at_least_0(a.add[b]);
-      const uint64_t want = (len + more + round) >> a.shift;
-      const bool fits = want <= a.width && at_token + more <= a.tokens;
-      const uint64_t need = fits ? want - ((len + round) >> a.shift) : 0;
       const bool served = fits && (need == 0 || at_page + need <= n_free);
+      const uint32_t more = begin[b];
+      begin[b] = clip(at_token - more);
       first[b] = clip(at_page) | (served ? 0x80000000u : 0u);
-      begin[b] = clip(at_token);
       if (served && need) taken = uint32_t(at_page + need);
       if (blockIdx.x == 0) {
-        a.new_lens[b] = int32_t(served ? len + more : len);
+        a.new_lens[b] = int32_t(served ? len[b] + more : len[b]);
         a.starts[b] = int32_t(begin[b]);
       }
-      at_page += need;
-      at_token += more;
     } else {
-      const uint64_t have = (len + round) >> a.shift;
       first[b] = clip(at_page);
-      if (a.done[b]) at_page += have < a.width ? have : a.width;
-      if (blockIdx.x == 0) a.new_lens[b] = a.done[b] ? 0 : int32_t(len);
+      if (blockIdx.x == 0) a.new_lens[b] = fits ? 0 : int32_t(len[b]);
     }
+    at_page += need;
   }
+  if (EXTEND && threadIdx.x == 0) begin[a.batch] = clip(all_tokens);
+  if (EXTEND && taken) atomicMax(&most, taken);
+  __syncthreads();
   const uint32_t id = blockIdx.x * kStepThreads + threadIdx.x, step = gridDim.x * kStepThreads;
   if constexpr (EXTEND) {
-    __shared__ uint32_t most;
-    if (threadIdx.x == 0) most = 0;
-    if (threadIdx.x == 0) begin[a.batch] = clip(all_tokens);
-    __syncthreads();
-    if (taken) atomicMax(&most, taken);
-    __syncthreads();
     taken = most;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       a.starts[a.batch] = int32_t(clip(all_tokens));
       *a.n_left = int32_t(n_free - taken);
     }
+    // tokens, four in a row a thread; a page that this step enters is looked up on the stack
+    const uint32_t end = begin[a.batch];
+    for (uint64_t t0 = 4ull * id; t0 < a.tokens; t0 += 4ull * step) {
+      uint32_t b = t0 < end ? owner(begin, a.batch, uint32_t(t0)) : 0;
+      int32_t page[4], place[4];
+      bool live[4];
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++) {
+        const uint64_t t = t0 + i;
+        live[i] = t < end && t < a.tokens;
+        page[i] = -1;
+        place[i] = 0;
+        if (!live[i]) continue;
+        while (t >= begin[b + 1]) b++;
+        live[i] = first[b] >> 31;
+        if (!live[i]) continue;
+        const uint32_t p = len[b] + uint32_t(t) - begin[b], at = p >> a.shift, have = uint32_t(pages_of(len[b]));
+        place[i] = int32_t(p);
+        page[i] = at < have ? a.table[b * a.table_stride + at] : a.free[n_free - 1 - ((first[b] & kMost) + at - have)];
+      }
+#pragma unroll
+      for (uint32_t i = 0; i < 4; i++) {
+        if (t0 + i >= a.tokens) break;
+        const bool good = page[i] >= 0 && uint32_t(page[i]) < a.n_pages;
+        a.slots[t0 + i] = good ? int32_t((uint32_t(page[i]) << a.shift) | (uint32_t(place[i]) & round)) : -1;
+        a.positions[t0 + i] = place[i];
+      }
+    }
     // pages: the i-th one taken is the i-th from the stack's end
     for (uint32_t i = id; i < taken; i += step) {
       const uint32_t b = owner(first, a.batch, i);
-      const uint32_t have = (at_least_0(a.lens[b]) + round) >> a.shift;
-      a.table[b * a.table_stride + have + i - (first[b] & kMost)] = a.free[n_free - 1 - i];
-    }
-    // tokens; a page that this step enters is looked up on the stack
-    for (uint64_t t = id; t < a.tokens; t += step) {
-      int32_t slot = -1, position = 0;
-      if (t < begin[a.batch]) {
-        const uint32_t b = owner(begin, a.batch, uint32_t(t));
-        if (first[b] >> 31) {
-          const uint32_t len = at_least_0(a.lens[b]), have = (len + round) >> a.shift;
-          const uint32_t p = len + uint32_t(t) - begin[b], at = p >> a.shift;
-          const int32_t page =
-              at < have ? a.table[b * a.table_stride + at] : a.free[n_free - 1 - ((first[b] & kMost) + at - have)];
-          position = int32_t(p);
-          if (page >= 0 && uint32_t(page) < a.n_pages) slot = int32_t((uint32_t(page) << a.shift) | (p & round));
-        }
-      }
-      a.slots[t] = slot;
-      a.positions[t] = position;
+      a.table[b * a.table_stride + pages_of(len[b]) + i - (first[b] & kMost)] = a.free[n_free - 1 - i];
     }
   } else {
-    __syncthreads();
     const uint32_t room = a.free_cap - n_free;
     const uint32_t back = all_pages < room ? uint32_t(all_pages) : room;
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.n_left = int32_t(n_free + back);
@@ -178,12 +162,12 @@ __global__ __launch_bounds__(kStepThreads) void k_kv_step(KvStepArgs a) {
 
 template <bool EXTEND>
 hipError_t step(const KvStepArgs &a, uint64_t work, hipStream_t s) {
-  // four pieces of work a thread; more workgroups only repeat the sums
+  // four tokens a thread; more workgroups only repeat the sums
   const uint64_t grid = (work + 4 * kStepThreads - 1) / (4 * kStepThreads);
-  const uint32_t lds = (2 * a.batch + 2) * sizeof(uint32_t);
+  const uint32_t lds = (3 * a.batch + 1) * sizeof(uint32_t);
   if (lds > 48 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(&k_kv_step<EXTEND>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, 72 * 1024);
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
     if (e != hipSuccess) return e;
   }
   k_kv_step<EXTEND><<<uint32_t(grid < 1 ? 1 : grid > 256 ? 256 : grid), kStepThreads, lds, s>>>(a);
