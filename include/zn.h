@@ -449,8 +449,8 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * Keys that a query does not see have no effect on it, whatever they hold.
  *   Values of keys and values are taken as stored; products, sums, maxima and
  * exponentials are FP32 (before they meet the values the weights are rounded: beside
- * BF16 queries to 11 bits, or 16 for few rows a request, beside FP32 to 24), and the
- * result is rounded once.  Weights are at
+ * BF16 queries to 11 bits and 2^-32 of the row's largest, or to 16 bits for few rows a
+ * request, beside FP32 to 24), and the result is rounded once.  Weights are at
  * most 1: n keys whose values pass 2^127 / n may give infinities and NaNs.  A
  * scale byte over 252, which the write makes only (255) of infinities and NaNs,
  * is a NaN.
@@ -462,6 +462,7 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  *   max_new: the most queries of one request, as far as the caller knows (0 if
  * not).  It chooses between kernels and has no effect on what is computed but
  * the order of sums.
+ * Rows of out do not overlap (one of its strides holds all rows of the other).
  * scale is finite and > 0, batch at most 8192, window at most 2^31 - 1, tokens *
  * heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
  * 16-byte aligned device scratch (ZN_ERR_CAPACITY if it is less; 0 for some

@@ -7,8 +7,8 @@
 namespace zn {
 
 constexpr uint32_t kTile = 64;  // keys that a wave takes at a time
-// The weights' bound m rises to this much (as a power of two) above a score that
-// passes it.
+// A weight is 2^(c (score - m) - kRise): m is a score, the largest of those so far or
+// one that none passes by more than 2^kRise.
 constexpr float kRise = 8.0f;
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -191,8 +191,8 @@ __device__ __forceinline__ void store4(uint8_t *p, f32x4 v) {
 
 // Result of a row from its sums, weight and bound.
 __device__ __forceinline__ float over(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
-__device__ __forceinline__ float log_sum(float m, float l) {
-  return l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * 0.6931471805599453f;
+__device__ __forceinline__ float log_sum(float m, float l, float scale) {
+  return l == 0.0f ? -__builtin_inff() : __builtin_fmaf(m, scale, (kRise + __builtin_log2f(l)) * 0.6931471805599453f);
 }
 
 // NaNs among a tile's values would meet the weight 0 of rows that do not see their
@@ -210,9 +210,9 @@ __device__ __attribute__((noinline)) uint32_t marked(const uint8_t *scales, uint
   return bad;
 }
 
-// A piece's share of a row: 2^(its bound - the largest one).
-__device__ __forceinline__ float share(float m, float top) {
-  return m == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+// A piece's share of a row, whose largest m is `top`.
+__device__ __forceinline__ float share(float m, float top, float c) {
+  return m == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c);
 }
 // The last request b with before[b] <= v (before rises from 0), by one wave: 64
 // places a step.

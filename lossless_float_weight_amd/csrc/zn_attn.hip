@@ -1,10 +1,12 @@
 // zn_attn.hip -- attention over the key-value cache in 4 bits.
 //
-//   out = sum_j w_j v_j / sum_j w_j,  w_j = 2^(c q.k_j - m),  c = scale log2(e),
+//   out = sum_j w_j v_j / sum_j w_j,  w_j = 2^(c (q.k_j - m) - 8),  c = scale log2(e),
 //
-// in one pass over the keys: m is a running bound of the exponents.  When one
-// passes it, it rises to 8 above that one and the sums so far are multiplied by
-// 2^(old - new); with the 8 this is seldom, and weights stay under 1.
+// in one pass over the keys: m is one of the scores so far.  When one passes it by
+// more than 2^8 in weight, m becomes that one and the sums so far are multiplied by
+// 2^(c (old - new)); with the 8 this is seldom, and weights stay under 1.  Scores
+// are subtracted before they are scaled: the largest weights are exact however
+// large the scores.
 //
 // Rows and tiles.  All queries of a request that read one key head share its
 // keys: row r of such a group is query r / group, query head r % group.  A wave
@@ -271,10 +273,10 @@ __device__ __forceinline__ void take_tiles(const AttnArgs &a, const Request &rq,
     for (int g = 0; g < 4; g++)
 #pragma unroll
       for (int i = 0; i < 4; i++) top = fmaxf(top, s[g][i]);
-    top = max_j(top) * c;
-    if (__any(top > r.m)) {
-      const float m = top > r.m ? top + kRise : r.m;
-      const float f = m > r.m ? __builtin_amdgcn_exp2f(r.m - m) : 1.0f;
+    top = max_j(top);
+    if (__any((top - r.m) * c > kRise)) {
+      const float m = fmaxf(top, r.m);
+      const float f = m > r.m ? __builtin_amdgcn_exp2f((r.m - m) * c) : 1.0f;
       r.l *= f;
 #pragma unroll
       for (int d = 0; d < 2 * NB; d++) r.o[d] *= f;
@@ -314,7 +316,7 @@ __device__ __forceinline__ void take_tiles(const AttnArgs &a, const Request &rq,
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * h + i / 4][i & 3], c, -m));
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * h + i / 4][i & 3] - m, c, -kRise));
           r.l += x[i];
         }
         pieces<R::WP>(x, wp);
@@ -350,7 +352,7 @@ __device__ __forceinline__ void put_row(const AttnArgs &a, const Request &rq, ui
                                         f32x4 o, float m, float l) {
   const uint64_t y = rq.start + token;
   store4<DT>(a.out + (y * a.out_token + qh * a.out_head + col) * esize(DT), o * over(l));
-  if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l);
+  if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l, a.scale);
 }
 
 template <int DT, int NB>
@@ -470,7 +472,7 @@ __global__ __launch_bounds__((64 * kShortWaves<DT, NB>)) void k_attend_short(Att
 #pragma unroll
     for (int w = 0; w < W; w++) {
       const float2 ml = ml_of[w][rr];
-      const float f = share(ml.x, top);
+      const float f = share(ml.x, top, c);
       l += ml.y * f;
       o += *reinterpret_cast<const f32x4 *>(sums + (w * 16 + rr) * kPad + col) * f;
     }
@@ -483,7 +485,7 @@ __global__ __launch_bounds__((64 * kShortWaves<DT, NB>)) void k_attend_short(Att
 // 256 / (D / 4) teams that take every so manieth piece in order, and their sums are
 // added in order.
 template <int DT, int NB>
-__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group, bool by_edges) {
+__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group, float c, bool by_edges) {
   constexpr int D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
   __shared__ float tops[4];
   __shared__ __attribute__((aligned(16))) float sums[kTeams][D + 4];
@@ -538,7 +540,7 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
     for (uint32_t i = team; i < count; i += kTeams) {
       const uint64_t p = piece(i);
       const float2 ml = in.ml[p];
-      const float f = share(ml.x, top);
+      const float f = share(ml.x, top, c);
       l += ml.y * f;
       o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
     }
@@ -607,7 +609,7 @@ struct Few {
     const uint32_t rows = a.starts || a.group > 16 ? 16 : a.group;
     // a workgroup for each row of every group, or of every group that an edge between two shares can lie in
     const bool by_edges = z.plan.takers - 1 < z.groups;
-    k_join<DT, NB><<<dim3((by_edges ? z.plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, by_edges);
+    k_join<DT, NB><<<dim3((by_edges ? z.plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, c, by_edges);
     return hipGetLastError();
   }
 };

@@ -95,7 +95,6 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       if (p > 1) parts += g * p;
     }
   const uint64_t upto = scan(items), parts_upto = scan(parts), all = of_lane(upto, 63);
-  if (number >= all) return false;
   // the requests' numbers of pieces for the join
   if (tell && threadIdx.x < 64) {
     uint64_t at = parts_upto - parts;
@@ -111,6 +110,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       *whole = parts_upto;
     }
   }
+  if (number >= all) return false;
   const uint64_t want = all - 1 - number;
   const uint32_t owner = uniform(uint32_t(__popcll(__ballot(upto <= want))));
   uint64_t first = of_lane(upto - items, owner), slot = of_lane(parts_upto - parts, owner);
@@ -168,9 +168,11 @@ struct Rows32 {
 // The product with the values is one of two.
 //   HALF, beside BF16 queries: weights and values in FP16, one product.  Weights go up
 // to 2^15 and keep 11 bits down to 2^-14 (beside a largest one of 2^7 or more), the
-// values are held relative to a scale of the first tile and are exact while the tiles'
-// scales lie within 2^-23 and 2^12 of it (FP4 times that is FP16).  A tile with others
-// ends it, false is returned, and the rows are taken again the other way.
+// values are held relative to the largest scale of the first tile and are exact normal
+// numbers while the tiles' scales lie within 2^-13 and 2^12 of it.  (Subnormal ones are
+// exact too, but the instruction adds them with fewer bits: at 2^-23 sums were off by
+// 2^-13.)  A tile with others ends it, false is returned, and the rows are taken again
+// the other way.
 //   Otherwise weights in BF16 pieces (two beside BF16 queries, three beside FP32),
 // a product each, and values in BF16, exact whatever their scales.
 // The first takes two thirds of the matrix instructions and three quarters of the
@@ -182,7 +184,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
   using S = Shape<DT, NB>;
   constexpr int WP = HALF ? 1 : DT == BF16 ? 2 : 3;      // pieces of a weight
   constexpr float kTop = HALF ? 15.0f : 0.0f;            // weights stay under 2^kTop
-  constexpr int kBelow = 23, kAbove = 12;                // scales that HALF takes
+  constexpr int kBelow = 13, kAbove = 12;                // scales that HALF takes
   const uint32_t lane = threadIdx.x & 63, n = lane & 31, h = lane >> 5;
   const uint8_t *kc = a.c.k + head * a.c.head_stride * 16, *vc = a.c.v + head * a.c.head_stride * 16;
   const uint8_t *ksc = a.c.ks + head * a.c.head_stride, *vsc = a.c.vs + head * a.c.head_stride;
@@ -335,16 +337,16 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
       for (int g = 0; g < 2; g++)
 #pragma unroll
         for (int i = 0; i < 16; i++) top = fmaxf(top, s[g][i]);
-      top = max_h(top) * c;
-      if (__any(top > r.m + kTop)) {
-        const float up = top > r.m + kTop ? top + (kRise - kTop) : r.m;
-        const float f = up > r.m ? __builtin_amdgcn_exp2f(r.m - up) : 1.0f;
+      top = max_h(top);
+      if (__any((top - r.m) * c > kRise)) {
+        const float up = fmaxf(top, r.m);
+        const float f = up > r.m ? __builtin_amdgcn_exp2f((r.m - up) * c) : 1.0f;
         r.l *= f;
 #pragma unroll
         for (int d = 0; d < NB; d++) r.o[d] *= f;
         r.m = up;
       }
-      const float bound = r.m == -__builtin_inff() ? 0.0f : r.m;
+      const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
       // 16 keys of 32 values at a time; the weights of the next 16 keys are made while
       // the matrix unit takes these
       const uint8_t *from = lds.v[buf] + (4 * h + (lane & 15) / 4) * S::kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
@@ -357,7 +359,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, -bound));
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i] - m, c, kTop - kRise));
           r.l += x[i];
         }
         if constexpr (HALF)
@@ -383,7 +385,6 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
   }
   if constexpr (HALF) {   // weights under 1 again, as the other way leaves them
     constexpr float kDown = 0x1p-15f;
-    r.m += kTop;
     r.l *= kDown;
 #pragma unroll
     for (int d = 0; d < NB; d++) r.o[d] *= kDown;
@@ -467,7 +468,7 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
         for (int e = 0; e < 4; e++) v[e] = __builtin_ldexpf(r.o[d][4 * i + e] * f, unit);
         store4<DT>(p + (32 * d + 8 * i) * esize(DT), v);
       }
-    if (a.lse && h == 0) a.lse[y * a.heads + qh] = log_sum(r.m, l);
+    if (a.lse && h == 0) a.lse[y * a.heads + qh] = log_sum(r.m, l, a.scale);
   } else if (it.slot < out.slots) {   // starts out of order can make more pieces than there is room for
     const uint64_t p = (uint64_t(head) * out.slots + it.slot) * kRows + wave * 32 + n;
 #pragma unroll
@@ -487,7 +488,7 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
 // many rows a workgroup as it has teams.  Groups are named by their first piece's
 // slot; the workgroups go through those there are.
 template <int DT, int NB>
-__global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv per_group) {
+__global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv per_group, float c) {
   constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes, kShares = (kRows + kTeams - 1) / kTeams;
   const uint32_t head = blockIdx.y, team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
   const uint64_t all = min(*in.all, uint64_t(in.slots)) * kShares, piece = *in.each;
@@ -513,14 +514,14 @@ __global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv
     for (uint32_t i = 0; i < count; i++) {
       const uint64_t p = p0 + i * uint64_t(kRows);
       const float2 ml = in.ml[p];
-      const float f = share(ml.x, top);
+      const float f = share(ml.x, top, c);
       l += ml.y * f;
       o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
     }
     const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
     const uint64_t y = rq.start + tk;
     store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
-    if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l);
+    if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l, a.scale);
   }
 }
 
@@ -556,12 +557,12 @@ struct Tall {
     Parts p = {};
     if (z.slots) p = parts(a.scratch, a.batch, a.c.heads, z.slots, kRows);
     const FastDiv per_group(a.group);
-    k_attend_tall<DT, NB><<<z.items * a.c.heads, kThreads, 0, s>>>(
-        a, z.plan, p, per_group, float(double(a.scale) * 1.4426950408889634));
+    const float c = float(double(a.scale) * 1.4426950408889634);
+    k_attend_tall<DT, NB><<<z.items * a.c.heads, kThreads, 0, s>>>(a, z.plan, p, per_group, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !z.slots) return e;
     const uint32_t shares = (kRows * NB * 8 + 255) / 256 + 1, most = 4096 / a.c.heads + 1;
-    k_join_tall<DT, NB><<<dim3(std::min(z.slots * shares, most), a.c.heads), 256, 0, s>>>(a, p, per_group);
+    k_join_tall<DT, NB><<<dim3(std::min(z.slots * shares, most), a.c.heads), 256, 0, s>>>(a, p, per_group, c);
     return hipGetLastError();
   }
 };

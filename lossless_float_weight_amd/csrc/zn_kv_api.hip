@@ -56,6 +56,15 @@ bool good_step(const void *lens, const void *flags, uint32_t batch, const void *
   return at4(lens) && flags && at4(new_lens) && new_lens != lens && (width == 0 || at4(table));
 }
 
+// Rows of `row` elements, m by n of them at two strides (at most 2^40), do not run into each other.
+bool apart(uint64_t m, uint64_t m_stride, uint64_t n, uint64_t n_stride, uint64_t row) {
+  if (m < 2 || n < 2) return (m < 2 || m_stride >= row) && (n < 2 || n_stride >= row);
+  const bool m_first = m_stride <= n_stride;
+  const uint64_t low = m_first ? m_stride : n_stride, high = m_first ? n_stride : m_stride;
+  // steps of the shorter stride fit the longer one, which holds for every layout of a dense axis order
+  return low >= row && high >= row && (high - row) / low >= (m_first ? m : n) - 1;
+}
+
 bool attention_of(const zn_mx_cache *cache, const zn_mx_attention_args *g, bool used, AttnArgs *a) {
   *a = AttnArgs{};
   if (!g || !good_cache(cache, used, &a->c) || !plain(g->dtype)) return false;
@@ -69,6 +78,7 @@ bool attention_of(const zn_mx_cache *cache, const zn_mx_attention_args *g, bool 
   if (g->table_stride > kMostStride || (g->batch > 1 && g->table_stride < g->width)) return false;
   for (uint64_t s : {g->q_token_stride, g->q_head_stride, g->out_token_stride, g->out_head_stride})
     if (s > kMostStride) return false;
+  if (!apart(g->heads, g->out_head_stride, g->tokens, g->out_token_stride, cache->head_dim)) return false;
   a->q = static_cast<const uint8_t *>(g->q);
   a->q_token = g->q_token_stride;
   a->q_head = g->q_head_stride;

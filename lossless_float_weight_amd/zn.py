@@ -907,11 +907,11 @@ def mx_kv_read(cache, slots: torch.Tensor, dtype=torch.bfloat16, out=None, strea
 
 
 @functools.lru_cache(maxsize=4096)
-def _attention_scratch(dt, heads, batch, tokens, max_new, width, causal, window, with_starts, lay) -> int:
+def _attention_scratch(dt, heads, batch, tokens, max_new, width, with_starts, lay) -> int:
     """zn_mx_attention_scratch_bytes, which goes by sizes alone."""
     c = _CACHE_ARGS.pack(0, 0, 0, 0, *lay[:4], 0, *lay[4])
-    g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, 0, 0, 0, 0, 0, 0, 0, 0, 0, with_starts, width, width,
-                             1.0, causal, window)
+    g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, 0, 0, 0, 0, heads * lay[3], lay[3], 0, 0, 0, with_starts,
+                             width, width, 1.0, 1, 0)
     b = C.c_uint64()
     _check(lib().zn_mx_attention_scratch_bytes(c, g, C.byref(b)), "mx_attention")
     return b.value
@@ -953,13 +953,17 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     elif not (math.isfinite(scale) and scale > 0):
         raise ZnError(-1, f"{where}: scale is {scale}")
     max_new = min(max(int(max_new), 0), tokens)
-    need = _attention_scratch(dt, heads, batch, tokens, max_new, width, bool(causal), window, starts is not None, lay)
+    need = _attention_scratch(dt, heads, batch, tokens, max_new, width, starts is not None, lay)
     if out is None:
         out, ot, oh = _mx_new(q.dtype, dev, stream, tokens, heads, dim), heads * dim, dim
     else:
         ot, oh = _kv_rows(where, "out", out, q.shape, q.dtype)
-        if (tokens > 1 and ot < dim) or (heads > 1 and oh < dim):
-            raise ZnError(-1, f"{where}: out's rows overlap")
+        inner = dim
+        for st, n in sorted(((oh, heads), (ot, tokens))):
+            if n > 1:
+                if st < inner:
+                    raise ZnError(-1, f"{where}: out's rows overlap")
+                inner += st * (n - 1)
     if given is not None:
         _mx_given(where, "lse", given, (tokens, heads), (torch.float32,))
     elif lse:

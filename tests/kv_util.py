@@ -83,7 +83,7 @@ def check_attention(q, c, table, lens, starts, page, got, got_lse=None, causal=T
     mine = (size != -1)                                        # rows that some request has
     bound = (2 * d[..., None] + 2 * n * 2.0 ** -23 + 8 * 2.0 ** -24) * size + torch.finfo(q.dtype).eps / 2 * np.abs(out)
     least = 2.0 ** -32 if q.dtype == torch.bfloat16 else 2.0 ** -118
-    bound = bound + 2 * n * least * np.nanmax(np.abs(v)) + 2.0 ** -134
+    bound = bound + 2 * n * least * np.nanmax(np.abs(v), (0, 1, 2)) + 2.0 ** -134      # of the result's own column
     y = f64(got)
     nan = np.isnan(out)
     if n * np.nanmax(np.abs(v)) >= 2.0 ** 127:

@@ -226,7 +226,7 @@ def test_attention_of_every_head_size(dim, t):
 
 
 @pytest.mark.parametrize("t", ["bf16", "fp32"])
-@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (5, 5), (3, 1), (14, 2), (16, 1), (40, 2), (33, 1)])
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (5, 5), (3, 1), (14, 2), (16, 1), (40, 2), (33, 1), (128, 1)])
 def test_attention_of_every_group(heads, kv_heads, t):
     run_attention([5, 130], None, heads, kv_heads, 64, 32, t, heads)
 
@@ -302,6 +302,29 @@ def test_scores_far_apart():
         check_attention(q, c, table, [700], None, 64, out, scale=1e-3)
 
 
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,new", [([300], None), ([3000], None), ([300], [200]), ([3000], [40])])
+def test_scores_past_the_weights_precision(lens, new, t):
+    # scores to 2^60, whose last bits are worth far more than a weight's exponent: one key has all the weight
+    q, c, table, starts = attend_case(lens, new, 2, 1, 64, 64, t, 3)
+    c.k_scales.view(torch.uint8).copy_(torch.randint(60, 187, c.k_scales.shape))
+    out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), None if new is None else i32(starts), lse=True)
+    assert not out.isnan().any() and not lse.isnan().any()
+    k, v = values(c)
+    rows = [(b, t) for b, n in enumerate(lens) for t in range(1 if new is None else new[b])]
+    at = np.arange(lens[0])
+    pages = np.array(table[0])[at // 64]
+    kk, vv, x = k[pages, 0, at % 64], v[pages, 0, at % 64], f64(q)
+    for r, (b, i) in enumerate(rows):
+        seen = lens[0] - len(rows) + i + 1
+        for h in range(2):
+            s = kk[:seen] @ x[r, h] / 8
+            order = np.argsort(s)
+            if seen == 1 or s[order[-1]] - s[order[-2]] > 2.0 ** -18 * s[order[-1]] + 200:
+                assert np.array_equal(f64(out)[r, h], vv[order[-1]].astype(np.float32)), (r, h)
+                assert abs(f64(lse)[r, h] - s[order[-1]]) <= 2.0 ** -16 * abs(s[order[-1]]) + 2.0 ** -20
+
+
 def test_rows_behind_the_last_request_stay():
     q, c, table, starts = attend_case([30, 50], [3, 4], 4, 2, 64, 16, "bf16", 3, pad=9)
     for n in (9, 0):
@@ -362,7 +385,7 @@ def test_what_a_query_does_not_see_has_no_effect(t):
             u.copy_(old)
 
 
-@pytest.mark.parametrize("kind", ["near", "far", "rising", "zeros first", "one far block", "far where nobody looks"])
+@pytest.mark.parametrize("kind", ["near", "less near", "far", "rising", "zeros first", "one far block", "far where nobody looks"])
 def test_values_of_many_sizes(kind):
     # values whose scales leave FP16's reach of the first tile's are taken another way
     lens, new = [300, 90], [200, 90]
@@ -373,7 +396,9 @@ def test_values_of_many_sizes(kind):
         for p in range(n):
             where[row[p // 16], p % 16] = p
     pos = where[:, None, :, None].expand(vs.shape)
-    if kind == "near":        # as far as it reaches: 12 above and 23 below the first tile's largest
+    if kind == "near":        # as far as it reaches: 12 above and 13 below the first tile's largest
+        vs.copy_(torch.where(pos < 64, 127, torch.from_numpy(rng.integers(114, 140, vs.shape)).cuda()))
+    elif kind == "less near":
         vs.copy_(torch.where(pos < 64, 127, torch.from_numpy(rng.integers(104, 140, vs.shape)).cuda()))
     elif kind == "far":
         vs.copy_(torch.from_numpy(rng.integers(60, 200, vs.shape)))
@@ -395,6 +420,72 @@ def test_values_of_many_sizes(kind):
     for mask in (dict(), dict(window=70), dict(causal=False)):
         out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts), lse=True, **mask)
         check_attention(q, c, table, lens, starts, 16, out, lse, **mask)
+
+
+def test_small_values_beside_large_ones_keep_their_bits():
+    lens, new = [150], [100]
+    q, c, table, starts = attend_case(lens, new, 4, 1, 64, 16, "bf16", 9)
+    vs = c.v_scales.view(torch.uint8)
+    vs.fill_(127)
+    args = (q, c, i32(table.tolist()), i32(lens), i32(starts))
+    want = zn.mx_attention(*args)
+    for byte in (104, 110, 113, 114, 120, 139, 140):
+        vs[..., 1] = byte
+        out = zn.mx_attention(*args)
+        check_attention(q, c, table, lens, starts, 16, out)
+        if 114 <= byte <= 139:    # 2^-13 to 2^12 of the other block: powers of two, exact
+            assert torch.equal(out[..., :32], want[..., :32])
+            assert torch.equal(out[..., 32:].float() * 2.0 ** (127 - byte), want[..., 32:].float())
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_many_small_weights_add_up(new):
+    # one key with a weight of 1 and a value of 0, 300 with weights of 2^-23 and values of 6
+    q, c, table, starts = attend_case([301], [new], 1, 1, 32, 64, "bf16", 9)
+    q.zero_()
+    q[:, :, 0] = 23.0
+    c.k.zero_()
+    c.k_scales.view(torch.uint8).fill_(127)
+    c.k[table[0][0], 0, 0, 0] = 2                                  # 1.0
+    c.v.fill_(0x77)
+    c.v_scales.view(torch.uint8).fill_(127)
+    c.v[table[0][0], 0, 0] = 0
+    out = zn.mx_attention(q, c, i32(table.tolist()), i32([301]), i32(starts), scale=float(np.log(2.0)), causal=False)
+    want = 300 * 6 * 2.0 ** -23 / (1 + 300 * 2.0 ** -23)
+    # each weight within 2^-11 of itself and 2^-32, the scale's rounding 23 * 2^-24, the result's half a step
+    assert (np.abs(f64(out) - want) <= want * (2.0 ** -11 + 2.0 ** -9 + 2.0 ** -16 + 2.0 ** -8)).all()
+
+
+def test_offsets_past_32_bits():
+    heads, page, dim, n_pages = 8, 64, 128, 150000                 # 4.9 GB of codes each
+    c = zn.mx_kv_cache(n_pages, heads, page, dim)
+    small = zn.mx_kv_cache(8, heads, page, dim)
+    high = [149999, 140001, 75000, 131073, 3, 149000]
+    lens = [300, 70]
+    table = i32([high[:5], [high[5], 0, 0, 0, 0]])
+    near = i32([[0, 1, 2, 3, 4], [5, 6, 6, 6, 6]])
+    rng = np.random.default_rng(0)
+    k, v = (torch.from_numpy(rng.normal(0, 1, (370, heads, dim))).bfloat16().cuda() for _ in range(2))
+    def slots(t):
+        t = t.tolist()
+        return i32([t[b][p // page] * page + p % page for b, n in enumerate(lens) for p in range(n)])
+    table[1, 1] = 99999
+    near[1, 1] = 6
+    for cache, t in ((c, table), (small, near)):
+        zn.mx_kv_write(k, v, cache, slots(t))
+    for a, b in zip(zn.mx_kv_read(c, slots(table)), zn.mx_kv_read(small, slots(near))):
+        assert torch.equal(a, b)
+    for new in ([1, 1], [60, 20], [300, 70]):
+        starts = i32([0, new[0], sum(new)])
+        q = torch.randn(sum(new), 16, dim, device="cuda").bfloat16()
+        for hint in (1, 300):
+            assert torch.equal(zn.mx_attention(q, c, table, i32(lens), starts, max_new=hint),
+                               zn.mx_attention(q, small, near, i32(lens), starts, max_new=hint))
+
+
+def test_the_largest_page():
+    run_attention([70000, 5], None, 2, 1, 32, 65536, "bf16", 3)
+    run_attention([66000], [20], 2, 1, 32, 65536, "bf16", 4)
 
 
 def test_nans_among_the_largest_values():
@@ -615,6 +706,44 @@ def test_a_captured_step_replayed():
             torch.cuda.synchronize()
         assert torch.equal(got, want), i
         assert all(torch.equal(a, b) for a, b in zip(captured[1:], eager[1:]))
+
+
+@pytest.mark.parametrize("lens,new,spread", [([600, 40], None, 2), ([7000, 900], None, 2), ([500, 300], [90, 300], 2),
+                                             ([6000], [33], 2), ([500, 300], [90, 300], 60)])
+def test_every_kernel_captured_and_replayed(lens, new, spread):
+    q, c, table, starts = attend_case(lens, new, 8, 2, 128, 64, "bf16", 1, spread=spread)
+    args = [q, c, i32(table.tolist()), i32(lens)] + ([i32(starts)] if new else [])
+    g = torch.cuda.CUDAGraph()
+    zn.mx_attention(*args, lse=True)
+    with torch.cuda.graph(g):
+        out, lse = zn.mx_attention(*args, lse=True)
+    for i in range(6):
+        q.normal_()
+        if i == 3:
+            args[3].sub_(7)                                        # lengths are looked at by every replay
+        want = zn.mx_attention(*args, lse=True)
+        out.zero_()
+        g.replay()
+        if i % 2:
+            torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_the_most_requests_captured():
+    lens, add, table, free, n_pages = step_case(8192, 16, 9, longest=40, new=3)
+    total = int(add.sum())
+    a = (i32(lens.tolist()), i32(add.tolist()), i32(table.tolist()), i32(free.tolist()), i32([len(free)]), 16, n_pages, total)
+    want = zn.kv_extend(*a)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = zn.kv_extend(*a)
+        gone = zn.kv_release(got.lens, torch.ones(8192, dtype=torch.bool, device="cuda"), a[2], a[3].clone(), got.n_free, 16)
+    for _ in range(3):
+        for x in got:
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want)) and not gone[0].any()
 
 
 def test_two_graphs_at_once():

@@ -97,7 +97,9 @@ def attend(scratch=None, nbytes=0, c=None, **change):
     dict(dtype=FP8), dict(heads=0), dict(heads=3), dict(batch=8193, tokens=8193), dict(tokens=1), dict(batch=1),
     dict(tokens=(1 << 27) + 1, starts=P), dict(qt=FAR), dict(qh=FAR), dict(ot=FAR), dict(oh=FAR), dict(ts=FAR),
     dict(batch=2, tokens=2, ts=7), dict(width=1 << 27, ts=1 << 27), dict(scale=0.0), dict(scale=-1.0),
-    dict(scale=math.nan), dict(scale=math.inf), dict(window=1 << 31), dict(window=4, causal=0)])
+    dict(scale=math.nan), dict(scale=math.inf), dict(window=1 << 31), dict(window=4, causal=0),
+    dict(batch=2, tokens=2, oh=63), dict(batch=2, tokens=2, ot=255), dict(batch=2, tokens=2, ot=64, oh=64),
+    dict(batch=3, tokens=3, ot=64, oh=191), dict(batch=2, tokens=2, ot=0), dict(batch=2, tokens=2, oh=0)])
 def test_attention_refuses(bad):
     assert attend() == 0
     assert attend(**bad) == ARG
@@ -129,6 +131,13 @@ def test_cache_addresses_refused(bad):
     assert L.zn_mx_kv_write(*dict(WRITE, cache=c, tokens=1).values()) == ARG
     assert L.zn_mx_kv_read(*dict(READ, cache=c, tokens=1).values()) == ARG
     assert attend(c=c, batch=1, tokens=1, width=4, scratch=P, nbytes=1 << 40) == ARG
+
+
+def test_results_may_lie_either_way():
+    b = ctypes.c_uint64()
+    for change in (dict(), dict(ot=64, oh=192), dict(ot=64, oh=FAR - 1), dict(ot=300, oh=70), dict(heads=2, batch=1, tokens=1, oh=64, ot=0)):
+        g = zn._ATTENTION_ARGS.pack(*dict(ATTEND, **dict(dict(batch=3, tokens=3), **change)).values())
+        assert zn.lib().zn_mx_attention_scratch_bytes(cache(), g, ctypes.byref(b)) == 0
 
 
 def test_attention_scratch_is_asked_and_checked():
