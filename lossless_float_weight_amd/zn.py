@@ -773,6 +773,17 @@ def _kv_cache(where: str, cache):
     return _CACHE_ARGS.pack(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), *lay[:4], 0, *lay[4]), lay
 
 
+_INT32 = torch.int32
+
+
+def _kv_dense_ints(*tensors) -> bool:
+    """Whether all are dense int32 tensors of one axis."""
+    for t in tensors:
+        if t.dtype is not _INT32 or t.dim() != 1 or not t.is_contiguous():
+            return False
+    return True
+
+
 def _kv_ints(where: str, name: str, t: torch.Tensor, shape) -> None:
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted dense int32 {tuple(shape)}")
@@ -780,6 +791,10 @@ def _kv_ints(where: str, name: str, t: torch.Tensor, shape) -> None:
 
 def _kv_table(where: str, table: torch.Tensor, batch: int):
     """(row stride, width) of a block table."""
+    if table.dtype is _INT32 and table.dim() == 2 and table.is_contiguous():
+        n, width = table.shape
+        if n == batch:
+            return width, width
     if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch:
         raise ZnError(-1, f"{where}: table is {table.dtype} {tuple(table.shape)}, wanted int32 rows of {batch} requests")
     width = table.shape[1]
@@ -795,6 +810,8 @@ def _kv_page(where: str, page_size: int) -> None:
 
 def _kv_rows(where: str, name: str, t: torch.Tensor, shape, dtype):
     """(token stride, head stride) of [tokens, heads, head_dim] whose rows are dense."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return (shape[1] * shape[2] if shape[0] > 1 else 0), (shape[2] if shape[1] > 1 else 0)
     if t.dtype != dtype or t.shape != shape:
         raise ZnError(-1, f"{where}: {name} is {t.dtype} {tuple(t.shape)}, wanted {dtype} {tuple(shape)}")
     st = t.stride()
@@ -811,25 +828,25 @@ def kv_extend(lens: torch.Tensor, add: torch.Tensor, table: torch.Tensor, free: 
     its tokens get slot -1.  tokens: length of slots and positions."""
     where = "kv_extend"
     dev = _mx_device(where, stream, lens, add, table, free, n_free, *(out or ()))
-    batch = lens.numel()
-    _kv_ints(where, "lens", lens, (batch,))
-    _kv_ints(where, "add", add, (batch,))
-    _kv_ints(where, "free", free, (free.numel(),))
-    _kv_ints(where, "n_free", n_free, (1,))
+    batch, cap = lens.numel(), free.numel()
+    if not _kv_dense_ints(lens, add, free, n_free) or add.numel() != batch or n_free.numel() != 1:
+        for name, t, n in (("lens", lens, batch), ("add", add, batch), ("free", free, cap), ("n_free", n_free, 1)):
+            _kv_ints(where, name, t, (n,))
     stride, width = _kv_table(where, table, batch)
     _kv_page(where, page_size)
     if not 0 <= tokens < 1 << 31 or n_pages < 0 or n_pages * page_size >= 1 << 31:
         raise ZnError(-1, f"{where}: {tokens} tokens, {n_pages} pages of {page_size}")
     shapes = (batch,), (batch + 1,), (tokens,), (tokens,), (1,)
     if out is None:
-        made = _mx_new(torch.int32, dev, stream, 2 * batch + 2 + 2 * tokens)
-        out = KvStep(*made.split([batch, batch + 1, tokens, tokens, 1]))
+        n = 2 * batch + 2 + 2 * tokens
+        made = lens.new_empty(n) if stream is None else _mx_new(_INT32, dev, stream, n)
+        out = KvStep(*torch.split_with_sizes(made, (batch, batch + 1, tokens, tokens, 1)))
     else:
         out = KvStep(*out)
         for name, t, shape in zip(KvStep._fields, out, shapes):
             _kv_ints(where, "out." + name, t, shape)
     _mx_call(where, dev, stream, lib().zn_kv_extend, lens.data_ptr(), add.data_ptr(), batch, table.data_ptr(), stride,
-             width, free.data_ptr(), free.numel(), n_free.data_ptr(), page_size, n_pages, tokens, out[0].data_ptr(),
+             width, free.data_ptr(), cap, n_free.data_ptr(), page_size, n_pages, tokens, out[0].data_ptr(),
              out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr())
     if stream is not None:
         _mx_use(stream, lens, add, table, free, n_free, *out)
@@ -842,23 +859,23 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
     back onto the stack; (lens, n_free) after that."""
     where = "kv_release"
     dev = _mx_device(where, stream, lens, done, table, free, n_free, *(out or ()))
-    batch = lens.numel()
-    _kv_ints(where, "lens", lens, (batch,))
-    if done.dtype not in (torch.bool, torch.uint8) or done.shape != (batch,) or not done.is_contiguous():
+    batch, cap = lens.numel(), free.numel()
+    if not _kv_dense_ints(lens, free, n_free) or n_free.numel() != 1:
+        for name, t, n in (("lens", lens, batch), ("free", free, cap), ("n_free", n_free, 1)):
+            _kv_ints(where, name, t, (n,))
+    if done.dtype not in (torch.bool, torch.uint8) or done.shape != lens.shape or not done.is_contiguous():
         raise ZnError(-1, f"{where}: done is {done.dtype} {tuple(done.shape)}, wanted dense bool {(batch,)}")
-    _kv_ints(where, "free", free, (free.numel(),))
-    _kv_ints(where, "n_free", n_free, (1,))
     stride, width = _kv_table(where, table, batch)
     _kv_page(where, page_size)
     if out is None:
-        made = _mx_new(torch.int32, dev, stream, batch + 1)
-        out = made[:batch], made[batch:]
+        made = lens.new_empty(batch + 1) if stream is None else _mx_new(_INT32, dev, stream, batch + 1)
+        out = torch.split_with_sizes(made, (batch, 1))
     else:
         out = tuple(out)
         _kv_ints(where, "out's lens", out[0], (batch,))
         _kv_ints(where, "out's n_free", out[1], (1,))
     _mx_call(where, dev, stream, lib().zn_kv_release, lens.data_ptr(), done.data_ptr(), batch, table.data_ptr(), stride,
-             width, free.data_ptr(), free.numel(), n_free.data_ptr(), page_size, out[0].data_ptr(), out[1].data_ptr())
+             width, free.data_ptr(), cap, n_free.data_ptr(), page_size, out[0].data_ptr(), out[1].data_ptr())
     if stream is not None:
         _mx_use(stream, lens, done, table, free, n_free, *out)
     return out
@@ -873,7 +890,8 @@ def mx_kv_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, st
     dev = _mx_device(where, stream, k, v, slots, *cache)
     c, (_, _, heads, dim, _) = _kv_cache(where, cache)
     tokens = slots.numel()
-    _kv_ints(where, "slots", slots, (tokens,))
+    if not _kv_dense_ints(slots):
+        _kv_ints(where, "slots", slots, (tokens,))
     kt, kh = _kv_rows(where, "k", k, (tokens, heads, dim), k.dtype)
     vt, vh = _kv_rows(where, "v", v, (tokens, heads, dim), k.dtype)
     _mx_call(where, dev, stream, lib().zn_mx_kv_write, dt, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh,
@@ -892,7 +910,7 @@ def mx_kv_read(cache, slots: torch.Tensor, dtype=torch.bfloat16, out=None, strea
     _kv_ints(where, "slots", slots, (tokens,))
     if out is None:
         _mx_plain(where, "dtype", dtype)
-        out = tuple(_mx_new(dtype, dev, stream, tokens, heads, dim) for _ in range(2))
+        out = _mx_new(dtype, dev, stream, 2, tokens, heads, dim).unbind(0)
     else:
         k, v = out = tuple(out)
         _mx_no_grad(where, k=k, v=v)
@@ -931,7 +949,8 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     one is refused while gradients are recorded."""
     where = "mx_attention"
     given = lse if isinstance(lse, torch.Tensor) else None
-    _mx_no_grad(where, q=q, out=out, lse=given)
+    if q.requires_grad or out is not None or given is not None:
+        _mx_no_grad(where, q=q, out=out, lse=given)
     dt = _mx_plain(where, "q", q.dtype)
     dev = _mx_device(where, stream, q, table, lens, starts, out, given, scratch, *cache)
     c, lay = _kv_cache(where, cache)
@@ -940,7 +959,8 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     tokens, heads, dim = q.shape
     qt, qh = _kv_rows(where, "q", q, q.shape, q.dtype)
     batch = lens.numel()
-    _kv_ints(where, "lens", lens, (batch,))
+    if not _kv_dense_ints(lens):
+        _kv_ints(where, "lens", lens, (batch,))
     stride, width = _kv_table(where, table, batch)
     if starts is not None:
         _kv_ints(where, "starts", starts, (batch + 1,))
@@ -955,7 +975,8 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     max_new = min(max(int(max_new), 0), tokens)
     need = _attention_scratch(dt, heads, batch, tokens, max_new, width, starts is not None, lay)
     if out is None:
-        out, ot, oh = _mx_new(q.dtype, dev, stream, tokens, heads, dim), heads * dim, dim
+        out = q.new_empty((tokens, heads, dim)) if stream is None else _mx_new(q.dtype, dev, stream, tokens, heads, dim)
+        ot, oh = heads * dim, dim
     else:
         ot, oh = _kv_rows(where, "out", out, q.shape, q.dtype)
         inner = dim
