@@ -133,7 +133,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
 }
 
 template <int DT, int NB>
-constexpr int kResident = DT == BF16 ? NB == 1 ? 4 : NB == 2 ? 3 : NB <= 4 ? 2 : 1 : NB <= 2 ? 2 : 1;   // waves a SIMD
+constexpr int kResident = DT == BF16 ? NB <= 2 ? 3 : NB <= 4 ? 2 : 1 : NB <= 2 ? 2 : 1;   // waves a SIMD
 
 template <int DT, int NB>
 struct Shape {
@@ -302,6 +302,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
     put(key0, t & 1, 0);
   }
   __syncthreads();
+  f32x16 less = {};   // -m, 0 before the first key
   for (uint32_t flag = 0; t < end; t++) {
     const uint32_t next = flag == 2 ? 0 : flag + 1;
     if (threadIdx.x == 0) lds.odd[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
@@ -314,7 +315,8 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
       ask_pages(key0 + 2 * kTile);
     }
     if (key0 < r.high && key0 + kTile > r.low) {   // some row of this wave sees the tile
-      f32x16 s[2] = {};
+      // scores less m, which the sums begin with
+      f32x16 s[2] = {less, less};
       const uint8_t *keys = lds.k[buf] + n * S::kKeyPitch + 16 * h;
 #pragma unroll
       for (int st = 0; st < S::kSteps; st++)
@@ -338,15 +340,24 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
 #pragma unroll
         for (int i = 0; i < 16; i++) top = fmaxf(top, s[g][i]);
       top = max_h(top);
-      if (__any((top - r.m) * c > kRise)) {
-        const float up = fmaxf(top, r.m);
-        const float f = up > r.m ? __builtin_amdgcn_exp2f((r.m - up) * c) : 1.0f;
-        r.l *= f;
+      if (__any(r.m == -__builtin_inff() ? top > -__builtin_inff() : top * c > kRise)) {
+        const bool none = r.m == -__builtin_inff();
+        const float up = none || top > 0.0f ? top : 0.0f;
+        const float f = none ? 0.0f : __builtin_amdgcn_exp2f(-up * c);
+        if (up > -__builtin_inff()) {
+          r.l *= f;
+          r.m = none ? up : r.m + up;
+        }
 #pragma unroll
         for (int d = 0; d < NB; d++) r.o[d] *= f;
-        r.m = up;
+#pragma unroll
+        for (int i = 0; i < 16; i++) {
+          const float by = up > -__builtin_inff() ? up : 0.0f;
+          s[0][i] -= by;
+          s[1][i] -= by;
+          less[i] -= by;
+        }
       }
-      const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
       // 16 keys of 32 values at a time; the weights of the next 16 keys are made while
       // the matrix unit takes these
       const uint8_t *from = lds.v[buf] + (4 * h + (lane & 15) / 4) * S::kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
@@ -359,7 +370,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i] - m, c, kTop - kRise));
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, kTop - kRise));
           r.l += x[i];
         }
         if constexpr (HALF)
