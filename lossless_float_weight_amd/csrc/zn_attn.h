@@ -195,6 +195,15 @@ __device__ __forceinline__ float log_sum(float m, float l, float scale) {
   return l == 0.0f ? -__builtin_inff() : __builtin_fmaf(m, scale, (kRise + __builtin_log2f(l)) * 0.6931471805599453f);
 }
 
+// A row's result from its sums over all keys.
+template <int DT>
+__device__ __forceinline__ void put_row(const AttnArgs &a, const Request &rq, uint32_t token, uint32_t qh, uint32_t col,
+                                        f32x4 o, float m, float l) {
+  const uint64_t y = rq.start + token;
+  store4<DT>(a.out + (y * a.out_token + qh * a.out_head + col) * esize(DT), o * over(l));
+  if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l, a.scale);
+}
+
 // NaNs among a tile's values would meet the weight 0 of rows that do not see their
 // key, so such a block goes in as zeros, and the rows that see it are marked: bit i
 // for block i of the values.  For the seldom tile that has some; a lane reads the
@@ -214,6 +223,82 @@ __device__ __attribute__((noinline)) uint32_t marked(const uint8_t *scales, uint
 __device__ __forceinline__ float share(float m, float top, float c) {
   return m == -__builtin_inff() && top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m - top) * c);
 }
+
+// Joins `count` pieces of a row, by a workgroup of 256: teams of D / 4 lanes, four
+// values each; `each` neighbouring teams (a power of two) have a row, take every so
+// manieth piece in order and are joined in order.  The row's sums are its first
+// team's.  All threads of a workgroup call it, with the same count and each.
+template <int NB>
+struct Join {
+  static constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
+  struct Lds {
+    __attribute__((aligned(16))) float sums[kTeams][D + 4];
+    float2 ml[kTeams];
+  };
+  uint32_t team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  float top, l;
+  f32x4 o;
+  // at least `least` teams a row, four pieces or more for each of further ones
+  static __host__ __device__ __forceinline__ uint32_t teams(uint32_t least, uint32_t count) {
+    while (4 * least <= count && 2 * least <= kTeams) least *= 2;
+    return least;
+  }
+  template <class P>
+  __device__ __forceinline__ void row(const Parts &in, P piece, uint32_t count, uint32_t each, bool live, float c, Lds &lds) {
+    const uint32_t mine = team & (each - 1);
+    top = -__builtin_inff();
+    l = 0.0f;
+    o = f32x4{0, 0, 0, 0};
+    if (live) {
+      constexpr uint32_t U = 8;   // asked for together
+      for (uint32_t i0 = mine; i0 < count; i0 += U * each) {
+        float2 ml[U];
+        f32x4 v[U];
+        float up = top;
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++) {
+          const uint32_t i = i0 + u * each;
+          ml[u] = make_float2(-__builtin_inff(), 0.0f);
+          v[u] = f32x4{0, 0, 0, 0};
+          if (i < count) {
+            const uint64_t p = piece(i);
+            ml[u] = in.ml[p];
+            v[u] = *reinterpret_cast<const f32x4 *>(in.sums + p * D + col);
+          }
+        }
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++) up = fmaxf(up, ml[u].x);
+        const float f = share(top, up, c);
+        l *= f;
+        o *= f;
+        top = up;
+#pragma unroll
+        for (uint32_t u = 0; u < U; u++) {
+          const float g = share(ml[u].x, top, c);
+          l += ml[u].y * g;
+          o += v[u] * g;
+        }
+      }
+    }
+    if (each == 1) return;
+    if (live) {
+      *reinterpret_cast<f32x4 *>(&lds.sums[team][col]) = o;
+      if (col == 0) lds.ml[team] = make_float2(top, l);
+    }
+    __syncthreads();
+    if (live && mine == 0) {
+      for (uint32_t i = 1; i < each; i++) top = fmaxf(top, lds.ml[team + i].x);
+      l = 0.0f;
+      o = f32x4{0, 0, 0, 0};
+      for (uint32_t i = 0; i < each; i++) {
+        const float f = share(lds.ml[team + i].x, top, c);
+        l += lds.ml[team + i].y * f;
+        o += *reinterpret_cast<const f32x4 *>(&lds.sums[team + i][col]) * f;
+      }
+    }
+    __syncthreads();
+  }
+};
 // The last request b with before[b] <= v (before rises from 0), by one wave: 64
 // places a step.
 __device__ __forceinline__ uint32_t holder(const uint64_t *before, uint32_t batch, uint64_t v) {

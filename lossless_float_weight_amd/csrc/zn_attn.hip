@@ -31,7 +31,6 @@ namespace zn {
 namespace {
 
 constexpr int kWaves = 4;       // of a workgroup
-constexpr uint32_t kShort = 16;  // tiles of a short cache
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -346,15 +345,6 @@ __device__ __forceinline__ void take_tiles(const AttnArgs &a, const Request &rq,
 template <int DT, int NB>
 constexpr int kResident = DT == BF16 && NB <= 2 ? 3 : DT == BF16 && NB <= 4 ? 2 : 1;   // waves a SIMD
 
-// A row's result from its sums over all keys.
-template <int DT>
-__device__ __forceinline__ void put_row(const AttnArgs &a, const Request &rq, uint32_t token, uint32_t qh, uint32_t col,
-                                        f32x4 o, float m, float l) {
-  const uint64_t y = rq.start + token;
-  store4<DT>(a.out + (y * a.out_token + qh * a.out_head + col) * esize(DT), o * over(l));
-  if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l, a.scale);
-}
-
 template <int DT, int NB>
 __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(AttnArgs a, Plan plan, Parts out,
                                                                         FastDiv per_group, float c) {
@@ -408,28 +398,29 @@ __global__ __launch_bounds__(64 * kWaves, (kResident<DT, NB>)) void k_attend(Att
 }
 
 // Group x of all requests' groups of 16 rows, numbered with gaps where requests have
-// starts: request b's from starts[b] group / 16 + b on.
+// starts: request b's from starts[b] group / 16 + b on.  By one wave, 64 places a step.
 __device__ __forceinline__ void group_at(const AttnArgs &a, uint32_t x, uint32_t &b, uint32_t &group) {
-  if (a.starts) {
-    uint32_t lo = 0, hi = a.batch;
-    while (hi - lo > 1) {
-      const uint32_t mid = (lo + hi) >> 1;
-      const int32_t s = a.starts[mid];
-      const uint32_t from = s < 0 ? 0 : min(uint32_t(s), a.tokens);
-      if (from * a.group / 16 + mid <= x)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    b = lo;
-    const int32_t s = a.starts[b];
-    group = x - ((s < 0 ? 0 : min(uint32_t(s), a.tokens)) * a.group / 16 + b);
-  } else {
-    b = x / ((a.group + 15) / 16);
-    group = x % ((a.group + 15) / 16);
+  if (!a.starts) {
+    const uint32_t groups = (a.group + 15) / 16;
+    b = x / groups;
+    group = x - b * groups;
+    return;
+  }
+  auto from = [&](uint32_t i) {
+    const int32_t s = a.starts[i];
+    return (s < 0 ? 0 : min(uint32_t(s), a.tokens)) * a.group / 16 + i;
+  };
+  const uint32_t lane = threadIdx.x & 63;
+  b = 0;
+  for (uint32_t n = a.batch; n > 1;) {
+    const uint32_t step = (n + 63) / 64, i = lane * step;
+    const bool upto = from(b + min(i, n - 1)) <= x;
+    const uint32_t last = max(__popcll(__ballot(i < n && upto)), 1) - 1;
+    b += last * step;
+    n = min(step, n - last * step);
   }
   b = uniform(b);
-  group = uniform(group);
+  group = uniform(x - from(b));   // past the last one's where x is before all
 }
 
 // Short caches: a workgroup for each group of rows, whose waves take turns at its
@@ -481,18 +472,14 @@ __global__ __launch_bounds__((64 * kShortWaves<DT, NB>)) void k_attend_short(Att
   }
 }
 
-// Joins the pieces of a row: a workgroup a row, four values a lane; its lanes make
-// 256 / (D / 4) teams that take every so manieth piece in order, and their sums are
-// added in order.
+// Joins the pieces of a group's rows, `most` rows a workgroup (a workgroup a row
+// where groups have two pieces each: 64 x 512 keys of 2 groups 51 us, of eight 14).
 template <int DT, int NB>
-__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group, float c, bool by_edges) {
-  constexpr int D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes;
-  __shared__ float tops[4];
-  __shared__ __attribute__((aligned(16))) float sums[kTeams][D + 4];
-  __shared__ float weights[kTeams];
-  const uint32_t head = blockIdx.y;
-  const uint32_t rows = a.starts ? 16 : min(16u, a.group);   // of a group, at most
-  const uint32_t x = blockIdx.x / rows, rr = blockIdx.x - x * rows;
+__global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_group, float c, bool by_edges, uint32_t most,
+                                              uint32_t shares) {
+  using J = Join<NB>;
+  __shared__ typename J::Lds lds;
+  const uint32_t head = blockIdx.y, x = blockIdx.x / shares, first = (blockIdx.x - x * shares) * most;
   const uint64_t each = *in.each;
   uint32_t b, group;
   uint64_t at;     // the group's first tile
@@ -514,50 +501,24 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
     at = in.before[b] + uint64_t(group) * max(r.tiles, 1u);
   }
   const Request rq = uniform(request(a, b));
-  const uint32_t row = group * 16 + rr;
-  if (row >= rq.n * a.group) return;
+  const uint32_t rows = min(16u, rq.n * a.group - group * 16), end = min(first + most, rows);
   const uint64_t f = at / each, pieces = (at + max(rq.tiles, 1u) - 1) / each - f + 1;
   if (pieces <= 1) return;
   if (pieces > in.slots || 2 * f > in.slots - pieces) return;   // starts out of order: not all tiles had a taker
   const uint32_t count = uint32_t(pieces);
   const uint64_t p0 = uint64_t(head) * in.slots + 2 * f;
-  // a row's piece i
-  auto piece = [&](uint32_t i) { return (p0 + (i ? 2 * i : 1)) * 16 + rr; };
-
-  float top = -__builtin_inff();
-  for (uint32_t i = threadIdx.x; i < count; i += 256) top = fmaxf(top, in.ml[piece(i)].x);
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-
-  const uint32_t team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
-  if (team < kTeams) {
-    float l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-#pragma unroll 4
-    for (uint32_t i = team; i < count; i += kTeams) {
-      const uint64_t p = piece(i);
-      const float2 ml = in.ml[p];
-      const float f = share(ml.x, top, c);
-      l += ml.y * f;
-      o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
-    }
-    *reinterpret_cast<f32x4 *>(&sums[team][col]) = o;
-    if (col == 0) weights[team] = l;
+  uint32_t least = 1;
+  while (2 * least * most <= J::kTeams) least *= 2;
+  const uint32_t teams = J::teams(least, count), at_once = J::kTeams / teams;
+  J j;
+  for (uint32_t r0 = first; r0 < end; r0 += at_once) {
+    const uint32_t rr = r0 + j.team / teams;
+    const bool live = j.team / teams < at_once && rr < end;
+    j.row(in, [&](uint32_t i) { return (p0 + (i ? 2 * i : 1)) * 16 + rr; }, count, teams, live, c, lds);
+    if (!live || (j.team & (teams - 1))) continue;
+    const uint32_t row = group * 16 + rr, token = per_group.div(row);
+    put_row<DT>(a, rq, token, head * a.group + row - token * a.group, j.col, j.o, j.top, j.l);
   }
-  __syncthreads();
-  if (threadIdx.x >= kLanes) return;
-  float l = 0.0f;
-  f32x4 o = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < kTeams; i++) {
-    l += weights[i];
-    o += *reinterpret_cast<const f32x4 *>(&sums[i][col]);
-  }
-  const uint32_t token = per_group.div(row);
-  put_row<DT>(a, rq, token, head * a.group + row - token * a.group, col, o, top, l);
 }
 
 // ------------------------------------------------------------------ launch --
@@ -568,18 +529,29 @@ struct Few {
     uint32_t groups;       // row groups of a key head, at most
     bool brief;            // taken by k_attend_short
     bool split;            // some group may be cut into pieces
+    bool few;              // not by workgroups for 128 rows
   };
+  // Times below: 8 key heads of 128 values, 4 query heads each, us.
   static Sizes sizes(const AttnArgs &a) {
     Sizes z;
     z.groups = a.starts ? uint32_t(uint64_t(a.tokens) * a.group / 16 + a.batch) : a.batch * ((a.group + 15) / 16);
-    const uint64_t tiles = ((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile;
-    // One launch for two where the waves of a workgroup have two tiles each: 8 requests
-    // of 500 or 1000 keys (8 key heads of 128 values) take 6.8 and 9.4 us for 10.7 and
-    // 11.3, of 2000 14.0 for 13.9; 64 of 100 or 1000 10.4 and 20.0 for 13.3 and 22.5.
-    // Where workgroups wait for each other, shares win: 256 of 100 or 1000 keys 37 and
-    // 64 us for 25 and 53, but not for heads of 64 values (17 and 31 for 22 and 39),
-    // of which more run at a time.
-    z.brief = tiles <= kShort && uint64_t(z.groups) * a.c.heads <= (NB <= 2 ? 1u << 20 : 1024u);
+    // a request's queries, and the tiles that a group of them sees, as far as the sizes tell
+    const uint64_t queries = !a.starts ? 1 : a.max_new ? a.max_new : (uint64_t(a.tokens) + a.batch - 1) / a.batch;
+    uint64_t tiles = ((uint64_t(a.width) << a.c.shift) + kTile - 1) / kTile;
+    if (a.window) tiles = std::min<uint64_t>(tiles, (a.window + queries) / kTile + 2);
+    const uint64_t all = uint64_t(z.groups) * a.c.heads;
+    // One launch for two where a wave has four tiles at most (8 requests of 500 or 1000
+    // keys 7.5 and 10.1 for 11.4 and 13.2, 32 of 2000 18.4 for 24.0) and workgroups do not
+    // wait for each other: 64 of 1000 23.4 for 24.2, 128 of 300 26.2 for 21.8; 1000
+    // workgroups of FP32 queries 25.8 for 29.5, of heads of 64 values 14.5 for 26.6.
+    z.brief = tiles <= 4 * kShortWaves<DT, NB> && all <= (DT == BF16 && NB > 2 ? 640 : 1024);
+    // Waves of 16 rows take tiles that hold more rows again and again, but there are more
+    // of them.  They win with one or two groups a request (64 x 2048 keys, 32 rows 61 for
+    // 71, 48 rows 89 for 83), beside FP32 queries with four (64 x 2048 keys, 64 rows 155
+    // for 211, 128 rows 294 for 227), or where there is little to do: 8 x 2048 keys of 128
+    // rows 43 for 46, of 256 62 for 56.  With few tiles workgroups of 128 rows need no
+    // pieces and win (16 x 200 keys of 256 rows 17 for 23).
+    z.few = z.brief || queries * a.group <= (DT == BF16 ? 32 : 64) || (tiles > 8 && all * tiles <= 20480);
     // the takers fill the chip once, so that they all run at the same time; no more
     // of them than tiles (one more a group where a window begins inside one)
     const uint64_t n = std::min<uint64_t>(1024 * kResident<DT, NB> / a.c.heads, z.groups * (tiles + 1));
@@ -606,31 +578,27 @@ struct Few {
     k_attend<DT, NB><<<dim3((z.plan.takers + kWaves - 1) / kWaves, a.c.heads), 64 * kWaves, 0, s>>>(a, z.plan, p, per_group, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !z.split) return e;
+    // for the rows of every group, or of every group that an edge between two shares can
+    // lie in: as many rows a workgroup as it has teams for the pieces that are to be
+    // expected
     const uint32_t rows = a.starts || a.group > 16 ? 16 : a.group;
-    // a workgroup for each row of every group, or of every group that an edge between two shares can lie in
     const bool by_edges = z.plan.takers - 1 < z.groups;
-    k_join<DT, NB><<<dim3((by_edges ? z.plan.takers - 1 : z.groups) * rows, a.c.heads), 256, 0, s>>>(a, p, per_group, c, by_edges);
+    const uint32_t most = std::max(1u, Join<NB>::kTeams / Join<NB>::teams(1, z.plan.takers / z.groups + 1));
+    const uint32_t shares = (rows + most - 1) / most;
+    k_join<DT, NB><<<dim3((by_edges ? z.plan.takers - 1 : z.groups) * shares, a.c.heads), 256, 0, s>>>(
+        a, p, per_group, c, by_edges, most, shares);
     return hipGetLastError();
   }
 };
 
-// Sixteen rows a request or fewer, as far as the sizes tell, are taken by single
-// waves, more by workgroups for 128.
-bool few(const AttnArgs &a) {
-  const uint64_t most = !a.starts ? 1 : a.max_new ? a.max_new : (uint64_t(a.tokens) + a.batch - 1) / a.batch;
-  return most * a.group <= 16;
-}
-
 }  // namespace
 
 uint64_t attention_scratch(int dtype, const AttnArgs &a) {
-  if (!few(a)) return attention_tall_scratch(dtype, a);
-  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.scratch(a); });
+  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.sizes(a).few ? k.scratch(a) : attention_tall_scratch(dtype, a); });
 }
 
 hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s) {
-  if (!few(a)) return launch_attention_tall(dtype, a, s);
-  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.run(a, s); });
+  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.sizes(a).few ? k.run(a, s) : launch_attention_tall(dtype, a, s); });
 }
 
 }  // namespace zn

@@ -19,7 +19,7 @@ namespace {
 
 constexpr uint32_t kRows = 128;     // of a workgroup
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kLeast = 4;      // tiles of a piece at least
+constexpr uint32_t kLeast = 16;     // tiles of a piece at least
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -85,7 +85,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
     }
   const uint64_t total = of_lane(scan(mine), 63);
   uint64_t piece = (total + plan.items - 1) / plan.items;
-  it.tiles = piece = piece < kLeast ? kLeast : piece;
+  piece = piece < kLeast ? kLeast : piece;
   uint64_t items = 0, parts = 0;
   for (uint32_t i = 0; i < per; i++)
     if (lane * per + i < a.batch) {
@@ -124,7 +124,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
       it.group = uniform(i / it.pieces);
       it.piece = uniform(i - it.group * it.pieces);
       it.slot = uniform(slot + i);
-      it.tiles = uniform(piece);
+      it.tiles = uniform((r.tiles + p - 1) / p);   // pieces of a request are alike
       return true;
     }
     first += g * p;
@@ -495,44 +495,37 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   }
 }
 
-// Joins the pieces of a group, in their order: a team of D / 4 lanes a row, and as
-// many rows a workgroup as it has teams.  Groups are named by their first piece's
-// slot; the workgroups go through those there are.
+// Joins the pieces of a group.  Its rows are shared out over the workgroups of all
+// its slots, with few pieces a team a row, with many up to a workgroup's teams (64
+// pieces of 32 rows by a team a row took 40 us, so 14); the workgroups go through the
+// slots that there are.
 template <int DT, int NB>
 __global__ __launch_bounds__(256) void k_join_tall(AttnArgs a, Parts in, FastDiv per_group, float c) {
-  constexpr uint32_t D = 32 * NB, kLanes = D / 4, kTeams = 256 / kLanes, kShares = (kRows + kTeams - 1) / kTeams;
-  const uint32_t head = blockIdx.y, team = threadIdx.x / kLanes, col = threadIdx.x % kLanes * 4;
+  using J = Join<NB>;
+  constexpr uint32_t kShares = (kRows + J::kTeams - 1) / J::kTeams;
+  __shared__ typename J::Lds lds;
+  const uint32_t head = blockIdx.y;
   const uint64_t all = min(*in.all, uint64_t(in.slots)) * kShares, piece = *in.each;
+  J j;
   for (uint64_t x = blockIdx.x; x < all; x += gridDim.x) {
     const uint32_t slot = uint32_t(x / kShares);
     const uint32_t b = uniform(holder(in.before, a.batch, slot));
     const Request rq = uniform(request(a, b));
-    const uint64_t count = (max(rq.tiles, 1u) + piece - 1) / piece, rel = slot - in.before[b];
-    const uint32_t r = uint32_t(x - uint64_t(slot) * kShares) * kTeams + team;
-    const uint64_t group = rel / count, row64 = group * kRows + r;
+    const uint64_t pieces = (max(rq.tiles, 1u) + piece - 1) / piece, rel = slot - in.before[b], group = rel / pieces;
+    const uint32_t count = uint32_t(pieces), nth = uint32_t(rel - group * pieces);
     // (the last: starts out of order can make more pieces than there is room for)
-    if (count <= 1 || rel % count || team >= kTeams || r >= kRows || row64 >= uint64_t(rq.n) * a.group ||
-        slot + count > in.slots)
-      continue;
-    const uint32_t row = uint32_t(row64);
-    const uint64_t p0 = (uint64_t(head) * in.slots + slot) * kRows + r;
-    float top = -__builtin_inff();
-#pragma unroll 4
-    for (uint32_t i = 0; i < count; i++) top = fmaxf(top, in.ml[p0 + i * uint64_t(kRows)].x);
-    float l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-#pragma unroll 4
-    for (uint32_t i = 0; i < count; i++) {
-      const uint64_t p = p0 + i * uint64_t(kRows);
-      const float2 ml = in.ml[p];
-      const float f = share(ml.x, top, c);
-      l += ml.y * f;
-      o += *reinterpret_cast<const f32x4 *>(in.sums + p * D + col) * f;
-    }
-    const uint32_t tk = per_group.div(row), h = head * a.group + row - tk * a.group;
-    const uint64_t y = rq.start + tk;
-    store4<DT>(a.out + (y * a.out_token + h * a.out_head + col) * esize(DT), o * over(l));
-    if (a.lse && col == 0) a.lse[y * a.heads + h] = log_sum(top, l, a.scale);
+    if (count <= 1 || group * kRows >= uint64_t(rq.n) * a.group || slot - nth + pieces > in.slots) continue;
+    // no more teams a row than half the pieces: `count * kShares` workgroups have all rows
+    const uint32_t teams = J::teams(1, count), rows = J::kTeams / teams;
+    const uint32_t first = (nth * kShares + uint32_t(x - uint64_t(slot) * kShares)) * rows;
+    if (first >= kRows) continue;
+    const uint32_t r = first + j.team / teams, row = uint32_t(group) * kRows + r;
+    const bool live = j.team / teams < rows && r < kRows && row < rq.n * a.group;
+    const uint64_t p0 = (uint64_t(head) * in.slots + (slot - nth)) * kRows + r;
+    j.row(in, [&](uint32_t i) { return p0 + i * uint64_t(kRows); }, count, teams, live, c, lds);
+    if (!live || (j.team & (teams - 1))) continue;
+    const uint32_t token = per_group.div(row);
+    put_row<DT>(a, rq, token, head * a.group + row - token * a.group, j.col, j.o, j.top, j.l);
   }
 }
 

@@ -925,11 +925,11 @@ def mx_kv_read(cache, slots: torch.Tensor, dtype=torch.bfloat16, out=None, strea
 
 
 @functools.lru_cache(maxsize=4096)
-def _attention_scratch(dt, heads, batch, tokens, max_new, width, with_starts, lay) -> int:
+def _attention_scratch(dt, heads, batch, tokens, max_new, width, with_starts, window, lay) -> int:
     """zn_mx_attention_scratch_bytes, which goes by sizes alone."""
     c = _CACHE_ARGS.pack(0, 0, 0, 0, *lay[:4], 0, *lay[4])
     g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, 0, 0, 0, 0, heads * lay[3], lay[3], 0, 0, 0, with_starts,
-                             width, width, 1.0, 1, 0)
+                             width, width, 1.0, 1, window)
     b = C.c_uint64()
     _check(lib().zn_mx_attention_scratch_bytes(c, g, C.byref(b)), "mx_attention")
     return b.value
@@ -973,7 +973,7 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     elif not (math.isfinite(scale) and scale > 0):
         raise ZnError(-1, f"{where}: scale is {scale}")
     max_new = min(max(int(max_new), 0), tokens)
-    need = _attention_scratch(dt, heads, batch, tokens, max_new, width, starts is not None, lay)
+    need = _attention_scratch(dt, heads, batch, tokens, max_new, width, starts is not None, window, lay)
     if out is None:
         out = q.new_empty((tokens, heads, dim)) if stream is None else _mx_new(q.dtype, dev, stream, tokens, heads, dim)
         ot, oh = heads * dim, dim

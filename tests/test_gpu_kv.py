@@ -765,3 +765,91 @@ def test_two_graphs_at_once():
         torch.cuda.synchronize()
         for g, got, want, s, _ in made:
             assert torch.equal(got, want)
+
+
+# ------------------------------------------------- the kernels by their sizes --
+# Which kernel takes a call goes by the sizes that the host sees, the table's width and the hint among them: wide tables
+# send the cases above to kernels that their lengths would not choose.
+def by_sizes(kind):
+    attention = zn.mx_attention
+
+    def call(q, c, table, lens, starts=None, max_new=0, **kw):
+        kv_heads, page = c.k.shape[1:3]
+        if kind == "few":        # waves of 16 rows that share out all tiles: a cache past 32 tiles, one query a request
+            tiles, max_new = 40, 1
+        else:                    # workgroups for 128 rows: many queries a request, 20480 tiles and more
+            tiles, max_new = 20480 // kv_heads + 1, q.shape[0]
+            if starts is None:
+                starts = torch.arange(q.shape[0] + 1, dtype=torch.int32, device="cuda")
+        width = max(-(-tiles * 64 // page), table.shape[1])
+        wide = torch.full((table.shape[0], width), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        return attention(q, c, wide, lens, starts, max_new=max_new, **kw)
+    return call
+
+
+@pytest.mark.parametrize("kind", ["few", "many"])
+@pytest.mark.parametrize("test,args", [
+    *((test_attention_of_several_queries, ([300, 0, 20], [129, 0, 1], m, t)) for m in (dict(), dict(causal=False)) for t in TYPE),
+    *((test_attention_of_several_queries, (lens, new, {}, t)) for lens, new in (([3, 200], [9, 33]), ([700], [700]),
+                                                                             ([65, 64, 63, 130], [2, 64, 63, 100])) for t in TYPE),
+    *((test_attention_of_long_caches, (lens, new, {}, t)) for lens, new in (([5000, 1, 2500], [4, 1, 2]), ([4100], [300]),
+                                                                         ([9000, 4000], [20, 100])) for t in TYPE),
+    *((test_attention_of_many_rows, ([700, 150, 0], [300, 150, 0], d)) for d in (32, 64, 96, 128, 256)),
+    (test_attention_of_many_requests, (300,)), (test_attention_of_pages_and_orders, (128, "beside")),
+    (test_attention_of_pages_and_orders, (16, "tokens")), (test_equal_weights_give_means, ()),
+    *((test_scores_past_the_weights_precision, ([3000], [40], t)) for t in TYPE),
+    *((test_what_a_query_does_not_see_has_no_effect, (t,)) for t in TYPE),
+    *((test_values_of_many_sizes, (k,)) for k in ("near", "less near", "far", "rising", "zeros first", "one far block",
+                                                  "far where nobody looks")),
+    (test_small_values_beside_large_ones_keep_their_bits, ()), (test_many_small_weights_add_up, (40,)),
+    (test_nans_among_the_largest_values, ()), (test_values_of_many_sizes_in_pieces, ()),
+    (test_queries_that_are_not_finite_stay_by_themselves, ()), (test_rows_behind_the_last_request_stay, ()),
+    *((test_a_serving_loop, (t,)) for t in TYPE)],
+    ids=lambda x: x.__name__[5:] if callable(x) else "-".join(str(i).replace(" ", "") for i in x) if isinstance(x, tuple) else x)
+def test_by_other_sizes(test, args, kind, monkeypatch):
+    monkeypatch.setattr(zn, "mx_attention", by_sizes(kind))
+    test(*args)
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_attention_of_every_head_size_and_kernel(dim, t, monkeypatch):
+    for kind in ("few", "many"):
+        monkeypatch.setattr(zn, "mx_attention", by_sizes(kind))
+        run_attention([70, 0, 333], [40, 0, 33], 4, 2, dim, 16, t, dim)
+        run_attention([3000], [40], 4, 2, dim, 64, t, dim)
+        monkeypatch.undo()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,new,kv_heads,window", [([300, 40, 0], [300, 40, 0], 64, 1), ([300, 40, 0], [300, 40, 0], 64, 50),
+                                                      ([300, 40, 9], [299, 40, 1], 64, 5000), ([6000], [40], 96, 3000),
+                                                      ([70, 500], [64, 40], 200, 130)])
+def test_windows_of_many_heads(lens, new, kv_heads, window, t):
+    q, c, table, starts = attend_case(lens, new, 2 * kv_heads, kv_heads, 32, 16, t, window)
+    for hint in (1, max(new)):
+        out, lse = zn.mx_attention(q, c, i32(table.tolist()), i32(lens), i32(starts), max_new=hint, window=window, lse=True)
+        check_attention(q, c, table, lens, starts, 16, out, lse, window=window)
+
+
+def test_kernels_of_many_rows_captured_and_replayed():
+    for lens, new in (([500, 300], [90, 300]), ([6000, 40], [50, 40])):
+        q, c, table, starts = attend_case(lens, new, 8, 2, 128, 64, "bf16", 1, spread=60)
+        wide = torch.full((2, 11000), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = i32(table.tolist())
+        args = [q, c, wide, i32(lens), i32(starts)]
+        zn.mx_attention(*args, lse=True)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out, lse = zn.mx_attention(*args, lse=True)
+        for i in range(6):
+            q.normal_()
+            if i == 3:
+                args[3].sub_(7)
+            want = zn.mx_attention(*args, lse=True)
+            out.zero_()
+            g.replay()
+            if i % 2:
+                torch.cuda.synchronize()
+            assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
