@@ -463,7 +463,7 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * not).  It chooses between kernels and has no effect on what is computed but
  * the order of sums.
  * Rows of out do not overlap (one of its strides holds all rows of the other).
- * scale is finite and > 0, batch at most 8192, window at most 2^31 - 1, tokens *
+ * scale is > 0 and at most 2^127, batch at most 8192, window at most 2^31 - 1, tokens *
  * heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
  * 16-byte aligned device scratch (ZN_ERR_CAPACITY if it is less; 0 for some
  * sizes, then d_scratch may be NULL); calls that may run at the same time, and

@@ -543,8 +543,10 @@ struct Few {
     // One launch for two where a wave has four tiles at most (8 requests of 500 or 1000
     // keys 7.5 and 10.1 for 11.4 and 13.2, 32 of 2000 18.4 for 24.0) and workgroups do not
     // wait for each other: 64 of 1000 23.4 for 24.2, 128 of 300 26.2 for 21.8; 1000
-    // workgroups of FP32 queries 25.8 for 29.5, of heads of 64 values 14.5 for 26.6.
-    z.brief = tiles <= 4 * kShortWaves<DT, NB> && all <= (DT == BF16 && NB > 2 ? 640 : 1024);
+    // workgroups of FP32 queries 25.8 for 29.5.  Smaller heads have more of them at a time:
+    // with 64 values 1008 workgroups 14.5 for 26.6, 2048 of 2 tiles 17.9 for 13.3, of 16
+    // 37.1 for 41.7.
+    z.brief = tiles <= 4 * kShortWaves<DT, NB> && all <= (DT != BF16 ? 1024 : NB > 2 ? 640 : tiles > 8 ? 2048 : 1024);
     // Waves of 16 rows take tiles that hold more rows again and again, but there are more
     // of them.  They win with one or two groups a request (64 x 2048 keys, 32 rows 61 for
     // 71, 48 rows 89 for 83), beside FP32 queries with four (64 x 2048 keys, 64 rows 155

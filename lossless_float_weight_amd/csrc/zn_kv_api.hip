@@ -1,7 +1,5 @@
 // zn_kv_api.hip -- the C ABI of the key-value cache (include/zn.h): argument
 // checks and the launch; nothing here allocates or synchronises.
-#include <math.h>
-
 #include "../../include/zn.h"
 #include "zn_kv.h"
 
@@ -73,7 +71,7 @@ bool attention_of(const zn_mx_cache *cache, const zn_mx_attention_args *g, bool 
   // workgroups of 256 threads, one for 128 rows and one more for every request and key head, fit a grid
   if (g->tokens > (1ull << 29) / g->heads) return false;
   if (uint64_t(g->width) * cache->page_size > kMost || g->window > kMost || (g->window && !g->causal)) return false;
-  if (!(g->scale > 0.0f) || !isfinite(g->scale)) return false;
+  if (!(g->scale > 0.0f) || g->scale > 0x1p127f) return false;   // times log2(e) it is finite
   if (!g->starts && g->tokens != g->batch) return false;
   if (g->table_stride > kMostStride || (g->batch > 1 && g->table_stride < g->width)) return false;
   for (uint64_t s : {g->q_token_stride, g->q_head_stride, g->out_token_stride, g->out_head_stride})

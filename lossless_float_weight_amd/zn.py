@@ -970,7 +970,7 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
         raise ZnError(-1, f"{where}: window is {window}" + ("" if causal else ", and causal is False"))
     if scale is None:
         scale = 1.0 / math.sqrt(dim)
-    elif not (math.isfinite(scale) and scale > 0):
+    elif not 0 < scale <= 2.0 ** 127:
         raise ZnError(-1, f"{where}: scale is {scale}")
     max_new = min(max(int(max_new), 0), tokens)
     need = _attention_scratch(dt, heads, batch, tokens, max_new, width, starts is not None, window, lay)

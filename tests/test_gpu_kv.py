@@ -853,3 +853,24 @@ def test_kernels_of_many_rows_captured_and_replayed():
             if i % 2:
                 torch.cuda.synchronize()
             assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_the_largest_and_smallest_scales(new):
+    # one key whose score is 1 among scores of 0, and weights that are all alike
+    q, c, table, _ = attend_case([100], [new], 2, 1, 32, 16, "bf16", 9)
+    q.zero_()
+    q[:, :, 0] = 1.0
+    c.k.zero_()
+    c.k_scales.view(torch.uint8).fill_(127)
+    c.k[table[0][3], 0, 2, 0] = 2                                  # 1.0, at 50
+    v = torch.from_numpy(values(c)[1])
+    seen = torch.stack([v[table[0][p // 16], 0, p % 16] for p in range(100)])
+    for kind in ("few", "many"):
+        args = (q, c, i32(table.tolist()), i32([100]), i32([0, new]))
+        for attend in (zn.mx_attention, by_sizes(kind)):
+            assert torch.equal(attend(*args, scale=2.0 ** 127, causal=False).cpu(), seen[50].bfloat16().expand(new, 2, 32))
+            out = attend(*args, scale=2.0 ** -149, causal=False).cpu().double()
+            # weights alike: sums of 100 within 100 2^-24 of the sum of sizes, a half step of the mean
+            mean, size = seen.mean(0), seen.abs().mean(0)
+            assert ((out - mean).abs() <= size * 100 * 2.0 ** -23 + mean.abs() * 2.0 ** -8 + 2.0 ** -24 * size).all()

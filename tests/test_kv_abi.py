@@ -108,6 +108,11 @@ def test_attention_refuses(bad):
     assert zn.lib().zn_mx_attention_scratch_bytes(cache(), g, ctypes.byref(b)) == ARG
 
 
+def test_attention_takes_scales_to_2_127():
+    assert attend(scale=2.0 ** 127) == 0 and attend(scale=2.0 ** -149) == 0
+    assert attend(scale=2.0 ** 127 * (1 + 2.0 ** -23)) == ARG
+
+
 @pytest.mark.parametrize("bad", [
     dict(q=0), dict(q=P + 1), dict(dtype=FP32, q=P + 2), dict(out=0), dict(out=P + 1), dict(lse=P + 2), dict(table=0),
     dict(table=P + 2), dict(lens=0), dict(lens=P + 1), dict(starts=P + 2)])
