@@ -437,10 +437,10 @@ __device__ __forceinline__ void group_at(const AttnArgs &a, uint32_t x, uint32_t
 template <int DT, int NB>
 constexpr int kShortWaves = kResident<DT, NB> >= 2 ? 8 : 4;
 
-template <int DT, int NB>
-__global__ __launch_bounds__((64 * kShortWaves<DT, NB>)) void k_attend_short(AttnArgs a, FastDiv per_group, float c) {
+template <int DT, int NB, int W>
+__global__ __launch_bounds__(64 * W, (W == 2 ? kResident<DT, NB> : 1)) void k_attend_short(AttnArgs a, FastDiv per_group, float c) {
   using R = Rows16<DT, NB>;
-  constexpr int D = 32 * NB, W = kShortWaves<DT, NB>, kPad = D + 4;
+  constexpr int D = 32 * NB, kPad = D + 4;
   constexpr int kShared = R::kLds > 16 * kPad * 4 ? R::kLds : 16 * kPad * 4;
   __shared__ __attribute__((aligned(16))) uint8_t lds[W * kShared];
   __shared__ float2 ml_of[W][16];
@@ -537,7 +537,7 @@ struct Few {
   struct Sizes {
     Plan plan;
     uint32_t groups;       // row groups of a key head, at most
-    bool brief;            // taken by k_attend_short
+    bool brief, pairs;     // taken by k_attend_short; with two waves a workgroup
     bool split;            // some group may be cut into pieces
     bool few;              // not by workgroups for 128 rows
   };
@@ -557,6 +557,16 @@ struct Few {
     // with 64 values 1008 workgroups 14.5 for 26.6, 2048 of 2 tiles 17.9 for 13.3, of 16
     // 37.1 for 41.7.
     z.brief = tiles <= 4 * kShortWaves<DT, NB> && all <= (DT != BF16 ? 1024 : NB > 2 ? 640 : tiles > 8 ? 2048 : 1024);
+    // With two waves a workgroup more of them run at a time.  They win with two tiles a
+    // cache as soon as larger ones would wait (33 requests of 100 keys 6.8 for 10.8, 128
+    // 7.7 for 14.7), with eight where those would wait twice (64 of 500 keys 14.8 for 14.6,
+    // 128 18.3 for 23.9), up to one and a half rounds of them (256 of 300 keys 29.4 for
+    // 26.5 by shares), and beyond where heads are small (64 values, 256 of 300 14.3 for
+    // 24.5, 1024 43 for 62; rows of several groups go better by 128 then).
+    const uint64_t at_once = NB <= 2 || (DT != BF16 && NB <= 4) ? 512 : 256, two = (tiles + 1) / 2;
+    const uint64_t most = NB > (DT == BF16 ? 2 : 4) ? 1536 : queries * a.group <= 16 ? 1u << 30 : 2560;
+    z.pairs = tiles <= 8 && all * 7 > at_once * (5 + 2 * two) && all <= most;
+    z.brief = z.brief || z.pairs;
     // Waves of 16 rows take tiles that hold more rows again and again, but there are more
     // of them.  They win with one or two groups a request (64 x 2048 keys, 32 rows 61 for
     // 71, 48 rows 89 for 83), beside FP32 queries with four (64 x 2048 keys, 64 rows 155
@@ -582,7 +592,11 @@ struct Few {
     const FastDiv per_group(a.group);
     const float c = float(double(a.scale) * 1.4426950408889634);
     if (z.brief) {
-      k_attend_short<DT, NB><<<dim3(z.groups, a.c.heads), 64 * kShortWaves<DT, NB>, 0, s>>>(a, per_group, c);
+      const dim3 grid(z.groups, a.c.heads);
+      if (z.pairs)
+        k_attend_short<DT, NB, 2><<<grid, 128, 0, s>>>(a, per_group, c);
+      else
+        k_attend_short<DT, NB, kShortWaves<DT, NB>><<<grid, 64 * kShortWaves<DT, NB>, 0, s>>>(a, per_group, c);
       return hipGetLastError();
     }
     Parts p = {};

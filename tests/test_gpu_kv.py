@@ -874,3 +874,42 @@ def test_the_largest_and_smallest_scales(new):
             # weights alike: sums of 100 within 100 2^-24 of the sum of sizes, a half step of the mean
             mean, size = seen.mean(0), seen.abs().mean(0)
             assert ((out - mean).abs() <= size * 100 * 2.0 ** -23 + mean.abs() * 2.0 ** -8 + 2.0 ** -24 * size).all()
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("dim", [32, 64, 96, 128, 160, 192, 224, 256])
+def test_short_caches_of_many_heads(dim, t):
+    # more groups of rows than workgroups of many waves run at a time, caches of eight tiles at most
+    run_attention([300, 0, 77], None, 800, 400, dim, 16, t, dim)
+    run_attention([300, 40, 0], [40, 40, 0], 192, 96, dim, 16, t, dim)
+    run_attention([129, 500], [7, 20], 384, 96, dim, 64, t, dim, window=60)
+
+
+def test_short_caches_of_many_heads_see_their_own():
+    lens = [100, 45, 200]
+    q, c, table, _ = attend_case(lens, None, 800, 400, 64, 16, "bf16", 8)
+    tb = i32(table.tolist())
+    want = zn.mx_attention(q, c, tb, i32(lens))
+    vs = c.v_scales.view(torch.uint8)
+    vs[table[0][60 // 16], 399, 60 % 16, 1] = 255                  # seen by one request's last heads
+    vs[table[1][45 // 16], :, 45 % 16] = 255                       # behind a length
+    out = zn.mx_attention(q, c, tb, i32(lens))
+    nan = torch.zeros_like(out, dtype=torch.bool)
+    nan[0, 798:, 32:] = True
+    assert torch.equal(out.isnan(), nan) and torch.equal(out[~nan], want[~nan])
+    bad = table.copy()
+    bad[1, 2] = -1
+    out = zn.mx_attention(q, c, i32(bad.tolist()), i32([100, 45, 10 ** 9]))
+    assert out[1:].isnan().all() and torch.equal(out[0].isnan(), nan[0])
+    now = i32(lens)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = zn.mx_attention(q, c, tb, now)
+    for i in range(4):
+        q.normal_()
+        now.copy_(i32([100 - i, 45 + i, 200 - 50 * i]))
+        want = zn.mx_attention(q, c, tb, now)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.isnan(), want.isnan()) and torch.equal(out.nan_to_num(), want.nan_to_num())
