@@ -449,8 +449,7 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * Keys that a query does not see have no effect on it, whatever they hold.
  *   Values of keys and values are taken as stored; products, sums, maxima and
  * exponentials are FP32 (before they meet the values the weights are rounded: beside
- * BF16 queries to 11 bits and 2^-32 of the row's largest, or to 16 bits for few rows a
- * request, beside FP32 to 24), and the result is rounded once.  Weights are at
+ * BF16 queries to 16 bits, beside FP32 to 24), and the result is rounded once.  Weights are at
  * most 1: n keys whose values pass 2^127 / n may give infinities and NaNs.  A
  * scale byte over 252, which the write makes only (255) of infinities and NaNs,
  * is a NaN.
@@ -467,7 +466,18 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * heads at most 2^29.  Needs zn_mx_attention_scratch_bytes() bytes of
  * 16-byte aligned device scratch (ZN_ERR_CAPACITY if it is less; 0 for some
  * sizes, then d_scratch may be NULL); calls that may run at the same time, and
- * graphs that may replay at the same time, need scratch of their own. */
+ * graphs that may replay at the same time, need scratch of their own.
+ *
+ * zn_mx_attention2 -- zn_mx_attention with flags, in the same scratch.
+ * ZN_MX_FAST_WEIGHTS, for ZN_BF16 (ZN_ERR_ARG for ZN_FP32 and for unknown
+ * flags): where requests have many rows (queries times query heads of a key
+ * head) their weights are held in FP16, 11 bits and at worst 2^-32 of the row's
+ * largest, which takes a third of the matrix instructions off.  A result is off
+ * by up to 2^-11 of the sum of softmax |v|, so what cancels can keep few bits.
+ * (Over random keys and values the errors' norm is 3e-5 of the results', whose
+ * own rounding has 1.7e-3.)  Whether a call has many rows goes by its sizes and
+ * max_new; others ignore the flag. */
+enum { ZN_MX_FAST_WEIGHTS = 1 };
 typedef struct zn_mx_attention_args {
   zn_dtype dtype;                       /* of q and out */
   uint32_t heads, batch;
@@ -486,6 +496,8 @@ typedef struct zn_mx_attention_args {
 zn_status zn_mx_attention_scratch_bytes(const zn_mx_cache *cache, const zn_mx_attention_args *args, uint64_t *bytes);
 zn_status zn_mx_attention(const zn_mx_cache *cache, const zn_mx_attention_args *args, void *d_scratch,
                           uint64_t scratch_bytes, hipStream_t stream);
+zn_status zn_mx_attention2(const zn_mx_cache *cache, const zn_mx_attention_args *args, uint32_t flags,
+                           void *d_scratch, uint64_t scratch_bytes, hipStream_t stream);
 
 /* ---- single steps, for parity tests of each stage (asynchronous) ----
  * zn_debug_histograms: order-0 histograms of every coded stream of every

@@ -568,12 +568,14 @@ struct Few {
     z.pairs = tiles <= 8 && all * 7 > at_once * (5 + 2 * two) && all <= most;
     z.brief = z.brief || z.pairs;
     // Waves of 16 rows take tiles that hold more rows again and again, but there are more
-    // of them.  They win with one or two groups a request (64 x 2048 keys, 32 rows 61 for
-    // 71, 48 rows 89 for 83), beside FP32 queries with four (64 x 2048 keys, 64 rows 155
-    // for 211, 128 rows 294 for 227), or where there is little to do: 8 x 2048 keys of 128
-    // rows 43 for 46, of 256 62 for 56.  With few tiles workgroups of 128 rows need no
+    // of them.  They win with up to four groups a request (64 x 2048 keys, 32 rows 59 for
+    // 77, 64 rows 93 for 96, 96 rows 140 for 100; 256 x 1024 keys, 48 rows 166 for 219, 64
+    // rows 220 for 223; FP32 64 x 2048 keys, 64 rows 155 for 211, 128 rows 294 for 227), or
+    // where there is little to do: 8 x 2048 keys of 128 rows 40 for 50, of 256 59 for 58.
+    // (With fast weights the others win from 48 rows on, 80 for 86; the rule is one, so that
+    // the scratch is.)  With few tiles workgroups of 128 rows need no
     // pieces and win (16 x 200 keys of 256 rows 17 for 23).
-    z.few = z.brief || queries * a.group <= (DT == BF16 ? 32 : 64) || (tiles > 8 && all * tiles <= 20480);
+    z.few = z.brief || queries * a.group <= 64 || (tiles > 8 && all * tiles <= 20480);
     // the takers fill the chip once, so that they all run at the same time; no more
     // of them than tiles (one more a group where a window begins inside one)
     const uint64_t n = std::min<uint64_t>(1024 * kResident<DT, NB> / a.c.heads, z.groups * (tiles + 1));

@@ -176,7 +176,7 @@ struct Rows32 {
 };
 
 // The product with the values is one of two.
-//   HALF, beside BF16 queries: weights and values in FP16, one product.  Weights go up
+//   HALF, beside BF16 queries where the caller asks for fast weights: weights and values in FP16, one product.  Weights go up
 // to 2^15 and keep 11 bits down to 2^-14 (beside a largest one of 2^7 or more), the
 // values are held relative to the largest scale of the first tile and are exact normal
 // numbers while the tiles' scales lie within 2^-13 and 2^12 of it.  (Subnormal ones are
@@ -186,8 +186,8 @@ struct Rows32 {
 //   Otherwise weights in BF16 pieces (two beside BF16 queries, three beside FP32),
 // a product each, and values in BF16, exact whatever their scales.
 // The first takes two thirds of the matrix instructions and three quarters of the
-// others: 8192 queries of 32 heads 790 -> 650 us (676 with exact weights for scores
-// past 2^24, 659 with sums that begin with -m).
+// others: 8192 queries of 32 heads 585 us for 750, 64 x 4096 keys of 128 rows 178 for
+// 216.
 template <int DT, int NB, bool HALF>
 __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq, const int32_t *pages, uint32_t head,
                                            uint32_t t, uint32_t end, float c, typename Shape<DT, NB>::Lds &lds,
@@ -414,7 +414,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
   return true;
 }
 
-template <int DT, int NB>
+template <int DT, int NB, bool FAST>
 __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(AttnArgs a, Plan plan, Parts out,
                                                                           FastDiv per_group, float c) {
   constexpr int D = 32 * NB;
@@ -464,7 +464,7 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   uint32_t end = uint32_t(min((it.piece + 1) * it.tiles, uint64_t(rq.tiles)));
   end = r.wg_high > rq.lo ? min(end, (r.wg_high - rq.lo + kTile - 1) / kTile) : 0;
   if (r.wg_low > rq.lo) t = max(t, (r.wg_low - rq.lo) / kTile);
-  if (DT != BF16 || !take_tiles<DT, NB, DT == BF16>(a, rq, pages, head, t, end, c, lds, r)) {
+  if (!FAST || !take_tiles<DT, NB, FAST>(a, rq, pages, head, t, end, c, lds, r)) {
     __syncthreads();
     take_tiles<DT, NB, false>(a, rq, pages, head, t, end, c, lds, r);
   }
@@ -573,7 +573,11 @@ struct Tall {
     if (z.slots) p = parts(a.scratch, a.batch, a.c.heads, z.slots, kRows);
     const FastDiv per_group(a.group);
     const float c = float(double(a.scale) * 1.4426950408889634);
-    k_attend_tall<DT, NB><<<z.items * a.c.heads, kThreads, 0, s>>>(a, z.plan, p, per_group, c);
+    const dim3 grid(z.items * a.c.heads);
+    if (DT == BF16 && a.fast_weights)
+      k_attend_tall<DT, NB, DT == BF16><<<grid, kThreads, 0, s>>>(a, z.plan, p, per_group, c);
+    else
+      k_attend_tall<DT, NB, false><<<grid, kThreads, 0, s>>>(a, z.plan, p, per_group, c);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !z.slots) return e;
     const uint32_t shares = (kRows * NB * 8 + 255) / 256 + 1, most = 4096 / a.c.heads + 1;

@@ -60,6 +60,7 @@ struct AttnArgs {
   float scale;
   uint32_t causal, window;
   uint32_t max_new;                            // 0: not known
+  bool fast_weights;                           // beside BF16 queries
   uint8_t *scratch;
 };
 // Bytes of scratch, by the sizes alone.

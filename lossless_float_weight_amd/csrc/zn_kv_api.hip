@@ -201,7 +201,13 @@ extern "C" zn_status zn_mx_attention_scratch_bytes(const zn_mx_cache *cache, con
 
 extern "C" zn_status zn_mx_attention(const zn_mx_cache *cache, const zn_mx_attention_args *args, void *d_scratch,
                                      uint64_t scratch_bytes, hipStream_t stream) {
+  return zn_mx_attention2(cache, args, 0, d_scratch, scratch_bytes, stream);
+}
+
+extern "C" zn_status zn_mx_attention2(const zn_mx_cache *cache, const zn_mx_attention_args *args, uint32_t flags,
+                                      void *d_scratch, uint64_t scratch_bytes, hipStream_t stream) {
   AttnArgs a;
+  if (flags & ~uint32_t(ZN_MX_FAST_WEIGHTS) || (flags && args && args->dtype != ZN_BF16)) return ZN_ERR_ARG;
   if (!attention_of(cache, args, args && args->tokens && args->batch, &a)) return ZN_ERR_ARG;
   if (a.tokens == 0 || a.batch == 0) return ZN_OK;
   if (!at(a.q, args->dtype) || !at(a.out, args->dtype) || (a.lse && !at4(a.lse))) return ZN_ERR_ARG;
@@ -210,5 +216,6 @@ extern "C" zn_status zn_mx_attention(const zn_mx_cache *cache, const zn_mx_atten
   if (need && !at16(d_scratch)) return ZN_ERR_ARG;
   if (scratch_bytes < need) return ZN_ERR_CAPACITY;
   a.scratch = static_cast<uint8_t *>(d_scratch);
+  a.fast_weights = flags & ZN_MX_FAST_WEIGHTS;
   return done(launch_attention(args->dtype, a, stream));
 }

@@ -86,6 +86,7 @@ def lib() -> C.CDLL:
         L.zn_mx_kv_read.argtypes = [P, P, U64, I, P, P, P]
         L.zn_mx_attention_scratch_bytes.argtypes = [P, P, PU64]
         L.zn_mx_attention.argtypes = [P, P, P, U64, P]
+        L.zn_mx_attention2.argtypes = [P, P, U32, P, U64, P]
         for f in ("zn_setup", "zn_setup_transfer", "zn_plan_from_container", "zn_header_info",
                   "zn_tableset_info", "zn_compress_bound",
                   "zn_scratch_bytes", "zn_compress", "zn_decompress", "zn_decompress_noalloc",
@@ -95,7 +96,7 @@ def lib() -> C.CDLL:
                   "zn_debug_kernel_events", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
                   "zn_mx_matmul_scratch_bytes", "zn_mx_matmul", "zn_mx_matmul2", "zn_kv_extend",
                   "zn_kv_release", "zn_mx_kv_write", "zn_mx_kv_read", "zn_mx_attention_scratch_bytes",
-                  "zn_mx_attention"):
+                  "zn_mx_attention", "zn_mx_attention2"):
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
@@ -413,6 +414,7 @@ def decompress_noalloc(ts: Tableset, blob: torch.Tensor, outs: Sequence[torch.Te
 # every 32 values; the last axis is the row, filled up to whole blocks.
 MX_BLOCK = 32
 MX_FAST_SUMS = 1
+MX_FAST_WEIGHTS = 1
 _MX_FMT = {torch.float8_e4m3fn: FP8_E4M3, torch.uint8: FP4X2_E2M1}
 _MX_PLAIN = {torch.bfloat16: BF16, torch.float32: FP32}
 _MX_SCALE = (torch.float8_e8m0fnu, torch.uint8)
@@ -938,20 +940,24 @@ def _attention_scratch(dt, heads, batch, tokens, max_new, width, with_starts, wi
 def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor | None = None,
                  max_new: int = 0, causal: bool = True, window: int = 0, scale: float | None = None,
                  out: torch.Tensor | None = None, lse: bool | torch.Tensor = False,
-                 scratch: torch.Tensor | None = None, stream=None):
+                 scratch: torch.Tensor | None = None, stream=None, fast_weights: bool = False):
     """zn_mx_attention: queries q [tokens, heads, head_dim] (BF16 or FP32) over
     the cache.  Request b has lens[b] keys in the pages of table[b]; its queries
     are q[starts[b]:starts[b + 1]], the last of them at position lens[b] - 1, or
     the one row q[b] without starts.  scale is 1 / sqrt(head_dim) when None.
     max_new: the most queries of one request, if known; it only helps to choose
     kernels.  With lse (True, or an FP32 tensor [tokens, heads]) the result is
-    (out, logarithm of the sums of the weights).  No gradient: a q that requires
+    (out, logarithm of the sums of the weights).  fast_weights (zn_mx_attention2
+    with ZN_MX_FAST_WEIGHTS, BF16 only) holds the weights of requests with many
+    rows in 11 bits: faster, with fewer bits.  No gradient: a q that requires
     one is refused while gradients are recorded."""
     where = "mx_attention"
     given = lse if isinstance(lse, torch.Tensor) else None
     if q.requires_grad or out is not None or given is not None:
         _mx_no_grad(where, q=q, out=out, lse=given)
     dt = _mx_plain(where, "q", q.dtype)
+    if fast_weights and dt != BF16:
+        raise ZnError(-1, f"{where}: fast_weights is for bfloat16 queries, not {q.dtype}")
     dev = _mx_device(where, stream, q, table, lens, starts, out, given, scratch, *cache)
     c, lay = _kv_cache(where, cache)
     if q.dim() != 3 or q.shape[2] != lay[3] or q.shape[1] == 0 or q.shape[1] % lay[2]:
@@ -996,8 +1002,8 @@ def mx_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor
     g = _ATTENTION_ARGS.pack(dt, heads, batch, tokens, max_new, q.data_ptr(), qt, qh, out.data_ptr(), ot, oh,
                              given.data_ptr() if given is not None else 0, table.data_ptr(), lens.data_ptr(),
                              starts.data_ptr() if starts is not None else 0, stride, width, scale, bool(causal), window)
-    _mx_call(where, dev, stream, lib().zn_mx_attention, c, g, scratch.data_ptr() if scratch is not None else None,
-             scratch.numel() if scratch is not None else 0)
+    _mx_call(where, dev, stream, lib().zn_mx_attention2, c, g, MX_FAST_WEIGHTS if fast_weights else 0,
+             scratch.data_ptr() if scratch is not None else None, scratch.numel() if scratch is not None else 0)
     if stream is not None:
         _mx_use(stream, q, table, lens, starts, out, given, scratch, *cache)
     return out if given is None else (out, given)

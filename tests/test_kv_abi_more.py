@@ -1,0 +1,32 @@
+"""Refusals of the key-value cache's calls that take flags, on the CPU."""
+import os
+
+import pytest
+import torch
+
+from lossless_float_weight_amd import zn
+from test_kv_abi import ARG, ATTEND, CAPACITY, FP32, LIB, P, _raises, cache, i32
+
+pytestmark = pytest.mark.skipif(not os.path.exists(LIB), reason="libzn.so not built")
+
+
+def attend2(flags, scratch=None, nbytes=0, **change):
+    return zn.lib().zn_mx_attention2(cache(), zn._ATTENTION_ARGS.pack(*dict(ATTEND, **change).values()), flags, scratch, nbytes, None)
+
+
+def test_attention_flags():
+    assert attend2(0) == 0 and attend2(zn.MX_FAST_WEIGHTS) == 0             # no queries: nothing is launched
+    assert attend2(0, dtype=FP32) == 0
+    for flags, bad in ((2, {}), (3, {}), (1 << 31, {}), (1, dict(dtype=FP32)), (1, dict(heads=3)), (1, dict(window=4, causal=0)),
+                       (1, dict(dtype=9))):
+        assert attend2(flags, **bad) == ARG
+    assert zn.lib().zn_mx_attention2(cache(), None, 1, None, 0, None) == ARG
+    size = dict(batch=8, tokens=4096, starts=P, width=4096, ts=4096)
+    assert attend2(1, P, 16, **size) == CAPACITY and attend2(1, **size) == ARG
+
+
+def test_binding_refuses_fast_weights_beside_fp32():
+    c = zn.mx_kv_cache(6, 2, 16, 64, device="cpu")
+    q = torch.zeros(5, 4, 64)
+    _raises(zn.mx_attention, q, c, i32(5, 4), i32(5), fast_weights=True, match="fast_weights is for bfloat16")
+    _raises(zn.mx_attention, q.bfloat16(), c, i32(5, 4), i32(5), fast_weights=True, match="not on a CUDA device")
