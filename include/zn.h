@@ -504,11 +504,17 @@ zn_status zn_mx_attention2(const zn_mx_cache *cache, const zn_mx_attention_args 
  *   chunk of the plan: d_hist[n_chunks][n_coded][256] u32.
  * zn_debug_code_lengths: code lengths of n histograms (d_hist[n][256] u64)
  *   by the device package-merge; group_rule != 0 applies the group-table
- *   rule for single-symbol histograms; d_len[n][256]. */
+ *   rule for single-symbol histograms; d_len[n][256].
+ * zn_debug_attention_kernel: which kernel a zn_mx_attention call of these
+ *   sizes goes to: 0 one workgroup of many waves for 16 rows of a request, 1
+ *   one of two waves, 2 waves of 16 rows with equal shares of all keys, 3
+ *   workgroups of 128 rows; -1 where there is nothing to launch.  Reads no
+ *   array; a test of a kernel asks it whether its sizes still reach it. */
 zn_status zn_debug_histograms(const zn_tableset *ts, const void *const *d_in_ptrs,
                               uint32_t *d_hist, hipStream_t stream);
 zn_status zn_debug_code_lengths(const uint64_t *d_hist, int n, int alphabet, int group_rule,
                                 uint8_t *d_len, hipStream_t stream);
+zn_status zn_debug_attention_kernel(const zn_mx_cache *cache, const zn_mx_attention_args *args, int *kernel);
 
 /* ---- kernel timing, for measurement tools ----
  * zn_debug_kernel_events: from now on, every launch of the named kernel

@@ -625,6 +625,13 @@ uint64_t attention_scratch(int dtype, const AttnArgs &a) {
   return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.sizes(a).few ? k.scratch(a) : attention_tall_scratch(dtype, a); });
 }
 
+int attention_kernel(int dtype, const AttnArgs &a) {
+  return by_kind<Few>(dtype, a.c.blocks, [&](auto k) {
+    const auto z = k.sizes(a);
+    return z.pairs ? 1 : z.brief ? 0 : z.few ? 2 : 3;
+  });
+}
+
 hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s) {
   return by_kind<Few>(dtype, a.c.blocks, [&](auto k) { return k.sizes(a).few ? k.run(a, s) : launch_attention_tall(dtype, a, s); });
 }

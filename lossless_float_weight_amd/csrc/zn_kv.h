@@ -65,6 +65,8 @@ struct AttnArgs {
 };
 // Bytes of scratch, by the sizes alone.
 uint64_t attention_scratch(int dtype, const AttnArgs &a);
+// 0, 1: one launch, with many waves a workgroup or two; 2: waves of 16 rows; 3: workgroups of 128.
+int attention_kernel(int dtype, const AttnArgs &a);
 hipError_t launch_attention(int dtype, const AttnArgs &a, hipStream_t s);
 
 // ------------------------------------------------------------ device side --

@@ -199,6 +199,13 @@ extern "C" zn_status zn_mx_attention_scratch_bytes(const zn_mx_cache *cache, con
   return ZN_OK;
 }
 
+extern "C" zn_status zn_debug_attention_kernel(const zn_mx_cache *cache, const zn_mx_attention_args *args, int *kernel) {
+  AttnArgs a;
+  if (!kernel || !attention_of(cache, args, false, &a)) return ZN_ERR_ARG;
+  *kernel = a.tokens && a.batch ? attention_kernel(args->dtype, a) : -1;
+  return ZN_OK;
+}
+
 extern "C" zn_status zn_mx_attention(const zn_mx_cache *cache, const zn_mx_attention_args *args, void *d_scratch,
                                      uint64_t scratch_bytes, hipStream_t stream) {
   return zn_mx_attention2(cache, args, 0, d_scratch, scratch_bytes, stream);

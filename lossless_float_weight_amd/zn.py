@@ -74,6 +74,7 @@ def lib() -> C.CDLL:
         L.zn_debug_histograms.argtypes = [P, P, P, P]
         L.zn_debug_code_lengths.argtypes = [P, I, I, I, P, P]
         L.zn_debug_kernel_events.argtypes = [C.c_char_p, P, P]
+        L.zn_debug_attention_kernel.argtypes = [P, P, C.POINTER(I)]
         L.zn_mx_quantize.argtypes = [I, P, U64, U64, U64, I, P, P, P]
         L.zn_mx_dequantize.argtypes = [I, P, P, U64, U64, I, P, U64, P]
         L.zn_mx_rms_norm.argtypes = [I, P, U64, P, U64, P, C.c_float, U64, U64, P, U64, I, P, P, P]
@@ -93,7 +94,7 @@ def lib() -> C.CDLL:
                   "zn_tableset_save",
                   "zn_tableset_load", "zn_tableset_lengths", "zn_tableset_map",
                   "zn_tableset_cost_history", "zn_debug_histograms", "zn_debug_code_lengths",
-                  "zn_debug_kernel_events", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
+                  "zn_debug_kernel_events", "zn_debug_attention_kernel", "zn_mx_quantize", "zn_mx_dequantize", "zn_mx_rms_norm",
                   "zn_mx_matmul_scratch_bytes", "zn_mx_matmul", "zn_mx_matmul2", "zn_kv_extend",
                   "zn_kv_release", "zn_mx_kv_write", "zn_mx_kv_read", "zn_mx_attention_scratch_bytes",
                   "zn_mx_attention", "zn_mx_attention2"):
@@ -1030,6 +1031,24 @@ def debug_code_lengths(hist: torch.Tensor, alphabet: int = 256, group_rule: bool
                                        _stream(stream)), "code_lengths")
     torch.cuda.synchronize()
     return out
+
+
+ATTENTION_KERNELS = {-1: "none", 0: "short", 1: "short pairs", 2: "few rows", 3: "many rows"}
+
+
+def debug_attention_kernel(q: torch.Tensor, cache, table: torch.Tensor, starts: torch.Tensor | None = None,
+                           max_new: int = 0, window: int = 0) -> str:
+    """zn_debug_attention_kernel: the kernel (of ATTENTION_KERNELS) that an
+    mx_attention call of these shapes goes to.  The tensors may lie anywhere."""
+    where = "debug_attention_kernel"
+    c, lay = _kv_cache(where, cache)
+    tokens, heads, dim = q.shape
+    batch, width = table.shape
+    g = _ATTENTION_ARGS.pack(_mx_plain(where, "q", q.dtype), heads, batch, tokens, min(max_new, tokens), 0, 0, 0, 0, heads * dim,
+                             dim, 0, 0, 0, starts is not None, width, width, 1.0, 1, window)
+    got = C.c_int()
+    _check(lib().zn_debug_attention_kernel(c, g, C.byref(got)), where)
+    return ATTENTION_KERNELS[got.value]
 
 
 def debug_kernel_events(kernel: str, before=None, after=None) -> None:

@@ -1,4 +1,5 @@
-"""Refusals of the key-value cache's calls that take flags, on the CPU."""
+"""Refusals of the key-value cache's calls that take flags, and which kernel takes a call, on the CPU."""
+import ctypes
 import os
 
 import pytest
@@ -30,3 +31,24 @@ def test_binding_refuses_fast_weights_beside_fp32():
     q = torch.zeros(5, 4, 64)
     _raises(zn.mx_attention, q, c, i32(5, 4), i32(5), fast_weights=True, match="fast_weights is for bfloat16")
     _raises(zn.mx_attention, q.bfloat16(), c, i32(5, 4), i32(5), fast_weights=True, match="not on a CUDA device")
+
+
+def kernel_of(batch, width, tokens=None, heads=4, kv_heads=2, dim=64, dtype=torch.bfloat16, page=16, **kw):
+    c = zn.mx_kv_cache(1, kv_heads, page, dim, device="cpu")
+    starts = None if tokens is None else i32(batch + 1)
+    # (no memory behind the queries' and the table's shapes)
+    q = torch.zeros(1, 1, 1, dtype=dtype).expand(batch if tokens is None else tokens, heads, dim)
+    return zn.debug_attention_kernel(q, c, i32(1, 1).expand(batch, width), starts, **kw)
+
+
+def test_which_kernel_takes_a_call():
+    assert kernel_of(0, 8) == "none" and kernel_of(3, 8, tokens=0) == "none"
+    for dtype in (torch.bfloat16, torch.float32):
+        assert kernel_of(1, 64, dtype=dtype) == "short" and kernel_of(600, 8, dtype=dtype) == "short pairs"
+        assert kernel_of(1, 4096, dtype=dtype) == "few rows"
+        assert kernel_of(4, 65536, tokens=1000, max_new=250, dtype=dtype) == "many rows"
+    L, b = zn.lib(), ctypes.c_int()
+    g = zn._ATTENTION_ARGS.pack(*ATTEND.values())
+    assert L.zn_debug_attention_kernel(cache(), g, None) == ARG
+    assert L.zn_debug_attention_kernel(cache(), None, ctypes.byref(b)) == ARG
+    assert L.zn_debug_attention_kernel(cache(), zn._ATTENTION_ARGS.pack(*dict(ATTEND, heads=3).values()), ctypes.byref(b)) == ARG
