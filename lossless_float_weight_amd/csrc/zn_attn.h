@@ -38,8 +38,16 @@ __device__ __forceinline__ float scale_of(uint32_t s) {
   return __uint_as_float(s > 252u ? 0x7FC00000u : s << 23);
 }
 
+// x held to BF16's finite values.  (What an infinity or a NaN loses here lies in its
+// rest, which stays infinite or NaN.)
+__device__ __forceinline__ float bf16_range(float x) {
+  constexpr float kMost = 0x1.fep127f;
+  return fminf(fmaxf(x, -kMost), kMost);
+}
+
 // Eight FP32 values as N BF16 pieces whose sum they are (up to 2^-(8 N) of them).
-template <int N>
+// WIDE: values up to FP32's largest, whose first piece would round to infinity.
+template <int N, bool WIDE = false>
 __device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&out)[N]) {
   float rest[8];
 #pragma unroll
@@ -51,7 +59,8 @@ __device__ __forceinline__ void pieces(const float (&x)[8], bf16x8 (&out)[N]) {
       bf16x8 all;
     } o;
 #pragma unroll
-    for (int i = 0; i < 4; i++) o.w[i] = f32_bf16x2(rest[2 * i], rest[2 * i + 1]);
+    for (int i = 0; i < 4; i++) o.w[i] = WIDE && n == 0 ? f32_bf16x2(bf16_range(rest[2 * i]), bf16_range(rest[2 * i + 1]))
+                                                        : f32_bf16x2(rest[2 * i], rest[2 * i + 1]);
     out[n] = o.all;
     if (n + 1 < N) {
 #pragma unroll
@@ -142,7 +151,7 @@ __device__ __forceinline__ void take_query8(const uint8_t *p, bool live, bf16x8 
   } else {
     float x[8] = {};
     if (live) take_row8<DT>(p, x);
-    pieces<N>(x, out);
+    pieces<N, true>(x, out);
   }
 }
 
