@@ -11,11 +11,9 @@
 // by all four waves, into one of two places in LDS while the other is used: one
 // barrier a tile.
 //
-// A product's sums begin with -m instead of 0, so that no score needs a subtraction
-// of its own (a prompt of 8192 queries, 32 heads: 678 -> 659 us).  That prompt runs at
-// 0.83 PFLOP/s: the matrix units are busy 39% of the cycles and the vector units 51%
-// (a fifth of that exponentials, a fifth conversions), and the two run beside each
-// other little: two waves, one of each kind, take 0.83 of the sum of their times.
+// A prompt of 8192 queries, 32 heads, takes 741 us, 0.74 PFLOP/s.  Matrix and vector
+// instructions run beside each other little: two waves, one of each kind, take 0.83 of
+// the sum of their times.
 #include <algorithm>
 
 #include "zn_attn.h"
@@ -143,7 +141,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
 }
 
 template <int DT, int NB>
-constexpr int kResident = DT == BF16 ? NB <= 2 ? 3 : NB <= 4 ? 2 : 1 : NB <= 2 ? 2 : 1;   // waves a SIMD
+constexpr int kResident = DT == BF16 ? NB == 1 ? 4 : NB == 2 ? 3 : NB <= 4 ? 2 : 1 : NB <= 2 ? 2 : 1;   // waves a SIMD
 
 template <int DT, int NB>
 struct Shape {
@@ -313,7 +311,6 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
     put(key0, t & 1, 0);
   }
   __syncthreads();
-  f32x16 less = {};   // -m, 0 before the first key
   for (uint32_t flag = 0; t < end; t++) {
     const uint32_t next = flag == 2 ? 0 : flag + 1;
     if (threadIdx.x == 0) lds.odd[next == 2 ? 0 : next + 1] = 0;   // read a tile ago, written in the next one
@@ -326,8 +323,10 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
       ask_pages(key0 + 2 * kTile);
     }
     if (key0 < r.high && key0 + kTile > r.low) {   // some row of this wave sees the tile
-      // scores less m, which the sums begin with
-      f32x16 s[2] = {less, less};
+      // Scores by themselves: sums that begin with -m would save the subtraction below (no
+      // time that could be measured; 2% with fast weights), but round where an old m is
+      // large: a score of 0 after a first tile of scores around -768 was off by 2^-15.
+      f32x16 s[2] = {};
       const uint8_t *keys = lds.k[buf] + n * S::kKeyPitch + 16 * h;
 #pragma unroll
       for (int st = 0; st < S::kSteps; st++)
@@ -351,24 +350,15 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
 #pragma unroll
         for (int i = 0; i < 16; i++) top = fmaxf(top, s[g][i]);
       top = max_h(top);
-      if (__any(r.m == -__builtin_inff() ? top > -__builtin_inff() : top * c > kRise)) {
-        const bool none = r.m == -__builtin_inff();
-        const float up = none || top > 0.0f ? top : 0.0f;
-        const float f = none ? 0.0f : __builtin_amdgcn_exp2f(-up * c);
-        if (up > -__builtin_inff()) {
-          r.l *= f;
-          r.m = none ? up : r.m + up;
-        }
+      if (__any((top - r.m) * c > kRise)) {
+        const float up = fmaxf(top, r.m);
+        const float f = up > r.m ? __builtin_amdgcn_exp2f((r.m - up) * c) : 1.0f;
+        r.l *= f;
 #pragma unroll
         for (int d = 0; d < NB; d++) r.o[d] *= f;
-#pragma unroll
-        for (int i = 0; i < 16; i++) {
-          const float by = up > -__builtin_inff() ? up : 0.0f;
-          s[0][i] -= by;
-          s[1][i] -= by;
-          less[i] -= by;
-        }
+        r.m = up;
       }
+      const float m = r.m == -__builtin_inff() ? 0.0f : r.m;
       // 16 keys of 32 values at a time; the weights of the next 16 keys are made while
       // the matrix unit takes these
       const uint8_t *from = lds.v[buf] + (4 * h + (lane & 15) / 4) * S::kPitch + (lane >> 4 & 1) * 32 + (lane & 3) * 8;
@@ -381,7 +371,7 @@ __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq,
         float x[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i], c, kTop - kRise));
+          x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g & 1) + i] - m, c, kTop - kRise));
           r.l += x[i];
         }
         if constexpr (HALF)

@@ -137,3 +137,15 @@ def test_fast_weights(test, args, monkeypatch):
     attention = gpu.by_sizes("many")
     monkeypatch.setattr(zn, "mx_attention", lambda *a, **kw: attention(*a, **dict(kw, fast_weights=True)))
     test(*args)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t,bits", [("bf16", 17), ("fp32", 24), ("bf16", 11)])
+@pytest.mark.parametrize("kind", ["short", "few", "many"])
+@pytest.mark.parametrize("n,at_a,at_b", [(200, 199, 64), (200, 64, 199), (320, 130, 300), (256, 255, 128)])
+def test_keys_far_below_leave_no_rounding(n, at_a, at_b, kind, t, bits):
+    # tiles whose scores are all around -768 come first: what follows them is not rounded at their size
+    d, out = run_pairs(t, kind, n, 64, at_a, at_b, **(dict(fast_weights=True) if bits == 11 else {}))
+    want = np.tanh(d * np.log(2) / 2)[:, None, None]
+    worst = (np.abs(out - want) / bound(d[:, None, None], want, t, bits)).max()
+    assert worst <= 1
