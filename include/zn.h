@@ -448,11 +448,12 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * zeros and -infinity.  Rows behind the last request are left as they were.
  * Keys that a query does not see have no effect on it, whatever they hold.
  *   Values of keys and values are taken as stored; products, sums, maxima and
- * exponentials are FP32 (before they meet the values the weights are rounded: beside
- * BF16 queries to 16 bits, beside FP32 to 24), and the result is rounded once.  Weights are at
- * most 1: n keys whose values pass 2^127 / n may give infinities and NaNs.  A
- * scale byte over 252, which the write makes only (255) of infinities and NaNs,
- * is a NaN.
+ * exponentials are FP32 (before they meet the values the weights are rounded:
+ * beside BF16 queries to 16 bits, beside FP32 to 24), and the result is rounded
+ * once.  Weights are at most 1: n keys whose values pass 2^127 / n may give
+ * infinities and NaNs.  Scores q . k past FP32's range are infinite: a query with
+ * one of +infinity, or with -infinity alone, gives NaNs.  A scale byte over 252,
+ * which the write makes only (255) of infinities and NaNs, is a NaN.
  *   Bad arrays: starts are clamped to [0, tokens], and a request that ends before
  * it starts has no queries (rows that starts out of order name twice, or any row
  * beside them, may be left as they were); a length that passes the table's width

@@ -204,11 +204,14 @@ __device__ __forceinline__ float log_sum(float m, float l, float scale) {
   return l == 0.0f ? -__builtin_inff() : __builtin_fmaf(m, scale, (kRise + __builtin_log2f(l)) * 0.6931471805599453f);
 }
 
-// A row's result from its sums over all keys.
+// A row's result from its sums over all keys.  A weight of the largest score is at least
+// 2^-8, so a row without weights that sees keys has scores of -infinity alone: a NaN, as
+// infinities less each other are.
 template <int DT>
 __device__ __forceinline__ void put_row(const AttnArgs &a, const Request &rq, uint32_t token, uint32_t qh, uint32_t col,
                                         f32x4 o, float m, float l) {
   const uint64_t y = rq.start + token;
+  if (l == 0.0f && span(a, rq, token, true).count) l = __builtin_nanf("");
   store4<DT>(a.out + (y * a.out_token + qh * a.out_head + col) * esize(DT), o * over(l));
   if (a.lse && col == 0) a.lse[y * a.heads + qh] = log_sum(m, l, a.scale);
 }

@@ -469,6 +469,7 @@ __global__ __launch_bounds__(kThreads, (kResident<DT, NB>)) void k_attend_tall(A
   const int unit = int(r.unit) - 127;
   if (it.pieces == 1) {
     const uint64_t y = rq.start + token;
+    if (l == 0.0f && sees.count) l = __builtin_nanf("");   // as in put_row
     const float f = over(l);
     uint8_t *p = a.out + (y * a.out_token + qh * a.out_head + 4 * h) * esize(DT);
 #pragma unroll

@@ -58,3 +58,49 @@ def test_infinite_and_nan_queries_stay_by_themselves(kind, t):
     gone[2, 1] = gone[97, 0] = gone[40, 1] = True
     out = call(kind, q, c, table, lens, starts)
     assert torch.equal(out[~gone], want[~gone]) and out[gone].isnan().all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [float("inf"), 3e38])
+def test_scores_of_minus_infinity_alone_are_nan(kind, t, value):
+    # every key is negative where the query is infinite, or so large that the product passes FP32's range
+    q, c, table, lens, starts = case_for(kind, t=t)
+    want, want_lse = call(kind, q, c, table, lens, starts, lse=True)
+    c.k[..., 0] = 0xFF                                             # -6, -6
+    c.k_scales.view(torch.uint8)[..., 0] = 130
+    want, want_lse = call(kind, q, c, table, lens, starts, lse=True)
+    gone = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    for row, head in ((0, 0), (3, 1), (89, 0), (90, 1), (134, 0)):
+        q[row, head, :2] = value
+        gone[row, head] = True
+    out, lse = call(kind, q, c, table, lens, starts, lse=True)
+    assert out[gone].isnan().all() and lse[gone].isnan().all()
+    assert torch.equal(out[~gone], want[~gone]) and torch.equal(lse[~gone], want_lse[~gone])
+    # a key that is not: it has all the weight
+    keep = table[0][5 // 16], 5 % 16
+    c.k[keep[0], :, keep[1], 0] = 0
+    out, lse = call(kind, q, c, table, lens, starts, lse=True)
+    rows = torch.tensor([3, 89], device="cuda") if value < 1e39 else torch.tensor([], dtype=torch.long, device="cuda")
+    for row in rows.tolist():
+        head = 1 if row == 3 else 0
+        v = zn.mx_kv_read(c, i32([int(keep[0]) * 16 + keep[1]]), dtype=torch.float32)[1][0]
+        assert torch.equal(out[row, head].float(), v[head * v.shape[0] // q.shape[1]].to(q.dtype).float())
+        assert lse[row, head].isfinite()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_queries_that_see_nothing_stay_zeros(kind, t):
+    # more queries than keys, an empty request, and a piece or a wave whose tiles a row does not see
+    q, c, table, lens, starts = case_for(kind, lens=(70, 0, 300), new=(90, 40, 60), t=t)
+    # (a window leaves few tiles, which the other kernels take)
+    masks = {"few rows": (dict(window=2100),), "many rows": ()}.get(kind, (dict(window=3),))
+    for kw in (dict(), *masks, dict(causal=False)):
+        out, lse = call(kind, q, c, table, lens, starts, lse=True, **kw)
+        nothing = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+        nothing[90:130] = True
+        nothing[:20] = kw.get("causal", True)
+        assert (out[nothing] == 0).all() and (lse[nothing] == -torch.inf).all()
+        assert lse[~nothing].isfinite().all()
+        check_attention(q, c, table, lens, starts, 16, out, lse, **kw)
