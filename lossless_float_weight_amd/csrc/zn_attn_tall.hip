@@ -113,9 +113,11 @@ __device__ __forceinline__ bool find_item(const AttnArgs &a, const Plan &plan, u
         const uint64_t g = groups_of(a, r, kRows), p = (max(r.tiles, 1u) + piece - 1) / piece;
         if (p > 1) at += g * p;
       }
+    // starts out of order can make more items than there are workgroups: pieces are
+    // missing then, and none are joined
     if (lane == 63) {
       *each = piece;
-      *whole = parts_upto;
+      *whole = all > gridDim.x / a.c.heads ? 0 : parts_upto;
     }
   }
   if (number >= all) return false;

@@ -104,3 +104,23 @@ def test_queries_that_see_nothing_stay_zeros(kind, t):
         assert (out[nothing] == 0).all() and (lse[nothing] == -torch.inf).all()
         assert lse[~nothing].isfinite().all()
         check_attention(q, c, table, lens, starts, 16, out, lse, **kw)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_starts_out_of_order_leave_rows_or_answer_them(kind, t):
+    # requests that all name the same rows and keys, each followed by one that ends before it starts: far more groups of
+    # rows than the sizes let the host expect, so that workgroups run out, of pieces among others
+    n, lens, heads, kv_heads, page = (512, 3000, 16, 8, 64) if kind == "many rows" else (64, 200, 4, 2, 64)
+    if kind == "short pairs":
+        heads, kv_heads = 600, 300
+    times = 7 if t == "fp32" else 12
+    q, c, table, _ = attend_case([lens], [n], heads, kv_heads, 32, page, t, 3)
+    all_lens, starts = [lens] * (2 * times), [0, n] * times + [0]
+    scratch = torch.full((1 << 24,), 1e30, device="cuda").view(torch.uint8)      # no piece has such numbers
+    out, lse = torch.full_like(q, 7.0), torch.full(q.shape[:2], 7.0, device="cuda")
+    call(kind, q, c, np.repeat(table, 2 * times, 0), all_lens, starts, out=out, lse=lse, scratch=scratch)
+    left = (out == 7).all(-1) & (lse == 7)
+    want, want_lse = zn.mx_attention(q, c, i32(table.tolist()), i32([lens]), i32([0, n]), lse=True)
+    got, got_lse = torch.where(left[..., None], want, out), torch.where(left, want_lse, lse)
+    check_attention(q, c, table, [lens], [0, n], page, got, got_lse)
