@@ -565,7 +565,8 @@ struct Few {
     // 24.5, 1024 43 for 62; rows of several groups go better by 128 then).
     const uint64_t at_once = NB <= 2 || (DT != BF16 && NB <= 4) ? 512 : 256, two = (tiles + 1) / 2;
     const uint64_t most = NB > (DT == BF16 ? 2 : 4) ? 1536 : queries * a.group <= 16 ? 1u << 30 : 2560;
-    z.pairs = tiles <= 8 && all * 7 > at_once * (5 + 2 * two) && all <= most;
+    // (queries is what the caller says: the grid's 2^32 threads hold whatever it is)
+    z.pairs = tiles <= 8 && all * 7 > at_once * (5 + 2 * two) && all <= most && z.groups <= 1u << 24;
     z.brief = z.brief || z.pairs;
     // Waves of 16 rows take tiles that hold more rows again and again, but there are more
     // of them.  They win with up to four groups a request (64 x 2048 keys, 32 rows 59 for

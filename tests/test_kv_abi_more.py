@@ -52,3 +52,11 @@ def test_which_kernel_takes_a_call():
     assert L.zn_debug_attention_kernel(cache(), g, None) == ARG
     assert L.zn_debug_attention_kernel(cache(), None, ctypes.byref(b)) == ARG
     assert L.zn_debug_attention_kernel(cache(), zn._ATTENTION_ARGS.pack(*dict(ATTEND, heads=3).values()), ctypes.byref(b)) == ARG
+
+
+def test_a_wrong_hint_makes_no_grid_too_large():
+    # 2^25 groups of 16 rows: with two waves each more than the 2^32 threads of a grid
+    for dtype, dim in ((torch.bfloat16, 32), (torch.bfloat16, 64), (torch.float32, 128)):
+        size = dict(tokens=1 << 29, heads=1, kv_heads=1, dim=dim, dtype=dtype)
+        assert kernel_of(8192, 8, max_new=1, **size) != "short pairs"
+        assert kernel_of(8192, 8, max_new=1, **dict(size, tokens=1 << 20)) == "short pairs"
