@@ -514,7 +514,9 @@ __global__ __launch_bounds__(256) void k_join(AttnArgs a, Parts in, FastDiv per_
   const uint32_t rows = min(16u, rq.n * a.group - group * 16), end = min(first + most, rows);
   const uint64_t f = at / each, pieces = (at + max(rq.tiles, 1u) - 1) / each - f + 1;
   if (pieces <= 1) return;
-  if (pieces > in.slots || 2 * f > in.slots - pieces) return;   // starts out of order: not all tiles had a taker
+  // the last piece is taker f + pieces - 1's; `each` being all tiles over the takers, rounded
+  // up, that is one of them as long as the arrays hold what the first launch saw
+  if (f + pieces > in.slots / 2) return;
   const uint32_t count = uint32_t(pieces);
   const uint64_t p0 = uint64_t(head) * in.slots + 2 * f;
   uint32_t least = 1;
