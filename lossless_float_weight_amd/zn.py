@@ -913,7 +913,7 @@ def mx_kv_read(cache, slots: torch.Tensor, dtype=torch.bfloat16, out=None, strea
     _kv_ints(where, "slots", slots, (tokens,))
     if out is None:
         _mx_plain(where, "dtype", dtype)
-        out = _mx_new(dtype, dev, stream, 2, tokens, heads, dim).unbind(0)
+        out = _mx_new(dtype, dev, stream, tokens, heads, dim), _mx_new(dtype, dev, stream, tokens, heads, dim)
     else:
         k, v = out = tuple(out)
         _mx_no_grad(where, k=k, v=v)
