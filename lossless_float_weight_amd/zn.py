@@ -887,8 +887,11 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
 def mx_kv_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, stream=None) -> None:
     """zn_mx_kv_write: rows of k and v [tokens, kv_heads, head_dim] (BF16 or
     FP32) quantised into the cache at slots [tokens]; a token whose slot is
-    negative or past the last page is left out."""
+    negative or past the last page is left out.  No gradient: a k or v that
+    requires one is refused while gradients are recorded."""
     where = "mx_kv_write"
+    if k.requires_grad or v.requires_grad:
+        _mx_no_grad(where, k=k, v=v)
     dt = _mx_plain(where, "k", k.dtype)
     dev = _mx_device(where, stream, k, v, slots, *cache)
     c, (_, _, heads, dim, _) = _kv_cache(where, cache)

@@ -60,3 +60,14 @@ def test_a_wrong_hint_makes_no_grid_too_large():
         size = dict(tokens=1 << 29, heads=1, kv_heads=1, dim=dim, dtype=dtype)
         assert kernel_of(8192, 8, max_new=1, **size) != "short pairs"
         assert kernel_of(8192, 8, max_new=1, **dict(size, tokens=1 << 20)) == "short pairs"
+
+
+def test_binding_refuses_to_cut_keys_and_values_from_a_graph():
+    c = zn.mx_kv_cache(6, 2, 16, 64, device="cpu")
+    x = torch.zeros(5, 2, 64, dtype=torch.bfloat16)
+    g = torch.zeros(5, 2, 64, dtype=torch.bfloat16, requires_grad=True)
+    _raises(zn.mx_kv_write, g, x, c, i32(5), match="k requires a gradient")
+    _raises(zn.mx_kv_write, x, g * 2, c, i32(5), match="v requires a gradient")
+    _raises(zn.mx_kv_write, g.detach(), x, c, i32(5), match="not on a CUDA device")
+    with torch.no_grad():
+        _raises(zn.mx_kv_write, g, g, c, i32(5), match="not on a CUDA device")
