@@ -420,8 +420,9 @@ zn_status zn_kv_release(const int32_t *d_lens, const uint8_t *d_done, uint32_t b
 /* zn_mx_kv_write -- rows of keys and values (ZN_BF16 or ZN_FP32), quantised as
  * zn_mx_quantize does, into the cache.  Element d of token t's head h is at t *
  * token_stride + h * head_stride + d.  Tokens whose slot is negative or past
- * the last page are left out.  Slots of a call are distinct: of two tokens with
- * one slot, either one's blocks of 32 values are left there. */
+ * the last page are left out.  Slots of a call are to be distinct: where tokens
+ * share one, codes of any of them may be left there under the scale of another,
+ * not the same ones every time; other slots are as they should be. */
 zn_status zn_mx_kv_write(zn_dtype dtype, const void *d_k, uint64_t k_token_stride, uint64_t k_head_stride,
                          const void *d_v, uint64_t v_token_stride, uint64_t v_head_stride, const int32_t *d_slots,
                          uint64_t tokens, const zn_mx_cache *cache, hipStream_t stream);

@@ -887,7 +887,8 @@ def kv_release(lens: torch.Tensor, done: torch.Tensor, table: torch.Tensor, free
 def mx_kv_write(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, stream=None) -> None:
     """zn_mx_kv_write: rows of k and v [tokens, kv_heads, head_dim] (BF16 or
     FP32) quantised into the cache at slots [tokens]; a token whose slot is
-    negative or past the last page is left out.  No gradient: a k or v that
+    negative or past the last page is left out; what tokens that share a slot
+    leave there is not defined.  No gradient: a k or v that
     requires one is refused while gradients are recorded."""
     where = "mx_kv_write"
     if k.requires_grad or v.requires_grad:

@@ -33,3 +33,27 @@ def test_rows_read_back_are_a_programs_own(dtype, given):
     assert torch.equal(k.detach(), old_k * 2) and torch.equal(v, old_v) and not v.requires_grad
     # the sum over rows of what w multiplied: 12 values in whole 16ths (codes in halves, scales from 1/8), exact in FP32
     assert torch.equal(w.grad.float(), old_k.float().sum((0, 1)).to(dtype).float())
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+def test_tokens_that_share_a_slot_touch_no_other(t):
+    c, d = (random_cache(40, 2, 16, 64, 7) for _ in range(2))
+    tokens = 600
+    k, v = plain_rows(tokens, 2, 64, t, 1).cuda(), plain_rows(tokens, 2, 64, t, 2).cuda()
+    slots = np.random.default_rng(0).permutation(640)[:tokens]
+    shared = np.arange(tokens) % 3 == 0                           # far from each other: in several workgroups
+    zn.mx_kv_write(k, v, d, i32(np.where(shared, -1, slots).tolist()))
+    slots[shared] = slots[0]
+    zn.mx_kv_write(k, v, c, i32(slots.tolist()))
+    page, place = int(slots[0]) // 16, int(slots[0]) % 16
+    for i, x in ((0, k), (2, v)):
+        codes, scales = kv.rows(f64(x[torch.from_numpy(shared).cuda()]))
+        left, mine = c[i][page, :, place].cpu().numpy(), c[i + 1].view(torch.uint8)[page, :, place].cpu().numpy()
+        # four bytes at a time of one of the tokens, and a scale of one of them
+        for h in range(2):
+            assert all((codes[:, h, at:at + 4] == left[h, at:at + 4]).all(1).any() for at in range(0, 32, 4))
+            assert all((scales[:, h, b] == mine[h, b]).any() for b in range(2))
+        for a, b in ((c[i], d[i]), (c[i + 1], d[i + 1])):
+            a, b = a.view(torch.uint8).clone(), b.view(torch.uint8).clone()
+            a[page, :, place], b[page, :, place] = 0, 0
+            assert torch.equal(a, b)
