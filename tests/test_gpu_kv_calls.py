@@ -3,11 +3,10 @@ import numpy as np
 import pytest
 import torch
 
-from kv_kernels import KINDS, attention_by, widened
-from kv_util import check_attention, dealt, f64, i32, random_cache, values
+from kv_util import f64, i32, random_cache
 from lossless_float_weight_amd import zn
 from oracle import kv
-from test_gpu_kv import attend_case, plain_rows
+from test_gpu_kv import plain_rows
 
 pytestmark = pytest.mark.gpu
 
