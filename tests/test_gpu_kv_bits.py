@@ -37,17 +37,22 @@ def differences(n, t, seed=3):
     return torch.exp2(torch.rand(n, generator=g, dtype=torch.float64) * 16 - 14).to(TYPE[t])
 
 
-def pair_cache(n, page, at_a, at_b, device="cpu"):
-    """(k, v) codes and scales of n keys of 32 values: A's key is 0, B's -1 in place 0, the others' -768 in place 1."""
-    k = torch.zeros(n, 16, dtype=torch.uint8)
-    ks = torch.full((n, 1), 127, dtype=torch.uint8)
-    v = torch.full((n, 16), 0x77, dtype=torch.uint8)         # 6 where nothing should count
-    vs = torch.full((n, 1), 127, dtype=torch.uint8)
-    k[:, 0] = 0xF0                                            # -6 in place 1
-    ks[:] = 134
+def pair_cache(n, at_a, at_b, dim, block, apart=False):
+    """(k, v) codes and scales of n keys: in a block of 32 places A's key is 0, B's -1 in place 0, the others' -768 in
+    place 1.  apart: A's is 1 in place 0, B's 1 in place 2."""
+    k = torch.zeros(n, dim // 2, dtype=torch.uint8)
+    ks = torch.full((n, dim // 32), 127, dtype=torch.uint8)
+    v = torch.full((n, dim // 2), 0x77, dtype=torch.uint8)   # 6 where nothing should count
+    vs = torch.full((n, dim // 32), 127, dtype=torch.uint8)
+    at = 16 * block
+    k[:, at] = 0xF0                                           # -6 in place 1
+    ks[:, block] = 134
     k[at_a], ks[at_a], v[at_a] = 0, 127, 0x22                 # 1
     k[at_b], ks[at_b], v[at_b] = 0, 127, 0xAA                 # -1
-    k[at_b, 0] = 0x0A                                         # -1 in place 0
+    if apart:
+        k[at_a, at], k[at_b, at + 1] = 0x02, 0x02
+    else:
+        k[at_b, at] = 0x0A                                    # -1 in place 0
     return k, ks, v, vs
 
 
@@ -73,25 +78,50 @@ def test_the_bound_tells_pieces_apart(t, bits, enough, few):
     assert (off[enough] <= b).all() and (off[few] > b).sum() > 20
 
 
-def run_pairs(t, kind, n, page, at_a, at_b, **kw):
+def large_pairs(n):
+    """(s, s - d) for queries: s from 20 to 32 in 24 bits, and d from 2^-14 to 4 as FP32 has it."""
+    s = (20 + 12 * torch.rand(n, generator=torch.Generator().manual_seed(8), dtype=torch.float64)).float()
+    return s, (s.double() - differences(n, "fp32").double()).float()
+
+
+def large_bound(d, want):
+    """Scores of 32 on top: three pieces' products add to them exactly or within a half step each, 2 * 2^-24 * 32 a score."""
+    return bound(d, want, "fp32", 24) + 2 * 2.0 ** -24 * 32 * np.log(2)
+
+
+def test_the_bound_tells_pieces_of_queries_apart():
+    s, less = large_pairs(400)
+    d = s.double() - less.double()
+    want = np.tanh(d.numpy() * np.log(2) / 2)
+    off = {p: np.abs(np.tanh((rounded(s.double(), p) - rounded(less.double(), p)).numpy() * np.log(2) / 2) - want) for p in (3, 2)}
+    b = large_bound(d.numpy(), want)
+    assert (off[3] <= b).all() and (off[2] > b).sum() > 20
+
+
+def run_pairs(t, kind, n, page, at_a, at_b, dim=32, block=0, large=False, **kw):
     """(d, result) of 160 queries over n keys, by the kernel that `kind` names."""
     rows = 160
-    codes = pair_cache(n, page, at_a, at_b)
+    codes = pair_cache(n, at_a, at_b, dim, block, large)
     n_pages = -(-n // page)
-    c = zn.mx_kv_cache(n_pages, 1, page, 32)
+    c = zn.mx_kv_cache(n_pages, 1, page, dim)
     for to, x in zip(c, codes):
         to.view(torch.uint8).view(n_pages * page, -1)[:n] = x.cuda()
     d = differences(rows, t)
-    q = torch.zeros(rows, 1, 32, dtype=TYPE[t])
-    q[:, 0, 0] = d
-    q[:, 0, 1] = 1
+    q = torch.zeros(rows, 1, dim, dtype=TYPE[t])
+    q[:, 0, 32 * block] = d
+    q[:, 0, 32 * block + 1] = 1
+    if large:
+        q[:, 0, 32 * block], q[:, 0, 32 * block + 2] = large_pairs(rows)
+        d = q[:, 0, 32 * block].double() - q[:, 0, 32 * block + 2].double()
     # the kernel goes by the sizes that the host sees: one with many queries, the hint of one, the table's width
     tiles = {"short": n_pages * page // 64, "few": 3000, "many": 20480}[kind]
     width = max(n_pages, tiles * 64 // page)
     table = torch.full((1, width), -1, dtype=torch.int32)
     table[0, :n_pages] = torch.arange(n_pages)
-    out = zn.mx_attention(q.cuda(), c, table.cuda(), i32([n]), i32([0, rows]), max_new=rows if kind == "many" else 1, causal=False,
-                          scale=LN2, **kw)
+    hint = rows if kind == "many" else 1
+    args = (q.cuda(), c, table.cuda(), i32([n]), i32([0, rows]))
+    assert zn.debug_attention_kernel(args[0], c, args[2], args[4], hint).startswith(kind)
+    out = zn.mx_attention(*args, max_new=hint, causal=False, scale=LN2, **kw)
     return f64(d), f64(out)
 
 
@@ -104,6 +134,27 @@ def test_weights_keep_their_bits(n, at_a, at_b, kind, t):
     want = np.tanh(d * np.log(2) / 2)[:, None, None]
     b = bound(d[:, None, None], want, t, 17 if t == "bf16" else 24)
     worst = (np.abs(out - want) / b).max()
+    assert worst <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["short", "few", "many"])
+@pytest.mark.parametrize("dim,block", [(64, 1), (96, 0), (96, 2), (128, 3), (160, 4), (192, 1), (224, 6), (256, 7)])
+def test_weights_keep_their_bits_in_every_head_size(dim, block, kind, t):
+    d, out = run_pairs(t, kind, 130, 64, 100, 20, dim, block)
+    want = np.tanh(d * np.log(2) / 2)[:, None, None]
+    worst = (np.abs(out - want) / bound(d[:, None, None], want, t, 17 if t == "bf16" else 24)).max()
+    assert worst <= 1
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["short", "few", "many"])
+@pytest.mark.parametrize("dim,block", [(32, 0), (64, 0), (96, 1), (128, 2), (160, 4), (192, 5), (224, 3), (256, 6)])
+def test_queries_keep_their_bits(dim, block, kind):
+    d, out = run_pairs("fp32", kind, 130, 64, 20, 100, dim, block, large=True)
+    want = np.tanh(d * np.log(2) / 2)[:, None, None]
+    worst = (np.abs(out - want) / large_bound(d[:, None, None], want)).max()
     assert worst <= 1
 
 
