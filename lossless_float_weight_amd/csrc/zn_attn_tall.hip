@@ -11,9 +11,11 @@
 // by all four waves, into one of two places in LDS while the other is used: one
 // barrier a tile.
 //
-// A prompt of 8192 queries, 32 heads, takes 741 us, 0.74 PFLOP/s.  Matrix and vector
-// instructions run beside each other little: two waves, one of each kind, take 0.83 of
-// the sum of their times.
+// A prompt of 8192 queries, 32 heads, takes 741 to 776 us, 0.72 PFLOP/s, or 1.09 with the
+// second product that weights of 16 bits take: the matrix units are busy 49% of the
+// cycles and the vector units 57% (exponentials, conversions, the split of the weights),
+// and the two run beside each other little: two waves, one of each kind, take 0.83 of the
+// sum of their times.
 #include <algorithm>
 
 #include "zn_attn.h"
@@ -24,7 +26,7 @@ namespace {
 constexpr uint32_t kRows = 128;     // of a workgroup
 constexpr uint32_t kThreads = 256;
 // Tiles of a piece at least.  A piece of 128 rows is 67 KB that the join reads back: 16
-// requests of 1000 keys, 64 queries each, 56 us with pieces of 8 tiles, 42 with 16; a
+// requests of 1000 keys, 64 queries each, 60 us with pieces of 8 tiles, 44 with 16; a
 // group by itself loses (one request of 1000 keys, 64 queries: 24 us with 4, 37 with
 // 16), but so little work is not taken here.
 constexpr uint32_t kLeast = 16;
@@ -186,8 +188,8 @@ struct Rows32 {
 //   Otherwise weights in BF16 pieces (two beside BF16 queries, three beside FP32),
 // a product each, and values in BF16, exact whatever their scales.
 // The first takes two thirds of the matrix instructions and three quarters of the
-// others: 8192 queries of 32 heads 585 us for 750, 64 x 4096 keys of 128 rows 178 for
-// 216.
+// others: 8192 queries of 32 heads 609 us for 769, 64 x 4096 keys of 128 rows 179 for
+// 220 (one card).
 template <int DT, int NB, bool HALF>
 __device__ __forceinline__ bool take_tiles(const AttnArgs &a, const Request &rq, const int32_t *pages, uint32_t head,
                                            uint32_t t, uint32_t end, float c, typename Shape<DT, NB>::Lds &lds,
