@@ -56,3 +56,13 @@ def test_tokens_that_share_a_slot_touch_no_other(t):
             a, b = a.view(torch.uint8).clone(), b.view(torch.uint8).clone()
             a[page, :, place], b[page, :, place] = 0, 0
             assert torch.equal(a, b)
+
+
+def test_a_table_without_columns():
+    # nothing fits but what asks for nothing
+    none = torch.zeros(3, 0, dtype=torch.int32, device="cuda")
+    step = zn.kv_extend(i32([0, 0, 0]), i32([2, 0, 1]), none, i32([4, 5]), i32([2]), 16, 8, 5)
+    assert step.lens.tolist() == [0, 0, 0] and step.starts.tolist() == [0, 2, 2, 3] and step.n_free.tolist() == [2]
+    assert step.slots.tolist() == [-1] * 5 and step.positions.tolist() == [0] * 5
+    lens, n = zn.kv_release(i32([7, 0, 3]), torch.ones(3, dtype=torch.bool, device="cuda"), none, i32([4, 5]), i32([2]), 16)
+    assert lens.tolist() == [0, 0, 0] and n.tolist() == [2]

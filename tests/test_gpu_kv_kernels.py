@@ -289,3 +289,36 @@ def test_a_loop_in_which_requests_are_refused():
                 np.testing.assert_array_equal(x[tb[b][i // page], :, i % page], held[b][:, j])
         check_attention(q, c, tb, want[0], at.tolist(), page, out)
     assert refused >= 2 and served_later >= 1
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["few rows", "many rows"])
+def test_the_most_heads(kind, t):
+    # 1024 key heads leave one to four waves, or pieces of work, for each
+    lens, new = [200, 0, 70, 33], [40, 0, 70, 2]
+    q, c, table, starts = attend_case(lens, new, 1024, 1024, 32, 16, t, 5)
+    out, lse = attention_by(kind)(q, c, i32(table.tolist()), i32(lens), i32(starts), lse=True)
+    for h in (slice(0, 3), slice(127, 130), slice(510, 514), slice(769, 771), slice(1021, 1024)):
+        part = zn.MxCache(*(x[:, h] for x in c))
+        check_attention(q[:, h], part, table, lens, starts, 16, out[:, h], lse[:, h])
+
+
+@pytest.mark.parametrize("t", ["bf16", "fp32"])
+@pytest.mark.parametrize("kind", ["short pairs", "few rows", "many rows"])
+def test_the_most_requests(kind, t):
+    rng = np.random.default_rng(2)
+    lens = rng.integers(0, 60, 8192).tolist()
+    new = rng.integers(0, 3, 8192).tolist()
+    if kind != "short pairs":
+        lens[17], lens[8191] = 3000, 2500
+    if kind == "many rows":
+        new[17], new[8000] = 200, 33
+    pool = 400                                                     # pages that requests share
+    c = random_cache(pool, 1, 16, 32, 4)
+    width = -(-max(lens) // 16)
+    table = rng.integers(0, pool, (8192, width))
+    starts = np.concatenate([[0], np.cumsum(new)])
+    q = torch.randn(int(starts[-1]), 2, 32, generator=torch.Generator().manual_seed(1)).to(
+        torch.bfloat16 if t == "bf16" else torch.float32).cuda()
+    out, lse = attention_by(kind)(q, c, i32(table.tolist()), i32(lens), i32(starts.tolist()), lse=True)
+    check_attention(q, c, table, lens, starts.tolist(), 16, out, lse)
