@@ -476,9 +476,10 @@ zn_status zn_mx_kv_read(const zn_mx_cache *cache, const int32_t *d_slots, uint64
  * head) their weights are held in FP16, 11 bits and at worst 2^-32 of the row's
  * largest, which takes a third of the matrix instructions off.  A result is off
  * by up to 2^-11 of the sum of softmax |v|, so what cancels can keep few bits.
- * (Over random keys and values the errors' norm is 3e-5 of the results', whose
- * own rounding has 1.7e-3.)  Whether a call has many rows goes by its sizes and
- * max_new; others ignore the flag. */
+ * (A prompt's results over random keys and values differ by 6e-4 to 7e-4 of their
+ * norm from those without the flag; each has 1.7e-3 by its own rounding.)
+ * Whether a call has many rows goes by its sizes and max_new; others ignore the
+ * flag. */
 enum { ZN_MX_FAST_WEIGHTS = 1 };
 typedef struct zn_mx_attention_args {
   zn_dtype dtype;                       /* of q and out */
